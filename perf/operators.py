@@ -155,6 +155,7 @@ def prepare(case, seed):
         n_used = int(used.sum())
         s["free_blocks"] = perm.clone()
         s["free_range"] = torch.tensor([n_used, num_blocks], **i32)
+        s["plan"] = [torch.empty(n, **i32) for n in (B + 1, B, T, T, 2)]  # a server's own buffers
         return s
     Hkv, d = case["kv_heads"], case["dim"]
     s["pool"] = _e4m3((num_blocks, LAYERS, 2, Hkv, bl, d), seed, 1)
@@ -169,6 +170,7 @@ def prepare(case, seed):
     else:
         s["q"] = torch.randn((T, case["q_heads"], d), generator=_generator(seed, 5), device=DEV).to(torch.bfloat16)
         s["out"] = torch.empty_like(s["q"])
+        s["workspace"] = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
     return s
 
 
@@ -279,14 +281,14 @@ def run(s):
         from attention_cached_kv_gb300 import binding
         if op == "plan":
             p = binding.gist_paged_plan(s["cached_len"], s["new_len"], s["block_table"], s["free_blocks"], s["free_range"],
-                                        dims=s["dims"])
+                                        s["plan"], dims=s["dims"])
             return {"block_table": s["block_table"], "q_start": p.q_start, "kv_len": p.kv_len, "slot": p.slot,
                     "position": p.position, "free_range": p.free_range}
         if op == "append":
             binding.gist_kv_append_fp8(s["k"], s["v"], s["pool"], s["scale"], s["slot"], s["position"], dims=s["dims"])
             return {"pool": s["pool"], "scale": s["scale"]}
         return binding.gist_attn_paged_fp8kv(s["q"], s["pool"], s["scale"], s["block_table"], s["q_start"], s["kv_len"],
-                                             s["out"], dims=s["dims"])
+                                             s["out"], s["workspace"], dims=s["dims"])
     return {"plan": _plain_plan, "append": _plain_append, "attn": _plain_attn}[op](s)
 
 
