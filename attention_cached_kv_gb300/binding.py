@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -18,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libgistattn.so")
 
 OK, ERR_NULL, ERR_DIMS, ERR_UNSUPPORTED, ERR_ALIGN, ERR_LAUNCH, ERR_SCRATCH = 0, -1, -2, -3, -4, -5, -6
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GIST_ATTN_NOALLOC_SCRATCH_BYTES
-STATUS_BAD_BLOCK, STATUS_TIMEOUT, STATUS_RANGE = 1, 2, 4
+STATUS_BAD_BLOCK, STATUS_TIMEOUT, STATUS_RANGE, STATUS_NOT_SERVED = 1, 2, 4, 8
 FLAG_PREROTATED = 1
 FLAG_TEST_WITHHOLD = 2  # tests of the timeout path only (see the header)
 # gist_attn_route: entry points and the kernels they run (GIST_ATTN_ENTRY_* / _ROUTE_*)
@@ -29,7 +30,9 @@ ROUTES = {0: "none", 1: "prefill_tc", 2: "prefill_long", 3: "prefill_stream", 4:
 EXPORTS = ("gist_attn_fwd", "gist_attn_workspace_bytes", "gist_attn_fwd_ws", "gist_attn_fwd_noalloc", "gist_attn_fwd_fp8kv", "gist_attn_fwd_block_mass", "gist_kv_append",
            "gist_attn_fwd_gist_mask", "gist_kv_store", "gist_qkv_rope", "gist_out_proj",
            "gist_attn_gather_debug", "gist_kv_bytes_per_position", "gist_kv_bytes_per_item",
-           "gist_kv_bytes_batch", "gist_attn_status_string", "gist_attn_route")
+           "gist_kv_bytes_batch", "gist_attn_status_string", "gist_attn_route",
+           "gist_paged_plan", "gist_kv_append_fp8", "gist_attn_paged_workspace_bytes",
+           "gist_attn_paged_fp8kv")
 
 
 class GistAttnError(RuntimeError):
@@ -56,6 +59,37 @@ class Dims(ctypes.Structure):
         ("status", ctypes.c_void_p),
         ("flags", ctypes.c_int32),
     ]
+
+
+class PagedDims(ctypes.Structure):
+    """Mirror of gist_paged_dims."""
+    _fields_ = [
+        ("num_requests", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("block_len", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("num_layers", ctypes.c_int32),
+        ("layer", ctypes.c_int32),
+        ("rope_theta", ctypes.c_float),
+        ("softmax_scale", ctypes.c_float),
+        ("status", ctypes.c_void_p),
+        ("flags", ctypes.c_int32),
+    ]
+
+
+class PagedPlan(NamedTuple):
+    """What gist_paged_plan writes (int32): q_start [B + 1], kv_len [B], slot [T],
+    position [T], free_range [2] (the free blocks left after the step)."""
+    q_start: torch.Tensor
+    kv_len: torch.Tensor
+    slot: torch.Tensor
+    position: torch.Tensor
+    free_range: torch.Tensor
 
 
 _lock = threading.Lock()
@@ -109,6 +143,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             lib.gist_attn_status_string.argtypes = [ctypes.c_int]
             lib.gist_attn_route.restype = ctypes.c_int
             lib.gist_attn_route.argtypes = [ctypes.c_int, ctypes.POINTER(Dims)]
+            PD = ctypes.POINTER(PagedDims)
+            lib.gist_paged_plan.restype = ctypes.c_int
+            lib.gist_paged_plan.argtypes = [V, V, V, V, ctypes.c_int32, V, V, V, V, V, V, PD, V]
+            lib.gist_kv_append_fp8.restype = ctypes.c_int
+            lib.gist_kv_append_fp8.argtypes = [V, V, V, V, V, V, PD, V]
+            lib.gist_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+            lib.gist_attn_paged_workspace_bytes.argtypes = [PD]
+            lib.gist_attn_paged_fp8kv.restype = ctypes.c_int
+            lib.gist_attn_paged_fp8kv.argtypes = [V, V, V, V, V, V, V, V, ctypes.c_size_t, PD, V]
             _lib = lib
     return _lib
 
@@ -392,3 +435,115 @@ def kv_bytes_per_item(L, Hkv, d, k, elem_bytes) -> int:
 
 def kv_bytes_batch(B, L, T, Hkv, d, elem_bytes) -> int:
     return int(load_library().gist_kv_bytes_batch(B, L, T, Hkv, d, elem_bytes))
+
+
+# ------------------------------------------------- the ragged serving step ---
+
+_PAGED_FIELDS = tuple(n for n, _ in PagedDims._fields_ if n not in ("status", "flags"))
+
+
+def make_paged_dims(d: dict, status: torch.Tensor | None = None) -> PagedDims:
+    out = PagedDims(*[d[n] for n in _PAGED_FIELDS])
+    out.flags = d.get("flags", 0)
+    if status is not None:
+        _check(status, torch.int32, "status")
+        out.status = status.data_ptr()
+    return out
+
+
+def _sized(t, dtype, name, numel, device):
+    """Raw pointer of a contiguous CUDA tensor on `device` with at least `numel` elements."""
+    _check(t, dtype, name)
+    if t.device != device:
+        raise TypeError(f"{name} must be on {device}, got {t.device}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, the dimensions need {numel}")
+    return t.data_ptr()
+
+
+def _pool_ptr(pool, dims, device):
+    if not isinstance(pool, torch.Tensor) or pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError("kv_pool_e4m3 must be float8_e4m3fn or uint8")
+    n = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
+    return _sized(pool, pool.dtype, "kv_pool_e4m3", n * dims["block_len"] * dims["head_dim"], device), n
+
+
+def _call(device, fn, *args, stream):
+    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
+    if torch.cuda.current_device() == device.index:
+        _raise(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _raise(fn(*args, _stream(stream)))
+
+
+def gist_paged_plan(cached_len, new_len, block_table, free_blocks, free_range, out=None, *,
+                    dims: dict, status: torch.Tensor | None = None, stream=None) -> PagedPlan:
+    """Blocks, slots and positions of one step from the requests' lengths (int32
+    CUDA tensors throughout); writes the entries of newly taken blocks into
+    block_table and returns a PagedPlan.  `out`: five int32 tensors in PagedPlan's
+    order to write into (allocated if None), so that a captured step keeps its
+    buffers."""
+    lib = load_library()
+    B, T, i32, dev = dims["num_requests"], dims["num_tokens"], torch.int32, new_len.device
+    plan = PagedPlan(*(out if out is not None else
+                       (torch.empty(n, dtype=i32, device=dev) for n in (B + 1, B, T, T, 2))))
+    D = make_paged_dims(dims, status)
+    _call(dev, lib.gist_paged_plan, _sized(cached_len, i32, "cached_len", B, dev),
+          _sized(new_len, i32, "new_len", B, dev),
+          _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
+          _sized(free_blocks, i32, "free_blocks", 0, dev), free_blocks.numel(),
+          _sized(free_range, i32, "free_range", 2, dev), _sized(plan.q_start, i32, "q_start", B + 1, dev),
+          _sized(plan.kv_len, i32, "kv_len", B, dev), _sized(plan.slot, i32, "slot", T, dev),
+          _sized(plan.position, i32, "position", T, dev),
+          _sized(plan.free_range, i32, "free_range (out)", 2, dev), ctypes.byref(D), stream=stream)
+    return plan
+
+
+def gist_kv_append_fp8(k_new, v_new, kv_pool_e4m3, kv_scale, slot, position=None, *, dims: dict,
+                       status: torch.Tensor | None = None, stream=None):
+    """Writes T new tokens' K (rotated at `position`) and V into the E4M3 pool at
+    their slots, growing block scales where needed (pool and scales in place)."""
+    lib = load_library()
+    T, n, dev = dims["num_tokens"], dims["num_tokens"] * dims["num_kv_heads"] * dims["head_dim"], k_new.device
+    bf, i32 = torch.bfloat16, torch.int32
+    pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
+    D = make_paged_dims(dims, status)
+    _call(dev, lib.gist_kv_append_fp8, _sized(k_new, bf, "k_new", n, dev), _sized(v_new, bf, "v_new", n, dev),
+          pool, _sized(kv_scale, torch.float32, "kv_scale", planes, dev), _sized(slot, i32, "slot", T, dev),
+          None if position is None else _sized(position, i32, "position", T, dev), ctypes.byref(D),
+          stream=stream)
+    return kv_pool_e4m3, kv_scale
+
+
+def paged_workspace_bytes(dims: dict) -> int:
+    """Device bytes gist_attn_paged_fp8kv needs for these dimensions."""
+    D = make_paged_dims(dims)
+    return int(load_library().gist_attn_paged_workspace_bytes(ctypes.byref(D)))
+
+
+def gist_attn_paged_fp8kv(q, kv_pool_e4m3, kv_scale, block_table, q_start, kv_len, out=None,
+                          workspace=None, *, dims: dict, status: torch.Tensor | None = None,
+                          stream=None):
+    """Causal attention of every request's new tokens over its cached sequence,
+    which already holds them; returns `out` [T][Hq][d] (allocated if None; rows of
+    padding tokens are not written).  `workspace`: a uint8 tensor of at least
+    paged_workspace_bytes(dims) bytes, one per call in flight (allocated if None)."""
+    lib = load_library()
+    B, dev = dims["num_requests"], q.device
+    if out is None:
+        out = torch.empty_like(q)
+    bf, i32 = torch.bfloat16, torch.int32
+    n = dims["num_tokens"] * dims["num_q_heads"] * dims["head_dim"]
+    pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
+    D = make_paged_dims(dims, status)
+    if workspace is None:
+        need = int(lib.gist_attn_paged_workspace_bytes(ctypes.byref(D)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(dev, lib.gist_attn_paged_fp8kv, _sized(q, bf, "q", n, dev), pool,
+          _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
+          _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
+          _sized(q_start, i32, "q_start", B + 1, dev), _sized(kv_len, i32, "kv_len", B, dev),
+          _sized(out, bf, "out", n, dev), _sized(workspace, torch.uint8, "workspace", 0, dev),
+          workspace.numel(), ctypes.byref(D), stream=stream)
+    return out

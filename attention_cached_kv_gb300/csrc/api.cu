@@ -463,13 +463,17 @@ extern "C" const char* gist_attn_status_string(int status) {
     case GIST_ATTN_ERR_ALIGN: return "a pointer is not aligned as required";
     case GIST_ATTN_ERR_LAUNCH: return "the CUDA launch failed";
     case GIST_ATTN_ERR_SCRATCH:
-      return "the call needs more scratch than the library's fixed no-allocation array holds";
+      return "the call needs more scratch than it was given or the library's fixed no-allocation array holds";
     case GIST_ATTN_STATUS_BAD_BLOCK: return "device: a block id was out of range (pair zeroed)";
     case GIST_ATTN_STATUS_TIMEOUT: return "device: a bounded wait on an asynchronous copy gave up";
     case GIST_ATTN_STATUS_BAD_BLOCK | GIST_ATTN_STATUS_TIMEOUT:
       return "device: out-of-range block id and a timed-out wait";
     case GIST_ATTN_STATUS_RANGE:
       return "device: a softmax row was not finite in fp32 (a NaN input or values near the fp32 limit)";
+    case GIST_ATTN_STATUS_NOT_SERVED:
+      return "device: a request was not served in this step (lengths, table, token rows or free blocks)";
+    case GIST_ATTN_STATUS_NOT_SERVED | GIST_ATTN_STATUS_BAD_BLOCK:
+      return "device: out-of-range block id and a request not served";
     default: return status < 0 ? "unknown error" : "unknown device status bits";
   }
 }

@@ -70,6 +70,41 @@ int launch_qkv_rope(const Problem& pb, const void* x, const void* w, int d_model
 int launch_out_proj(const Problem& pb, const void* attn, const void* w, int d_model, void* y,
                     cudaStream_t stream);
 
+// ---- the ragged serving step (paged_*.cu) ----
+struct PagedProblem {
+  const void* q;
+  void* out;
+  const uint8_t* pool;  // E4M3
+  const float* scale;
+  const int32_t* block_table;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  int32_t* status;
+  int B, T, max_new, Hq, Hkv, G, d, block_len, W, num_blocks, L, layer, flags;
+  float scale_log2;      // softmax scale * log2(e)
+  uint64_t turn[64];     // RoPE: theta_j / 2 pi modulo 1, in units of 2^-64 (0: no rotation)
+};
+struct PlanArgs {
+  const int32_t* cached_len;
+  const int32_t* new_len;
+  int32_t* block_table;
+  const int32_t* free_blocks;
+  const int32_t* free_range;
+  int32_t* q_start;
+  int32_t* kv_len;
+  int32_t* slot;
+  int32_t* position;
+  int32_t* free_range_out;
+  int32_t* status;
+  int B, T, block_len, W, num_blocks, num_free;
+};
+int launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
+int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v_new, void* pool,
+                        float* scale, const int32_t* slot, const int32_t* position,
+                        cudaStream_t stream);
+int launch_paged_attn(const PagedProblem& pb, void* workspace, cudaStream_t stream);
+size_t paged_attn_workspace(const PagedProblem& pb);
+
 // Whether the prefill kernel can hold this problem's tiles in shared memory.
 bool prefill_fits(const Problem& pb);
 bool prefill_tc_fits(const Problem& pb);

@@ -1,0 +1,240 @@
+// paged_append.cu -- new tokens' K/V into the E4M3 paged pool
+// ([KV page, "Reusable-state"]: the new K/V are appended to the cache;
+// [Suffix page, §2 and the end of §5]: one byte an element).
+//
+// A block's scale is a power of two, so a code's precision does not depend on it
+// (E4M3's four significant bits) and rescaling a block's earlier rows when its
+// scale grows is exact but for subnormal codes.  It is chosen from the unrotated
+// keys (|R(k)| <= sqrt 2 max |k|, hence 316 in 448's place): one pass finds it
+// without a sine, and it does not hang on how a rotation rounds.
+//
+// A unit is the new tokens of one block (consecutive rows, some perhaps skipped), a
+// KV head and K or V; one CTA takes the units whose first token lies in its `chunk`
+// tokens.  A thread holds elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row,
+// so it rotates its own pairs with four sines, and the rows stay in registers
+// between the pass for the largest magnitude and the one that converts.
+// Bound: HBM (three bytes an element: bf16 in, E4M3 out); few tokens: latency.
+//
+// Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
+//        [Suffix page] icman.com.cn news 64898.
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace gattn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kHold = 8;  // rows a thread keeps in registers
+
+struct PagedAppendParams {
+  const bf16* x[2];  // k_new, v_new
+  uint8_t* pool;
+  float* scale;
+  const int32_t* slot;
+  const int32_t* position;
+  int32_t* status;
+  int T, Hkv, block_len, num_blocks, L, layer, chunk;
+  uint64_t turn[64];
+};
+
+// |x| of finite bf16 values as bits, 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t finite_abs2(uint32_t v) {  // max of the two halves
+  uint32_t a = v & 0x7fffu, b = (v >> 16) & 0x7fffu;
+  a = a < 0x7f80u ? a : 0u;
+  b = b < 0x7f80u ? b : 0u;
+  return max(a, b);
+}
+
+// Codes of a and b (already divided by the scale); non-finite x become NaN.
+__device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
+  uint32_t r = (uint32_t)e4m3x2(f[0], f[1]) | (uint32_t)e4m3x2(f[2], f[3]) << 16;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (!(fabsf(f[e]) <= 3.4e38f)) r = (r & ~(0xffu << (8 * e))) | (0x7fu << (8 * e));
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    append_fp8_kernel(const __grid_constant__ PagedAppendParams prm) {
+  constexpr int kLanes = D / 8;               // threads of a row
+  constexpr int kRows = kThreads / kLanes;    // rows of a pass
+  __shared__ uint32_t red[kThreads / 32];
+  __shared__ int run_len;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kv = blockIdx.y & 1, g = blockIdx.y >> 1;
+  const int bl = prm.block_len, j = (tid % kLanes) * 4, row0 = tid / kLanes;
+  const bf16* x = prm.x[kv];
+  const int t0 = blockIdx.x * prm.chunk, t1 = min(t0 + prm.chunk, prm.T);
+  const bool rotate = kv == 0 && prm.position != nullptr;
+
+  const unsigned rows_in_pool = (unsigned)prm.num_blocks * bl;
+  auto skipped = [&](int s) { return (unsigned)s >= rows_in_pool; };  // negative or outside
+  for (int t = t0; t < t1; ++t) {
+    const int s = prm.slot[t];
+    if (skipped(s)) {
+      if (s >= 0 && tid == 0) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+      continue;
+    }
+    const int blk = s / bl, off = s - blk * bl;
+    // Token t opens the block's unit unless an earlier token of the call lies in the
+    // block: entry t - i of the slots is then s - i, with skipped ones between.
+    bool inside = off > 0 && t > 0 && prm.slot[t - 1] == s - 1;
+    if (off > 0 && t > 0 && skipped(prm.slot[t - 1])) {
+      bool found = false;
+      for (int i = 1 + tid; i <= min(off, t); i += kThreads) found |= prm.slot[t - i] == s - i;
+      inside = __syncthreads_or(found);
+    }
+    if (inside) continue;
+    // its tokens: entries t + e that are s + e, up to one that is neither that nor skipped
+    const int most = min(bl - off, prm.T - t);
+    int len = most;
+    bool holes = false;
+    for (int i = 0; i < most; i += kThreads) {
+      if (tid == 0) run_len = most;
+      __syncthreads();
+      const int e = i + tid, v = e < most ? prm.slot[t + e] : s + e;
+      if (!skipped(v) && v != s + e) atomicMin(&run_len, e);
+      holes |= __syncthreads_or(skipped(v));
+      len = run_len;
+      __syncthreads();
+      if (len < most) break;
+    }
+    if (holes) {  // up to the last token that is there
+      if (tid == 0) run_len = 0;
+      __syncthreads();
+      for (int e = tid; e < len; e += kThreads)
+        if (!skipped(prm.slot[t + e])) atomicMax(&run_len, e + 1);
+      __syncthreads();
+      len = run_len;
+      __syncthreads();
+    }
+    auto live = [&](int i) { return i < len && (!holes || !skipped(prm.slot[t + i])); };
+
+    const int64_t plane = (((int64_t)blk * prm.L + prm.layer) * 2 + kv) * prm.Hkv + g;
+    const bf16* src = x + ((int64_t)t * prm.Hkv + g) * D + j;
+    const int64_t pitch = (int64_t)prm.Hkv * D;
+    uint2 lo[kHold], hi[kHold];
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < kHold; ++p) {
+      const int i = row0 + p * kRows;
+      lo[p] = hi[p] = make_uint2(0, 0);
+      if (live(i)) {
+        lo[p] = *reinterpret_cast<const uint2*>(src + i * pitch);
+        hi[p] = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
+      }
+      top = max(top, max(max(finite_abs2(lo[p].x), finite_abs2(lo[p].y)),
+                         max(finite_abs2(hi[p].x), finite_abs2(hi[p].y))));
+    }
+    for (int i = row0 + kHold * kRows; i < len; i += kRows) {
+      if (!live(i)) continue;
+      const uint2 a = *reinterpret_cast<const uint2*>(src + i * pitch);
+      const uint2 b = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
+      top = max(top, max(max(finite_abs2(a.x), finite_abs2(a.y)), max(finite_abs2(b.x), finite_abs2(b.y))));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) red[warp] = top;
+    const float old = off > 0 ? prm.scale[plane] : 0.f;
+    __syncthreads();
+    top = max(max(red[0], red[1]), max(red[2], red[3]));
+    // the smallest power of two >= top / limit (limit / 512 = 0.875 or 0.6171875)
+    const uint32_t bits = top << 16;
+    const int e2 = (int)(bits >> 23) - 126;  // top = m 2^e2, m in [0.5, 1)
+    const float m = __uint_as_float((bits & 0x7fffffu) | 0x3f000000u);
+    int e = m <= (rotate ? 0.6171875f : 0.875f) ? e2 - 9 : e2 - 8;
+    e = top == 0 ? -100 : min(max(e, -100), 119);
+    const float need = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float scale = fmaxf(old, need);
+    uint8_t* dst = prm.pool + plane * bl * D + (int64_t)off * D + j;
+    if (off > 0 && scale > old) {  // the earlier rows (skipped ones too) at the larger scale
+      const float f = old / scale;
+      uint32_t* rows = reinterpret_cast<uint32_t*>(prm.pool + plane * bl * D);
+      for (int i = tid; i < (off + (holes ? len : 0)) * (D / 4); i += kThreads) {
+        if (i >= off * (D / 4) && live(i / (D / 4) - off)) continue;
+        const uint32_t c = rows[i];
+        const float2 a = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)c));
+        const float2 b = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(c >> 16)));
+        const float v[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
+        rows[i] = encode4(v);
+      }
+    }
+    if (tid == 0 && (off == 0 || scale > old)) prm.scale[plane] = scale;
+    const float inv = 1.f / scale;
+    auto put = [&](int i, uint2 a, uint2 b) {
+      float f[4], h[4];
+      const float2 a0 = bf16x2_to_float2(a.x), a1 = bf16x2_to_float2(a.y);
+      const float2 b0 = bf16x2_to_float2(b.x), b1 = bf16x2_to_float2(b.y);
+      // times 1 / scale first: a rotation of the largest bf16 values cannot overflow then
+      const float xs[4] = {a0.x * inv, a0.y * inv, a1.x * inv, a1.y * inv};
+      const float ys[4] = {b0.x * inv, b0.y * inv, b1.x * inv, b1.y * inv};
+      if (rotate) {
+        const int pos = prm.position[t + i];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float sn, cs;
+          __sincosf(turn_angle(pos, prm.turn[j + q]), &sn, &cs);
+          f[q] = xs[q] * cs - ys[q] * sn;
+          h[q] = ys[q] * cs + xs[q] * sn;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f[q] = xs[q];
+          h[q] = ys[q];
+        }
+      }
+      *reinterpret_cast<uint32_t*>(dst + (int64_t)i * D) = encode4(f);
+      *reinterpret_cast<uint32_t*>(dst + (int64_t)i * D + D / 2) = encode4(h);
+    };
+#pragma unroll
+    for (int p = 0; p < kHold; ++p) {
+      const int i = row0 + p * kRows;
+      if (live(i)) put(i, lo[p], hi[p]);
+    }
+    for (int i = row0 + kHold * kRows; i < len; i += kRows)
+      if (live(i))
+        put(i, *reinterpret_cast<const uint2*>(src + i * pitch),
+            *reinterpret_cast<const uint2*>(src + i * pitch + D / 2));
+    __syncthreads();  // `red` is free again
+  }
+}
+
+}  // namespace
+
+int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v_new, void* pool,
+                        float* scale, const int32_t* slot, const int32_t* position,
+                        cudaStream_t stream) {
+  PagedAppendParams prm{};
+  prm.x[0] = static_cast<const bf16*>(k_new);
+  prm.x[1] = static_cast<const bf16*>(v_new);
+  prm.pool = static_cast<uint8_t*>(pool);
+  prm.scale = scale;
+  prm.slot = slot;
+  prm.position = (pb.flags & GIST_ATTN_FLAG_PREROTATED) ? nullptr : position;
+  prm.status = pb.status;
+  prm.T = pb.T;
+  prm.Hkv = pb.Hkv;
+  prm.block_len = pb.block_len;
+  prm.num_blocks = pb.num_blocks;
+  prm.L = pb.L;
+  prm.layer = pb.layer;
+  for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
+  // A token a CTA while there are few (each may be a run of its own); more for
+  // long inputs, whose tokens mostly continue a run.
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  const int64_t units = (int64_t)pb.T * 2 * pb.Hkv;
+  prm.chunk = (int)(units <= 16LL * sms ? 1 : units / (16LL * sms) < 16 ? units / (16LL * sms) : 16);
+  if (2LL * pb.Hkv > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)((pb.T + prm.chunk - 1) / prm.chunk), (unsigned)(2 * pb.Hkv));
+  if (pb.d == 64)
+    append_fp8_kernel<64><<<grid, kThreads, 0, stream>>>(prm);
+  else
+    append_fp8_kernel<128><<<grid, kThreads, 0, stream>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+}  // namespace gattn

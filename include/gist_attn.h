@@ -55,7 +55,9 @@ extern "C" {
 #define GIST_ATTN_ERR_ALIGN (-4)       /* a pointer is not aligned as required          */
 #define GIST_ATTN_ERR_LAUNCH (-5)      /* the CUDA launch itself failed                 */
 #define GIST_ATTN_ERR_SCRATCH (-6)     /* gist_attn_fwd_noalloc: the call needs more
-                                          scratch than the library's fixed array holds */
+                                          scratch than the library's fixed array holds;
+                                          gist_attn_paged_fp8kv: the workspace is
+                                          missing, misaligned or too small             */
 
 /* Device status bits (OR-ed into *dims->status). */
 #define GIST_ATTN_STATUS_BAD_BLOCK 1 /* a block id was outside [0, num_blocks): that
@@ -68,6 +70,8 @@ extern "C" {
                                         (Values past the f16 range alone do not set it:
                                         the kernels that form q.K in f16 recompute the
                                         rows they reach in fp32.)                      */
+#define GIST_ATTN_STATUS_NOT_SERVED 8 /* gist_paged_plan: a request got no blocks or
+                                        tokens in this step (kv_len 0, slots -1)      */
 
 typedef struct {
   int32_t num_pairs;       /* P >= 0: pairs (or decode sequences) in this call          */
@@ -398,6 +402,134 @@ const char* gist_attn_status_string(int status);
 #define GIST_ATTN_ROUTE_DECODE 8         /* l = 1, the other shapes (CUDA cores)        */
 
 int gist_attn_route(int entry, const gist_attn_dims* dims);
+
+/*
+ * The ragged serving step over an E4M3 paged cache: the decode loop of
+ * [KV page, "Reusable-state"] (append the new K/V, attend to everything up to
+ * and including them) for a batch of requests that each have a length and a
+ * number of new tokens of their own, over the 1-byte pool of [Suffix page, §2
+ * and the end of §5] behind the block table of [Suffix page, §6 问题四].  Per
+ * step: gist_paged_plan once; then per layer gist_kv_append_fp8 and
+ * gist_attn_paged_fp8kv.  Tokens are packed: request r's new tokens are rows
+ * q_start[r] .. q_start[r + 1] - 1 of the token arrays, in order.  Rows from
+ * q_start[num_requests] on are padding: never read as tokens, outputs left as
+ * they were.  The pool and its scales have the layout of gist_attn_fwd_fp8kv.
+ * Lengths live on the device, so one captured graph serves every step.
+ */
+typedef struct {
+  int32_t num_requests;  /* B >= 0                                                        */
+  int32_t num_tokens;    /* T >= 0: rows of the token arrays, padding included            */
+  int32_t max_new;       /* host bound on every request's new tokens, 1 <= max_new        */
+  int32_t num_q_heads;   /* Hq >= 1                                                       */
+  int32_t num_kv_heads;  /* Hkv >= 1, Hq % Hkv == 0                                       */
+  int32_t head_dim;      /* d: 64 or 128                                                  */
+  int32_t block_len;     /* tokens per pool block, >= 1                                   */
+  int32_t max_blocks;    /* W >= 1: entries of a request's row of the block table         */
+  int32_t num_blocks;    /* pool extent; num_blocks * block_len < 2^31                    */
+  int32_t num_layers;    /* L                                                             */
+  int32_t layer;         /* 0 <= layer < L                                                */
+  float rope_theta;      /* RoPE base, > 0                                                */
+  float softmax_scale;   /* 0 selects 1/sqrt(d)                                           */
+  int32_t* status;       /* optional device int32 status word (may be NULL)               */
+  int32_t flags;         /* 0 or GIST_ATTN_FLAG_PREROTATED (q and k_new arrive rotated)   */
+} gist_paged_dims;
+
+/*
+ * gist_paged_plan -- block table, slots and positions of one step, built on the
+ * device from the requests' lengths.
+ *   cached_len  int32 [B]: tokens of each request already in the cache
+ *   new_len     int32 [B]: its new tokens in this step (0 allowed)
+ *   block_table int32 [B][W], in and out: entries [0, ceil(cached_len / block_len))
+ *               are the request's blocks; the entries of the blocks that its new
+ *               tokens open are written, the others left as they are
+ *   free_blocks int32 [num_free]: block ids; free_blocks[free_range[0] ..
+ *               free_range[1]) are free, taken from the front in request order
+ *   free_range  int32 [2] {begin, end}, read only
+ *   q_start     int32 [B + 1], written: exclusive sums of new_len (at most T)
+ *   kv_len      int32 [B], written: cached_len + new_len
+ *   slot        int32 [T], written: block * block_len + row of each token's place
+ *               in the cache, -1 for padding
+ *   position    int32 [T], written: cached_len + index of each token, -1 for padding
+ *   free_range_out int32 [2], written: free_range after the step
+ * A request is not served when its lengths are negative or pass W * block_len,
+ * when it ends past row T, or when it needs blocks and the needs summed in
+ * request order up to and including its own (those of requests not served for
+ * want of blocks too) pass the free ones: kv_len 0, its tokens' slots and
+ * positions -1, no entry written, GIST_ATTN_STATUS_NOT_SERVED.  Its rows stay in
+ * the packing.  A block id outside [0, num_blocks) in the table or the free list
+ * gives slot -1 and GIST_ATTN_STATUS_BAD_BLOCK.  No output may overlap an input
+ * (GIST_ATTN_ERR_DIMS where kv_len == cached_len or free_range_out ==
+ * free_range).  At most 16384 requests (GIST_ATTN_ERR_UNSUPPORTED).  Reads
+ * num_requests, num_tokens, block_len, max_blocks, num_blocks and status of dims.
+ */
+int gist_paged_plan(const int32_t* cached_len, const int32_t* new_len, int32_t* block_table,
+                    const int32_t* free_blocks, int32_t num_free, const int32_t* free_range,
+                    int32_t* q_start, int32_t* kv_len, int32_t* slot, int32_t* position,
+                    int32_t* free_range_out, const gist_paged_dims* dims, cudaStream_t stream);
+
+/*
+ * gist_kv_append_fp8 -- writes T new tokens' K/V into the E4M3 pool at `layer`.
+ * Token t goes to row slot[t] % block_len of block slot[t] / block_len, K rotated
+ * at position[t].  Tokens of one block are written together: with `off` the row
+ * of the first of them, top the largest finite magnitude of the block's new
+ * (unrotated) K or V in that head, and limit 448, or 316 for K that is rotated
+ * here (a rotation grows a value by at most sqrt 2 and 316 sqrt 2 < 448),
+ *   need  = the smallest power of two >= top / limit, within [2^-100, 2^119]
+ *   scale = need if off == 0, else max(scale, need)
+ * and a block's earlier rows [0, off) are rescaled (rounded to nearest) when its
+ * scale grows (as do rows between that skipped tokens leave unwritten); by a power
+ * of two that is exact but for E4M3's subnormals.
+ * Values are rounded to nearest, ties to even; an infinity or NaN is stored as
+ * NaN (E4M3 has no infinities).
+ *   k_new, v_new bf16 [T][Hkv][d]
+ *   kv_pool_e4m3 uint8 [num_blocks][L][2][Hkv][block_len][d], 16-byte aligned, written
+ *   kv_scale     float [num_blocks][L][2][Hkv], written
+ *   slot         int32 [T]; -1 (any negative) skips the token; a slot outside the
+ *                pool skips it and sets GIST_ATTN_STATUS_BAD_BLOCK
+ *   position     int32 [T]; NULL allowed with GIST_ATTN_FLAG_PREROTATED
+ * A block's new tokens must be consecutive in t with consecutive slots (skipped
+ * ones keeping their place), as gist_paged_plan gives them, and no block may get
+ * tokens of two requests: otherwise the block's rows and scale are unspecified
+ * (the writes stay in it).
+ * num_requests, max_new, max_blocks and Hq are not used.
+ */
+int gist_kv_append_fp8(const void* k_new, const void* v_new, void* kv_pool_e4m3, float* kv_scale,
+                       const int32_t* slot, const int32_t* position, const gist_paged_dims* dims,
+                       cudaStream_t stream);
+
+/*
+ * gist_attn_paged_workspace_bytes -- device bytes gist_attn_paged_fp8kv needs for
+ * these dimensions on the current device (host only; 0 for invalid dims).
+ */
+size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims);
+
+/*
+ * gist_attn_paged_fp8kv -- causal attention of every request's new tokens over its
+ * cached sequence, which already holds them: with n = q_start[r + 1] - q_start[r]
+ * and pos = kv_len[r] - n + i, new token i of request r attends to keys 0 .. pos,
+ *   out[q_start[r] + i][h] = sum_j softmax_j(scale R(q) . K_j) V_j,   j <= pos,
+ * K_j, V_j = e4m3 * scale, q rotated at pos unless GIST_ATTN_FLAG_PREROTATED.
+ *   q, out      bf16 [T][Hq][d]
+ *   kv_pool_e4m3, kv_scale as gist_attn_fwd_fp8kv (16-byte aligned pool)
+ *   block_table int32 [B][W]; entries past ceil(kv_len / block_len) are not read
+ *   q_start     int32 [B + 1], kv_len int32 [B]
+ *   workspace   device pointer, 256-byte aligned, at least
+ *               gist_attn_paged_workspace_bytes(dims) bytes (GIST_ATTN_ERR_SCRATCH
+ *               otherwise): scratch, overwritten by every call; two calls that may
+ *               overlap on the GPU need one each
+ * A token that sees no key (kv_len[r] < n) gets zeros.  Cached bytes that no token
+ * sees (rows past kv_len in the last block) may hold anything.  A block id outside
+ * the pool zeroes its request's rows and sets GIST_ATTN_STATUS_BAD_BLOCK, as does a
+ * kv_len past W * block_len; a q_start pair outside [0, T], out of order or more
+ * than max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
+ * elsewhere.  block_len must be a multiple of 16 and Hq / Hkv at most 128
+ * (GIST_ATTN_ERR_UNSUPPORTED).
+ */
+int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3, const float* kv_scale,
+                          const int32_t* block_table, const int32_t* q_start,
+                          const int32_t* kv_len, void* out, void* workspace,
+                          size_t workspace_bytes, const gist_paged_dims* dims,
+                          cudaStream_t stream);
 
 #ifdef __cplusplus
 }
