@@ -104,6 +104,9 @@ int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v
                         cudaStream_t stream);
 int launch_paged_attn(const PagedProblem& pb, void* workspace, cudaStream_t stream);
 size_t paged_attn_workspace(const PagedProblem& pb);
+int launch_paged_decode(const PagedProblem& pb, void* workspace, cudaStream_t stream);
+size_t paged_decode_workspace(const PagedProblem& pb);
+int paged_decode_rows(const PagedProblem& pb);
 
 // Whether the prefill kernel can hold this problem's tiles in shared memory.
 bool prefill_fits(const Problem& pb);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace gattn {
 
@@ -33,6 +34,44 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) {
       : "=f"(f.x), "=f"(f.y)
       : "r"(v));
   return f;
+}
+
+// The requests of a step, as the attention kernels walk them.
+struct Requests {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  int B, T, max_new, G, Hkv, W, block_len;
+  int max_rows;  // requests of more rows (new tokens x G) are another kernel's
+
+  // A request's cached tokens; -1 where the table cannot hold them.
+  __device__ __forceinline__ int length(int r) const {
+    const int kv = kv_len[r];
+    return kv > W * block_len ? -1 : max(kv, 0);
+  }
+  // New tokens of request r, 0 where its token rows are out of order or range.
+  __device__ __forceinline__ int tokens(int r, bool* bad = nullptr) const {
+    const int a = q_start[r], b = q_start[r + 1];
+    if (a < 0 || b > T || b < a || b - a > max_new) {
+      if (bad) *bad = true;
+      return 0;
+    }
+    return b - a;
+  }
+  // Tiles of KT keys of request r for one KV head, 0 if this kernel has nothing
+  // to do for it; one where it sees no key (its rows are zeros).
+  template <int KT>
+  __device__ __forceinline__ int tiles(int r, bool* bad = nullptr) const {
+    const int n = tokens(r, bad);
+    if (n == 0 || n > max_rows / G) return 0;
+    const int kv = length(r);
+    if (bad && kv < 0) *bad = true;
+    return max(1, (kv + KT - 1) / KT);
+  }
+};
+
+inline Requests requests_of(const PagedProblem& pb) {
+  return Requests{pb.q_start, pb.kv_len, pb.block_table, pb.B, pb.T, pb.max_new, pb.G, pb.Hkv, pb.W, pb.block_len, 0};
 }
 
 }  // namespace gattn

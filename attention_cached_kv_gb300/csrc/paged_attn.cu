@@ -21,7 +21,7 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t c) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ PagedProblem pb) {
+__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ PagedProblem pb, int min_new) {
   __shared__ float q[D], w[kThreads], red[8];
   __shared__ int who, bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int r = who;
-  if (r < 0) return;
+  if (r < 0 || pb.q_start[r + 1] - pb.q_start[r] < min_new) return;
   const int kv_len = pb.kv_len[r];
   const int pos = kv_len - (pb.q_start[r + 1] - t);
   const bool fits = kv_len <= pb.W * pb.block_len;
@@ -106,15 +106,20 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 
 }  // namespace
 
-size_t paged_attn_workspace(const PagedProblem&) { return 0; }
+size_t paged_attn_workspace(const PagedProblem& pb) { return paged_decode_workspace(pb); }
 
-int launch_paged_attn(const PagedProblem& pb, void*, cudaStream_t stream) {
+int launch_paged_attn(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
   if (pb.Hq > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
+  const int few = paged_decode_rows(pb) / pb.G;  // new tokens that the decode kernel takes
+  if (few > 0) {
+    const int rc = launch_paged_decode(pb, workspace, stream);
+    if (rc != GIST_ATTN_OK || pb.max_new <= few) return rc;
+  }
   const dim3 grid((unsigned)pb.T, (unsigned)pb.Hq);
   if (pb.d == 64)
-    attn_kernel<64><<<grid, kThreads, 0, stream>>>(pb);
+    attn_kernel<64><<<grid, kThreads, 0, stream>>>(pb, few + 1);
   else
-    attn_kernel<128><<<grid, kThreads, 0, stream>>>(pb);
+    attn_kernel<128><<<grid, kThreads, 0, stream>>>(pb, few + 1);
   return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 

@@ -1,0 +1,888 @@
+// paged_decode.cu -- few query rows a request (new tokens x heads of a KV group)
+// against its E4M3 paged cache: the decoding step and the check of drafted tokens
+// ([KV page, "Reusable-state"]; [Suffix page, §2, §5, §6 问题四]).
+//
+// The pool's bytes go to the tensor core as they lie in the cache.  A tile is 128
+// rows of 128 bytes of one KV head (128 keys for d = 128; 256 for d = 64, a row
+// then holding an even and an odd key).  Per tile
+//     S^T = K q^T      tcgen05 kind::f8f6f4, keys as M, the query rows as N
+//     O^T = V^T P^T    the V tile read transposed (M contiguous), P as N
+// so no cached element is ever converted.  q and P keep their precision as sums
+// of three E4M3 terms, x = x0 + x1 / 16 + x2 / 256 (each the rounded remainder of
+// the last, together 11 bits or more), side by side as columns of N: the few
+// query rows leave N room that costs nothing.  q is scaled by a power of two a
+// row, so its size does not matter; the K scale of a key's block multiplies its
+// fp32 scores, the V scale over the largest met so far its weights.
+//
+// A softmax thread owns one tile row (TMEM lane): its scores for all query rows,
+// the running maximum m of each (the same in all threads), its own part of the
+// sums.  m moves only when a score passes it by more than 2 (log2 units), all
+// threads together; then O in TMEM is rescaled.  P is at most 2^2 x 64 of 448.
+//
+// Work is the sequence of tiles of all (request, KV head) units; each of at most
+// two CTAs an SM takes an equal run of it, so one long request spreads over the
+// machine.  A unit that crosses CTAs leaves parts (O, m, sum) in the workspace;
+// combine_kernel joins them in key order, the same way every time.
+//
+// Bound: HBM (a byte a cached element).  Seven warps: 0-3 softmax, 4 TMA and
+// scales, 5 tcgen05, 6 q rows.
+//
+// Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
+//        [Suffix page] icman.com.cn news 64898.
+#include <math.h>
+#include <stddef.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace gattn {
+namespace {
+
+constexpr int kThreads = 224;
+constexpr uint32_t kStage = 128 * 128;  // bytes of a K or V tile
+constexpr float kNone = -3.0e38f;       // running maximum before any key
+constexpr float kSlack = 2.f;           // log2 units a score may pass it by
+constexpr float kPUnit = 64.f;          // P's scale into E4M3
+
+struct DecodeParams {
+  const bf16* q;
+  bf16* out;
+  const float* scale;
+  float* parts;  // workspace
+  int32_t* status;
+  Requests rq;
+  int Hq, L, layer, num_blocks;
+  int box_rows, box_shift;  // tile rows of one TMA box: 2^box_shift
+  float scale_log2;
+  uint64_t turn[64];
+};
+
+template <int D, int CH>
+struct Cfg {
+  static constexpr int KPR = 128 / D;           // keys a tile row
+  static constexpr int KT = 128 * KPR;          // keys a tile
+  static constexpr int ROWS = 8 * CH;           // query rows at most
+  static constexpr int NQ = CH <= 2 ? 2 : 1;    // q tiles
+  static constexpr int SP = (24 * CH + 15) & ~15;  // S columns a parity
+  static constexpr int OC = (KPR * 24 * CH + 15) & ~15;  // O columns
+  static constexpr int SB = 2 * KPR * SP + OC <= 256 ? 2 : 1;  // S buffers
+  static constexpr uint32_t QB = 3072 * CH, PB = KPR * 3072 * CH;
+  static constexpr int NK = D == 128 && CH <= 2 ? 3 : D == 64 && CH == 1 ? 3 : 2;
+  static constexpr int NV = D == 128 && CH == 1 ? 3 : 2;
+  static constexpr uint32_t kO = SB * KPR * SP;  // O's first TMEM column
+  static constexpr uint32_t offV = NK * kStage, offQ = offV + NV * kStage, offP = offQ + NQ * QB,
+                            offMisc = offP + 2 * PB + 1024;  // (an MMA's N may run 8 rows past a tile)
+  static_assert(kO + OC <= 256, "TMEM columns");
+};
+
+struct Seg {  // one unit's share of a CTA
+  int r, g, rows, q0, pos0, kv, kt0, kt1, nt, pad;
+};
+
+template <int D, int CH>
+struct Misc {
+  using C = Cfg<D, CH>;
+  uint64_t kfull[3], kfree[3], vfull[3], vfree[3], scfull[3];
+  uint64_t qfull[2], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], drain;
+  uint32_t tmem;
+  int bad[8];  // by segment: a block id outside the pool
+  Seg seg[2];
+  alignas(16) float rs[2][C::ROWS];  // softmax scale (log2) x q's power of two, by row
+  float ksc[3][16], vsc[3][16];  // scales of a tile's boxes
+  float wmax[4][C::ROWS], wv[4];
+  int nankey[D];  // first key past the first row's whose V is NaN, by element
+  // the scan
+  int warp_sum[kThreads / 32];
+  int start_r, start_pre, total;
+};
+
+template <int D, int CH>
+constexpr uint32_t smem_bytes() {
+  using M = Misc<D, CH>;
+  static_assert(offsetof(M, rs) % 16 == 0, "read as float4");
+  return Cfg<D, CH>::offMisc + (uint32_t)sizeof(Misc<D, CH>);
+}
+
+// S = f8 x f8 -> f32
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t N, uint32_t a_mn_major) {
+  return (1u << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Whether one of four E4M3 codes is a NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t has_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ void sts16b(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// An f16 pair (magnitudes at most 448) as three E4M3 pairs: x0 + x1 / 16 + x2 / 256.
+__device__ __forceinline__ void split3(uint32_t x, uint16_t& t0, uint16_t& t1, uint16_t& t2) {
+  asm("{\n\t.reg .b32 f, r, m, s;\n\t"
+      "mov.b32 m, 0xcc00cc00;\n\t"  // -16, -16
+      "mov.b32 s, 0x4c004c00;\n\t"  // 16, 16
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, %3;\n\t"
+      "cvt.rn.f16x2.e4m3x2 f, %0;\n\t"
+      "mul.rn.f16x2 r, %3, s;\n\t"
+      "fma.rn.f16x2 r, f, m, r;\n\t"  // 16 (x - x0), exact
+      "cvt.rn.satfinite.e4m3x2.f16x2 %1, r;\n\t"
+      "cvt.rn.f16x2.e4m3x2 f, %1;\n\t"
+      "mul.rn.f16x2 r, r, s;\n\t"
+      "fma.rn.f16x2 r, f, m, r;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %2, r;\n\t}"
+      : "=&h"(t0), "=&h"(t1), "=&h"(t2)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The walk over a CTA's segments; every role makes it for itself.
+template <int KT>
+struct Walk {
+  int x, x_end, r, pre, g, nt;
+  __device__ void init(const Requests& rq, int x0, int x1, int r0, int pre0) {
+    x = x0;
+    x_end = x1;
+    r = r0;
+    pre = pre0;
+    nt = rq.tiles<KT>(r);
+    g = (x - rq.Hkv * pre) / nt;
+  }
+  __device__ bool more() const { return x < x_end; }
+  __device__ void get(int& kt0, int& kt1, const Requests& rq) const {
+    const int a = rq.Hkv * pre + g * nt;
+    kt0 = x - a;
+    kt1 = min(nt, x_end - a);
+  }
+  __device__ void next(const Requests& rq) {
+    const int a = rq.Hkv * pre + g * nt;
+    x = min(a + nt, x_end);
+    if (x >= x_end) return;
+    if (++g == rq.Hkv) {
+      g = 0;
+      pre += nt;
+      do nt = ++r < rq.B ? rq.tiles<KT>(r) : 0;
+      while (nt == 0 && r < rq.B);
+      if (r >= rq.B) x = x_end;  // (lengths that changed under the kernel)
+    }
+  }
+};
+
+// Sums the tiles of all requests (kThreads threads of a CTA), finds the request
+// that holds tile `at(total)` and the tiles before it (a head's, at most).
+template <int KT, int NT, class At>
+__device__ __forceinline__ void scan_tiles(const Requests& rq, int* warp_sum, int* start_r, int* start_pre,
+                                           int* total, int32_t* status, At at) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (rq.B + NT - 1) / NT;
+  const int r0 = min(tid * per, rq.B), r1 = min(r0 + per, rq.B);
+  int own = 0;
+  bool bad = false;
+  for (int r = r0; r < r1; ++r) own += rq.tiles<KT>(r, &bad);
+  if (bad) report(status, GIST_ATTN_STATUS_BAD_BLOCK);
+  int inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  if (tid == 0) *start_r = -1;
+  __syncthreads();
+  int before = inc - own, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  const int x = at(all * rq.Hkv);
+  if (tid == 0) *total = all * rq.Hkv;
+  if (x < all * rq.Hkv && own > 0 && x >= before * rq.Hkv && x < (before + own) * rq.Hkv) {
+    int p = before;
+    for (int r = r0; r < r1; ++r) {
+      const int n = rq.tiles<KT>(r);
+      if (x < (p + n) * rq.Hkv) {
+        *start_r = r;
+        *start_pre = p;
+        break;
+      }
+      p += n;
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int share(int total, int w, int W) { return (int)((int64_t)total * w / W); }
+
+template <int D, int CH>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DecodeParams prm) {
+  using C = Cfg<D, CH>;
+  using M = Misc<D, CH>;
+  constexpr int KPR = C::KPR, KT = C::KT, ROWS = C::ROWS, NK = C::NK, NV = C::NV, NQ = C::NQ, SB = C::SB;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  M& ms = *reinterpret_cast<M*>(smem + C::offMisc);
+  const Requests& rq = prm.rq;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = rq.G;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int W = gridDim.x, me = blockIdx.x;
+  scan_tiles<KT, kThreads>(rq, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total, me == 0 ? prm.status : nullptr,
+                           [&](int total) { return share(total, me, W); });
+  const int x0 = share(ms.total, me, W), x1 = share(ms.total, me + 1, W);
+  if (x0 >= x1 || ms.start_r < 0) return;
+
+  if (warp == 5) {
+    tc::tmem_alloc(smem_u32(&ms.tmem), 256);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&ms.kfull[s], 1);
+      mbar_init(&ms.kfree[s], 1);
+      mbar_init(&ms.vfull[s], 1);
+      mbar_init(&ms.vfree[s], 1);
+      mbar_init(&ms.scfull[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms.qfull[s], 1);
+      mbar_init(&ms.qfree[s], 2);
+      mbar_init(&ms.sfull[s], 1);
+      mbar_init(&ms.sfree[s], 128);
+      mbar_init(&ms.pfull[s], 128);
+      mbar_init(&ms.pfree[s], 1);
+    }
+    mbar_init(&ms.drain, 1);
+    fence_mbar_init();
+  }
+  for (int i = tid; i < D; i += kThreads) ms.nankey[i] = INT32_MAX;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ms.tmem;
+  Walk<KT> wk;
+  wk.init(rq, x0, x1, ms.start_r, ms.start_pre);
+  bool failed = false;
+
+  if (warp == 4) {
+    // ================================================== K, V tiles and their scales
+    if (lane == 0) tma_prefetch_map(&tm);
+    const int br = prm.box_rows, vbl = rq.block_len / KPR, boxes = 128 / br;
+    int i = 0, seg = 0;
+    for (; wk.more() && !failed; wk.next(rq), ++seg) {
+      int kt0, kt1;
+      wk.get(kt0, kt1, rq);
+      const int kv = rq.length(wk.r);
+      const int32_t* table = rq.block_table + (int64_t)wk.r * rq.W;
+      auto block_of = [&](int kt) {  // this lane's box of tile kt: block id, -1 if there is none
+        const int row = kt * 128 + lane * br;
+        return lane < boxes && (int64_t)row * KPR < kv ? table[row / vbl] : -1;
+      };
+      int blk = block_of(kt0);
+      if (lane == 0) ms.bad[seg & 7] = kv < 0;
+      __syncwarp();
+      for (int kt = kt0; kt < kt1; ++kt, ++i) {
+        const int ks = i % NK, vs = i % NV;
+        const int row = kt * 128 + lane * br;
+        const bool want = lane < boxes && (int64_t)row * KPR < kv;
+        const bool ok = want && blk >= 0 && blk < prm.num_blocks;
+        if (want && !ok) {
+          ms.bad[seg & 7] = 1;
+          report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * br * 128;
+        const int inner = row % vbl;
+        const int plane = ((ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + wk.g;
+        if (__any_sync(0xffffffffu, (i >= NK && !mbar_wait(&ms.kfree[ks], ((uint32_t)(i / NK) & 1u) ^ 1u)))) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ms.kfull[ks], bytes);
+        __syncwarp();
+        if (ok) tma_load_3d(sbase + ks * kStage + lane * br * 128, &tm, &ms.kfull[ks], 0, inner, plane);
+        const float k_scale = ok ? __ldg(prm.scale + plane) : 0.f;
+        const float v_scale = ok ? __ldg(prm.scale + plane + rq.Hkv) : 0.f;
+        if (__any_sync(0xffffffffu, (i >= NV && !mbar_wait(&ms.vfree[vs], ((uint32_t)(i / NV) & 1u) ^ 1u)))) {
+          failed = true;
+          ++i;  // its K load is in flight
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ms.vfull[vs], bytes);
+        __syncwarp();
+        if (ok) tma_load_3d(sbase + C::offV + vs * kStage + lane * br * 128, &tm, &ms.vfull[vs], 0, inner, plane + rq.Hkv);
+        if (kt + 1 < kt1) blk = block_of(kt + 1);
+        if (lane < 16) {
+          ms.ksc[vs][lane] = k_scale;
+          ms.vsc[vs][lane] = v_scale;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.scfull[vs]);
+      }
+    }
+    if (failed) {  // the copies issued land before the CTA leaves
+      for (int s = 0; s < NK && s < i; ++s) mbar_wait(&ms.kfull[(i - 1 - s) % NK], (uint32_t)((i - 1 - s) / NK) & 1u);
+      for (int s = 0; s < NV && s < i; ++s) mbar_wait(&ms.vfull[(i - 1 - s) % NV], (uint32_t)((i - 1 - s) / NV) & 1u);
+    }
+  } else if (warp == 5) {
+    // ================================================== tcgen05
+    int i = 0, seg = 0;
+    bool pending = false, first = false;  // P V of tile i - 1 to issue; the first of its segment
+    int nch = 1;
+    auto issue_pv = [&]() {
+      const int t = i - 1, pb = t & 1, vs = t % NV;
+      if (__any_sync(0xffffffffu, !mbar_wait(&ms.pfull[pb], (uint32_t)(t >> 1) & 1u) ||
+                                      !mbar_wait(&ms.vfull[vs], (uint32_t)(t / NV) & 1u))) {
+        failed = true;
+        return;
+      }
+      tc::fence_after_sync();
+      if (lane == 0) {
+        const uint32_t id = idesc_e4m3((KPR * 24 * nch + 15) & ~15, 1);
+        const uint32_t vb = sbase + C::offV + vs * kStage, pp = sbase + C::offP + pb * C::PB;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f8(tmem + C::kO, tc::smem_desc_sw128(vb + k * 4096, kStage, 1024),
+                 tc::smem_desc_sw128(pp + k * 32, 16, 1024), id, !first || k > 0);
+        tc::commit(smem_u32(&ms.pfree[pb]));
+        tc::commit(smem_u32(&ms.vfree[vs]));
+      }
+      __syncwarp();
+    };
+    for (; wk.more() && !failed; wk.next(rq), ++seg) {
+      int kt0, kt1;
+      wk.get(kt0, kt1, rq);
+      if (pending) issue_pv();
+      pending = false;
+      const int qs = seg % NQ;
+      if (failed || __any_sync(0xffffffffu, !mbar_wait(&ms.qfull[qs], (uint32_t)(seg / NQ) & 1u))) {
+        failed = true;
+        break;
+      }
+      nch = (ms.seg[qs].rows + 7) >> 3;
+      const uint32_t id = idesc_e4m3((24 * nch + 15) & ~15, 0);
+      const uint32_t qb = sbase + C::offQ + qs * C::QB;
+      for (int kt = kt0; kt < kt1; ++kt) {
+        const int ks = i % NK, sb = i % SB;
+        if (__any_sync(0xffffffffu, !mbar_wait(&ms.kfull[ks], (uint32_t)(i / NK) & 1u) ||
+                                        (i >= SB && !mbar_wait(&ms.sfree[sb], ((uint32_t)(i / SB) & 1u) ^ 1u)))) {
+          failed = true;
+          break;
+        }
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t kb = sbase + ks * kStage;
+#pragma unroll
+          for (int p = 0; p < KPR; ++p)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
+                     tc::smem_desc_sw128(qb + k * 32, 16, 1024), id, k > 0);
+          tc::commit(smem_u32(&ms.sfull[sb]));
+          tc::commit(smem_u32(&ms.kfree[ks]));
+          if (kt == kt1 - 1) tc::commit(smem_u32(&ms.qfree[qs]));
+        }
+        __syncwarp();
+        if (pending) issue_pv();
+        if (failed) break;
+        first = kt == kt0;
+        pending = true;
+        ++i;
+      }
+    }
+    if (pending && !failed) issue_pv();
+    if (lane == 0) tc::commit(smem_u32(&ms.drain));
+    __syncwarp();
+    if (!mbar_wait(&ms.drain, 0)) failed = true;
+  } else if (warp == 6) {
+    // ================================================== q rows
+    for (int seg = 0; wk.more() && !failed; wk.next(rq), ++seg) {
+      int kt0, kt1;
+      wk.get(kt0, kt1, rq);
+      const int qs = seg % NQ;
+      const int q0 = rq.q_start[wk.r], n = rq.q_start[wk.r + 1] - q0, kv = rq.length(wk.r);
+      const int rows = n * G, pos0 = max(kv, 0) - n;
+      if (__any_sync(0xffffffffu, seg >= NQ && !mbar_wait(&ms.qfree[qs], ((uint32_t)(seg / NQ) & 1u) ^ 1u))) {
+        failed = true;
+        break;
+      }
+      constexpr int E = D / 64;  // frequencies a lane
+      const bf16* src = prm.q + ((int64_t)q0 * prm.Hq + wk.g * G) * D + lane * E;
+      for (int j0 = 0; j0 < rows; j0 += 8) {
+        float x[8][E], y[8][E];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int tok = (j0 + j) / G;
+          const bf16* p = src + (int64_t)tok * prm.Hq * D + (j0 + j - tok * G) * D;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[j][e] = j0 + j < rows ? __bfloat162float(p[e]) : 0.f;
+            y[j][e] = j0 + j < rows ? __bfloat162float(p[e + D / 2]) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int pos = pos0 + (j0 + j) / G;
+          float a[E], b[E];
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            float sn, cs;
+            __sincosf(turn_angle(pos, prm.turn[lane * E + e]), &sn, &cs);
+            a[e] = x[j][e] * cs - y[j][e] * sn;
+            b[e] = y[j][e] * cs + x[j][e] * sn;
+            top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+            if (!(fabsf(a[e]) <= 3.4e38f) || !(fabsf(b[e]) <= 3.4e38f)) top = INFINITY;
+          }
+          const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+          const int ex = max((int)(tb >> 23) - 127 - 7, -119);  // the row's largest lands in [128, 256)
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+          if (lane == 0)
+            ms.rs[qs][j0 + j] = j0 + j >= rows ? 0.f
+                                : tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                                                    : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
+          const uint32_t base = sbase + C::offQ + qs * C::QB + (j0 / 8) * 3072 + j * 128;
+          uint16_t t[3], u[3];
+          if constexpr (E == 2) {
+            split3(to_f16x2(a[0] * down, a[1] * down), t[0], t[1], t[2]);
+            split3(to_f16x2(b[0] * down, b[1] * down), u[0], u[1], u[2]);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+              sts16b(base + s * 1024 + ((2 * lane) ^ (j << 4)), t[s]);
+              sts16b(base + s * 1024 + ((64 + 2 * lane) ^ (j << 4)), u[s]);
+            }
+          } else {
+            split3(to_f16x2(a[0] * down, b[0] * down), t[0], t[1], t[2]);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+              sts8(base + s * 1024 + (lane ^ (j << 4)), t[s] & 0xff);
+              sts8(base + s * 1024 + ((32 + lane) ^ (j << 4)), t[s] >> 8);
+            }
+          }
+        }
+      }
+      if (lane == 0) ms.seg[qs] = Seg{wk.r, wk.g, rows, q0, pos0, max(kv, 0), kt0, kt1, wk.nt, 0};
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.qfull[qs]);
+    }
+  } else {
+    // ================================================== softmax, output
+    const int t = tid;  // tile row == TMEM lane
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    uint32_t pof[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pof[j] = sbase + C::offP + j * 128 + (t ^ (j << 4));
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!failed && !mbar_wait(bar, parity)) failed = true;
+    };
+    int i = 0, seg = 0;
+    for (; wk.more(); wk.next(rq), ++seg) {
+      int kt0, kt1;
+      wk.get(kt0, kt1, rq);
+      const int qs = seg % NQ;
+      wait(&ms.qfull[qs], (uint32_t)(seg / NQ) & 1u);
+      // a role that gave up ends this one's waits too: leave together
+      if (named_bar_or(1, 128, failed)) {
+        failed = true;
+        break;
+      }
+      const Seg sg = ms.seg[qs];
+      const int nch = (sg.rows + 7) >> 3;
+      float m[ROWS], l[ROWS];
+      float vref = 0.f, vmul = 0.f;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) m[j] = kNone, l[j] = 0.f;
+      for (int kt = kt0; kt < kt1; ++kt, ++i) {
+        const int sb = i % SB, vs = i % NV, pb = i & 1;
+        const int key0 = kt * KT + t * KPR;  // this thread's first key
+        const bool edge = kt * KT + KT > sg.pos0 + 1;  // some row does not see all of the tile
+        float s[ROWS * KPR];
+        wait(&ms.scfull[vs], (uint32_t)(i / NV) & 1u);
+        const int box = t >> prm.box_shift;
+        const float ks = ms.ksc[vs][box], vsc = ms.vsc[vs][box];
+        wait(&ms.sfull[sb], (uint32_t)(i / SB) & 1u);
+        tc::fence_after_sync();
+        bool over = vsc > vref;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (c < nch) {
+            uint32_t v[KPR][24];
+#pragma unroll
+            for (int p = 0; p < KPR; ++p)
+#pragma unroll
+              for (int k = 0; k < 3; ++k) ld8(tmem + lane_base + (sb * KPR + p) * C::SP + c * 24 + k * 8, v[p] + k * 8);
+            tc::wait_ld();
+            const float4* rp = reinterpret_cast<const float4*>(&ms.rs[qs][c * 8]);
+            const float4 ra = rp[0], rb = rp[1];
+            const float rs[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+            for (int p = 0; p < KPR; ++p)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float x = __uint_as_float(v[p][j]);
+                x = fmaf(__uint_as_float(v[p][8 + j]), 0.0625f, x);
+                x = fmaf(__uint_as_float(v[p][16 + j]), 0.00390625f, x);
+                x *= ks * rs[j];
+                if (edge && key0 + p > sg.pos0 + (c * 8 + j) / G) x = -INFINITY;
+                over |= x - m[c * 8 + j] > kSlack;
+                s[(c * KPR + p) * 8 + j] = x;
+              }
+          }
+        }
+        tc::fence_before_sync();
+        mbar_arrive(&ms.sfree[sb]);
+        if (named_bar_or(1, 128, over)) {
+          // new maxima, the same in all threads; the sums and O follow
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (c < nch) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float x = s[c * KPR * 8 + j];
+                if (KPR == 2) x = fmaxf(x, s[(c * KPR + KPR - 1) * 8 + j]);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if (lane == 0) ms.wmax[warp][c * 8 + j] = x;
+              }
+            }
+          float vm = vsc;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          if (lane == 0) ms.wv[warp] = vm;
+          named_bar_sync(1, 128);
+          vm = fmaxf(fmaxf(ms.wv[0], ms.wv[1]), fmaxf(ms.wv[2], ms.wv[3]));
+          const float vnew = fmaxf(vref, fmaxf(vm, 7.5e-37f));
+          const float fv = vref / vnew;
+          vref = vnew;
+          vmul = kPUnit / vnew;
+          if (kt > kt0) wait(&ms.pfree[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u);
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (c < nch) {
+              float f[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int q = c * 8 + j;
+                const float mn = fmaxf(m[q], fmaxf(fmaxf(ms.wmax[0][q], ms.wmax[1][q]), fmaxf(ms.wmax[2][q], ms.wmax[3][q])));
+                f[j] = ex2_approx(m[q] - mn);
+                l[q] *= f[j];
+                m[q] = mn;
+                f[j] *= fv;
+              }
+              if (kt > kt0) {
+#pragma unroll
+                for (int p = 0; p < KPR; ++p)
+#pragma unroll
+                  for (int k = 0; k < 3; ++k) {
+                    const uint32_t a = tmem + lane_base + C::kO + p * 24 * nch + c * 24 + k * 8;
+                    uint32_t v[8];
+                    ld8(a, v);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j]);
+                    tc::st8(a, v);
+                  }
+              }
+            }
+          tc::wait_st();
+        }
+        if (i >= 2) wait(&ms.pfree[pb], (uint32_t)((i >> 1) - 1) & 1u);
+        const float vr = vsc * vmul;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (c < nch) {
+#pragma unroll
+            for (int p = 0; p < KPR; ++p) {
+              const uint32_t at = pb * C::PB + (p * 3 * nch + c * 3) * 1024;
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) {
+                const int q = c * 8 + j;
+                const float p0 = ex2_approx(s[(c * KPR + p) * 8 + j] - m[q]);
+                const float p1 = ex2_approx(s[(c * KPR + p) * 8 + j + 1] - m[q + 1]);
+                l[q] += p0;
+                l[q + 1] += p1;
+                uint16_t u[3];
+                split3(to_f16x2(p0 * vr, p1 * vr), u[0], u[1], u[2]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                  sts8(pof[j] + at + k * 1024, u[k]);
+                  sts8(pof[j + 1] + at + k * 1024, u[k] >> 8);
+                }
+              }
+            }
+          }
+        if (edge) {
+          // V rows that not every query row sees: those past the end are cleared, and
+          // a NaN in the others too (0 x NaN would reach rows that do not see it),
+          // noted for the rows that do
+          wait(&ms.vfull[vs], (uint32_t)(i / NV) & 1u);
+          if (key0 + KPR - 1 > sg.pos0) {
+            const uint32_t vrow = sbase + C::offV + vs * kStage + t * 128;
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              const int key = key0 + (KPR == 2 ? ch >> 2 : 0);
+              const uint32_t a = vrow + ((ch ^ (t & 7)) << 4);
+              if (key >= sg.kv) {
+                sts16(a, make_uint4(0, 0, 0, 0));
+              } else if (key > sg.pos0) {
+                const uint4 w = lds16(a);
+                if (has_nan(w.x) | has_nan(w.y) | has_nan(w.z) | has_nan(w.w)) {
+                  for (int e = 0; e < 16; ++e)
+                    if ((lds8(a + e) & 0x7fu) == 0x7fu) {
+                      sts8(a + e, 0);
+                      atomicMin(&ms.nankey[(ch * 16 + e) % D], key);
+                    }
+                }
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc::fence_before_sync();
+        mbar_arrive(&ms.pfull[pb]);
+      }
+      // ---- the segment's O, m and sums
+      wait(&ms.pfree[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u);
+      tc::fence_after_sync();
+      const int par = KPR == 2 ? t >> 6 : 0;
+      const float od = vref * (1.f / kPUnit);
+      const bool whole = kt0 == 0 && kt1 == sg.nt;
+      const bool bad = ms.bad[seg & 7] != 0;
+      float* xch = reinterpret_cast<float*>(smem + C::offP);  // d = 64: [ROWS][64]
+      float o[ROWS];
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (c < nch) {
+          uint32_t v[24];
+#pragma unroll
+          for (int k = 0; k < 3; ++k) ld8(tmem + lane_base + C::kO + par * 24 * nch + c * 24 + k * 8, v + k * 8);
+          tc::wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float x = __uint_as_float(v[j]);
+            x = fmaf(__uint_as_float(v[8 + j]), 0.0625f, x);
+            x = fmaf(__uint_as_float(v[16 + j]), 0.00390625f, x);
+            o[c * 8 + j] = x * od;
+            if (KPR == 2 && par == 1) xch[(c * 8 + j) * 64 + (t & 63)] = x * od;
+            float ls = l[c * 8 + j];
+#pragma unroll
+            for (int sh = 16; sh; sh >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
+            if (lane == 0) ms.wmax[warp][c * 8 + j] = ls;
+          }
+        }
+      tc::fence_before_sync();
+      named_bar_sync(1, 128);
+      if (KPR == 1 || t < 64) {
+        const int nk = ms.nankey[t];
+        float* part = prm.parts + (int64_t)(2 * me + (kt0 > 0 || x0 == wk.x ? 0 : 1)) * ROWS * (D + 2);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (c < nch) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int q = c * 8 + j;
+              if (q < sg.rows) {
+                const int tok = q / G, pos = sg.pos0 + tok;
+                float x = o[q];
+                if (KPR == 2) x += xch[q * 64 + t];
+                if (nk <= pos) x = __int_as_float(0x7fc00000);
+                const float sum = (ms.wmax[0][q] + ms.wmax[1][q]) + (ms.wmax[2][q] + ms.wmax[3][q]);
+                if (whole) {
+                  const bool none = bad || pos < 0;
+                  if (t == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+                  prm.out[((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + q - tok * G) * D + t] =
+                      __float2bfloat16(none ? 0.f : x / sum);
+                } else {
+                  part[q * D + t] = x;
+                  if (t == 0) {
+                    part[ROWS * D + q] = m[q];
+                    part[ROWS * D + ROWS + q] = bad ? -1.f : sum;
+                  }
+                }
+              }
+            }
+          }
+      }
+      named_bar_sync(1, 128);  // the exchange, the sums and nankey are read
+      if (t < D) ms.nankey[t] = INT32_MAX;
+      if (t == 0) mbar_arrive(&ms.qfree[qs]);
+    }
+  }
+  if (failed) report(prm.status, GIST_ATTN_STATUS_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 256);
+  }
+}
+
+// Joins the parts of the units that cross CTAs: block w - 1 of the grid takes the
+// unit that the start of CTA w's run falls into, if no earlier start does.
+template <int D, int CH>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeParams prm, int W) {
+  using C = Cfg<D, CH>;
+  constexpr int KT = C::KT, ROWS = C::ROWS;
+  __shared__ int warp_sum[4], start_r, start_pre, total_s;
+  const Requests& rq = prm.rq;
+  const int tid = threadIdx.x, w = blockIdx.x + 1;
+  scan_tiles<KT, 128>(rq, warp_sum, &start_r, &start_pre, &total_s, nullptr,
+                      [&](int total) { return share(total, w, W); });
+  const int total = total_s, x = share(total, w, W), r = start_r;
+  if (x >= total || r < 0) return;
+  const int nt = rq.tiles<KT>(r), g = (x - rq.Hkv * start_pre) / nt;
+  const int a = rq.Hkv * start_pre + g * nt, b = a + nt;
+  if (x == a || share(total, w - 1, W) > a) return;
+  const int q0 = rq.q_start[r], n = rq.q_start[r + 1] - q0, pos0 = max(rq.length(r), 0) - n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // CTA w - 1 holds tile a
+  for (int q = 0; q < n * rq.G; ++q) {
+    const int tok = q / rq.G;
+    float m = kNone, sum = 0.f, o = 0.f;
+    bool bad = false;
+    for (int v = w - 1, s0; v < W && (s0 = share(total, v, W)) < b; ++v) {
+      if (share(total, v + 1, W) == s0) continue;
+      const float* part = prm.parts + (int64_t)(2 * v + (s0 >= a ? 0 : 1)) * ROWS * (D + 2);
+      const float pm = part[ROWS * D + q], ps = part[ROWS * D + ROWS + q];
+      const float mn = fmaxf(m, pm), f0 = exp2f(m - mn), f1 = exp2f(pm - mn);
+      bad |= ps < 0.f;
+      sum = sum * f0 + ps * f1;
+      if (tid < D) o = o * f0 + part[q * D + tid] * f1;
+      m = mn;
+    }
+    const bool none = bad || pos0 + tok < 0;
+    if (tid == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+    if (tid < D)
+      prm.out[((int64_t)(q0 + tok) * prm.Hq + g * rq.G + q - tok * rq.G) * D + tid] = __float2bfloat16(none ? 0.f : o / sum);
+  }
+}
+
+// The pool as {128 bytes, rows of 128 bytes a plane, planes}, boxes of `rows` rows.
+int encode_pool(CUtensorMap* m, const PagedProblem& pb, int rows) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return GIST_ATTN_ERR_LAUNCH;
+  const cuuint64_t plane_rows = (cuuint64_t)pb.block_len * pb.d / 128;
+  const cuuint64_t dims[3] = {128, plane_rows, (cuuint64_t)pb.num_blocks * pb.L * 2 * pb.Hkv};
+  const cuuint64_t strides[2] = {128, plane_rows * 128};
+  const cuuint32_t box[3] = {128, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(pb.pool), dims, strides, box,
+                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GIST_ATTN_OK : GIST_ATTN_ERR_UNSUPPORTED;
+}
+
+int device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  return GIST_ATTN_OK;
+}
+
+// CTAs: two an SM, or one a tile where the table cannot hold that many.
+int grid_of(const PagedProblem& pb, int sms) {
+  const double tiles = (double)pb.B * pb.Hkv * (((int64_t)pb.W * pb.block_len * pb.d + 16383) / 16384);
+  return tiles < 2.0 * sms ? (int)tiles : 2 * sms;
+}
+
+template <int D, int CH>
+int launch(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
+  int sms = 0;
+  int rc = device_sms(&sms);
+  if (rc != GIST_ATTN_OK) return rc;
+  DecodeParams prm{};
+  prm.q = static_cast<const bf16*>(pb.q);
+  prm.out = static_cast<bf16*>(pb.out);
+  prm.scale = pb.scale;
+  prm.parts = static_cast<float*>(workspace);
+  prm.status = pb.status;
+  prm.rq = requests_of(pb);
+  prm.rq.max_rows = Cfg<D, CH>::ROWS;
+  prm.Hq = pb.Hq;
+  prm.L = pb.L;
+  prm.layer = pb.layer;
+  prm.num_blocks = pb.num_blocks;
+  prm.scale_log2 = pb.scale_log2;
+  for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
+  const int plane_rows = pb.block_len * D / 128;
+  prm.box_shift = 7;
+  while (plane_rows & ((1 << prm.box_shift) - 1)) --prm.box_shift;
+  prm.box_rows = 1 << prm.box_shift;
+  alignas(64) CUtensorMap tm;
+  rc = encode_pool(&tm, pb, prm.box_rows);
+  if (rc != GIST_ATTN_OK) return rc;
+  constexpr uint32_t smem = smem_bytes<D, CH>();
+  static_assert(smem <= 113 * 1024, "two CTAs an SM");
+  if (cudaFuncSetAttribute(decode_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  const int grid = grid_of(pb, sms);
+  decode_kernel<D, CH><<<grid, kThreads, smem, stream>>>(tm, prm);
+  if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
+  if (grid == 1) return GIST_ATTN_OK;
+  // the combine's CTAs may start, and scan the lengths, while the last tiles run
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid - 1);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, CH>, prm, grid) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+// Rows (new tokens x group) the kernel takes for a request.
+int paged_decode_rows(const PagedProblem& pb) { return pb.d / 4; }
+
+size_t paged_decode_workspace(const PagedProblem& pb) {
+  int sms = 0;
+  if (device_sms(&sms) != GIST_ATTN_OK) sms = 256;
+  return (size_t)grid_of(pb, sms) * 2 * paged_decode_rows(pb) * (pb.d + 2) * sizeof(float);
+}
+
+int launch_paged_decode(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
+  const int64_t rows = (int64_t)pb.max_new * pb.G;
+  if (pb.d == 64) return rows <= 8 ? launch<64, 1>(pb, workspace, stream) : launch<64, 2>(pb, workspace, stream);
+  return rows <= 8    ? launch<128, 1>(pb, workspace, stream)
+         : rows <= 16 ? launch<128, 2>(pb, workspace, stream)
+                      : launch<128, 4>(pb, workspace, stream);
+}
+
+}  // namespace gattn
