@@ -22,7 +22,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgistattn.so")
 SOURCES = ["api.cu", "prefill.cu", "prefill_tc.cu", "prefill_long.cu", "decode.cu", "decode_long.cu",
            "decode_short.cu", "gather.cu", "append.cu", "gemm.cu", "stage.cu", "noalloc.cu",
-           "decode_gqa.cu", "paged_api.cu", "paged_plan.cu", "paged_append.cu", "paged_attn.cu", "paged_decode.cu"]
+           "decode_gqa.cu", "paged_api.cu", "paged_plan.cu", "paged_append.cu", "paged_decode.cu",
+           "paged_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

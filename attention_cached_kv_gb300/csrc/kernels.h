@@ -102,11 +102,15 @@ int launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
 int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v_new, void* pool,
                         float* scale, const int32_t* slot, const int32_t* position,
                         cudaStream_t stream);
-int launch_paged_attn(const PagedProblem& pb, void* workspace, cudaStream_t stream);
-size_t paged_attn_workspace(const PagedProblem& pb);
-int launch_paged_decode(const PagedProblem& pb, void* workspace, cudaStream_t stream);
-size_t paged_decode_workspace(const PagedProblem& pb);
+// Requests of at most paged_decode_rows query rows (new tokens x group): a run of
+// key tiles a CTA (paged_decode.cu); the others: row tiles (paged_prefill.cu),
+// which take the requests of min_new new tokens or more.
+int launch_paged_decode(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream);
+size_t paged_decode_workspace(const PagedProblem& pb, int sms);
 int paged_decode_rows(const PagedProblem& pb);
+int launch_paged_prefill(const PagedProblem& pb, void* workspace, int min_new, int sms,
+                         cudaStream_t stream);
+size_t paged_prefill_workspace(const PagedProblem& pb, int min_new, int sms);
 
 // Whether the prefill kernel can hold this problem's tiles in shared memory.
 bool prefill_fits(const Problem& pb);

@@ -128,19 +128,41 @@ namespace {
 int check_attn(const gist_paged_dims* dims, PagedProblem* pb) {
   const int rc = check_dims(dims, pb);
   if (rc != GIST_ATTN_OK) return rc;
-  if (pb->block_len % 16 != 0 || pb->G > 128) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (pb->block_len % 16 != 0 || pb->G > 128 || pb->Hkv > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   // key tiles over all requests and heads are counted in 32 bits
   const double tiles = (double)pb->B * pb->Hkv * ((double)pb->W * pb->block_len / 128 + 1);
   if (tiles > 2147483647.0) return GIST_ATTN_ERR_UNSUPPORTED;
   return GIST_ATTN_OK;
+}
+
+int device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  return GIST_ATTN_OK;
+}
+
+// New tokens of a request that paged_decode takes, at most (0: none of them).
+int few_tokens(const PagedProblem& pb) { return paged_decode_rows(pb) / pb.G; }
+
+// The two kernels run one after the other and share the workspace.
+size_t attn_workspace(const PagedProblem& pb, int sms) {
+  const int few = few_tokens(pb);
+  const size_t a = few > 0 ? paged_decode_workspace(pb, sms) : 0;
+  const size_t b = pb.max_new > few ? paged_prefill_workspace(pb, few + 1, sms) : 0;
+  return a > b ? a : b;
 }
 }  // namespace
 }  // namespace gattn
 
 extern "C" size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims) {
   PagedProblem pb{};
-  if (gattn::check_attn(dims, &pb) != GIST_ATTN_OK || pb.B == 0 || pb.T == 0) return 0;
-  return gattn::paged_attn_workspace(pb);
+  int sms = 0;
+  if (gattn::check_attn(dims, &pb) != GIST_ATTN_OK || pb.B == 0 || pb.T == 0 ||
+      gattn::device_sms(&sms) != GIST_ATTN_OK)
+    return 0;
+  return gattn::attn_workspace(pb, sms);
 }
 
 extern "C" int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3,
@@ -149,7 +171,7 @@ extern "C" int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3,
                                      void* workspace, size_t workspace_bytes,
                                      const gist_paged_dims* dims, cudaStream_t stream) {
   PagedProblem pb{};
-  const int rc = gattn::check_attn(dims, &pb);
+  int rc = gattn::check_attn(dims, &pb);
   if (rc != GIST_ATTN_OK) return rc;
   if (pb.B == 0 || pb.T == 0) return GIST_ATTN_OK;
   if (!q || !kv_pool_e4m3 || !kv_scale || !block_table || !q_start || !kv_len || !out)
@@ -158,7 +180,10 @@ extern "C" int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3,
       !aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
       !aligned(pb.status, 4))
     return GIST_ATTN_ERR_ALIGN;
-  const size_t need = gattn::paged_attn_workspace(pb);
+  int sms = 0;
+  rc = gattn::device_sms(&sms);
+  if (rc != GIST_ATTN_OK) return rc;
+  const size_t need = gattn::attn_workspace(pb, sms);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return GIST_ATTN_ERR_SCRATCH;
   pb.q = q;
@@ -168,5 +193,10 @@ extern "C" int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3,
   pb.block_table = block_table;
   pb.q_start = q_start;
   pb.kv_len = kv_len;
-  return gattn::launch_paged_attn(pb, workspace, stream);
+  const int few = gattn::few_tokens(pb);
+  if (few > 0) {
+    rc = gattn::launch_paged_decode(pb, workspace, sms, stream);
+    if (rc != GIST_ATTN_OK) return rc;
+  }
+  return pb.max_new > few ? gattn::launch_paged_prefill(pb, workspace, few + 1, sms, stream) : GIST_ATTN_OK;
 }

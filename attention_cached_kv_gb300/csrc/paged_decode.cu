@@ -137,8 +137,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Whether one of four E4M3 codes is a NaN (0x7f or 0xff).
-__device__ __forceinline__ uint32_t has_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ void sts16b(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
@@ -198,50 +196,6 @@ struct Walk {
   }
 };
 
-// Sums the tiles of all requests (kThreads threads of a CTA), finds the request
-// that holds tile `at(total)` and the tiles before it (a head's, at most).
-template <int KT, int NT, class At>
-__device__ __forceinline__ void scan_tiles(const Requests& rq, int* warp_sum, int* start_r, int* start_pre,
-                                           int* total, int32_t* status, At at) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (rq.B + NT - 1) / NT;
-  const int r0 = min(tid * per, rq.B), r1 = min(r0 + per, rq.B);
-  int own = 0;
-  bool bad = false;
-  for (int r = r0; r < r1; ++r) own += rq.tiles<KT>(r, &bad);
-  if (bad) report(status, GIST_ATTN_STATUS_BAD_BLOCK);
-  int inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  if (tid == 0) *start_r = -1;
-  __syncthreads();
-  int before = inc - own, all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    all += warp_sum[w];
-  }
-  const int x = at(all * rq.Hkv);
-  if (tid == 0) *total = all * rq.Hkv;
-  if (x < all * rq.Hkv && own > 0 && x >= before * rq.Hkv && x < (before + own) * rq.Hkv) {
-    int p = before;
-    for (int r = r0; r < r1; ++r) {
-      const int n = rq.tiles<KT>(r);
-      if (x < (p + n) * rq.Hkv) {
-        *start_r = r;
-        *start_pre = p;
-        break;
-      }
-      p += n;
-    }
-  }
-  __syncthreads();
-}
-
 __device__ __forceinline__ int share(int total, int w, int W) { return (int)((int64_t)total * w / W); }
 
 template <int D, int CH>
@@ -259,9 +213,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int W = gridDim.x, me = blockIdx.x;
-  scan_tiles<KT, kThreads>(rq, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total, me == 0 ? prm.status : nullptr,
-                           [&](int total) { return share(total, me, W); });
-  const int x0 = share(ms.total, me, W), x1 = share(ms.total, me + 1, W);
+  bool odd = false;
+  scan_requests<kThreads>(
+      rq.B, [&](int r) { return rq.tiles<KT>(r, &odd); }, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
+      [&](int all) { return share(all * rq.Hkv, me, W) / rq.Hkv; });
+  if (me == 0 && odd) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+  const int total = ms.total * rq.Hkv, x0 = share(total, me, W), x1 = share(total, me + 1, W);
   if (x0 >= x1 || ms.start_r < 0) return;
 
   if (warp == 5) {
@@ -659,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 sts16(a, make_uint4(0, 0, 0, 0));
               } else if (key > sg.pos0) {
                 const uint4 w = lds16(a);
-                if (has_nan(w.x) | has_nan(w.y) | has_nan(w.z) | has_nan(w.w)) {
+                if (e4m3_nan(w.x) | e4m3_nan(w.y) | e4m3_nan(w.z) | e4m3_nan(w.w)) {
                   for (int e = 0; e < 16; ++e)
                     if ((lds8(a + e) & 0x7fu) == 0x7fu) {
                       sts8(a + e, 0);
@@ -751,42 +708,93 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the parts of the units that cross CTAs: block w - 1 of the grid takes the
-// unit that the start of CTA w's run falls into, if no earlier start does.
+// unit that the start of CTA w's run falls into, if no earlier start does.  A warp
+// (several, if there are fewer rows than warps) takes a row: all parts' maxima and
+// sums at once, then their O with the final weights, so that no load waits for
+// another's result; the order of the sums is fixed.
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
 template <int D, int CH>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ DecodeParams prm, int W) {
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ DecodeParams prm, int W) {
   using C = Cfg<D, CH>;
-  constexpr int KT = C::KT, ROWS = C::ROWS;
-  __shared__ int warp_sum[4], start_r, start_pre, total_s;
+  constexpr int KT = C::KT, ROWS = C::ROWS, E = D / 32;  // E elements a lane
+  __shared__ int warp_sum[kJoinWarps], start_r, start_pre, total_s;
+  __shared__ float acc[kJoinWarps][D];
   const Requests& rq = prm.rq;
-  const int tid = threadIdx.x, w = blockIdx.x + 1;
-  scan_tiles<KT, 128>(rq, warp_sum, &start_r, &start_pre, &total_s, nullptr,
-                      [&](int total) { return share(total, w, W); });
-  const int total = total_s, x = share(total, w, W), r = start_r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x + 1;
+  scan_requests<kJoinThreads>(
+      rq.B, [&](int r) { return rq.tiles<KT>(r); }, warp_sum, &start_r, &start_pre, &total_s,
+      [&](int all) { return share(all * rq.Hkv, w, W) / rq.Hkv; });
+  const int total = total_s * rq.Hkv, x = share(total, w, W), r = start_r;
   if (x >= total || r < 0) return;
   const int nt = rq.tiles<KT>(r), g = (x - rq.Hkv * start_pre) / nt;
   const int a = rq.Hkv * start_pre + g * nt, b = a + nt;
-  if (x == a || share(total, w - 1, W) > a) return;
+  if (x == a || share(total, w - 1, W) > a) return;  // CTA w - 1 holds tile a
   const int q0 = rq.q_start[r], n = rq.q_start[r + 1] - q0, pos0 = max(rq.length(r), 0) - n;
+  int last = w;  // the CTA that holds tile b - 1
+  while (last + 1 < W && share(total, last + 1, W) < b) ++last;
+  const int np = last - w + 2, rows = n * rq.G;
+  int wpr = kJoinWarps;  // warps a row
+  while (wpr > 1 && kJoinWarps / wpr < rows) wpr >>= 1;
+  const int sub = warp % wpr;
+  // part v: O, m and sum of CTA w - 1 + v (an empty run has none)
+  auto part = [&](int v) {
+    const int c = w - 1 + v, s0 = share(total, c, W);
+    return prm.parts + (int64_t)(2 * c + (s0 >= a ? 0 : 1)) * ROWS * (D + 2);
+  };
+  auto there = [&](int v) { return v < np && share(total, w + v, W) > share(total, w - 1 + v, W); };
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // CTA w - 1 holds tile a
-  for (int q = 0; q < n * rq.G; ++q) {
-    const int tok = q / rq.G;
-    float m = kNone, sum = 0.f, o = 0.f;
+  for (int base = 0; base < rows; base += kJoinWarps / wpr) {
+    const int q = base + warp / wpr;
+    float m = kNone, sum = 0.f, o[E];
     bool bad = false;
-    for (int v = w - 1, s0; v < W && (s0 = share(total, v, W)) < b; ++v) {
-      if (share(total, v + 1, W) == s0) continue;
-      const float* part = prm.parts + (int64_t)(2 * v + (s0 >= a ? 0 : 1)) * ROWS * (D + 2);
-      const float pm = part[ROWS * D + q], ps = part[ROWS * D + ROWS + q];
-      const float mn = fmaxf(m, pm), f0 = exp2f(m - mn), f1 = exp2f(pm - mn);
-      bad |= ps < 0.f;
-      sum = sum * f0 + ps * f1;
-      if (tid < D) o = o * f0 + part[q * D + tid] * f1;
-      m = mn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    if (q < rows) {
+      for (int v = lane; v < np; v += 32)
+        if (there(v)) m = fmaxf(m, part(v)[ROWS * D + q]);
+#pragma unroll
+      for (int sh = 16; sh; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+      for (int v0 = 0; v0 < np; v0 += 32) {
+        float f = 0.f;
+        if (there(v0 + lane)) {
+          const float* p = part(v0 + lane);
+          const float ps = p[ROWS * D + ROWS + q];
+          f = exp2f(p[ROWS * D + q] - m);
+          bad |= ps < 0.f;
+          sum += ps * f;
+        }
+#pragma unroll 8
+        for (int j = sub; j < min(32, np - v0); j += wpr) {
+          const float fj = __shfl_sync(0xffffffffu, f, j);
+          if (there(v0 + j)) {
+            const float* p = part(v0 + j) + q * D + lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += fj * p[32 * e];
+          }
+        }
+      }
+#pragma unroll
+      for (int sh = 16; sh; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+      bad = __any_sync(0xffffffffu, bad);
     }
-    const bool none = bad || pos0 + tok < 0;
-    if (tid == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-    if (tid < D)
-      prm.out[((int64_t)(q0 + tok) * prm.Hq + g * rq.G + q - tok * rq.G) * D + tid] = __float2bfloat16(none ? 0.f : o / sum);
+    if (wpr > 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < wpr; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += acc[warp + k][lane + 32 * e];
+      __syncthreads();
+    }
+    if (q < rows && sub == 0) {
+      const int tok = q / rq.G;
+      const bool none = bad || pos0 + tok < 0;
+      if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+      bf16* dst = prm.out + ((int64_t)(q0 + tok) * prm.Hq + g * rq.G + q - tok * rq.G) * D + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) dst[32 * e] = __float2bfloat16(none ? 0.f : o[e] / sum);
+    }
   }
 }
 
@@ -805,14 +813,6 @@ int encode_pool(CUtensorMap* m, const PagedProblem& pb, int rows) {
   return r == CUDA_SUCCESS ? GIST_ATTN_OK : GIST_ATTN_ERR_UNSUPPORTED;
 }
 
-int device_sms(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return GIST_ATTN_ERR_LAUNCH;
-  return GIST_ATTN_OK;
-}
-
 // CTAs: two an SM, or one a tile where the table cannot hold that many.
 int grid_of(const PagedProblem& pb, int sms) {
   const double tiles = (double)pb.B * pb.Hkv * (((int64_t)pb.W * pb.block_len * pb.d + 16383) / 16384);
@@ -820,10 +820,7 @@ int grid_of(const PagedProblem& pb, int sms) {
 }
 
 template <int D, int CH>
-int launch(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
-  int sms = 0;
-  int rc = device_sms(&sms);
-  if (rc != GIST_ATTN_OK) return rc;
+int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
   DecodeParams prm{};
   prm.q = static_cast<const bf16*>(pb.q);
   prm.out = static_cast<bf16*>(pb.out);
@@ -843,7 +840,7 @@ int launch(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
   while (plane_rows & ((1 << prm.box_shift) - 1)) --prm.box_shift;
   prm.box_rows = 1 << prm.box_shift;
   alignas(64) CUtensorMap tm;
-  rc = encode_pool(&tm, pb, prm.box_rows);
+  const int rc = encode_pool(&tm, pb, prm.box_rows);
   if (rc != GIST_ATTN_OK) return rc;
   constexpr uint32_t smem = smem_bytes<D, CH>();
   static_assert(smem <= 113 * 1024, "two CTAs an SM");
@@ -856,7 +853,7 @@ int launch(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
   // the combine's CTAs may start, and scan the lengths, while the last tiles run
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid - 1);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -871,18 +868,17 @@ int launch(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
 // Rows (new tokens x group) the kernel takes for a request.
 int paged_decode_rows(const PagedProblem& pb) { return pb.d / 4; }
 
-size_t paged_decode_workspace(const PagedProblem& pb) {
-  int sms = 0;
-  if (device_sms(&sms) != GIST_ATTN_OK) sms = 256;
+size_t paged_decode_workspace(const PagedProblem& pb, int sms) {
   return (size_t)grid_of(pb, sms) * 2 * paged_decode_rows(pb) * (pb.d + 2) * sizeof(float);
 }
 
-int launch_paged_decode(const PagedProblem& pb, void* workspace, cudaStream_t stream) {
+int launch_paged_decode(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
   const int64_t rows = (int64_t)pb.max_new * pb.G;
-  if (pb.d == 64) return rows <= 8 ? launch<64, 1>(pb, workspace, stream) : launch<64, 2>(pb, workspace, stream);
-  return rows <= 8    ? launch<128, 1>(pb, workspace, stream)
-         : rows <= 16 ? launch<128, 2>(pb, workspace, stream)
-                      : launch<128, 4>(pb, workspace, stream);
+  if (pb.d == 64)
+    return rows <= 8 ? launch<64, 1>(pb, workspace, sms, stream) : launch<64, 2>(pb, workspace, sms, stream);
+  return rows <= 8    ? launch<128, 1>(pb, workspace, sms, stream)
+         : rows <= 16 ? launch<128, 2>(pb, workspace, sms, stream)
+                      : launch<128, 4>(pb, workspace, sms, stream);
 }
 
 }  // namespace gattn
