@@ -55,6 +55,7 @@ struct DecodeParams {
   int Hq, L, layer, num_blocks;
   int box_rows, box_shift;  // tile rows of one TMA box: 2^box_shift
   float scale_log2;
+  uint32_t per_g;  // 2^16 / G rounded up: j / G = j per_g >> 16 for the rows there are
   uint64_t turn[64];
 };
 
@@ -196,7 +197,17 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int share(int total, int w, int W) { return (int)((int64_t)total * w / W); }
+// The run of CTA w among W is tiles [first(w), first(w + 1)): the lower ones are one
+// longer where W does not divide the total.
+struct Share {
+  int base, rest;
+  __device__ __forceinline__ Share(int total, int W) : base(total / W), rest(total % W) {}
+  __device__ __forceinline__ int first(int w) const { return w * base + min(w, rest); }
+  __device__ __forceinline__ int of(int x) const {  // the CTA that has tile x
+    const int cut = rest * (base + 1);
+    return x < cut ? x / (base + 1) : rest + (x - cut) / base;
+  }
+};
 
 template <int D, int CH>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -210,17 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Requests& rq = prm.rq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = rq.G;
+  auto token_of = [&](int row) { return (int)((uint32_t)row * prm.per_g >> 16); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int W = gridDim.x, me = blockIdx.x;
-  bool odd = false;
-  scan_requests<kThreads>(
-      rq.B, [&](int r) { return rq.tiles<KT>(r, &odd); }, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
-      [&](int all) { return share(all * rq.Hkv, me, W) / rq.Hkv; });
-  if (me == 0 && odd) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-  const int total = ms.total * rq.Hkv, x0 = share(total, me, W), x1 = share(total, me + 1, W);
-  if (x0 >= x1 || ms.start_r < 0) return;
-
   if (warp == 5) {
     tc::tmem_alloc(smem_u32(&ms.tmem), 256);
     tc::tmem_relinquish();
@@ -246,9 +250,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   for (int i = tid; i < D; i += kThreads) ms.nankey[i] = INT32_MAX;
   tc::fence_before_sync();
-  __syncthreads();
+  bool odd = false;
+  scan_requests<kThreads>(  // (its barriers publish the above too)
+      rq.B, [&](int r) { return rq.tiles<KT>(r, &odd); }, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
+      [&](int all) { return Share(all * rq.Hkv, W).first(me) / rq.Hkv; });
+  if (me == 0 && odd) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
   tc::fence_after_sync();
   const uint32_t tmem = ms.tmem;
+  const Share sh(ms.total * rq.Hkv, W);
+  const int x0 = sh.first(me), x1 = sh.first(me + 1);
+  if (x0 >= x1 || ms.start_r < 0) {
+    if (warp == 5) tc::tmem_dealloc(tmem, 256);
+    return;
+  }
   Walk<KT> wk;
   wk.init(rq, x0, x1, ms.start_r, ms.start_pre);
   bool failed = false;
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float x[8][E], y[8][E];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int tok = (j0 + j) / G;
+          const int tok = token_of(j0 + j);
           const bf16* p = src + (int64_t)tok * prm.Hq * D + (j0 + j - tok * G) * D;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int pos = pos0 + (j0 + j) / G;
+          const int pos = pos0 + token_of(j0 + j);
           float a[E], b[E];
           float top = 0.f;
 #pragma unroll
@@ -512,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 x = fmaf(__uint_as_float(v[p][8 + j]), 0.0625f, x);
                 x = fmaf(__uint_as_float(v[p][16 + j]), 0.00390625f, x);
                 x *= ks * rs[j];
-                if (edge && key0 + p > sg.pos0 + (c * 8 + j) / G) x = -INFINITY;
+                if (edge && key0 + p > sg.pos0 + token_of(c * 8 + j)) x = -INFINITY;
                 over |= x - m[c * 8 + j] > kSlack;
                 s[(c * KPR + p) * 8 + j] = x;
               }
@@ -672,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int j = 0; j < 8; ++j) {
               const int q = c * 8 + j;
               if (q < sg.rows) {
-                const int tok = q / G, pos = sg.pos0 + tok;
+                const int tok = token_of(q), pos = sg.pos0 + tok;
                 float x = o[q];
                 if (KPR == 2) x += xch[q * 64 + t];
                 if (nk <= pos) x = __int_as_float(0x7fc00000);
@@ -723,25 +737,26 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x + 1;
   scan_requests<kJoinThreads>(
       rq.B, [&](int r) { return rq.tiles<KT>(r); }, warp_sum, &start_r, &start_pre, &total_s,
-      [&](int all) { return share(all * rq.Hkv, w, W) / rq.Hkv; });
-  const int total = total_s * rq.Hkv, x = share(total, w, W), r = start_r;
+      [&](int all) { return Share(all * rq.Hkv, W).first(w) / rq.Hkv; });
+  const int total = total_s * rq.Hkv, r = start_r;
+  const Share sh(total, W);
+  const int x = sh.first(w);
   if (x >= total || r < 0) return;
   const int nt = rq.tiles<KT>(r), g = (x - rq.Hkv * start_pre) / nt;
   const int a = rq.Hkv * start_pre + g * nt, b = a + nt;
-  if (x == a || share(total, w - 1, W) > a) return;  // CTA w - 1 holds tile a
+  if (x == a || sh.first(w - 1) > a) return;  // CTA w - 1 holds tile a
   const int q0 = rq.q_start[r], n = rq.q_start[r + 1] - q0, pos0 = max(rq.length(r), 0) - n;
-  int last = w;  // the CTA that holds tile b - 1
-  while (last + 1 < W && share(total, last + 1, W) < b) ++last;
-  const int np = last - w + 2, rows = n * rq.G;
+  const int np = sh.of(b - 1) - w + 2, rows = n * rq.G;
   int wpr = kJoinWarps;  // warps a row
   while (wpr > 1 && kJoinWarps / wpr < rows) wpr >>= 1;
   const int sub = warp % wpr;
-  // part v: O, m and sum of CTA w - 1 + v (an empty run has none)
+  // part v: O, m and sum of CTA w - 1 + v.  Only CTA w - 1's run may start before the
+  // unit (its second part then); runs are not empty here, since a unit crosses two
+  // of them only if there are more tiles than CTAs, or a tile each
+  const int head = sh.first(w - 1) >= a ? 0 : 1;
   auto part = [&](int v) {
-    const int c = w - 1 + v, s0 = share(total, c, W);
-    return prm.parts + (int64_t)(2 * c + (s0 >= a ? 0 : 1)) * ROWS * (D + 2);
+    return prm.parts + (int64_t)(2 * (w - 1 + v) + (v == 0 ? head : 0)) * ROWS * (D + 2);
   };
-  auto there = [&](int v) { return v < np && share(total, w + v, W) > share(total, w - 1 + v, W); };
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int base = 0; base < rows; base += kJoinWarps / wpr) {
     const int q = base + warp / wpr;
@@ -751,12 +766,12 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     if (q < rows) {
       for (int v = lane; v < np; v += 32)
-        if (there(v)) m = fmaxf(m, part(v)[ROWS * D + q]);
+        m = fmaxf(m, part(v)[ROWS * D + q]);
 #pragma unroll
       for (int sh = 16; sh; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
       for (int v0 = 0; v0 < np; v0 += 32) {
         float f = 0.f;
-        if (there(v0 + lane)) {
+        if (v0 + lane < np) {
           const float* p = part(v0 + lane);
           const float ps = p[ROWS * D + ROWS + q];
           f = exp2f(p[ROWS * D + q] - m);
@@ -766,11 +781,9 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
 #pragma unroll 8
         for (int j = sub; j < min(32, np - v0); j += wpr) {
           const float fj = __shfl_sync(0xffffffffu, f, j);
-          if (there(v0 + j)) {
-            const float* p = part(v0 + j) + q * D + lane;
+          const float* p = part(v0 + j) + q * D + lane;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += fj * p[32 * e];
-          }
+          for (int e = 0; e < E; ++e) o[e] += fj * p[32 * e];
         }
       }
 #pragma unroll
@@ -834,6 +847,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   prm.layer = pb.layer;
   prm.num_blocks = pb.num_blocks;
   prm.scale_log2 = pb.scale_log2;
+  prm.per_g = (65536u + pb.G - 1) / pb.G;
   for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
   const int plane_rows = pb.block_len * D / 128;
   prm.box_shift = 7;
