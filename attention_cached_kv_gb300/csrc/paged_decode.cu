@@ -90,8 +90,11 @@ struct Misc {
   int bad[8];  // by segment: a block id outside the pool
   Seg seg[2];
   alignas(16) float rs[2][C::ROWS];  // softmax scale (log2) x q's power of two, by row
+  alignas(16) float wmax[4][C::ROWS];  // by warp: a tile's maxima, a segment's sums
+  alignas(16) float mrow[C::ROWS];
   float ksc[3][16], vsc[3][16];  // scales of a tile's boxes
-  float wmax[4][C::ROWS], wv[4];
+  float wv[4];
+  alignas(16)
   int nankey[D];  // first key past the first row's whose V is NaN, by element
   // the scan
   int warp_sum[kThreads / 32];
@@ -101,7 +104,9 @@ struct Misc {
 template <int D, int CH>
 constexpr uint32_t smem_bytes() {
   using M = Misc<D, CH>;
-  static_assert(offsetof(M, rs) % 16 == 0, "read as float4");
+  static_assert(offsetof(M, rs) % 16 == 0 && offsetof(M, wmax) % 16 == 0 && offsetof(M, mrow) % 16 == 0 &&
+                    offsetof(M, nankey) % 16 == 0,
+                "read as float4");
   return Cfg<D, CH>::offMisc + (uint32_t)sizeof(Misc<D, CH>);
 }
 
@@ -138,8 +143,14 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void sts16b(uint32_t addr, uint16_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// The largest of the warp's values (all lanes; NaN counts as no value).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // An f16 pair (magnitudes at most 448) as three E4M3 pairs: x0 + x1 / 16 + x2 / 256.
@@ -281,7 +292,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int row = kt * 128 + lane * br;
         return lane < boxes && (int64_t)row * KPR < kv ? table[row / vbl] : -1;
       };
-      int blk = block_of(kt0);
+      // ids are loaded two tiles ahead of their copies, scales one: no copy waits for
+      // either but a segment's first
+      auto plane_of = [&](int blk) {
+        return ((blk >= 0 && blk < prm.num_blocks ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + wk.g;
+      };
+      int blk = block_of(kt0), blk1 = kt0 + 1 < kt1 ? block_of(kt0 + 1) : -1;
+      int plane = plane_of(blk);
+      float k_scale = lane < boxes ? __ldg(prm.scale + plane) : 0.f;
+      float v_scale = lane < boxes ? __ldg(prm.scale + plane + rq.Hkv) : 0.f;
       if (lane == 0) ms.bad[seg & 7] = kv < 0;
       __syncwarp();
       for (int kt = kt0; kt < kt1; ++kt, ++i) {
@@ -295,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * br * 128;
         const int inner = row % vbl;
-        const int plane = ((ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + wk.g;
         if (__any_sync(0xffffffffu, (i >= NK && !mbar_wait(&ms.kfree[ks], ((uint32_t)(i / NK) & 1u) ^ 1u)))) {
           failed = true;
           break;
@@ -303,8 +321,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive_expect_tx(&ms.kfull[ks], bytes);
         __syncwarp();
         if (ok) tma_load_3d(sbase + ks * kStage + lane * br * 128, &tm, &ms.kfull[ks], 0, inner, plane);
-        const float k_scale = ok ? __ldg(prm.scale + plane) : 0.f;
-        const float v_scale = ok ? __ldg(prm.scale + plane + rq.Hkv) : 0.f;
+        const int plane1 = plane_of(blk1);
+        const float k1 = lane < boxes ? __ldg(prm.scale + plane1) : 0.f;
+        const float v1 = lane < boxes ? __ldg(prm.scale + plane1 + rq.Hkv) : 0.f;
+        const int blk2 = kt + 2 < kt1 ? block_of(kt + 2) : -1;
         if (__any_sync(0xffffffffu, (i >= NV && !mbar_wait(&ms.vfree[vs], ((uint32_t)(i / NV) & 1u) ^ 1u)))) {
           failed = true;
           ++i;  // its K load is in flight
@@ -313,13 +333,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive_expect_tx(&ms.vfull[vs], bytes);
         __syncwarp();
         if (ok) tma_load_3d(sbase + C::offV + vs * kStage + lane * br * 128, &tm, &ms.vfull[vs], 0, inner, plane + rq.Hkv);
-        if (kt + 1 < kt1) blk = block_of(kt + 1);
         if (lane < 16) {
-          ms.ksc[vs][lane] = k_scale;
-          ms.vsc[vs][lane] = v_scale;
+          ms.ksc[vs][lane] = ok ? k_scale : 0.f;
+          ms.vsc[vs][lane] = ok ? v_scale : 0.f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.scfull[vs]);
+        blk = blk1;
+        blk1 = blk2;
+        plane = plane1;
+        k_scale = k1;
+        v_scale = v1;
       }
     }
     if (failed) {  // the copies issued land before the CTA leaves
@@ -408,59 +432,59 @@ __global__ void __launch_bounds__(kThreads, 2)
         failed = true;
         break;
       }
-      constexpr int E = D / 64;  // frequencies a lane
-      const bf16* src = prm.q + ((int64_t)q0 * prm.Hq + wk.g * G) * D + lane * E;
-      for (int j0 = 0; j0 < rows; j0 += 8) {
-        float x[8][E], y[8][E];
+      // D / 16 lanes a row, each with elements j .. j + 7 and their partners j + D/2 ..
+      constexpr int LR = D / 16, RP = 32 / LR;
+      const int l = lane % LR, rl = lane / LR;
+      const bf16* src = prm.q + ((int64_t)q0 * prm.Hq + wk.g * G) * D + l * 8;
+      uint4 u, v;
+      auto fetch = [&](int row) {
+        const int rr = min(row, rows - 1), tok = token_of(rr);
+        const bf16* p = src + ((int64_t)tok * prm.Hq + rr - tok * G) * D;
+        u = ldg16(p);
+        v = ldg16(p + D / 2);
+      };
+      fetch(rl);
+      const int padded = (rows + 7) & ~7;
+#pragma unroll 1
+      for (int j0 = 0; j0 < padded; j0 += RP) {
+        const int row = j0 + rl;
+        const bool real = row < rows;
+        const int pos = pos0 + token_of(row);
+        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        if (j0 + RP < padded) fetch(row + RP);
+        float a[8], b[8], top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int tok = token_of(j0 + j);
-          const bf16* p = src + (int64_t)tok * prm.Hq * D + (j0 + j - tok * G) * D;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            x[j][e] = j0 + j < rows ? __bfloat162float(p[e]) : 0.f;
-            y[j][e] = j0 + j < rows ? __bfloat162float(p[e + D / 2]) : 0.f;
-          }
+        for (int e = 0; e < 8; ++e) {
+          const float x = real ? __uint_as_float(e & 1 ? uw[e >> 1] & 0xffff0000u : uw[e >> 1] << 16) : 0.f;
+          const float y = real ? __uint_as_float(e & 1 ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16) : 0.f;
+          float sn, cs;
+          __sincosf(turn_angle(pos, prm.turn[l * 8 + e]), &sn, &cs);
+          a[e] = x * cs - y * sn;
+          b[e] = y * cs + x * sn;
+          top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+          if (!(fabsf(a[e]) <= 3.4e38f) || !(fabsf(b[e]) <= 3.4e38f)) top = INFINITY;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int pos = pos0 + token_of(j0 + j);
-          float a[E], b[E];
-          float top = 0.f;
+        for (int o = LR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t tb = __float_as_uint(top);
+        const int ex = max((int)(tb >> 23) - 127 - 7, -119);  // the row's largest lands in [128, 256)
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        if (l == 0)
+          ms.rs[qs][row] = !real                ? 0.f
+                           : tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                                               : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
+        const uint32_t base = sbase + C::offQ + qs * C::QB + (row >> 3) * 3072 + (row & 7) * 128;
+        const uint32_t at = (uint32_t)(l * 8) ^ ((row & 7) << 4), bt = (uint32_t)(D / 2 + l * 8) ^ ((row & 7) << 4);
+        uint16_t ta[3][4], tb2[3][4];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            float sn, cs;
-            __sincosf(turn_angle(pos, prm.turn[lane * E + e]), &sn, &cs);
-            a[e] = x[j][e] * cs - y[j][e] * sn;
-            b[e] = y[j][e] * cs + x[j][e] * sn;
-            top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
-            if (!(fabsf(a[e]) <= 3.4e38f) || !(fabsf(b[e]) <= 3.4e38f)) top = INFINITY;
-          }
-          const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-          const int ex = max((int)(tb >> 23) - 127 - 7, -119);  // the row's largest lands in [128, 256)
-          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-          if (lane == 0)
-            ms.rs[qs][j0 + j] = j0 + j >= rows ? 0.f
-                                : tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
-                                                    : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
-          const uint32_t base = sbase + C::offQ + qs * C::QB + (j0 / 8) * 3072 + j * 128;
-          uint16_t t[3], u[3];
-          if constexpr (E == 2) {
-            split3(to_f16x2(a[0] * down, a[1] * down), t[0], t[1], t[2]);
-            split3(to_f16x2(b[0] * down, b[1] * down), u[0], u[1], u[2]);
+        for (int e = 0; e < 4; ++e) {
+          split3(to_f16x2(a[2 * e] * down, a[2 * e + 1] * down), ta[0][e], ta[1][e], ta[2][e]);
+          split3(to_f16x2(b[2 * e] * down, b[2 * e + 1] * down), tb2[0][e], tb2[1][e], tb2[2][e]);
+        }
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-              sts16b(base + s * 1024 + ((2 * lane) ^ (j << 4)), t[s]);
-              sts16b(base + s * 1024 + ((64 + 2 * lane) ^ (j << 4)), u[s]);
-            }
-          } else {
-            split3(to_f16x2(a[0] * down, b[0] * down), t[0], t[1], t[2]);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) {
-              sts8(base + s * 1024 + (lane ^ (j << 4)), t[s] & 0xff);
-              sts8(base + s * 1024 + ((32 + lane) ^ (j << 4)), t[s] >> 8);
-            }
-          }
+        for (int s = 0; s < 3; ++s) {
+          sts64(base + s * 1024 + at, (uint32_t)ta[s][0] | (uint32_t)ta[s][1] << 16, (uint32_t)ta[s][2] | (uint32_t)ta[s][3] << 16);
+          sts64(base + s * 1024 + bt, (uint32_t)tb2[s][0] | (uint32_t)tb2[s][1] << 16, (uint32_t)tb2[s][2] | (uint32_t)tb2[s][3] << 16);
         }
       }
       if (lane == 0) ms.seg[qs] = Seg{wk.r, wk.g, rows, q0, pos0, max(kv, 0), kt0, kt1, wk.nt, 0};
@@ -539,18 +563,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int c = 0; c < CH; ++c)
             if (c < nch) {
+              float w[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float x = s[c * KPR * 8 + j];
-                if (KPR == 2) x = fmaxf(x, s[(c * KPR + KPR - 1) * 8 + j]);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                if (lane == 0) ms.wmax[warp][c * 8 + j] = x;
+              for (int j = 0; j < 8; ++j)
+                w[j] = warp_max(fmaxf(s[c * KPR * 8 + j], s[(c * KPR + KPR - 1) * 8 + j]));
+              if (lane == 0) {
+                float4* at = reinterpret_cast<float4*>(&ms.wmax[warp][c * 8]);
+                at[0] = make_float4(w[0], w[1], w[2], w[3]);
+                at[1] = make_float4(w[4], w[5], w[6], w[7]);
               }
             }
-          float vm = vsc;
-#pragma unroll
-          for (int o = 16; o; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+          float vm = warp_max(vsc);
           if (lane == 0) ms.wv[warp] = vm;
           named_bar_sync(1, 128);
           vm = fmaxf(fmaxf(ms.wv[0], ms.wv[1]), fmaxf(ms.wv[2], ms.wv[3]));
@@ -565,27 +588,39 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (c < nch) {
               float f[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int q = c * 8 + j;
-                const float mn = fmaxf(m[q], fmaxf(fmaxf(ms.wmax[0][q], ms.wmax[1][q]), fmaxf(ms.wmax[2][q], ms.wmax[3][q])));
-                f[j] = ex2_approx(m[q] - mn);
-                l[q] *= f[j];
-                m[q] = mn;
-                f[j] *= fv;
+              for (int j = 0; j < 8; j += 4) {
+                float4 w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const float4*>(&ms.wmax[k][c * 8 + j]);
+                const float top[4] = {fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x)),
+                                      fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y)),
+                                      fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z)),
+                                      fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w))};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int q = c * 8 + j + k;
+                  const float mn = fmaxf(m[q], top[k]);
+                  f[j + k] = ex2_approx(m[q] - mn);
+                  l[q] *= f[j + k];
+                  m[q] = mn;
+                  f[j + k] *= fv;
+                }
               }
               if (kt > kt0) {
 #pragma unroll
-                for (int p = 0; p < KPR; ++p)
+                for (int p = 0; p < KPR; ++p) {
+                  const uint32_t a = tmem + lane_base + C::kO + p * 24 * nch + c * 24;
+                  uint32_t v[3][8];
+#pragma unroll
+                  for (int k = 0; k < 3; ++k) ld8(a + k * 8, v[k]);
+                  tc::wait_ld();
 #pragma unroll
                   for (int k = 0; k < 3; ++k) {
-                    const uint32_t a = tmem + lane_base + C::kO + p * 24 * nch + c * 24 + k * 8;
-                    uint32_t v[8];
-                    ld8(a, v);
-                    tc::wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f[j]);
-                    tc::st8(a, v);
+                    for (int j = 0; j < 8; ++j) v[k][j] = __float_as_uint(__uint_as_float(v[k][j]) * f[j]);
+                    tc::st8(a + k * 8, v[k]);
                   }
+                }
               }
             }
           tc::wait_st();
@@ -622,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           wait(&ms.vfull[vs], (uint32_t)(i / NV) & 1u);
           if (key0 + KPR - 1 > sg.pos0) {
             const uint32_t vrow = sbase + C::offV + vs * kStage + t * 128;
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < 8; ++ch) {
               const int key = key0 + (KPR == 2 ? ch >> 2 : 0);
               const uint32_t a = vrow + ((ch ^ (t & 7)) << 4);
@@ -631,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               } else if (key > sg.pos0) {
                 const uint4 w = lds16(a);
                 if (e4m3_nan(w.x) | e4m3_nan(w.y) | e4m3_nan(w.z) | e4m3_nan(w.w)) {
+#pragma unroll 1
                   for (int e = 0; e < 16; ++e)
                     if ((lds8(a + e) & 0x7fu) == 0x7fu) {
                       sts8(a + e, 0);
@@ -648,66 +684,89 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- the segment's O, m and sums
       wait(&ms.pfree[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u);
       tc::fence_after_sync();
-      const int par = KPR == 2 ? t >> 6 : 0;
+      // through shared memory (P's room), a warp a row then
       const float od = vref * (1.f / kPUnit);
-      const bool whole = kt0 == 0 && kt1 == sg.nt;
-      const bool bad = ms.bad[seg & 7] != 0;
-      float* xch = reinterpret_cast<float*>(smem + C::offP);  // d = 64: [ROWS][64]
-      float o[ROWS];
+      float* stage = reinterpret_cast<float*>(smem + C::offP);  // [ROWS][128]
+      static_assert(C::ROWS * 512 <= 2 * C::PB, "the stage fits P's buffers");
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         if (c < nch) {
           uint32_t v[24];
 #pragma unroll
-          for (int k = 0; k < 3; ++k) ld8(tmem + lane_base + C::kO + par * 24 * nch + c * 24 + k * 8, v + k * 8);
+          for (int k = 0; k < 3; ++k)
+            ld8(tmem + lane_base + C::kO + (KPR == 2 ? (t >> 6) * 24 * nch : 0) + c * 24 + k * 8, v + k * 8);
           tc::wait_ld();
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float x = __uint_as_float(v[j]);
             x = fmaf(__uint_as_float(v[8 + j]), 0.0625f, x);
             x = fmaf(__uint_as_float(v[16 + j]), 0.00390625f, x);
-            o[c * 8 + j] = x * od;
-            if (KPR == 2 && par == 1) xch[(c * 8 + j) * 64 + (t & 63)] = x * od;
-            float ls = l[c * 8 + j];
+            stage[(c * 8 + j) * 128 + t] = x * od;
+          }
+          // the warp's sums of 8 rows: halves, quarters, eighths of the rows a lane
+          float h[4];
 #pragma unroll
-            for (int sh = 16; sh; sh >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
-            if (lane == 0) ms.wmax[warp][c * 8 + j] = ls;
+          for (int k = 0; k < 4; ++k) {
+            const float keep = lane & 16 ? l[c * 8 + 4 + k] : l[c * 8 + k], send = lane & 16 ? l[c * 8 + k] : l[c * 8 + 4 + k];
+            h[k] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float keep = lane & 8 ? h[2 + k] : h[k], send = lane & 8 ? h[k] : h[2 + k];
+            h[k] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
+          }
+          float y = (lane & 4 ? h[1] : h[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? h[0] : h[1], 4);
+          y += __shfl_xor_sync(0xffffffffu, y, 2);
+          y += __shfl_xor_sync(0xffffffffu, y, 1);
+          if ((lane & 3) == 0) ms.wmax[warp][c * 8 + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] = y;
+          if (t == 0) {
+            float4* at = reinterpret_cast<float4*>(&ms.mrow[c * 8]);
+            at[0] = make_float4(m[c * 8], m[c * 8 + 1], m[c * 8 + 2], m[c * 8 + 3]);
+            at[1] = make_float4(m[c * 8 + 4], m[c * 8 + 5], m[c * 8 + 6], m[c * 8 + 7]);
           }
         }
       tc::fence_before_sync();
       named_bar_sync(1, 128);
-      if (KPR == 1 || t < 64) {
-        const int nk = ms.nankey[t];
-        float* part = prm.parts + (int64_t)(2 * me + (kt0 > 0 || x0 == wk.x ? 0 : 1)) * ROWS * (D + 2);
+      const bool whole = kt0 == 0 && kt1 == sg.nt, bad = ms.bad[seg & 7] != 0;
+      float* part = prm.parts + (int64_t)(2 * me + (x0 == wk.x ? 0 : 1)) * ROWS * (D + 2);
+      constexpr int E = D / 32;  // elements a lane
+#pragma unroll 1
+      for (int q = warp; q < sg.rows; q += 4) {
+        const int tok = token_of(q), pos = sg.pos0 + tok;
+        float x[E];
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-          if (c < nch) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int q = c * 8 + j;
-              if (q < sg.rows) {
-                const int tok = token_of(q), pos = sg.pos0 + tok;
-                float x = o[q];
-                if (KPR == 2) x += xch[q * 64 + t];
-                if (nk <= pos) x = __int_as_float(0x7fc00000);
-                const float sum = (ms.wmax[0][q] + ms.wmax[1][q]) + (ms.wmax[2][q] + ms.wmax[3][q]);
-                if (whole) {
-                  const bool none = bad || pos < 0;
-                  if (t == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-                  prm.out[((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + q - tok * G) * D + t] =
-                      __float2bfloat16(none ? 0.f : x / sum);
-                } else {
-                  part[q * D + t] = x;
-                  if (t == 0) {
-                    part[ROWS * D + q] = m[q];
-                    part[ROWS * D + ROWS + q] = bad ? -1.f : sum;
-                  }
-                }
-              }
-            }
+        for (int e = 0; e < E; e += 2) {
+          const float2 a = *reinterpret_cast<const float2*>(&stage[q * 128 + lane * E + e]);
+          x[e] = a.x;
+          x[e + 1] = a.y;
+          if (KPR == 2) {
+            const float2 b = *reinterpret_cast<const float2*>(&stage[q * 128 + 64 + lane * E + e]);
+            x[e] += b.x;
+            x[e + 1] += b.y;
           }
+          const int2 nk = *reinterpret_cast<const int2*>(&ms.nankey[lane * E + e]);
+          if (nk.x <= pos) x[e] = __int_as_float(0x7fc00000);
+          if (nk.y <= pos) x[e + 1] = __int_as_float(0x7fc00000);
+        }
+        const float sum = (ms.wmax[0][q] + ms.wmax[1][q]) + (ms.wmax[2][q] + ms.wmax[3][q]);
+        if (whole) {
+          const bool none = bad || pos < 0;
+          if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+          const float inv = 1.f / sum;
+          bf16* dst = prm.out + ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + q - tok * G) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = none ? 0u : float2_to_bf16x2(x[e] * inv, x[e + 1] * inv);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(part + q * D + lane * E + e) = make_float2(x[e], x[e + 1]);
+          if (lane == 0) {
+            part[ROWS * D + q] = ms.mrow[q];
+            part[ROWS * D + ROWS + q] = bad ? -1.f : sum;
+          }
+        }
       }
-      named_bar_sync(1, 128);  // the exchange, the sums and nankey are read
+      named_bar_sync(1, 128);  // the stage, the sums and nankey are read
       if (t < D) ms.nankey[t] = INT32_MAX;
       if (t == 0) mbar_arrive(&ms.qfree[qs]);
     }
