@@ -8,6 +8,7 @@ is no fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import NamedTuple
@@ -99,6 +100,8 @@ _lib = None
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load the built library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -439,42 +442,56 @@ def kv_bytes_batch(B, L, T, Hkv, d, elem_bytes) -> int:
 
 # ------------------------------------------------- the ragged serving step ---
 
-_PAGED_FIELDS = tuple(n for n, _ in PagedDims._fields_ if n not in ("status", "flags"))
+# One of these calls is a few microseconds of GPU work, so the marshalling stays short:
+# one pass over the dims, one test a tensor, the raw stream handle.
+_paged_values = operator.itemgetter(*[n for n, _ in PagedDims._fields_ if n not in ("status", "flags")])
 
 
 def make_paged_dims(d: dict, status: torch.Tensor | None = None) -> PagedDims:
-    out = PagedDims(*[d[n] for n in _PAGED_FIELDS])
-    out.flags = d.get("flags", 0)
+    out = PagedDims(*_paged_values(d))
+    if "flags" in d:
+        out.flags = d["flags"]
     if status is not None:
         _check(status, torch.int32, "status")
         out.status = status.data_ptr()
     return out
 
 
-def _sized(t, dtype, name, numel, device):
-    """Raw pointer of a contiguous CUDA tensor on `device` with at least `numel` elements."""
+def _index(t, name):
+    """The CUDA device number of tensor `t`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _sized(t, dtype, name, numel, dev):
+    """Raw pointer of a contiguous tensor on CUDA device `dev` with at least `numel` elements."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
+            and t.is_contiguous()):
+        return t.data_ptr()
     _check(t, dtype, name)
-    if t.device != device:
-        raise TypeError(f"{name} must be on {device}, got {t.device}")
-    if t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, the dimensions need {numel}")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise TypeError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} holds {t.numel()} elements, the dimensions need {numel}")
 
 
-def _pool_ptr(pool, dims, device):
+def _pool_ptr(pool, dims, dev):
     if not isinstance(pool, torch.Tensor) or pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError("kv_pool_e4m3 must be float8_e4m3fn or uint8")
     n = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
-    return _sized(pool, pool.dtype, "kv_pool_e4m3", n * dims["block_len"] * dims["head_dim"], device), n
+    return _sized(pool, pool.dtype, "kv_pool_e4m3", n * dims["block_len"] * dims["head_dim"], dev), n
 
 
-def _call(device, fn, *args, stream):
-    """fn(*args, stream) with `device` current, on `stream` or the device's current one."""
-    if torch.cuda.current_device() == device.index:
-        _raise(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(device):
-            _raise(fn(*args, _stream(stream)))
+def _call(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current, on `stream` or the device's current one."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _call(dev, stream, fn, *args)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if rc != OK:
+        _raise(rc)
 
 
 def gist_paged_plan(cached_len, new_len, block_table, free_blocks, free_range, out=None, *,
@@ -485,18 +502,18 @@ def gist_paged_plan(cached_len, new_len, block_table, free_blocks, free_range, o
     order to write into (allocated if None), so that a captured step keeps its
     buffers."""
     lib = load_library()
-    B, T, i32, dev = dims["num_requests"], dims["num_tokens"], torch.int32, new_len.device
+    B, T, i32, dev = dims["num_requests"], dims["num_tokens"], torch.int32, _index(new_len, "new_len")
     plan = PagedPlan(*(out if out is not None else
-                       (torch.empty(n, dtype=i32, device=dev) for n in (B + 1, B, T, T, 2))))
+                       (torch.empty(n, dtype=i32, device=new_len.device) for n in (B + 1, B, T, T, 2))))
     D = make_paged_dims(dims, status)
-    _call(dev, lib.gist_paged_plan, _sized(cached_len, i32, "cached_len", B, dev),
+    _call(dev, stream, lib.gist_paged_plan, _sized(cached_len, i32, "cached_len", B, dev),
           _sized(new_len, i32, "new_len", B, dev),
           _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
           _sized(free_blocks, i32, "free_blocks", 0, dev), free_blocks.numel(),
           _sized(free_range, i32, "free_range", 2, dev), _sized(plan.q_start, i32, "q_start", B + 1, dev),
           _sized(plan.kv_len, i32, "kv_len", B, dev), _sized(plan.slot, i32, "slot", T, dev),
           _sized(plan.position, i32, "position", T, dev),
-          _sized(plan.free_range, i32, "free_range (out)", 2, dev), ctypes.byref(D), stream=stream)
+          _sized(plan.free_range, i32, "free_range (out)", 2, dev), ctypes.byref(D))
     return plan
 
 
@@ -505,19 +522,19 @@ def gist_kv_append_fp8(k_new, v_new, kv_pool_e4m3, kv_scale, slot, position=None
     """Writes T new tokens' K (rotated at `position`) and V into the E4M3 pool at
     their slots, growing block scales where needed (pool and scales in place)."""
     lib = load_library()
-    T, n, dev = dims["num_tokens"], dims["num_tokens"] * dims["num_kv_heads"] * dims["head_dim"], k_new.device
-    bf, i32 = torch.bfloat16, torch.int32
+    T, dev, bf, i32 = dims["num_tokens"], _index(k_new, "k_new"), torch.bfloat16, torch.int32
+    n = T * dims["num_kv_heads"] * dims["head_dim"]
     pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
     D = make_paged_dims(dims, status)
-    _call(dev, lib.gist_kv_append_fp8, _sized(k_new, bf, "k_new", n, dev), _sized(v_new, bf, "v_new", n, dev),
-          pool, _sized(kv_scale, torch.float32, "kv_scale", planes, dev), _sized(slot, i32, "slot", T, dev),
-          None if position is None else _sized(position, i32, "position", T, dev), ctypes.byref(D),
-          stream=stream)
+    _call(dev, stream, lib.gist_kv_append_fp8, _sized(k_new, bf, "k_new", n, dev),
+          _sized(v_new, bf, "v_new", n, dev), pool, _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
+          _sized(slot, i32, "slot", T, dev),
+          None if position is None else _sized(position, i32, "position", T, dev), ctypes.byref(D))
     return kv_pool_e4m3, kv_scale
 
 
 def paged_workspace_bytes(dims: dict) -> int:
-    """Device bytes gist_attn_paged_fp8kv needs for these dimensions."""
+    """Device bytes gist_attn_paged_fp8kv needs for these dimensions on the current device."""
     D = make_paged_dims(dims)
     return int(load_library().gist_attn_paged_workspace_bytes(ctypes.byref(D)))
 
@@ -528,22 +545,25 @@ def gist_attn_paged_fp8kv(q, kv_pool_e4m3, kv_scale, block_table, q_start, kv_le
     """Causal attention of every request's new tokens over its cached sequence,
     which already holds them; returns `out` [T][Hq][d] (allocated if None; rows of
     padding tokens are not written).  `workspace`: a uint8 tensor of at least
-    paged_workspace_bytes(dims) bytes, one per call in flight (allocated if None)."""
+    paged_workspace_bytes(dims) bytes, one per call in flight (allocated if None,
+    on the current stream)."""
     lib = load_library()
-    B, dev = dims["num_requests"], q.device
+    B, dev, bf, i32 = dims["num_requests"], _index(q, "q"), torch.bfloat16, torch.int32
     if out is None:
         out = torch.empty_like(q)
-    bf, i32 = torch.bfloat16, torch.int32
     n = dims["num_tokens"] * dims["num_q_heads"] * dims["head_dim"]
     pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
     D = make_paged_dims(dims, status)
     if workspace is None:
-        need = int(lib.gist_attn_paged_workspace_bytes(ctypes.byref(D)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(dev, lib.gist_attn_paged_fp8kv, _sized(q, bf, "q", n, dev), pool,
+        with torch.cuda.device(dev):
+            need = int(lib.gist_attn_paged_workspace_bytes(ctypes.byref(D)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None and hasattr(stream, "cuda_stream"):
+            workspace.record_stream(stream)
+    _call(dev, stream, lib.gist_attn_paged_fp8kv, _sized(q, bf, "q", n, dev), pool,
           _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
           _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
           _sized(q_start, i32, "q_start", B + 1, dev), _sized(kv_len, i32, "kv_len", B, dev),
           _sized(out, bf, "out", n, dev), _sized(workspace, torch.uint8, "workspace", 0, dev),
-          workspace.numel(), ctypes.byref(D), stream=stream)
+          workspace.numel(), ctypes.byref(D))
     return out

@@ -10,7 +10,7 @@
 //
 // A unit is the new tokens of one block (consecutive rows, some perhaps skipped), a
 // KV head and K or V; one CTA takes the units whose first token lies in its `chunk`
-// tokens.  A thread holds elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row,
+// tokens (all of a prompt's block, a single token of a decoding step).  A thread holds elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row,
 // so it rotates its own pairs with four sines, and the rows stay in registers
 // between the pass for the largest magnitude and the one that converts.
 // Bound: HBM (three bytes an element: bf16 in, E4M3 out); few tokens: latency.
@@ -55,11 +55,11 @@ __device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
     append_fp8_kernel(const __grid_constant__ PagedAppendParams prm) {
   constexpr int kLanes = D / 8;               // threads of a row
   constexpr int kRows = kThreads / kLanes;    // rows of a pass
-  __shared__ uint32_t red[kThreads / 32];
+  __shared__ uint32_t red[kThreads / 32], heads[kThreads / 32];
   __shared__ int run_len;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kv = blockIdx.y & 1, g = blockIdx.y >> 1;
@@ -70,22 +70,29 @@ __global__ void __launch_bounds__(kThreads)
 
   const unsigned rows_in_pool = (unsigned)prm.num_blocks * bl;
   auto skipped = [&](int s) { return (unsigned)s >= rows_in_pool; };  // negative or outside
-  for (int t = t0; t < t1; ++t) {
-    const int s = prm.slot[t];
-    if (skipped(s)) {
-      if (s >= 0 && tid == 0) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-      continue;
+  // Token t opens the block's unit unless an earlier token of the call lies in the
+  // block: entry t - i of the slots is then s - i, with skipped ones between.
+  {
+    const int t = t0 + tid;
+    bool head = false;
+    if (t < t1) {
+      const int s = prm.slot[t];
+      head = !skipped(s);
+      if (!head && s >= 0) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+      if (head && t > 0) {
+        const int off = s % bl, before = prm.slot[t - 1];
+        if (off > 0 && before == s - 1) head = false;
+        if (off > 0 && skipped(before))
+          for (int i = 2; i <= min(off, t) && head; ++i) head = prm.slot[t - i] != s - i;
+      }
     }
-    const int blk = s / bl, off = s - blk * bl;
-    // Token t opens the block's unit unless an earlier token of the call lies in the
-    // block: entry t - i of the slots is then s - i, with skipped ones between.
-    bool inside = off > 0 && t > 0 && prm.slot[t - 1] == s - 1;
-    if (off > 0 && t > 0 && skipped(prm.slot[t - 1])) {
-      bool found = false;
-      for (int i = 1 + tid; i <= min(off, t); i += kThreads) found |= prm.slot[t - i] == s - i;
-      inside = __syncthreads_or(found);
-    }
-    if (inside) continue;
+    const uint32_t set = __ballot_sync(0xffffffffu, head);
+    if (lane == 0) heads[warp] = set;
+    __syncthreads();
+  }
+  for (int h = 0; h < t1 - t0; ++h) {
+    if (!(heads[h >> 5] >> (h & 31) & 1u)) continue;
+    const int t = t0 + h, s = prm.slot[t], blk = s / bl, off = s - blk * bl;
     // its tokens: entries t + e that are s + e, up to one that is neither that nor skipped
     const int most = min(bl - off, prm.T - t);
     int len = most;
@@ -115,12 +122,15 @@ __global__ void __launch_bounds__(kThreads)
     const bf16* src = x + ((int64_t)t * prm.Hkv + g) * D + j;
     const int64_t pitch = (int64_t)prm.Hkv * D;
     uint2 lo[kHold], hi[kHold];
+    int at[kHold];
     uint32_t top = 0;
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
       const int i = row0 + p * kRows;
       lo[p] = hi[p] = make_uint2(0, 0);
+      at[p] = 0;
       if (live(i)) {
+        if (rotate) at[p] = prm.position[t + i];
         lo[p] = *reinterpret_cast<const uint2*>(src + i * pitch);
         hi[p] = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
       }
@@ -149,19 +159,23 @@ __global__ void __launch_bounds__(kThreads)
     uint8_t* dst = prm.pool + plane * bl * D + (int64_t)off * D + j;
     if (off > 0 && scale > old) {  // the earlier rows (skipped ones too) at the larger scale
       const float f = old / scale;
-      uint32_t* rows = reinterpret_cast<uint32_t*>(prm.pool + plane * bl * D);
-      for (int i = tid; i < (off + (holes ? len : 0)) * (D / 4); i += kThreads) {
-        if (i >= off * (D / 4) && live(i / (D / 4) - off)) continue;
-        const uint32_t c = rows[i];
+      uint4* rows = reinterpret_cast<uint4*>(prm.pool + plane * bl * D);
+      auto turn4 = [&](uint32_t c) {
         const float2 a = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)c));
         const float2 b = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(c >> 16)));
         const float v[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
-        rows[i] = encode4(v);
+        return encode4(v);
+      };
+#pragma unroll 4
+      for (int i = tid; i < (off + (holes ? len : 0)) * (D / 16); i += kThreads) {
+        if (i >= off * (D / 16) && live(i / (D / 16) - off)) continue;
+        const uint4 c = rows[i];
+        rows[i] = make_uint4(turn4(c.x), turn4(c.y), turn4(c.z), turn4(c.w));
       }
     }
     if (tid == 0 && (off == 0 || scale > old)) prm.scale[plane] = scale;
     const float inv = 1.f / scale;
-    auto put = [&](int i, uint2 a, uint2 b) {
+    auto put = [&](int i, int pos, uint2 a, uint2 b) {
       float f[4], h[4];
       const float2 a0 = bf16x2_to_float2(a.x), a1 = bf16x2_to_float2(a.y);
       const float2 b0 = bf16x2_to_float2(b.x), b1 = bf16x2_to_float2(b.y);
@@ -169,7 +183,6 @@ __global__ void __launch_bounds__(kThreads)
       const float xs[4] = {a0.x * inv, a0.y * inv, a1.x * inv, a1.y * inv};
       const float ys[4] = {b0.x * inv, b0.y * inv, b1.x * inv, b1.y * inv};
       if (rotate) {
-        const int pos = prm.position[t + i];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float sn, cs;
@@ -190,11 +203,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
       const int i = row0 + p * kRows;
-      if (live(i)) put(i, lo[p], hi[p]);
+      if (live(i)) put(i, at[p], lo[p], hi[p]);
     }
     for (int i = row0 + kHold * kRows; i < len; i += kRows)
       if (live(i))
-        put(i, *reinterpret_cast<const uint2*>(src + i * pitch),
+        put(i, rotate ? prm.position[t + i] : 0, *reinterpret_cast<const uint2*>(src + i * pitch),
             *reinterpret_cast<const uint2*>(src + i * pitch + D / 2));
     __syncthreads();  // `red` is free again
   }
@@ -220,14 +233,15 @@ int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v
   prm.L = pb.L;
   prm.layer = pb.layer;
   for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
-  // A token a CTA while there are few (each may be a run of its own); more for
-  // long inputs, whose tokens mostly continue a run.
+  // Tokens a CTA: one while there are few (each may be a unit of its own), up to a
+  // block's worth where the tokens are many, so that no CTA is without a unit.
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  const int64_t units = (int64_t)pb.T * 2 * pb.Hkv;
-  prm.chunk = (int)(units <= 16LL * sms ? 1 : units / (16LL * sms) < 16 ? units / (16LL * sms) : 16);
+  const int64_t share = (int64_t)pb.T * 2 * pb.Hkv / (8LL * sms);
+  const int most = pb.block_len < 16 ? 16 : pb.block_len < kThreads ? pb.block_len : kThreads;
+  prm.chunk = share < 1 ? 1 : share < most ? (int)share : most;
   if (2LL * pb.Hkv > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)((pb.T + prm.chunk - 1) / prm.chunk), (unsigned)(2 * pb.Hkv));
   if (pb.d == 64)

@@ -24,8 +24,8 @@
 // machine.  A unit that crosses CTAs leaves parts (O, m, sum) in the workspace;
 // combine_kernel joins them in key order, the same way every time.
 //
-// Bound: HBM (a byte a cached element).  Seven warps: 0-3 softmax, 4 TMA and
-// scales, 5 tcgen05, 6 q rows.
+// Bound: HBM (a byte a cached element).  Eight warps: 0-3 softmax, 4 TMA and
+// scales, 5 tcgen05, 6-7 q rows.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.
@@ -39,17 +39,24 @@
 namespace gattn {
 namespace {
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr uint32_t kStage = 128 * 128;  // bytes of a K or V tile
 constexpr float kNone = -3.0e38f;       // running maximum before any key
 constexpr float kSlack = 2.f;           // log2 units a score may pass it by
 constexpr float kPUnit = 64.f;          // P's scale into E4M3
 
+// What the join needs of a unit that crosses CTAs, left by the CTA in whose run the
+// unit's second part begins (parts 0: nothing to join there).
+struct JoinUnit {
+  int parts, rows, q0, pos0, g, second;  // second: part 0 is the second of its CTA
+  int pad[2];
+};
 struct DecodeParams {
   const bf16* q;
   bf16* out;
   const float* scale;
-  float* parts;  // workspace
+  JoinUnit* join;  // workspace: [CTAs], then the parts
+  float* parts;
   int32_t* status;
   Requests rq;
   int Hq, L, layer, num_blocks;
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&ms.scfull[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ms.qfull[s], 1);
+      mbar_init(&ms.qfull[s], 2);
       mbar_init(&ms.qfree[s], 2);
       mbar_init(&ms.sfull[s], 1);
       mbar_init(&ms.sfree[s], 128);
@@ -271,11 +278,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Share sh(ms.total * rq.Hkv, W);
   const int x0 = sh.first(me), x1 = sh.first(me + 1);
   if (x0 >= x1 || ms.start_r < 0) {
+    if (tid == 0) prm.join[me].parts = 0;
     if (warp == 5) tc::tmem_dealloc(tmem, 256);
     return;
   }
   Walk<KT> wk;
   wk.init(rq, x0, x1, ms.start_r, ms.start_pre);
+  if (tid == 0) {
+    const int a = rq.Hkv * wk.pre + wk.g * wk.nt;  // the unit of this run's first tile
+    JoinUnit u{};
+    if (x0 > a && sh.first(me - 1) <= a) {
+      const int q0 = rq.q_start[wk.r], n = rq.q_start[wk.r + 1] - q0;
+      u.parts = sh.of(a + wk.nt - 1) - me + 2;
+      u.rows = n * G;
+      u.q0 = q0;
+      u.pos0 = max(rq.length(wk.r), 0) - n;
+      u.g = wk.g;
+      u.second = sh.first(me - 1) < a;
+    }
+    prm.join[me] = u;
+  }
   bool failed = false;
 
   if (warp == 4) {
@@ -420,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) tc::commit(smem_u32(&ms.drain));
     __syncwarp();
     if (!mbar_wait(&ms.drain, 0)) failed = true;
-  } else if (warp == 6) {
+  } else if (warp >= 6) {
     // ================================================== q rows
     for (int seg = 0; wk.more() && !failed; wk.next(rq), ++seg) {
       int kt0, kt1;
@@ -443,15 +465,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         u = ldg16(p);
         v = ldg16(p + D / 2);
       };
-      fetch(rl);
-      const int padded = (rows + 7) & ~7;
+      const int padded = (rows + 7) & ~7, mine = (warp - 6) * RP;
+      fetch(mine + rl);
 #pragma unroll 1
-      for (int j0 = 0; j0 < padded; j0 += RP) {
+      for (int j0 = mine; j0 < padded; j0 += 2 * RP) {
         const int row = j0 + rl;
         const bool real = row < rows;
         const int pos = pos0 + token_of(row);
         const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
-        if (j0 + RP < padded) fetch(row + RP);
+        if (j0 + 2 * RP < padded) fetch(row + 2 * RP);
         float a[8], b[8], top = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -487,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           sts64(base + s * 1024 + bt, (uint32_t)tb2[s][0] | (uint32_t)tb2[s][1] << 16, (uint32_t)tb2[s][2] | (uint32_t)tb2[s][3] << 16);
         }
       }
-      if (lane == 0) ms.seg[qs] = Seg{wk.r, wk.g, rows, q0, pos0, max(kv, 0), kt0, kt1, wk.nt, 0};
+      if (warp == 6 && lane == 0) ms.seg[qs] = Seg{wk.r, wk.g, rows, q0, pos0, max(kv, 0), kt0, kt1, wk.nt, 0};
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.qfull[qs]);
@@ -780,93 +802,94 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the parts of the units that cross CTAs: block w - 1 of the grid takes the
-// unit that the start of CTA w's run falls into, if no earlier start does.  A warp
-// (several, if there are fewer rows than warps) takes a row: all parts' maxima and
-// sums at once, then their O with the final weights, so that no load waits for
-// another's result; the order of the sums is fixed.
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32;
+// Joins the parts of the units that cross CTAs, a block of the grid a CTA w that may
+// hold a unit's second part.  A warp (several, if there are fewer rows than warps)
+// takes a row: all parts' maxima and sums at once, then their O with the final
+// weights, so that no load waits for another's result; the order of the sums is
+// fixed.
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kJoinHeld = 2048;
 template <int D, int CH>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ DecodeParams prm, int W) {
-  using C = Cfg<D, CH>;
-  constexpr int KT = C::KT, ROWS = C::ROWS, E = D / 32;  // E elements a lane
-  __shared__ int warp_sum[kJoinWarps], start_r, start_pre, total_s;
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ DecodeParams prm) {
+  constexpr int ROWS = Cfg<D, CH>::ROWS, E = D / 32;  // E elements a lane
+  __shared__ float2 held[kJoinHeld];                  // [row][part]: maximum and sum
   __shared__ float acc[kJoinWarps][D];
-  const Requests& rq = prm.rq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x + 1;
-  scan_requests<kJoinThreads>(
-      rq.B, [&](int r) { return rq.tiles<KT>(r); }, warp_sum, &start_r, &start_pre, &total_s,
-      [&](int all) { return Share(all * rq.Hkv, W).first(w) / rq.Hkv; });
-  const int total = total_s * rq.Hkv, r = start_r;
-  const Share sh(total, W);
-  const int x = sh.first(w);
-  if (x >= total || r < 0) return;
-  const int nt = rq.tiles<KT>(r), g = (x - rq.Hkv * start_pre) / nt;
-  const int a = rq.Hkv * start_pre + g * nt, b = a + nt;
-  if (x == a || sh.first(w - 1) > a) return;  // CTA w - 1 holds tile a
-  const int q0 = rq.q_start[r], n = rq.q_start[r + 1] - q0, pos0 = max(rq.length(r), 0) - n;
-  const int np = sh.of(b - 1) - w + 2, rows = n * rq.G;
-  int wpr = kJoinWarps;  // warps a row
-  while (wpr > 1 && kJoinWarps / wpr < rows) wpr >>= 1;
-  const int sub = warp % wpr;
-  // part v: O, m and sum of CTA w - 1 + v.  Only CTA w - 1's run may start before the
-  // unit (its second part then); runs are not empty here, since a unit crosses two
-  // of them only if there are more tiles than CTAs, or a tile each
-  const int head = sh.first(w - 1) >= a ? 0 : 1;
-  auto part = [&](int v) {
-    return prm.parts + (int64_t)(2 * (w - 1 + v) + (v == 0 ? head : 0)) * ROWS * (D + 2);
-  };
+  const int G = prm.rq.G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int base = 0; base < rows; base += kJoinWarps / wpr) {
-    const int q = base + warp / wpr;
-    float m = kNone, sum = 0.f, o[E];
-    bool bad = false;
+  const JoinUnit u = prm.join[w];
+  if (u.parts == 0) return;
+  int wpr = kJoinWarps;  // warps a row
+  while (wpr > 1 && kJoinWarps / wpr < u.rows) wpr >>= 1;
+  const int sub = warp % wpr, q = warp / wpr;
+  const bool mine = q < u.rows;
+  auto part = [&](int v) {
+    return prm.parts + (int64_t)(2 * (w - 1 + v) + (v == 0 ? u.second : 0)) * ROWS * (D + 2);
+  };
+  float m = kNone, sum = 0.f, o[E];
+  bool bad = false;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (q < rows) {
-      for (int v = lane; v < np; v += 32)
-        m = fmaxf(m, part(v)[ROWS * D + q]);
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  const int most = kJoinHeld / u.rows;
+  for (int v0 = 0; v0 < u.parts; v0 += most) {
+    const int nv = min(most, u.parts - v0);
+    for (int i = tid; i < nv * u.rows; i += kJoinThreads) {
+      const int v = i / u.rows, row = i - v * u.rows;
+      const float* p = part(v0 + v) + ROWS * D + row;
+      held[row * most + v] = make_float2(p[0], p[ROWS]);
+    }
+    __syncthreads();
+    if (mine) {
+      const float2* h = held + q * most;
+      float top = kNone;
+      for (int v = lane; v < nv; v += 32) top = fmaxf(top, h[v].x);
 #pragma unroll
-      for (int sh = 16; sh; sh >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-      for (int v0 = 0; v0 < np; v0 += 32) {
-        float f = 0.f;
-        if (v0 + lane < np) {
-          const float* p = part(v0 + lane);
-          const float ps = p[ROWS * D + ROWS + q];
-          f = exp2f(p[ROWS * D + q] - m);
-          bad |= ps < 0.f;
-          sum += ps * f;
-        }
+      for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      top = fmaxf(top, m);
+      const float f = exp2f(m - top);
+      m = top;
+      sum *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+      for (int v = lane; v < nv; v += 32) {
+        const float2 x = h[v];
+        sum += x.y * exp2f(x.x - m);
+        bad |= x.y < 0.f;
+      }
 #pragma unroll 8
-        for (int j = sub; j < min(32, np - v0); j += wpr) {
-          const float fj = __shfl_sync(0xffffffffu, f, j);
-          const float* p = part(v0 + j) + q * D + lane;
+      for (int v = sub; v < nv; v += wpr) {
+        const float* p = part(v0 + v) + q * D + lane * E;
+        const float fv = exp2f(h[v].x - m);
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += fj * p[32 * e];
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p + e);
+          o[e] += fv * x.x;
+          o[e + 1] += fv * x.y;
         }
       }
-#pragma unroll
-      for (int sh = 16; sh; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
-      bad = __any_sync(0xffffffffu, bad);
     }
-    if (wpr > 1) {
+    __syncthreads();
+  }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
-      __syncthreads();
-      if (sub == 0)
-        for (int k = 1; k < wpr; ++k)
+  for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  bad = __any_sync(0xffffffffu, bad);
+  if (wpr > 1) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += acc[warp + k][lane + 32 * e];
-      __syncthreads();
-    }
-    if (q < rows && sub == 0) {
-      const int tok = q / rq.G;
-      const bool none = bad || pos0 + tok < 0;
-      if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-      bf16* dst = prm.out + ((int64_t)(q0 + tok) * prm.Hq + g * rq.G + q - tok * rq.G) * D + lane;
+    for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (sub == 0)
+      for (int k = 1; k < wpr; ++k)
 #pragma unroll
-      for (int e = 0; e < E; ++e) dst[32 * e] = __float2bfloat16(none ? 0.f : o[e] / sum);
-    }
+        for (int e = 0; e < E; ++e) o[e] += acc[warp + k][lane * E + e];
+  }
+  if (mine && sub == 0) {
+    const int tok = q / G;
+    const bool none = bad || u.pos0 + tok < 0;
+    if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+    const float inv = 1.f / sum;
+    bf16* dst = prm.out + ((int64_t)(u.q0 + tok) * prm.Hq + u.g * G + q - tok * G) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = none ? 0u : float2_to_bf16x2(o[e] * inv, o[e + 1] * inv);
   }
 }
 
@@ -897,7 +920,9 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   prm.q = static_cast<const bf16*>(pb.q);
   prm.out = static_cast<bf16*>(pb.out);
   prm.scale = pb.scale;
-  prm.parts = static_cast<float*>(workspace);
+  const int grid = grid_of(pb, sms);
+  prm.join = static_cast<JoinUnit*>(workspace);
+  prm.parts = reinterpret_cast<float*>(prm.join + grid);
   prm.status = pb.status;
   prm.rq = requests_of(pb);
   prm.rq.max_rows = Cfg<D, CH>::ROWS;
@@ -919,7 +944,6 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   static_assert(smem <= 113 * 1024, "two CTAs an SM");
   if (cudaFuncSetAttribute(decode_kernel<D, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  const int grid = grid_of(pb, sms);
   decode_kernel<D, CH><<<grid, kThreads, smem, stream>>>(tm, prm);
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
   if (grid == 1) return GIST_ATTN_OK;
@@ -933,7 +957,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D, CH>, prm, grid) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D, CH>, prm) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -942,7 +966,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
 int paged_decode_rows(const PagedProblem& pb) { return pb.d / 4; }
 
 size_t paged_decode_workspace(const PagedProblem& pb, int sms) {
-  return (size_t)grid_of(pb, sms) * 2 * paged_decode_rows(pb) * (pb.d + 2) * sizeof(float);
+  return (size_t)grid_of(pb, sms) * (sizeof(JoinUnit) + 2 * paged_decode_rows(pb) * (pb.d + 2) * sizeof(float));
 }
 
 int launch_paged_decode(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
