@@ -7,13 +7,13 @@
 
 namespace gattn {
 
-// Angle of position `pos` at frequency `turn` (theta / 2 pi modulo 1, in units of
-// 2^-64): the product modulo 2^64 is the angle modulo a whole turn, so nothing is
-// lost at far positions (off by at most pos 2^-53 turns, the double that `turn`
-// came from) and no range reduction is left.  In [-pi, pi).
+// Angle of position `pos` (not negative) at frequency `turn` (theta / 2 pi modulo 1,
+// in units of 2^-64): the product modulo 2^64 is the angle modulo a whole turn, so
+// nothing is lost at far positions (off by at most pos 2^-53 turns, the double that
+// `turn` came from) and no range reduction is left.  In [-pi, pi).
 __device__ __forceinline__ float turn_angle(int pos, uint64_t turn) {
-  const uint64_t a = (uint64_t)(int64_t)pos * turn;
-  return (float)(int32_t)(a >> 32) * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  const uint32_t a = (uint32_t)pos * (uint32_t)(turn >> 32) + __umulhi((uint32_t)pos, (uint32_t)turn);
+  return (float)(int32_t)a * 1.4629180792671596e-09f;  // 2 pi / 2^32
 }
 
 // Two floats to two E4M3 codes (nearest even, saturating at 448; `lo` in the low byte).

@@ -45,13 +45,19 @@ __device__ __forceinline__ uint32_t finite_abs2(uint32_t v) {  // max of the two
   return max(a, b);
 }
 
-// Codes of a and b (already divided by the scale); non-finite x become NaN.
 __device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
-  uint32_t r = (uint32_t)e4m3x2(f[0], f[1]) | (uint32_t)e4m3x2(f[2], f[3]) << 16;
+  return (uint32_t)e4m3x2(f[0], f[1]) | (uint32_t)e4m3x2(f[2], f[3]) << 16;
+}
+// As encode4 (which saturates infinities), with NaN codes for all that is not finite.
+__device__ __forceinline__ uint32_t encode4_odd(const float (&f)[4]) {
+  uint32_t r = encode4(f);
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (!(fabsf(f[e]) <= 3.4e38f)) r = (r & ~(0xffu << (8 * e))) | (0x7fu << (8 * e));
+    if (!(fabsf(f[e]) <= 3.4e38f)) r = (r & ~(0xffu << (8 * e))) | 0x7fu << (8 * e);
   return r;
+}
+__device__ __forceinline__ bool odd2(uint32_t v) {  // an infinity or NaN in a bf16 pair
+  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
 }
 
 template <int D>
@@ -62,11 +68,16 @@ __global__ void __launch_bounds__(kThreads, 5)
   __shared__ uint32_t red[kThreads / 32], heads[kThreads / 32];
   __shared__ int run_len;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kv = blockIdx.y & 1, g = blockIdx.y >> 1;
+  // heads vary fastest: CTAs that run together read whole token rows
+  const int y = blockIdx.x % (2 * prm.Hkv), first = blockIdx.x / (2 * prm.Hkv);
+  const int kv = y & 1, g = y >> 1;
   const int bl = prm.block_len, j = (tid % kLanes) * 4, row0 = tid / kLanes;
   const bf16* x = prm.x[kv];
-  const int t0 = blockIdx.x * prm.chunk, t1 = min(t0 + prm.chunk, prm.T);
+  const int t0 = first * prm.chunk, t1 = min(t0 + prm.chunk, prm.T);
   const bool rotate = kv == 0 && prm.position != nullptr;
+  uint64_t turn[4];  // (a constant read by 16 threads at 16 places is slow: once)
+#pragma unroll
+  for (int q = 0; q < 4; ++q) turn[q] = prm.turn[j + q];
 
   const unsigned rows_in_pool = (unsigned)prm.num_blocks * bl;
   auto skipped = [&](int s) { return (unsigned)s >= rows_in_pool; };  // negative or outside
@@ -124,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 5)
     uint2 lo[kHold], hi[kHold];
     int at[kHold];
     uint32_t top = 0;
+    bool odd = false;  // something that is not finite
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
       const int i = row0 + p * kRows;
@@ -136,17 +148,19 @@ __global__ void __launch_bounds__(kThreads, 5)
       }
       top = max(top, max(max(finite_abs2(lo[p].x), finite_abs2(lo[p].y)),
                          max(finite_abs2(hi[p].x), finite_abs2(hi[p].y))));
+      odd |= odd2(lo[p].x) | odd2(lo[p].y) | odd2(hi[p].x) | odd2(hi[p].y);
     }
     for (int i = row0 + kHold * kRows; i < len; i += kRows) {
       if (!live(i)) continue;
       const uint2 a = *reinterpret_cast<const uint2*>(src + i * pitch);
       const uint2 b = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
       top = max(top, max(max(finite_abs2(a.x), finite_abs2(a.y)), max(finite_abs2(b.x), finite_abs2(b.y))));
+      odd |= odd2(a.x) | odd2(a.y) | odd2(b.x) | odd2(b.y);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) red[warp] = top;
     const float old = off > 0 ? prm.scale[plane] : 0.f;
-    __syncthreads();
+    odd = __syncthreads_or(odd);
     top = max(max(red[0], red[1]), max(red[2], red[3]));
     // the smallest power of two >= top / limit (limit / 512 = 0.875 or 0.6171875)
     const uint32_t bits = top << 16;
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 5)
         const float2 a = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)c));
         const float2 b = f16x2_to_float2(e4m3x2_to_f16x2((uint16_t)(c >> 16)));
         const float v[4] = {a.x * f, a.y * f, b.x * f, b.y * f};
-        return encode4(v);
+        return encode4_odd(v);
       };
 #pragma unroll 4
       for (int i = tid; i < (off + (holes ? len : 0)) * (D / 16); i += kThreads) {
@@ -186,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 5)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float sn, cs;
-          __sincosf(turn_angle(pos, prm.turn[j + q]), &sn, &cs);
+          __sincosf(turn_angle(pos, turn[q]), &sn, &cs);
           f[q] = xs[q] * cs - ys[q] * sn;
           h[q] = ys[q] * cs + xs[q] * sn;
         }
@@ -197,8 +211,9 @@ __global__ void __launch_bounds__(kThreads, 5)
           h[q] = ys[q];
         }
       }
-      *reinterpret_cast<uint32_t*>(dst + (int64_t)i * D) = encode4(f);
-      *reinterpret_cast<uint32_t*>(dst + (int64_t)i * D + D / 2) = encode4(h);
+      uint8_t* row = dst + i * D;
+      *reinterpret_cast<uint32_t*>(row) = odd ? encode4_odd(f) : encode4(f);
+      *reinterpret_cast<uint32_t*>(row + D / 2) = odd ? encode4_odd(h) : encode4(h);
     };
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
@@ -242,12 +257,12 @@ int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v
   const int64_t share = (int64_t)pb.T * 2 * pb.Hkv / (8LL * sms);
   const int most = pb.block_len < 16 ? 16 : pb.block_len < kThreads ? pb.block_len : kThreads;
   prm.chunk = share < 1 ? 1 : share < most ? (int)share : most;
-  if (2LL * pb.Hkv > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)((pb.T + prm.chunk - 1) / prm.chunk), (unsigned)(2 * pb.Hkv));
+  const int64_t grid = ((int64_t)pb.T + prm.chunk - 1) / prm.chunk * 2 * pb.Hkv;
+  if (grid > 0x7fffffff) return GIST_ATTN_ERR_UNSUPPORTED;
   if (pb.d == 64)
-    append_fp8_kernel<64><<<grid, kThreads, 0, stream>>>(prm);
+    append_fp8_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(prm);
   else
-    append_fp8_kernel<128><<<grid, kThreads, 0, stream>>>(prm);
+    append_fp8_kernel<128><<<(unsigned)grid, kThreads, 0, stream>>>(prm);
   return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 

@@ -26,6 +26,8 @@
 //        [Suffix page] icman.com.cn news 64898.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -53,7 +55,6 @@ struct PrefillParams {
 
 template <int D>
 struct PCfg {
-  static constexpr int NP = D / 64;                     // 64-column panels
   static constexpr uint32_t kTile = 128 * D * 2;        // bytes of a 128-row f16 tile
   static constexpr uint32_t kPanel = 128 * 128;
   static constexpr uint32_t offK = 2 * kTile, offV = 4 * kTile, offMisc = 6 * kTile;
@@ -67,7 +68,11 @@ struct PMisc {
   int bad, any_nan;
   int warp_sum[kThreads / 32 + 1];
   int start_r, start_pre, total;
-  alignas(16) float ksc[4][8];  // K scales of a tile's 16-key groups
+  // by tile (modulo 4) and 16-key group: K and V scale, first byte of the K rows in
+  // the pool (-1: no key that is seen, or a block outside the pool)
+  alignas(16) float ksc[4][8], vsc[4][8];
+  int64_t at[4][8];
+  int even[4];  // the groups' K scales are equal in pairs
   float vref, vpart[4];
   int nankey[D];  // first key past the first row's whose V is NaN, by element
 };
@@ -77,6 +82,17 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// As ld32, waited for, the maximum only.
+__device__ __forceinline__ float ld32_max(uint32_t taddr) {
+  uint32_t r[32];
+  float m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m)::"memory");
+  return m;
 }
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -251,25 +267,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const float vref = fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
     if (ct == 0) ms.vref = vref;  // (read by the softmax after vready -> pfull -> sfull)
     const float rvref = 1.f / vref;
+    // Threads 0 .. 7 look up the groups of the tiles ahead: an id four tiles ahead of
+    // its use, the scales three, in shared memory two.
+    float gk = 0.f, gv = 0.f;
+    int64_t ga = -1;
+    int gid = -1;
+    bool want = false;  // there are such keys
+    auto look_up = [&](int i) {
+      const int key = (kt0 + i) * kKT + ct * 16;
+      want = i < nt && key < kend && kv >= 0;
+      gid = want ? table[key / rq.block_len] : -1;
+    };
+    auto scales_of = [&](int kt) {
+      gk = gv = 0.f;
+      ga = -1;
+      if (want && gid >= 0 && gid < prm.num_blocks) {
+        const int64_t plane = ((int64_t)gid * prm.L + prm.layer) * 2 * rq.Hkv + g;
+        ga = (plane * rq.block_len + (kt * kKT + ct * 16) % rq.block_len) * D;
+        gk = prm.scale[plane];
+        gv = prm.scale[plane + rq.Hkv];
+      } else if (want) {
+        ms.bad = 1;
+        report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+      }
+    };
+    auto publish = [&](int i) {
+      ms.ksc[i & 3][ct] = gk;
+      ms.vsc[i & 3][ct] = gv;
+      ms.at[i & 3][ct] = ga;
+      const bool same = __shfl_xor_sync(0xffu, gk, 1) == gk;
+      const bool all = __all_sync(0xffu, same);
+      if (ct == 0) ms.even[i & 3] = all;
+    };
+    if (ct < 8) {
+      for (int i = 0; i < 2; ++i) {
+        look_up(i);
+        scales_of(kt0 + i);
+        publish(i);
+      }
+      look_up(2);
+      scales_of(kt0 + 2);
+      look_up(3);
+    }
+    named_bar_sync(2, 128);
     uint4 kx[kPass], vx[kPass];
-    float vr[kPass];
-    auto fetch = [&](int kt, uint4 (&x)[kPass], bool v) {
+    auto fetch = [&](int i, uint4 (&x)[kPass], int64_t more) {
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
-        const int key = kt * kKT + p * kRows + row0;
+        const int row = p * kRows + row0;
+        const int64_t at = ms.at[i & 3][row >> 4];
         x[p] = make_uint4(0, 0, 0, 0);
-        if (v) vr[p] = 0.f;
-        if (key < kend && kv >= 0) {
-          const int b = key / rq.block_len, blk = table[b];
-          if (blk >= 0 && blk < prm.num_blocks) {
-            const int64_t plane = ((int64_t)blk * prm.L + prm.layer) * 2 * rq.Hkv + g;
-            x[p] = ldg16(prm.pool + (plane * rq.block_len + key - b * rq.block_len) * D + c * 16 + (v ? vstep : 0));
-            if (v) vr[p] = prm.scale[plane + rq.Hkv];
-          } else {
-            ms.bad = 1;
-            report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-          }
-        }
+        if (at >= 0 && (kt0 + i) * kKT + row < kend) x[p] = ldg16(prm.pool + at + (row & 15) * D + c * 16 + more);
       }
     };
     // 16 codes as two 16-byte chunks of f16 of tile row `row`; the second half of a
@@ -292,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sts16(base + swz128(row, ch + odd), odd ? hi : lo);
       sts16(base + swz128(row, ch + 1 - odd), odd ? lo : hi);
     };
-    if (nt > 0) fetch(kt0, kx, false), fetch(kt0, vx, true);
+    if (nt > 0) fetch(0, kx, 0), fetch(0, vx, vstep);
     for (int i = 0; i < nt && !failed; ++i) {
       const int kt = kt0 + i, b = i & 1;
       if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
@@ -301,18 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) put(sbase + C::offK + b * C::kTile, p * kRows + row0, kx[p], 0, false);
-      if (ct < 8) {  // K scales of the tile's 16-key groups (softmax scale apart)
-        const int key = kt * kKT + ct * 16;
-        float s = 0.f;
-        if (key < kend && kv >= 0) {
-          const int blk = table[key / rq.block_len];
-          if (blk >= 0 && blk < prm.num_blocks) s = prm.scale[((int64_t)blk * prm.L + prm.layer) * 2 * rq.Hkv + g];
-        }
-        ms.ksc[i & 3][ct] = s;
-      }
       fence_proxy_async_smem();
       mbar_arrive(&ms.kready[b]);
-      if (i + 1 < nt) fetch(kt + 1, kx, false);
+      if (i + 1 < nt) fetch(i + 1, kx, 0);
       if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
@@ -339,12 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
-        const float f = vr[p] * rvref;
+        const float f = ms.vsc[i & 3][(p * kRows + row0) >> 4] * rvref;
         put(sbase + C::offV + b * C::kTile, p * kRows + row0, vx[p], to_f16x2(f, f), true);
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.vready[b]);
-      if (i + 1 < nt) fetch(kt + 1, vx, true);
+      if (i + 1 < nt) fetch(i + 1, vx, vstep);
+      if (ct < 8) {
+        publish(i + 2);
+        scales_of(kt + 3);
+        look_up(i + 4);
+      }
+      named_bar_sync(2, 128);
     }
   } else {
     // ================================================== q rows, softmax, output
@@ -408,26 +453,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool edge = key0 + kKT > lim_all;
       wait(&ms.sfull[x], (uint32_t)i & 1u);
       tc::fence_after_sync();
-      const float4 s0 = *reinterpret_cast<const float4*>(&ms.ksc[i & 3][0]);
-      const float4 s1 = *reinterpret_cast<const float4*>(&ms.ksc[i & 3][4]);
-      const float f[8] = {s0.x * rs, s0.y * rs, s0.z * rs, s0.w * rs, s1.x * rs, s1.y * rs, s1.z * rs, s1.w * rs};
+      const float* ksc = ms.ksc[i & 3];
       float mx = kNone;
+      if (!edge && ms.even[i & 3]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        ld32(ts + c * 32, v);
-        tc::wait_ld();
+        for (int c = 0; c < 4; ++c) mx = fmaxf(mx, ld32_max(ts + c * 32) * (ksc[2 * c] * rs));
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          ld32(ts + c * 32, v);
+          tc::wait_ld();
+          const int left = lim - key0 - c * 32;  // columns of these that the row sees
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float t = -INFINITY;
-          if (edge) {
+          for (int h = 0; h < 2; ++h) {
+            float t = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) t = fmaxf(t, key0 + c * 32 + h * 16 + e < lim ? __uint_as_float(v[h * 16 + e]) : -INFINITY);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) t = max3f(t, __uint_as_float(v[h * 16 + e]), __uint_as_float(v[h * 16 + e + 1]));
+            for (int e = 0; e < 16; ++e) t = fmaxf(t, h * 16 + e < left || !edge ? __uint_as_float(v[h * 16 + e]) : -INFINITY);
+            mx = fmaxf(mx, t * (ksc[2 * c + h] * rs));
           }
-          mx = fmaxf(mx, t * f[2 * c + h]);
         }
       }
       // a row whose maximum jumps scales its O and sum down first; the TMEM load and
@@ -451,21 +495,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
       }
+      // 32 scores in registers, the next 32 on their way
       const uint64_t nm2 = f2_make(-m, -m);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], pk[16];
-        ld32(ts + c * 32, v);
-        tc::wait_ld();
+      uint32_t va[32], vb[32];
+      auto weights = [&](int c, uint32_t (&v)[32], auto masked) {
+        uint32_t pk[16];
+        const float2 k2 = *reinterpret_cast<const float2*>(ksc + 2 * c);
+        const float f0 = k2.x * rs, f1 = k2.y * rs;
+        const uint64_t g0 = f2_make(f0, f0), g1 = f2_make(f1, f1);
+        const int left = lim - key0 - c * 32;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float fg = f[2 * c + (e >> 3)];
           float a, b;
-          f2_split(f2_fma(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2_make(fg, fg), nm2), a, b);
-          if (edge) {
-            const int key = key0 + c * 32 + 2 * e;
-            if (key >= lim) a = -INFINITY;
-            if (key + 1 >= lim) b = -INFINITY;
+          f2_split(f2_fma(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), e < 8 ? g0 : g1, nm2), a, b);
+          if (masked) {
+            if (2 * e >= left) a = -INFINITY;
+            if (2 * e + 1 >= left) b = -INFINITY;
           }
           const float pa = ex2_approx(a), pb = ex2_approx(b);
           if (e & 1) acc = f2_add(acc, f2_make(pa, pb));
@@ -473,6 +518,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           pk[e] = to_f16x2(pa, pb);
         }
         st16(ts + c * 16, pk);
+      };
+      if (!edge) {
+        ld32(ts, va);
+        tc::wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          ld32(ts + c * 32 + 32, vb);
+          weights(c, va, std::false_type{});
+          tc::wait_ld();
+          if (c + 2 < 4) ld32(ts + c * 32 + 64, va);
+          weights(c + 1, vb, std::false_type{});
+          tc::wait_ld();
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          ld32(ts + c * 32, va);
+          tc::wait_ld();
+          weights(c, va, std::true_type{});
+        }
       }
       tc::wait_st();
       tc::fence_before_sync();
