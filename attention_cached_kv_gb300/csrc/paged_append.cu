@@ -37,12 +37,14 @@ struct PagedAppendParams {
   uint64_t turn[64];
 };
 
-// |x| of finite bf16 values as bits, 0 for infinities and NaN.
-__device__ __forceinline__ uint32_t finite_abs2(uint32_t v) {  // max of the two halves
-  uint32_t a = v & 0x7fffu, b = (v >> 16) & 0x7fffu;
-  a = a < 0x7f80u ? a : 0u;
-  b = b < 0x7f80u ? b : 0u;
-  return max(a, b);
+// Magnitude bits of a bf16 pair, and the larger of two pairs half by half.
+__device__ __forceinline__ uint32_t abs2(uint32_t v) { return v & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t top2(uint32_t m, uint2 v) { return __vmaxu2(m, __vmaxu2(abs2(v.x), abs2(v.y))); }
+constexpr uint32_t kInf = 0x7f80u;  // bf16 magnitudes from here on are not finite
+// The same with 0 for what is not finite.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  const uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
+  return (lo < kInf ? lo : 0u) | (hi < kInf ? hi : 0u) << 16;
 }
 
 __device__ __forceinline__ uint32_t encode4(const float (&f)[4]) {
@@ -56,17 +58,13 @@ __device__ __forceinline__ uint32_t encode4_odd(const float (&f)[4]) {
     if (!(fabsf(f[e]) <= 3.4e38f)) r = (r & ~(0xffu << (8 * e))) | 0x7fu << (8 * e);
   return r;
 }
-__device__ __forceinline__ bool odd2(uint32_t v) {  // an infinity or NaN in a bf16 pair
-  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
-}
-
 template <int D>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 7)
     append_fp8_kernel(const __grid_constant__ PagedAppendParams prm) {
   constexpr int kLanes = D / 8;               // threads of a row
   constexpr int kRows = kThreads / kLanes;    // rows of a pass
   __shared__ uint32_t red[kThreads / 32], heads[kThreads / 32];
-  __shared__ int run_len;
+  __shared__ int run_len, pos_of[kThreads];  // positions of a unit's first kThreads tokens
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // heads vary fastest: CTAs that run together read whole token rows
   const int y = blockIdx.x % (2 * prm.Hkv), first = blockIdx.x / (2 * prm.Hkv);
@@ -101,8 +99,12 @@ __global__ void __launch_bounds__(kThreads, 5)
     if (lane == 0) heads[warp] = set;
     __syncthreads();
   }
-  for (int h = 0; h < t1 - t0; ++h) {
-    if (!(heads[h >> 5] >> (h & 31) & 1u)) continue;
+  uint32_t left = 0;
+  for (int w = -1;;) {
+    while (left == 0 && ++w < kThreads / 32) left = heads[w];
+    if (w == kThreads / 32) break;
+    const int h = w * 32 + __ffs(left) - 1;
+    left &= left - 1;
     const int t = t0 + h, s = prm.slot[t], blk = s / bl, off = s - blk * bl;
     // its tokens: entries t + e that are s + e, up to one that is neither that nor skipped
     const int most = min(bl - off, prm.T - t);
@@ -113,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 5)
       __syncthreads();
       const int e = i + tid, v = e < most ? prm.slot[t + e] : s + e;
       if (!skipped(v) && v != s + e) atomicMin(&run_len, e);
+      if (i == 0 && rotate && e < most) pos_of[e] = prm.position[t + e];
       holes |= __syncthreads_or(skipped(v));
       len = run_len;
       __syncthreads();
@@ -133,35 +136,43 @@ __global__ void __launch_bounds__(kThreads, 5)
     const bf16* src = x + ((int64_t)t * prm.Hkv + g) * D + j;
     const int64_t pitch = (int64_t)prm.Hkv * D;
     uint2 lo[kHold], hi[kHold];
-    int at[kHold];
-    uint32_t top = 0;
-    bool odd = false;  // something that is not finite
+    uint32_t big = 0;
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
       const int i = row0 + p * kRows;
       lo[p] = hi[p] = make_uint2(0, 0);
-      at[p] = 0;
       if (live(i)) {
-        if (rotate) at[p] = prm.position[t + i];
         lo[p] = *reinterpret_cast<const uint2*>(src + i * pitch);
         hi[p] = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
       }
-      top = max(top, max(max(finite_abs2(lo[p].x), finite_abs2(lo[p].y)),
-                         max(finite_abs2(hi[p].x), finite_abs2(hi[p].y))));
-      odd |= odd2(lo[p].x) | odd2(lo[p].y) | odd2(hi[p].x) | odd2(hi[p].y);
     }
-    for (int i = row0 + kHold * kRows; i < len; i += kRows) {
-      if (!live(i)) continue;
-      const uint2 a = *reinterpret_cast<const uint2*>(src + i * pitch);
-      const uint2 b = *reinterpret_cast<const uint2*>(src + i * pitch + D / 2);
-      top = max(top, max(max(finite_abs2(a.x), finite_abs2(a.y)), max(finite_abs2(b.x), finite_abs2(b.y))));
-      odd |= odd2(a.x) | odd2(a.y) | odd2(b.x) | odd2(b.y);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) red[warp] = top;
+#pragma unroll
+    for (int p = 0; p < kHold; ++p) big = top2(top2(big, lo[p]), hi[p]);
+    for (int i = row0 + kHold * kRows; i < len; i += kRows)
+      if (live(i)) {
+        big = top2(big, *reinterpret_cast<const uint2*>(src + i * pitch));
+        big = top2(big, *reinterpret_cast<const uint2*>(src + i * pitch + D / 2));
+      }
+    auto over_cta = [&](uint32_t pair) {  // the largest half of all threads' pairs
+      const uint32_t m = __reduce_max_sync(0xffffffffu, max(pair & 0xffffu, pair >> 16));
+      if (lane == 0) red[warp] = m;
+      __syncthreads();
+      return max(max(red[0], red[1]), max(red[2], red[3]));
+    };
     const float old = off > 0 ? prm.scale[plane] : 0.f;
-    odd = __syncthreads_or(odd);
-    top = max(max(red[0], red[1]), max(red[2], red[3]));
+    uint32_t top = over_cta(big);
+    const bool odd = top >= kInf;  // something is not finite: the largest of the rest
+    if (odd) {
+      uint32_t m = 0;
+      for (int i = row0; i < len; i += kRows)
+        if (live(i))
+          for (int e = 0; e < D; e += D / 2) {
+            const uint2 x2 = *reinterpret_cast<const uint2*>(src + i * pitch + e);
+            m = __vmaxu2(m, __vmaxu2(finite2(x2.x), finite2(x2.y)));
+          }
+      __syncthreads();
+      top = over_cta(m);
+    }
     // the smallest power of two >= top / limit (limit / 512 = 0.875 or 0.6171875)
     const uint32_t bits = top << 16;
     const int e2 = (int)(bits >> 23) - 126;  // top = m 2^e2, m in [0.5, 1)
@@ -189,42 +200,53 @@ __global__ void __launch_bounds__(kThreads, 5)
     }
     if (tid == 0 && (off == 0 || scale > old)) prm.scale[plane] = scale;
     const float inv = 1.f / scale;
-    auto put = [&](int i, int pos, uint2 a, uint2 b) {
-      float f[4], h[4];
-      const float2 a0 = bf16x2_to_float2(a.x), a1 = bf16x2_to_float2(a.y);
-      const float2 b0 = bf16x2_to_float2(b.x), b1 = bf16x2_to_float2(b.y);
-      // times 1 / scale first: a rotation of the largest bf16 values cannot overflow then
-      const float xs[4] = {a0.x * inv, a0.y * inv, a1.x * inv, a1.y * inv};
-      const float ys[4] = {b0.x * inv, b0.y * inv, b1.x * inv, b1.y * inv};
+    const uint64_t inv2 = f2_make(inv, inv);
+    auto put = [&](int i, uint2 a, uint2 b) {
+      // divided by the scale before (or, as a factor of sine and cosine, in) the
+      // rotation: the largest bf16 values cannot overflow
+      uint64_t f0 = bf16x2_to_f2(a.x), f1 = bf16x2_to_f2(a.y), h0 = bf16x2_to_f2(b.x), h1 = bf16x2_to_f2(b.y);
       if (rotate) {
+        const int pos = i < kThreads ? pos_of[i] : prm.position[t + i];
+        float sn[4], cs[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float sn, cs;
-          __sincosf(turn_angle(pos, turn[q]), &sn, &cs);
-          f[q] = xs[q] * cs - ys[q] * sn;
-          h[q] = ys[q] * cs + xs[q] * sn;
-        }
+        for (int q = 0; q < 4; ++q) __sincosf(turn_angle(pos, turn[q]), &sn[q], &cs[q]);
+        const uint64_t c0 = f2_mul(f2_make(cs[0], cs[1]), inv2), c1 = f2_mul(f2_make(cs[2], cs[3]), inv2);
+        const uint64_t s0 = f2_mul(f2_make(sn[0], sn[1]), inv2), s1 = f2_mul(f2_make(sn[2], sn[3]), inv2);
+        const uint64_t x0 = f0, x1 = f1;
+        f0 = f2_sub(f2_mul(x0, c0), f2_mul(h0, s0));
+        f1 = f2_sub(f2_mul(x1, c1), f2_mul(h1, s1));
+        h0 = f2_fma(h0, c0, f2_mul(x0, s0));
+        h1 = f2_fma(h1, c1, f2_mul(x1, s1));
       } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f[q] = xs[q];
-          h[q] = ys[q];
-        }
+        f0 = f2_mul(f0, inv2);
+        f1 = f2_mul(f1, inv2);
+        h0 = f2_mul(h0, inv2);
+        h1 = f2_mul(h1, inv2);
+      }
+      float f[4], h[4];
+      f2_split(f0, f[0], f[1]);
+      f2_split(f1, f[2], f[3]);
+      f2_split(h0, h[0], h[1]);
+      f2_split(h1, h[2], h[3]);
+      uint32_t wf = encode4(f), wh = encode4(h);
+      if (odd) {
+        wf = encode4_odd(f);
+        wh = encode4_odd(h);
       }
       uint8_t* row = dst + i * D;
-      *reinterpret_cast<uint32_t*>(row) = odd ? encode4_odd(f) : encode4(f);
-      *reinterpret_cast<uint32_t*>(row + D / 2) = odd ? encode4_odd(h) : encode4(h);
+      *reinterpret_cast<uint32_t*>(row) = wf;
+      *reinterpret_cast<uint32_t*>(row + D / 2) = wh;
     };
 #pragma unroll
     for (int p = 0; p < kHold; ++p) {
       const int i = row0 + p * kRows;
-      if (live(i)) put(i, at[p], lo[p], hi[p]);
+      if (live(i)) put(i, lo[p], hi[p]);
     }
     for (int i = row0 + kHold * kRows; i < len; i += kRows)
       if (live(i))
-        put(i, rotate ? prm.position[t + i] : 0, *reinterpret_cast<const uint2*>(src + i * pitch),
+        put(i, *reinterpret_cast<const uint2*>(src + i * pitch),
             *reinterpret_cast<const uint2*>(src + i * pitch + D / 2));
-    __syncthreads();  // `red` is free again
+    __syncthreads();  // the shared arrays are free again
   }
 }
 
