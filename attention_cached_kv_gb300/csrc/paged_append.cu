@@ -73,9 +73,14 @@ __global__ void __launch_bounds__(kThreads, 7)
   const bf16* x = prm.x[kv];
   const int t0 = first * prm.chunk, t1 = min(t0 + prm.chunk, prm.T);
   const bool rotate = kv == 0 && prm.position != nullptr;
-  uint64_t turn[4];  // (a constant read by 16 threads at 16 places is slow: once)
+  // read once into registers: a constant read by 16 threads at 16 places is slow (and
+  // read again and again, unless the compiler cannot know that it is one)
+  uint64_t turn[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) turn[q] = prm.turn[j + q];
+  for (int q = 0; q < 4; ++q) {
+    turn[q] = prm.turn[j + q];
+    asm volatile("" : "+l"(turn[q]));
+  }
 
   const unsigned rows_in_pool = (unsigned)prm.num_blocks * bl;
   auto skipped = [&](int s) { return (unsigned)s >= rows_in_pool; };  // negative or outside
