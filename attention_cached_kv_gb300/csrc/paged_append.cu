@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 7)
   uint64_t turn[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    turn[q] = prm.turn[j + q];
+    turn[q] = rotate ? prm.turn[j + q] : 0;
     asm volatile("" : "+l"(turn[q]));
   }
 

@@ -444,6 +444,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!mbar_wait(&ms.drain, 0)) failed = true;
   } else if (warp >= 6) {
     // ================================================== q rows
+    // D / 16 lanes a row, each with elements j .. j + 7 and their partners j + D/2 ..
+    constexpr int LR = D / 16, RP = 32 / LR;
+    const int l = lane % LR, rl = lane / LR;
+    uint64_t turn[8];  // into registers once: a constant read at LR places by a warp is slow
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      turn[e] = prm.turn[l * 8 + e];
+      asm volatile("" : "+l"(turn[e]));
+    }
     for (int seg = 0; wk.more() && !failed; wk.next(rq), ++seg) {
       int kt0, kt1;
       wk.get(kt0, kt1, rq);
@@ -454,9 +463,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         failed = true;
         break;
       }
-      // D / 16 lanes a row, each with elements j .. j + 7 and their partners j + D/2 ..
-      constexpr int LR = D / 16, RP = 32 / LR;
-      const int l = lane % LR, rl = lane / LR;
       const bf16* src = prm.q + ((int64_t)q0 * prm.Hq + wk.g * G) * D + l * 8;
       uint4 u, v;
       auto fetch = [&](int row) {
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float x = real ? __uint_as_float(e & 1 ? uw[e >> 1] & 0xffff0000u : uw[e >> 1] << 16) : 0.f;
           const float y = real ? __uint_as_float(e & 1 ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16) : 0.f;
           float sn, cs;
-          __sincosf(turn_angle(pos, prm.turn[l * 8 + e]), &sn, &cs);
+          __sincosf(turn_angle(pos, turn[e]), &sn, &cs);
           a[e] = x * cs - y * sn;
           b[e] = y * cs + x * sn;
           top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
