@@ -71,7 +71,7 @@ struct Cfg {
   static constexpr int KPR = 128 / D;           // keys a tile row
   static constexpr int KT = 128 * KPR;          // keys a tile
   static constexpr int ROWS = 8 * CH;           // query rows at most
-  static constexpr int NQ = CH <= 2 ? 2 : 1;    // q tiles
+  static constexpr int NPB = CH <= 2 ? 2 : 1;   // P buffers (q tiles: two, one made ahead)
   static constexpr int SP = (24 * CH + 15) & ~15;  // S columns a parity
   static constexpr int OC = (KPR * 24 * CH + 15) & ~15;  // O columns
   static constexpr int SB = 2 * KPR * SP + OC <= 256 ? 2 : 1;  // S buffers
@@ -79,8 +79,9 @@ struct Cfg {
   static constexpr int NK = D == 128 && CH <= 2 ? 3 : D == 64 && CH == 1 ? 3 : 2;
   static constexpr int NV = D == 128 && CH == 1 ? 3 : 2;
   static constexpr uint32_t kO = SB * KPR * SP;  // O's first TMEM column
-  static constexpr uint32_t offV = NK * kStage, offQ = offV + NV * kStage, offP = offQ + NQ * QB,
-                            offMisc = offP + 2 * PB + 1024;  // (an MMA's N may run 8 rows past a tile)
+  static constexpr uint32_t offV = NK * kStage, offQ = offV + NV * kStage, offP = offQ + 2 * QB,
+                            kP = NPB * PB + 1024,  // (an MMA's N may run 8 rows past a tile)
+                            offMisc = offP + (kP > ROWS * 512 ? kP : ROWS * 512);
   static_assert(kO + OC <= 256, "TMEM columns");
 };
 
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DecodeParams prm) {
   using C = Cfg<D, CH>;
   using M = Misc<D, CH>;
-  constexpr int KPR = C::KPR, KT = C::KT, ROWS = C::ROWS, NK = C::NK, NV = C::NV, NQ = C::NQ, SB = C::SB;
+  constexpr int KPR = C::KPR, KT = C::KT, ROWS = C::ROWS, NK = C::NK, NV = C::NV, NPB = C::NPB, SB = C::SB;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   M& ms = *reinterpret_cast<M*>(smem + C::offMisc);
@@ -378,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool pending = false, first = false;  // P V of tile i - 1 to issue; the first of its segment
     int nch = 1;
     auto issue_pv = [&]() {
-      const int t = i - 1, pb = t & 1, vs = t % NV;
-      if (__any_sync(0xffffffffu, !mbar_wait(&ms.pfull[pb], (uint32_t)(t >> 1) & 1u) ||
+      const int t = i - 1, pb = t % NPB, vs = t % NV;
+      if (__any_sync(0xffffffffu, !mbar_wait(&ms.pfull[pb], (uint32_t)(t / NPB) & 1u) ||
                                       !mbar_wait(&ms.vfull[vs], (uint32_t)(t / NV) & 1u))) {
         failed = true;
         return;
@@ -402,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       wk.get(kt0, kt1, rq);
       if (pending) issue_pv();
       pending = false;
-      const int qs = seg % NQ;
-      if (failed || __any_sync(0xffffffffu, !mbar_wait(&ms.qfull[qs], (uint32_t)(seg / NQ) & 1u))) {
+      const int qs = seg & 1;
+      if (failed || __any_sync(0xffffffffu, !mbar_wait(&ms.qfull[qs], (uint32_t)(seg >> 1) & 1u))) {
         failed = true;
         break;
       }
@@ -456,10 +457,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int seg = 0; wk.more() && !failed; wk.next(rq), ++seg) {
       int kt0, kt1;
       wk.get(kt0, kt1, rq);
-      const int qs = seg % NQ;
+      const int qs = seg & 1;
       const int q0 = rq.q_start[wk.r], n = rq.q_start[wk.r + 1] - q0, kv = rq.length(wk.r);
       const int rows = n * G, pos0 = max(kv, 0) - n;
-      if (__any_sync(0xffffffffu, seg >= NQ && !mbar_wait(&ms.qfree[qs], ((uint32_t)(seg / NQ) & 1u) ^ 1u))) {
+      if (__any_sync(0xffffffffu, seg >= 2 && !mbar_wait(&ms.qfree[qs], ((uint32_t)(seg >> 1) & 1u) ^ 1u))) {
         failed = true;
         break;
       }
@@ -534,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (; wk.more(); wk.next(rq), ++seg) {
       int kt0, kt1;
       wk.get(kt0, kt1, rq);
-      const int qs = seg % NQ;
-      wait(&ms.qfull[qs], (uint32_t)(seg / NQ) & 1u);
+      const int qs = seg & 1;
+      wait(&ms.qfull[qs], (uint32_t)(seg >> 1) & 1u);
       // a role that gave up ends this one's waits too: leave together
       if (named_bar_or(1, 128, failed)) {
         failed = true;
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) m[j] = kNone, l[j] = 0.f;
       for (int kt = kt0; kt < kt1; ++kt, ++i) {
-        const int sb = i % SB, vs = i % NV, pb = i & 1;
+        const int sb = i % SB, vs = i % NV, pb = i % NPB;
         const int key0 = kt * KT + t * KPR;  // this thread's first key
         const bool edge = kt * KT + KT > sg.pos0 + 1;  // some row does not see all of the tile
         float s[ROWS * KPR];
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float fv = vref / vnew;
           vref = vnew;
           vmul = kPUnit / vnew;
-          if (kt > kt0) wait(&ms.pfree[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u);
+          if (kt > kt0) wait(&ms.pfree[(i - 1) % NPB], (uint32_t)((i - 1) / NPB) & 1u);
           tc::fence_after_sync();
 #pragma unroll
           for (int c = 0; c < CH; ++c)
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           tc::wait_st();
         }
-        if (i >= 2) wait(&ms.pfree[pb], (uint32_t)((i >> 1) - 1) & 1u);
+        if (i >= NPB) wait(&ms.pfree[pb], (uint32_t)(i / NPB - 1) & 1u);
         const float vr = vsc * vmul;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -710,12 +711,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive(&ms.pfull[pb]);
       }
       // ---- the segment's O, m and sums
-      wait(&ms.pfree[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u);
+      wait(&ms.pfree[(i - 1) % NPB], (uint32_t)((i - 1) / NPB) & 1u);
       tc::fence_after_sync();
       // through shared memory (P's room), a warp a row then
       const float od = vref * (1.f / kPUnit);
       float* stage = reinterpret_cast<float*>(smem + C::offP);  // [ROWS][128]
-      static_assert(C::ROWS * 512 <= 2 * C::PB, "the stage fits P's buffers");
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         if (c < nch) {
