@@ -73,35 +73,35 @@ struct Requests {
 // Sums count(r) over the requests (the NT threads of a CTA, all of them), finds the
 // request that holds unit at(total) of the running sum and the units before it.
 // *start_r is -1 where there is no such unit.
-template <int NT, class Count, class At>
-__device__ __forceinline__ void scan_requests(int B, Count count, int* warp_sum, int* start_r, int* start_pre,
-                                              int* total, At at) {
+template <int NT, class Int, class Count, class At>
+__device__ __forceinline__ void scan_requests(int B, Count count, Int* warp_sum, int* start_r, Int* start_pre,
+                                              Int* total, At at) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (B + NT - 1) / NT;
   const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
-  int own = 0;
+  Int own = 0;
   for (int r = r0; r < r1; ++r) own += count(r);
-  int inc = own;
+  Int inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    const Int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) warp_sum[warp] = inc;
   if (tid == 0) *start_r = -1;
   __syncthreads();
-  int before = inc - own, all = 0;
+  Int before = inc - own, all = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    const int s = warp_sum[w];
+    const Int s = warp_sum[w];
     if (w < warp) before += s;
     all += s;
   }
   if (tid == 0) *total = all;
-  const int x = at(all);
+  const Int x = at(all);
   if (x >= before && x < before + own) {
     for (int r = r0; r < r1; ++r) {
-      const int n = count(r);
+      const Int n = count(r);
       if (x < before + n) {
         *start_r = r;
         *start_pre = before;

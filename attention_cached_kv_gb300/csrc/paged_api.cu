@@ -128,7 +128,7 @@ namespace {
 int check_attn(const gist_paged_dims* dims, PagedProblem* pb) {
   const int rc = check_dims(dims, pb);
   if (rc != GIST_ATTN_OK) return rc;
-  if (pb->block_len % 16 != 0 || pb->G > 128 || pb->Hkv > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (pb->block_len % 16 != 0 || pb->G > 128 || (int64_t)pb->W * pb->block_len > 1 << 30) return GIST_ATTN_ERR_UNSUPPORTED;
   // key tiles over all requests and heads are counted in 32 bits
   const double tiles = (double)pb->B * pb->Hkv * ((double)pb->W * pb->block_len / 128 + 1);
   if (tiles > 2147483647.0) return GIST_ATTN_ERR_UNSUPPORTED;

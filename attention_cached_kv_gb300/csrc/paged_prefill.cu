@@ -5,21 +5,25 @@
 // floor(128 / G) tokens x G heads.  Its keys stream by in tiles of 128, one pass,
 //     S = q K^T, P = exp2(S - m), O += P V       (tcgen05 kind::f16, TMEM)
 // with m the row's running maximum, moved only when a tile's maximum passes it by
-// more than 8 (log2 units).  Twelve warps with registers to spare:
+// more than 8 (log2 units).  The warps:
 //   * 0-3, 4-7: a thread a row of each row tile, softmax and output; P goes back
 //     into S's columns as f16 (11 bits), A operand of the second product;
 //   * 8-11: cached rows from global memory through registers into f16 tiles.  E4M3
 //     to f16 is exact; values are also divided by the largest V scale of the
 //     request (exact for powers of two), K's block scales multiply the fp32 scores;
 //   * 12: the MMAs, alternating between the row tiles, so that one's products run
-//     while the other's softmax does.
+//     while the other's softmax does;
+//   * 13: block ids and scales, four tiles at a time, ahead of the copies.
 // One conversion of a key serves 256 rows, against 256 exponentials for it: that is
 // why rows are taken in pairs of tiles here and cached bytes are used as they are
 // where there are few rows (paged_decode.cu).  q is scaled by a power of two a row
 // before its one rounding to f16.
 //
-// Few CTAs (a short chunk behind a long context): the keys are split in `splits`
-// equal runs, whose parts join_kernel adds up in order.
+// Work is the sequence of (request, KV head, row-tile pair) units, each worth the keys
+// it sees and a constant for its start; each SM's CTA takes an equal run of it, cut
+// inside a unit between key tiles.  Units that cross CTAs leave parts (O, m, sum) in
+// the workspace and join_kernel adds them up in key order: chunks of unlike lengths,
+// or one short chunk behind a long context, spread evenly.
 // Bound: exponentials and tensor work, about equally.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
@@ -35,20 +39,32 @@
 namespace gattn {
 namespace {
 
-constexpr int kThreads = 416;         // 8 softmax + 4 converting + 1 MMA warp
+constexpr int kThreads = 448;         // 8 softmax, 4 converting, 1 MMA, 1 look-up warp
+constexpr int kRing = 8;              // tiles whose look-ups are held, in two halves
 constexpr int kKT = 128;              // keys a tile
 constexpr float kNone = -3.0e38f;     // running maximum before any key
 constexpr float kSlack = 8.f;         // log2 units a score may pass it by
+
+constexpr int kStartCost = 256;       // keys that a unit's start is worth
+
+// What the join needs of a unit that crosses CTAs, left by the CTA whose run starts in
+// it first (cost 0: nothing to join there).
+struct JoinRun {
+  int64_t at, total;  // the unit's first place in the sequence of costs, the sequence's end
+  int cost, tiles, q0, toks, pos0, g;
+  int pad[2];
+};
 
 struct PrefillParams {
   const bf16* q;
   bf16* out;
   const uint8_t* pool;
   const float* scale;
+  JoinRun* join;  // workspace: [CTAs], then the parts, two a CTA
   float* parts;
   int32_t* status;
   Requests rq;
-  int Hq, L, layer, num_blocks, min_new, Tm, splits;
+  int Hq, L, layer, num_blocks, min_new, Tm;
   float scale_log2;
   uint64_t turn[64];
 };
@@ -63,18 +79,18 @@ struct PCfg {
 
 template <int D>
 struct PMisc {
-  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], qready, drain;
+  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
   uint32_t tmem;
-  int bad, any_nan;
-  int warp_sum[kThreads / 32 + 1];
-  int start_r, start_pre, total;
-  // by tile (modulo 4) and 16-key group: K and V scale, first byte of the K rows in
+  int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
+  int64_t warp_sum[kThreads / 32], start_pre, total;
+  int start_r;
+  // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
   // the pool (-1: no key that is seen, or a block outside the pool)
-  alignas(16) float ksc[4][8], vsc[4][8];
-  int64_t at[4][8];
-  int even[4];  // the groups' K scales are equal in pairs
-  float vref, vpart[4];
-  int nankey[D];  // first key past the first row's whose V is NaN, by element
+  alignas(16) float ksc[kRing][8], vsc[kRing][8];
+  int64_t at[kRing][8];
+  int even[kRing];  // the groups' K scales are equal in pairs
+  float vref[4], vpart[4];
+  int nankey[4][D];  // first key past the first row's whose V is NaN, by element
 };
 
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -91,6 +107,7 @@ __device__ __forceinline__ float ld32_max(uint32_t taddr) {
       "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
       : "r"(taddr));
+  (void)r;
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m)::"memory");
   return m;
 }
@@ -118,6 +135,101 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return d;
 }
 
+// 16 bytes from global memory where `ok`, else zeros (no branch: the loads of a pass
+// go out together).
+__device__ __forceinline__ uint4 ldg16_if(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)ok));
+  return v;
+}
+
+// One unit's share of a CTA.
+struct PSeg {
+  int r, g, q0, toks, pos0, kend, kv, kt0, nt, slot;
+  bool two, whole;
+};
+
+// The walk over a CTA's segments; every role makes it for itself.  In a request
+// whose rows end at key `base` + n, pair p of row tiles (w tokens) costs
+// kStartCost + base + w (p + 1).
+struct PWalk {
+  int64_t x, x_end, pre;
+  int r, g, p;
+  int n, kv, base, np, w;
+  __device__ int64_t before(int q) const { return (int64_t)q * (kStartCost + base) + (int64_t)w * q * (q + 1) / 2; }
+  __device__ int64_t unit() const { return pre + g * before(np) + before(p); }
+  __device__ int cost() const { return kStartCost + base + w * (p + 1); }
+  __device__ void request(const PrefillParams& prm) {
+    const Requests& rq = prm.rq;
+    n = r < rq.B ? rq.tokens(r) : 0;
+    if (n < prm.min_new) n = 0;
+    kv = n > 0 ? rq.length(r) : 0;
+    base = max(max(kv, 0) - n, 0);
+    np = (n + w - 1) / w;
+  }
+  __device__ void init(const PrefillParams& prm, int64_t x0, int64_t x1, int r0, int64_t pre0) {
+    x = x0;
+    x_end = x1;
+    r = r0;
+    pre = pre0;
+    w = 2 * prm.Tm;
+    request(prm);
+    int64_t rem = x - pre;
+    const int64_t head = before(np);
+    g = (int)(rem / head);
+    rem -= g * head;
+    // before(p) <= rem < before(p + 1): a root in fp32, then the step or two it is off
+    const float b = (float)(kStartCost + base) + 0.5f * w;
+    p = max(0, min(np - 1, (int)((sqrtf(b * b + 2.f * w * (float)rem) - b) / w)));
+    while (p > 0 && before(p) > rem) --p;
+    while (p + 1 < np && before(p + 1) <= rem) ++p;
+  }
+  __device__ bool more() const { return x < x_end; }
+  // The segment at x; false where the run holds none of the unit's key tiles.
+  __device__ bool get(const PrefillParams& prm, PSeg& s) const {
+    const int64_t u = unit();
+    const int c = cost(), tok0 = p * w;
+    s.r = r;
+    s.g = g;
+    s.kv = kv;
+    s.toks = min(w, n - tok0);
+    s.q0 = prm.rq.q_start[r] + tok0;         // first token row
+    s.pos0 = max(kv, 0) - n + tok0;          // position of the first token
+    s.kend = max(0, s.pos0 + s.toks);        // keys that the last token sees
+    s.two = s.toks > prm.Tm;
+    const int all = (s.kend + kKT - 1) / kKT;
+    const int64_t o0 = x - u, o1 = x_end - u;
+    s.kt0 = (int)(all * o0 / c);
+    s.nt = (o1 >= c ? all : (int)(all * o1 / c)) - s.kt0;
+    s.whole = s.nt == all && o0 == 0;
+    if (s.kt0 == 0 && s.nt == all && all > 0) s.whole = true;  // (the cut fell before the first tile)
+    s.slot = o0 > 0 ? 0 : 1;
+    return s.nt > 0 || (all == 0 && o0 == 0);
+  }
+  __device__ void next(const PrefillParams& prm) {
+    x = min(unit() + cost(), x_end);
+    if (x >= x_end || ++p < np) return;
+    p = 0;
+    if (++g < prm.rq.Hkv) return;
+    g = 0;
+    pre += prm.rq.Hkv * before(np);
+    do {
+      ++r;
+      request(prm);
+    } while (n == 0 && r < prm.rq.B);
+    if (n == 0) x = x_end;  // (lengths that changed under the kernel)
+  }
+};
+
+__device__ __forceinline__ int64_t cut(int64_t total, int w, int W) {
+  return total / W * w + min((int64_t)w, total % W);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams prm) {
   using C = PCfg<D>;
@@ -127,30 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   M& ms = *reinterpret_cast<M*>(smem + C::offMisc);
   const Requests& rq = prm.rq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = rq.G, Tm = prm.Tm;
+  const int G = rq.G, Tm = prm.Tm, W = gridDim.x, me = blockIdx.x;
 
-  // ---- this CTA's request, KV head, row tiles and keys; the longest runs first
-  const int g = blockIdx.y, z = blockIdx.z;
-  scan_requests<kThreads>(
-      rq.B,
-      [&](int r) {
-        const int n = rq.tokens(r);
-        return n >= prm.min_new ? (n + 2 * Tm - 1) / (2 * Tm) : 0;
-      },
-      ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
-      [&](int all) { return min(all, (int)gridDim.x) - 1 - (int)blockIdx.x; });
-  const int item = min(ms.total, (int)gridDim.x) - 1 - (int)blockIdx.x, r = ms.start_r;
-  if (item < 0 || r < 0) return;
-  const int n = rq.q_start[r + 1] - rq.q_start[r], kv = rq.length(r);
-  const int tok0 = (item - ms.start_pre) * 2 * Tm, toks = min(2 * Tm, n - tok0);
-  const int q0 = rq.q_start[r] + tok0;             // the CTA's first token row
-  const int pos0 = max(kv, 0) - n + tok0;          // position of the first token
-  const int kend = max(0, pos0 + toks);            // keys that the last token sees
-  const int all_tiles = (kend + kKT - 1) / kKT;
-  const int kt0 = (int)((int64_t)all_tiles * z / prm.splits);
-  const int nt = (int)((int64_t)all_tiles * (z + 1) / prm.splits) - kt0;
-  const bool two = toks > Tm;
-
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 12) {
     tc::tmem_alloc(smem_u32(&ms.tmem), 512);
     tc::tmem_relinquish();
@@ -163,19 +254,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&ms.vfree[s], 1);
       mbar_init(&ms.sfull[s], 1);
       mbar_init(&ms.pfull[s], 128);
+      mbar_init(&ms.gready[s], 1);
+      mbar_init(&ms.gfree[s], 1);
     }
     mbar_init(&ms.qready, 256);
     mbar_init(&ms.drain, 1);
     fence_mbar_init();
-    ms.bad = kv < 0;
-    ms.any_nan = 0;
-    if (kv < 0) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+    for (int s = 0; s < 4; ++s) ms.bad[s] = ms.any_nan[s] = 0;
   }
-  for (int i = tid; i < D; i += kThreads) ms.nankey[i] = INT32_MAX;
+  for (int i = tid; i < 4 * D; i += kThreads) ms.nankey[i / D][i % D] = INT32_MAX;
   tc::fence_before_sync();
-  __syncthreads();
+  // ---- this CTA's run of the sequence (the scan's barriers publish the above too)
+  bool odd = false;
+  scan_requests<kThreads>(
+      rq.B,
+      [&](int r) {
+        PWalk k;
+        const int n = rq.tokens(r, &odd);
+        if (n < prm.min_new) return (int64_t)0;
+        const int kv = rq.length(r);
+        odd |= kv < 0;
+        k.base = max(max(kv, 0) - n, 0);
+        k.w = 2 * Tm;
+        return rq.Hkv * k.before((n + k.w - 1) / k.w);
+      },
+      ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total, [&](int64_t all) { return cut(all, me, W); });
+  if (me == 0 && odd) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
   tc::fence_after_sync();
   const uint32_t tmem = ms.tmem;
+  const int64_t total = ms.total, x0 = cut(total, me, W), x1 = cut(total, me + 1, W);
+  if (x0 >= x1 || ms.start_r < 0) {
+    if (tid == 0) prm.join[me].cost = 0;
+    if (warp == 12) tc::tmem_dealloc(tmem, 512);
+    return;
+  }
+  PWalk wk;
+  wk.init(prm, x0, x1, ms.start_r, ms.start_pre);
+  if (tid == 0) {
+    JoinRun j{};
+    if (x0 > wk.unit() && cut(total, me - 1, W) <= wk.unit()) {
+      PSeg s;
+      wk.get(prm, s);
+      j = JoinRun{wk.unit(), total, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {0, 0}};
+    }
+    prm.join[me] = j;
+  }
   bool failed = false;
 
   if (warp == 12) {
@@ -197,13 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int x, int i) {
+    auto issue_pv = [&](int x, int i, bool first) {
       if (lane == 0) {
         const uint32_t vb = sbase + C::offV + (i & 1) * C::kTile;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc::mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
-                     tc::smem_desc_sw128(vb + k * 2048, C::kPanel, 1024), tc::idesc_f16_f32(128, D, 1), i > 0 || k > 0);
+                     tc::smem_desc_sw128(vb + k * 2048, C::kPanel, 1024), tc::idesc_f16_f32(128, D, 1), !first || k > 0);
       }
       __syncwarp();
     };
@@ -211,16 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (lane == 0) tc::commit(smem_u32(bar));
       __syncwarp();
     };
-    if (nt > 0 && wait(&ms.qready, 0) && wait(&ms.kready[0], 0)) {
-      issue_s(0, 0);
-      if (two) issue_s(1, 0);
-      arrive(&ms.kfree[0]);
-      for (int i = 0; i < nt; ++i) {
-        const uint32_t ph = (uint32_t)i & 1u;
-        const bool more = i + 1 < nt;
-        if (!wait(&ms.vready[i & 1], (uint32_t)(i >> 1) & 1u) || !wait(&ms.pfull[0], ph)) break;
-        issue_pv(0, i);
-        if (!two) arrive(&ms.vfree[i & 1]);
+    int i0 = 0, seg = 0;       // tiles and segments so far
+    uint32_t np0 = 0, np1 = 0;  // P tiles so far of each row tile
+    for (; wk.more() && !failed; wk.next(prm)) {
+      PSeg sg;
+      if (!wk.get(prm, sg)) continue;
+      if (!wait(&ms.qready, (uint32_t)seg++ & 1u)) break;
+      if (sg.nt == 0 || !wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
+      const bool two = sg.two;
+      issue_s(0, i0);
+      if (two) issue_s(1, i0);
+      arrive(&ms.kfree[i0 & 1]);
+      for (int e = 0; e < sg.nt; ++e) {
+        const int i = i0 + e;
+        const bool more = e + 1 < sg.nt;
+        auto free_v = [&]() {
+          arrive(&ms.vfree[i & 1]);
+          if ((i & 3) == 3) arrive(&ms.gfree[(i >> 2) & 1]);  // (the tile's softmax is done too)
+        };
+        if (!wait(&ms.vready[i & 1], (uint32_t)(i >> 1) & 1u) || !wait(&ms.pfull[0], np0++ & 1u)) break;
+        issue_pv(0, i, e == 0);
+        if (!two) free_v();
         if (more) {
           if (!wait(&ms.kready[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
           issue_s(0, i + 1);
@@ -229,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           arrive(&ms.sfull[0]);  // the last P V is done
         }
         if (two) {
-          if (!wait(&ms.pfull[1], ph)) break;
-          issue_pv(1, i);
-          arrive(&ms.vfree[i & 1]);
+          if (!wait(&ms.pfull[1], np1++ & 1u)) break;
+          issue_pv(1, i, e == 0);
+          free_v();
           if (more) {
             issue_s(1, i + 1);
             arrive(&ms.kfree[(i + 1) & 1]);
@@ -240,85 +374,104 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
       }
+      i0 += sg.nt;
     }
     if (lane == 0) tc::commit(smem_u32(&ms.drain));
     __syncwarp();
     if (!mbar_wait(&ms.drain, 0)) failed = true;
+  } else if (warp == 13) {
+    // ================================================== look-ups, a lane a 16-key group
+    // lane group t walks to tiles t, t + 4, ... of the CTA's sequence by itself
+    const int t = lane >> 3, gr = lane & 7;
+    PSeg sg;
+    int e = t;  // the tile within the segment
+    bool have = false, want = false;
+    auto settle = [&]() {  // to the segment that tile e of this or a later one lies in
+      while (wk.more()) {
+        if (have && e < sg.nt) return;
+        if (have) {
+          e -= sg.nt;
+          wk.next(prm);
+        }
+        have = false;
+        while (wk.more() && !(have = wk.get(prm, sg))) wk.next(prm);
+      }
+      have = false;
+    };
+    int blk = -1, key = 0, at_g = 0, at_kend = 0;
+    auto look_up = [&]() {
+      settle();
+      want = false;
+      blk = -1;
+      if (have) {
+        key = (sg.kt0 + e) * kKT + gr * 16;
+        at_g = sg.g;
+        at_kend = sg.kend;
+        want = key < sg.kend;
+        if (want) blk = rq.block_table[(int64_t)sg.r * rq.W + key / rq.block_len];
+        e += 4;
+      }
+    };
+    look_up();
+    for (int i = 0; __any_sync(0xffffffffu, have); i += 4) {
+      const int half = (i >> 2) & 1;
+      const bool ok = want && blk >= 0 && blk < prm.num_blocks, lost = want && !ok;
+      if (lost) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+      const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + at_g;
+      const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : -1;
+      const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : lost ? -1.f : 0.f;
+      look_up();  // its load runs while this half is waited for
+      if (__any_sync(0xffffffffu, i >= kRing && !mbar_wait(&ms.gfree[half], ((uint32_t)(i >> 3) & 1u) ^ 1u))) {
+        failed = true;
+        break;
+      }
+      const int slot = (i + t) & (kRing - 1);
+      ms.ksc[slot][gr] = ks;
+      ms.vsc[slot][gr] = vs;  // (-1: the block id is outside the pool)
+      ms.at[slot][gr] = at;
+      const uint32_t same = __ballot_sync(0xffffffffu, __shfl_xor_sync(0xffffffffu, ks, 1) == ks);
+      if (gr == 0) ms.even[slot] = ((same >> (8 * t)) & 0xffu) == 0xffu;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.gready[half]);
+    }
   } else if (warp >= 8) {
     // ================================================== cached rows into f16 tiles
     constexpr int kLanes = D / 16;             // threads of a row (16 bytes each)
     constexpr int kRows = 128 / kLanes;        // rows of a pass
     constexpr int kPass = 128 / kRows;
     const int ct = tid - 256, c = ct % kLanes, row0 = ct / kLanes;
-    const int32_t* table = rq.block_table + (int64_t)r * rq.W;
     const int64_t vstep = (int64_t)rq.Hkv * rq.block_len * D;
-    // the largest V scale among the blocks that the rows see
-    float top = 0.f;
-    const int blocks = kv < 0 ? 0 : (kend + rq.block_len - 1) / rq.block_len;
-    for (int b = ct; b < blocks; b += 128) {
-      const int blk = table[b];
-      if (blk >= 0 && blk < prm.num_blocks)
-        top = fmaxf(top, prm.scale[(((int64_t)blk * prm.L + prm.layer) * 2 + 1) * rq.Hkv + g]);
-    }
+    // The largest V scale of the request's blocks.
+    auto largest = [&](const PSeg& sg) {
+      const int32_t* table = rq.block_table + (int64_t)sg.r * rq.W;
+      float top = 0.f;
+      const int blocks = (max(sg.kv, 0) + rq.block_len - 1) / rq.block_len;
+#pragma unroll 4
+      for (int b = ct; b < blocks; b += 128) {
+        const int blk = table[b];
+        const bool ok = blk >= 0 && blk < prm.num_blocks;
+        const float s = prm.scale[(((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 + 1) * rq.Hkv + sg.g];
+        top = fmaxf(top, ok ? s : 0.f);
+      }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) ms.vpart[warp - 8] = top;
-    named_bar_sync(2, 128);
-    const float vref = fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
-    if (ct == 0) ms.vref = vref;  // (read by the softmax after vready -> pfull -> sfull)
-    const float rvref = 1.f / vref;
-    // Threads 0 .. 7 look up the groups of the tiles ahead: an id four tiles ahead of
-    // its use, the scales three, in shared memory two.
-    float gk = 0.f, gv = 0.f;
-    int64_t ga = -1;
-    int gid = -1;
-    bool want = false;  // there are such keys
-    auto look_up = [&](int i) {
-      const int key = (kt0 + i) * kKT + ct * 16;
-      want = i < nt && key < kend && kv >= 0;
-      gid = want ? table[key / rq.block_len] : -1;
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      named_bar_sync(2, 128);
+      if (lane == 0) ms.vpart[warp - 8] = top;
+      named_bar_sync(2, 128);
+      return fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
     };
-    auto scales_of = [&](int kt) {
-      gk = gv = 0.f;
-      ga = -1;
-      if (want && gid >= 0 && gid < prm.num_blocks) {
-        const int64_t plane = ((int64_t)gid * prm.L + prm.layer) * 2 * rq.Hkv + g;
-        ga = (plane * rq.block_len + (kt * kKT + ct * 16) % rq.block_len) * D;
-        gk = prm.scale[plane];
-        gv = prm.scale[plane + rq.Hkv];
-      } else if (want) {
-        ms.bad = 1;
-        report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-      }
-    };
-    auto publish = [&](int i) {
-      ms.ksc[i & 3][ct] = gk;
-      ms.vsc[i & 3][ct] = gv;
-      ms.at[i & 3][ct] = ga;
-      const bool same = __shfl_xor_sync(0xffu, gk, 1) == gk;
-      const bool all = __all_sync(0xffu, same);
-      if (ct == 0) ms.even[i & 3] = all;
-    };
-    if (ct < 8) {
-      for (int i = 0; i < 2; ++i) {
-        look_up(i);
-        scales_of(kt0 + i);
-        publish(i);
-      }
-      look_up(2);
-      scales_of(kt0 + 2);
-      look_up(3);
-    }
-    named_bar_sync(2, 128);
     uint4 kx[kPass], vx[kPass];
-    auto fetch = [&](int i, uint4 (&x)[kPass], int64_t more) {
+    auto fetch = [&](int i, int left, uint4 (&x)[kPass], int64_t more) {  // `left`: rows of the tile that are seen
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int row = p * kRows + row0;
-        const int64_t at = ms.at[i & 3][row >> 4];
-        x[p] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && (kt0 + i) * kKT + row < kend) x[p] = ldg16(prm.pool + at + (row & 15) * D + c * 16 + more);
+        const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
+        x[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + more, at >= 0 && row < left);
       }
+    };
+    auto looked_up = [&](int i) {
+      if ((i & 3) == 0 && !mbar_wait(&ms.gready[(i >> 2) & 1], (uint32_t)(i >> 3) & 1u)) failed = true;
+      return !failed;
     };
     // 16 codes as two 16-byte chunks of f16 of tile row `row`; the second half of a
     // row's threads stores its chunks in the other order (bank conflicts)
@@ -340,9 +493,43 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sts16(base + swz128(row, ch + odd), odd ? hi : lo);
       sts16(base + swz128(row, ch + 1 - odd), odd ? lo : hi);
     };
-    if (nt > 0) fetch(0, kx, 0), fetch(0, vx, vstep);
-    for (int i = 0; i < nt && !failed; ++i) {
-      const int kt = kt0 + i, b = i & 1;
+    PSeg sg, ahead;  // this segment, the next one
+    auto find = [&](PSeg& s) {
+      while (wk.more())
+        if (wk.get(prm, s)) return true;
+        else wk.next(prm);
+      return false;
+    };
+    bool have = find(sg), have2 = false;
+    int seg = 0, i = 0, last_r = -1, last_g = -1;
+    float vref = 0.f, rvref = 0.f;
+    if (have && sg.nt > 0 && looked_up(0)) {
+      fetch(0, sg.kend - sg.kt0 * kKT, kx, 0);
+      fetch(0, sg.kend - sg.kt0 * kKT, vx, vstep);
+    }
+    for (; have && !failed; seg += sg.nt > 0, sg = ahead, have = have2) {
+      wk.next(prm);
+      have2 = find(ahead);
+      if (sg.nt == 0) {  // nothing to convert; the next segment's first tile
+        if (have2 && ahead.nt > 0 && looked_up(i)) {
+          fetch(i, ahead.kend - ahead.kt0 * kKT, kx, 0);
+          fetch(i, ahead.kend - ahead.kt0 * kKT, vx, vstep);
+        }
+        continue;
+      }
+      if (sg.r != last_r || sg.g != last_g) {
+        vref = largest(sg);
+        rvref = 1.f / vref;
+        last_r = sg.r;
+        last_g = sg.g;
+      }
+      const int sl = seg & 3;
+      if (ct == 0) ms.vref[sl] = vref;
+    for (int e = 0; e < sg.nt && !failed; ++e, ++i) {
+      const int kt = sg.kt0 + e, b = i & 1;
+      // the tile after this one, in this segment or the next
+      const bool more = e + 1 < sg.nt || (have2 && ahead.nt > 0);
+      const int left1 = e + 1 < sg.nt ? sg.kend - (kt + 1) * kKT : ahead.kend - ahead.kt0 * kKT;
       if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
@@ -351,26 +538,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int p = 0; p < kPass; ++p) put(sbase + C::offK + b * C::kTile, p * kRows + row0, kx[p], 0, false);
       fence_proxy_async_smem();
       mbar_arrive(&ms.kready[b]);
-      if (i + 1 < nt) fetch(i + 1, kx, 0);
+      if (more && looked_up(i + 1)) fetch(i + 1, left1, kx, 0);
       if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
       }
-      if (kt * kKT + kKT > pos0 + 1) {
+      if (kt * kKT + kKT > sg.pos0 + 1) {
         // keys that not every row sees: a NaN would reach the others (0 x NaN), so it
         // is noted for the rows that see it and cleared
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
           const int key = kt * kKT + p * kRows + row0;
           const uint32_t any = e4m3_nan(vx[p].x) | e4m3_nan(vx[p].y) | e4m3_nan(vx[p].z) | e4m3_nan(vx[p].w);
-          if (key > pos0 && any) {
+          if (key > sg.pos0 && any) {
             uint32_t w[4] = {vx[p].x, vx[p].y, vx[p].z, vx[p].w};
-            ms.any_nan = 1;
+            ms.any_nan[sl] = 1;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (((w[e >> 2] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {
                 w[e >> 2] &= ~(0xffu << (8 * (e & 3)));
-                atomicMin(&ms.nankey[c * 16 + e], key);
+                atomicMin(&ms.nankey[sl][c * 16 + e], key);
               }
             vx[p] = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -378,18 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
-        const float f = ms.vsc[i & 3][(p * kRows + row0) >> 4] * rvref;
+        const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
+        if (vs < 0.f) ms.bad[sl] = 1;
         put(sbase + C::offV + b * C::kTile, p * kRows + row0, vx[p], to_f16x2(f, f), true);
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.vready[b]);
-      if (i + 1 < nt) fetch(i + 1, vx, vstep);
-      if (ct < 8) {
-        publish(i + 2);
-        scales_of(kt + 3);
-        look_up(i + 4);
-      }
-      named_bar_sync(2, 128);
+      if (more && !failed) fetch(i + 1, left1, vx, vstep);
+    }
     }
   } else {
     // ================================================== q rows, softmax, output
@@ -397,65 +580,88 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::kS + x * 128, to = tmem + lane_base + C::kO + x * D;
     const int tok = x * Tm + row / G, head = row % G;
-    const bool valid = row < Tm * G && tok < toks;
-    const int lim = valid ? pos0 + tok + 1 : 0;         // keys the row sees
-    const int lim_all = pos0 + x * Tm + 1;              // keys every row of the tile sees
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!failed && !mbar_wait(bar, parity)) failed = true;
     };
+    int seg = 0, i0 = 0;
+    uint32_t ns = 0;  // S tiles (and last P V's) so far of this row tile
+    for (; wk.more(); wk.next(prm)) {
+    PSeg sg;
+    if (!wk.get(prm, sg)) continue;
+    // (both row tiles together, so that nothing of a segment before is still read; the
+    // slots of `seg` count the segments with key tiles)
+    named_bar_sync(3, 256);
+    const int sl = seg & 3, toks = sg.toks, pos0 = sg.pos0, nt = sg.nt;
+    const bool valid = row < Tm * G && tok < toks;
+    const int lim = valid ? pos0 + tok + 1 : 0;         // keys the row sees
+    const int lim_all = pos0 + x * Tm + 1;              // keys every row of the tile sees
+    const int64_t at = ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
+    if (nt > 0) {  // the next but one's
+      if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
+      if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
+    }
     float rs;  // softmax scale (log2) x the row's power of two
     {
-      const bf16* src = prm.q + ((int64_t)(q0 + tok) * prm.Hq + g * G + head) * D;
-      uint4 v[D / 8];
+      // the row into its place, rounded to f16 there after the rotation
+      const uint32_t tile = sbase + x * C::kTile;
+      auto place = [&](int ch) { return tile + (ch >> 3) * C::kPanel + swz128(row, ch & 7); };
+      const bf16* src = prm.q + at;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) v[j] = valid ? ldg16(src + j * 8) : make_uint4(0, 0, 0, 0);
-      uint32_t* w = reinterpret_cast<uint32_t*>(v);
-      float top = 0.f;
-      // two passes over the pairs (j, j + D/2): the largest magnitude bounds the
-      // rotated ones by sqrt 2, which the power of two leaves room for
-#pragma unroll
-      for (int j = 0; j < D / 2; ++j) {
-        const float2 f = bf16x2_to_float2(w[j]);
-        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-        if (!(fabsf(f.x) <= 3.4e38f) || !(fabsf(f.y) <= 3.4e38f)) top = INFINITY;
+      for (int ch = 0; ch < D / 8; ++ch) {
+        if (valid) cp_async16(place(ch), src + ch * 8);
+        else sts16(place(ch), make_uint4(0, 0, 0, 0));
       }
-      const uint32_t tb = __float_as_uint(top);
+      cp_async_wait_all();
+      // the largest magnitude bounds the rotated ones by sqrt 2, which the power of two
+      // leaves room for
+      uint32_t big = 0;
+#pragma unroll 4
+      for (int ch = 0; ch < D / 8; ++ch) {
+        const uint4 v = lds16(place(ch));
+        big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+      }
+      const uint32_t tb = max(big & 0xffffu, big >> 16) << 16;
       const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
       const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
       rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
-      const int pos = pos0 + tok;
-      const uint32_t tile = sbase + x * C::kTile;
-#pragma unroll
+      const int pos = max(pos0 + tok, 0);
+      const uint64_t down2 = f2_make(down, down);
+#pragma unroll 1
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
+        const uint32_t pa = place(ch), pb = place(ch + D / 16);
+        const uint4 va = lds16(pa), vb = lds16(pb);
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
         uint32_t a[4], b[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 u = bf16x2_to_float2(w[ch * 4 + e]), y = bf16x2_to_float2(w[D / 4 + ch * 4 + e]);
           float s0, c0, s1, c1;
           __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e]), &s0, &c0);
           __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e + 1]), &s1, &c1);
-          const float u0 = u.x * down, u1 = u.y * down, y0 = y.x * down, y1 = y.y * down;
-          a[e] = to_f16x2(u0 * c0 - y0 * s0, u1 * c1 - y1 * s1);
-          b[e] = to_f16x2(y0 * c0 + u0 * s0, y1 * c1 + u1 * s1);
+          const uint64_t u = f2_mul(bf16x2_to_f2(wa[e]), down2), y = f2_mul(bf16x2_to_f2(wb[e]), down2);
+          const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
+          float r0, r1;
+          f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
+          a[e] = to_f16x2(r0, r1);
+          f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
+          b[e] = to_f16x2(r0, r1);
         }
-        const int c2 = ch + D / 16;  // 16-byte chunk of the second half
-        sts16(tile + (ch / 8) * C::kPanel + swz128(row, ch % 8), make_uint4(a[0], a[1], a[2], a[3]));
-        sts16(tile + (c2 / 8) * C::kPanel + swz128(row, c2 % 8), make_uint4(b[0], b[1], b[2], b[3]));
+        sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
+        sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.qready);
     }
     float m = kNone;
     uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
-    const bool live = x == 0 || two;
-    for (int i = 0; live && i < nt; ++i) {
-      const int key0 = (kt0 + i) * kKT;
+    const bool live = x == 0 || sg.two;
+    for (int e = 0; live && e < nt; ++e) {
+      const int i = i0 + e, key0 = (sg.kt0 + e) * kKT;
       const bool edge = key0 + kKT > lim_all;
-      wait(&ms.sfull[x], (uint32_t)i & 1u);
+      wait(&ms.sfull[x], ns++ & 1u);
       tc::fence_after_sync();
-      const float* ksc = ms.ksc[i & 3];
+      const float* ksc = ms.ksc[i & (kRing - 1)];
       float mx = kNone;
-      if (!edge && ms.even[i & 3]) {
+      if (!edge && ms.even[i & (kRing - 1)]) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) mx = fmaxf(mx, ld32_max(ts + c * 32) * (ksc[2 * c] * rs));
       } else {
@@ -483,14 +689,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const uint64_t f2 = f2_make(fm, fm);
         acc = f2_mul(acc, f2);
         acc2 = f2_mul(acc2, f2);
-        if (i > 0) {
+        if (e > 0) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint32_t ov[16];
             tc::ld16(to + c * 16, ov);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * fm);
+            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * fm);
             st16(to + c * 16, ov);
           }
         }
@@ -544,42 +750,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_arrive(&ms.pfull[x]);
     }
     if (live) {
-      if (nt > 0) wait(&ms.sfull[x], (uint32_t)nt & 1u);
+      if (nt > 0) wait(&ms.sfull[x], ns++ & 1u);
       tc::fence_after_sync();
       float a0, a1, b0, b1;
       f2_split(acc, a0, a1);
       f2_split(acc2, b0, b1);
       const float sum = (a0 + a1) + (b0 + b1);
-      const bool none = lim <= 0 || ms.bad, whole = prm.splits == 1, nan = nt > 0 && ms.any_nan;
-      const float vref = nt > 0 ? ms.vref : 0.f;
+      const bool bad = nt > 0 && ms.bad[sl], none = lim <= 0 || bad, whole = sg.whole, nan = nt > 0 && ms.any_nan[sl];
+      const float vref = nt > 0 ? ms.vref[sl] : 0.f;
       if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-      const float inv = whole ? (none ? 0.f : vref / sum) : vref;
-      const int64_t dst = ((int64_t)(q0 + tok) * prm.Hq + g * G + head) * D;
-      float* part = prm.parts + ((((int64_t)item * rq.Hkv + g) * prm.splits + z) * 256 + tid) * (D + 2);
-#pragma unroll
+      const float inv = whole ? vref / sum : vref;
+      float* part = prm.parts + ((int64_t)(2 * me + sg.slot) * 256 + tid) * (D + 2);
+#pragma unroll 1
       for (int c = 0; c < D / 16; ++c) {
         float o[16];
-        if (nt > 0) {
-          uint32_t ov[16];
-          tc::ld16(to + c * 16, ov);
-          tc::wait_ld();
+        uint32_t ov[16];
+        tc::ld16(to + c * 16, ov);  // (without a tile: whatever is there, not used)
+        tc::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = none ? 0.f : __uint_as_float(ov[e]) * inv;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0.f;
-        }
+        for (int e = 0; e < 16; ++e) o[e] = none || nt == 0 ? 0.f : __uint_as_float(ov[e]) * inv;
         if (nan && !none) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (ms.nankey[c * 16 + e] < lim) o[e] = __int_as_float(0x7fc00000);
+            if (ms.nankey[sl][c * 16 + e] < lim) o[e] = __int_as_float(0x7fc00000);
         }
         if (valid && whole) {
           uint32_t w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = float2_to_bf16x2(o[2 * e], o[2 * e + 1]);
-          stg16(prm.out + dst + c * 16, make_uint4(w[0], w[1], w[2], w[3]));
-          stg16(prm.out + dst + c * 16 + 8, make_uint4(w[4], w[5], w[6], w[7]));
+          stg16(prm.out + at + c * 16, make_uint4(w[0], w[1], w[2], w[3]));
+          stg16(prm.out + at + c * 16 + 8, make_uint4(w[4], w[5], w[6], w[7]));
         } else if (valid) {
 #pragma unroll
           for (int e = 0; e < 16; e += 2) *reinterpret_cast<float2*>(part + c * 16 + e) = make_float2(o[e], o[e + 1]);
@@ -587,8 +787,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (valid && !whole) {
         part[D] = m;
-        part[D + 1] = ms.bad ? -1.f : sum;
+        part[D + 1] = bad ? -1.f : sum;
       }
+      tc::fence_before_sync();
+    }
+    i0 += nt;
+    seg += nt > 0;
     }
   }
   if (failed) report(prm.status, GIST_ATTN_STATUS_TIMEOUT);
@@ -600,81 +804,62 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
-// Adds up the splits' parts of a row, a warp a row: O, m and sum in key order.
+// Adds up the parts of the units that cross CTAs, a warp a row: O, m and sum in key
+// order.  Block y takes 8 rows of the unit that CTA blockIdx.x + 1 left a header for.
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillParams prm) {
-  __shared__ int warp_sum[8], start_r, start_pre, total;
-  const Requests& rq = prm.rq;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = rq.G, Tm = prm.Tm, g = blockIdx.y;
-  scan_requests<256>(
-      rq.B,
-      [&](int r) {
-        const int n = rq.tokens(r);
-        return n >= prm.min_new ? (n + 2 * Tm - 1) / (2 * Tm) : 0;
-      },
-      warp_sum, &start_r, &start_pre, &total, [&](int) { return (int)blockIdx.x; });
-  if ((int)blockIdx.x >= total || start_r < 0) return;
-  const int r = start_r, n = rq.q_start[r + 1] - rq.q_start[r];
-  const int tok0 = ((int)blockIdx.x - start_pre) * 2 * Tm, toks = min(2 * Tm, n - tok0);
-  const int q0 = rq.q_start[r] + tok0;
-  const int pos0 = max(rq.length(r), 0) - n + tok0;
-  const int row = blockIdx.z * 8 + warp, x = row >> 7, in = row & 127;
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillParams prm, int W) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = blockIdx.x + 1;
+  const int G = prm.rq.G, Tm = prm.Tm, row = blockIdx.y * 8 + warp, x = row >> 7, in = row & 127;
   const int tok = x * Tm + in / G, head = in % G;
-  if (in >= Tm * G || tok >= toks) return;
-  const float* part = prm.parts + (((int64_t)blockIdx.x * rq.Hkv + g) * prm.splits * 256 + row) * (D + 2);
-  const int64_t step = 256 * (D + 2);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const JoinRun u = prm.join[w];
+  if (u.cost == 0 || in >= Tm * G || tok >= u.toks) return;
   float m = kNone, sum = 0.f, o[D / 32];
   bool bad = false;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  for (int z = lane; z < prm.splits; z += 32) m = fmaxf(m, part[z * step + D]);
+  for (int v = w - 1; v < W; ++v) {
+    const int64_t o0 = max(cut(u.total, v, W) - u.at, (int64_t)0), o1 = cut(u.total, v + 1, W) - u.at;
+    if (o0 >= u.cost) break;
+    const int k0 = (int)(u.tiles * o0 / u.cost), k1 = o1 >= u.cost ? u.tiles : (int)(u.tiles * o1 / u.cost);
+    if (k0 == 0 && k1 == u.tiles) return;  // one CTA had all of its tiles
+    if (k0 == k1) continue;
+    const float* p = prm.parts + ((int64_t)(2 * v + (o0 > 0 ? 0 : 1)) * 256 + row) * (D + 2);
+    const float pm = p[D], ps = p[D + 1], top = fmaxf(m, pm), f0 = exp2f(m - top), f1 = exp2f(pm - top);
+    bad |= ps < 0.f;
+    m = top;
+    sum = sum * f0 + ps * f1;
 #pragma unroll
-  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-#pragma unroll 4
-  for (int z = 0; z < prm.splits; ++z) {
-    const float* p = part + z * step;
-    const float f = exp2f(p[D] - m), s = p[D + 1];
-    bad |= s < 0.f;
-    sum += s * f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] += f * p[lane + 32 * e];
+    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f0 + f1 * p[lane + 32 * e];
   }
-  const bool none = bad || pos0 + tok < 0;
+  const bool none = bad || u.pos0 + tok < 0;
   if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-  bf16* dst = prm.out + ((int64_t)(q0 + tok) * prm.Hq + g * G + head) * D + lane;
+  bf16* dst = prm.out + ((int64_t)(u.q0 + tok) * prm.Hq + u.g * G + head) * D + lane;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) dst[32 * e] = __float2bfloat16(none ? 0.f : o[e] / sum);
 }
 
-// Row-tile pairs at most: every request with min_new tokens or more may end in a
-// pair that is not full.
-int64_t pairs_of(const PagedProblem& pb, int min_new) {
+// CTAs: one an SM, fewer where the token rows and the table cannot hold that many key
+// tiles (every request with min_new tokens or more may end in a pair that is not full).
+int grid_of(const PagedProblem& pb, int min_new, int sms) {
   const int Tm = 128 / pb.G;
   const int64_t requests = pb.T / min_new < pb.B ? pb.T / min_new : pb.B;
-  return pb.T / (2 * Tm) + requests;
-}
-
-// Runs that the keys are cut into: one unless the pairs leave SMs idle; a run has
-// 8 tiles (1024 keys) or more of the longest request that the table can hold.
-int splits_of(const PagedProblem& pb, int min_new, int sms) {
-  const int64_t ctas = pairs_of(pb, min_new) * pb.Hkv;
-  const int64_t tiles = ((int64_t)pb.W * pb.block_len + kKT - 1) / kKT;
-  int64_t s = ctas > 0 ? sms / ctas : 1;
-  s = s < tiles / 8 ? s : tiles / 8;
-  return s < 1 ? 1 : (int)s;
+  const double pairs = (double)pb.T / (2 * Tm) + requests;
+  const double tiles = requests == 0 ? 0 : pairs * pb.Hkv * ((double)((int64_t)pb.W * pb.block_len + kKT - 1) / kKT);
+  return tiles < sms ? (int)tiles : sms;
 }
 
 template <int D>
 int launch(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaStream_t stream) {
-  const int64_t pairs = pairs_of(pb, min_new);
-  if (pairs == 0) return GIST_ATTN_OK;
+  const int grid = grid_of(pb, min_new, sms);
+  if (grid == 0) return GIST_ATTN_OK;
   PrefillParams prm{};
   prm.q = static_cast<const bf16*>(pb.q);
   prm.out = static_cast<bf16*>(pb.out);
   prm.pool = pb.pool;
   prm.scale = pb.scale;
-  prm.parts = static_cast<float*>(workspace);
+  prm.join = static_cast<JoinRun*>(workspace);
+  prm.parts = reinterpret_cast<float*>(prm.join + grid);
   prm.status = pb.status;
   prm.rq = requests_of(pb);
   prm.Hq = pb.Hq;
@@ -683,24 +868,31 @@ int launch(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaSt
   prm.num_blocks = pb.num_blocks;
   prm.min_new = min_new;
   prm.Tm = 128 / pb.G;
-  prm.splits = splits_of(pb, min_new, sms);
   prm.scale_log2 = pb.scale_log2;
   for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
   constexpr int smem = (int)(PCfg<D>::offMisc + sizeof(PMisc<D>));
   static_assert(smem <= 227 * 1024, "shared memory");
   if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  prefill_kernel<D><<<dim3((unsigned)pairs, pb.Hkv, prm.splits), kThreads, smem, stream>>>(prm);
+  prefill_kernel<D><<<grid, kThreads, smem, stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
-  if (prm.splits > 1) join_kernel<D><<<dim3((unsigned)pairs, pb.Hkv, 32), 256, 0, stream>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  if (grid == 1) return GIST_ATTN_OK;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid - 1, 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, prm, grid) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
 
 size_t paged_prefill_workspace(const PagedProblem& pb, int min_new, int sms) {
-  const int splits = splits_of(pb, min_new, sms);
-  return splits == 1 ? 0 : (size_t)pairs_of(pb, min_new) * pb.Hkv * splits * 256 * (pb.d + 2) * sizeof(float);
+  return (size_t)grid_of(pb, min_new, sms) * (sizeof(JoinRun) + 2 * 256 * (pb.d + 2) * sizeof(float));
 }
 
 int launch_paged_prefill(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaStream_t stream) {

@@ -522,8 +522,8 @@ size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims);
  * the pool zeroes its request's rows and sets GIST_ATTN_STATUS_BAD_BLOCK, as does a
  * kv_len past W * block_len; a q_start pair outside [0, T], out of order or more
  * than max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
- * elsewhere.  block_len must be a multiple of 16 and Hq / Hkv at most 128
- * (GIST_ATTN_ERR_UNSUPPORTED).
+ * elsewhere.  block_len must be a multiple of 16, Hq / Hkv at most 128 and
+ * W * block_len at most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).
  */
 int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3, const float* kv_scale,
                           const int32_t* block_table, const int32_t* q_start,
