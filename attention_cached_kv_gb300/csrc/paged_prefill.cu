@@ -52,8 +52,9 @@ constexpr int kStartCost = 256;       // keys that a unit's start is worth
 struct JoinRun {
   int64_t at, total;  // the unit's first place in the sequence of costs, the sequence's end
   int cost, tiles, q0, toks, pos0, g;
-  int pad[2];
+  int pad[6];
 };
+static_assert(sizeof(JoinRun) == 64, "the parts behind the headers are read 16 bytes at a time");
 
 struct PrefillParams {
   const bf16* q;
@@ -76,77 +77,6 @@ struct PCfg {
   static constexpr uint32_t offK = 2 * kTile, offV = 4 * kTile, offMisc = 6 * kTile;
   static constexpr int kS = 0, kO = 256;  // TMEM columns: S (P) of the row tiles, O
 };
-
-template <int D>
-struct PMisc {
-  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
-  uint32_t tmem;
-  int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
-  int64_t warp_sum[kThreads / 32], start_pre, total;
-  int start_r;
-  // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
-  // the pool (-1: no key that is seen, or a block outside the pool)
-  alignas(16) float ksc[kRing][8], vsc[kRing][8];
-  int64_t at[kRing][8];
-  int even[kRing];  // the groups' K scales are equal in pairs
-  float vref[4], vpart[4];
-  int nankey[4][D];  // first key past the first row's whose V is NaN, by element
-};
-
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// As ld32, waited for, the maximum only.
-__device__ __forceinline__ float ld32_max(uint32_t taddr) {
-  uint32_t r[32];
-  float m;
-  asm volatile(
-      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
-      : "r"(taddr));
-  (void)r;
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m)::"memory");
-  return m;
-}
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// 16 bytes from global memory where `ok`, else zeros (no branch: the loads of a pass
-// go out together).
-__device__ __forceinline__ uint4 ldg16_if(const void* p, bool ok) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-      "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((uint32_t)ok));
-  return v;
-}
 
 // One unit's share of a CTA.
 struct PSeg {
@@ -226,6 +156,97 @@ struct PWalk {
   }
 };
 
+// A key tile of the CTA's sequence, for the converting warps.
+struct Tile {
+  int left;  // rows that some query row sees (INT32_MIN: past the last tile)
+  int all;   // rows that every query row sees
+  int key0;  // its first key
+  int sl;    // its segment's slot
+  int r, g, kv;
+};
+
+template <int D>
+struct PMisc {
+  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
+  uint32_t tmem;
+  int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
+  int64_t warp_sum[kThreads / 32], start_pre, total;
+  int start_r;
+  PWalk walk;  // the softmax warps' walk and segment
+  PSeg seg;
+  int any_seg;  // 0: there is no further one
+  // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
+  // the pool (-1: no key that is seen, or a block outside the pool)
+  alignas(16) float ksc[kRing][8], vsc[kRing][8];
+  int64_t at[kRing][8];
+  Tile tile[kRing];
+  int even[kRing];  // the groups' K scales are equal in pairs
+  float vref[4], vpart[4];
+  int nankey[4][D];  // first key past the first row's whose V is NaN, by element
+};
+
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// As ld32, waited for, the maximum only.
+__device__ __forceinline__ float ld32_max(uint32_t taddr) {
+  uint32_t r[32];
+  float m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m)::"memory");
+  return m;
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// 16 bytes from global memory where `ok`, else zeros (no branch: the loads of a pass
+// go out together).
+__device__ __forceinline__ uint4 ldg16_if(const void* p, bool ok) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)ok));
+  return v;
+}
+
 __device__ __forceinline__ int64_t cut(int64_t total, int w, int W) {
   return total / W * w + min((int64_t)w, total % W);
 }
@@ -295,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (x0 > wk.unit() && cut(total, me - 1, W) <= wk.unit()) {
       PSeg s;
       wk.get(prm, s);
-      j = JoinRun{wk.unit(), total, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {0, 0}};
+      j = JoinRun{wk.unit(), total, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {}};
     }
     prm.join[me] = j;
+    ms.walk = wk;
   }
   bool failed = false;
 
@@ -384,13 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // lane group t walks to tiles t, t + 4, ... of the CTA's sequence by itself
     const int t = lane >> 3, gr = lane & 7;
     PSeg sg;
-    int e = t;  // the tile within the segment
+    int e = t, passed = 0;  // the tile within the segment; segments with tiles before
     bool have = false, want = false;
     auto settle = [&]() {  // to the segment that tile e of this or a later one lies in
       while (wk.more()) {
         if (have && e < sg.nt) return;
         if (have) {
           e -= sg.nt;
+          passed += sg.nt > 0;
           wk.next(prm);
         }
         have = false;
@@ -398,29 +421,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       have = false;
     };
-    int blk = -1, key = 0, at_g = 0, at_kend = 0;
+    int blk = -1, key = 0;
+    Tile tl;
     auto look_up = [&]() {
       settle();
       want = false;
       blk = -1;
+      tl = Tile{INT32_MIN, 0, 0, 0, 0, 0, 0};
       if (have) {
-        key = (sg.kt0 + e) * kKT + gr * 16;
-        at_g = sg.g;
-        at_kend = sg.kend;
+        const int key0 = (sg.kt0 + e) * kKT;
+        key = key0 + gr * 16;
+        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, sg.r, sg.g, sg.kv};
         want = key < sg.kend;
         if (want) blk = rq.block_table[(int64_t)sg.r * rq.W + key / rq.block_len];
         e += 4;
       }
     };
     look_up();
-    for (int i = 0; __any_sync(0xffffffffu, have); i += 4) {
+    for (int i = 0;; i += 4) {
+      const bool last = __any_sync(0xffffffffu, !have);  // this half ends the sequence
+      const Tile now = tl;
       const int half = (i >> 2) & 1;
       const bool ok = want && blk >= 0 && blk < prm.num_blocks, lost = want && !ok;
       if (lost) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-      const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + at_g;
+      const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + now.g;
       const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : -1;
       const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : lost ? -1.f : 0.f;
-      look_up();  // its load runs while this half is waited for
+      if (!last) look_up();  // its load runs while this half is waited for
       if (__any_sync(0xffffffffu, i >= kRing && !mbar_wait(&ms.gfree[half], ((uint32_t)(i >> 3) & 1u) ^ 1u))) {
         failed = true;
         break;
@@ -430,9 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       ms.vsc[slot][gr] = vs;  // (-1: the block id is outside the pool)
       ms.at[slot][gr] = at;
       const uint32_t same = __ballot_sync(0xffffffffu, __shfl_xor_sync(0xffffffffu, ks, 1) == ks);
-      if (gr == 0) ms.even[slot] = ((same >> (8 * t)) & 0xffu) == 0xffu;
+      if (gr == 0) {
+        ms.even[slot] = ((same >> (8 * t)) & 0xffu) == 0xffu;
+        ms.tile[slot] = now;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.gready[half]);
+      if (last) break;
     }
   } else if (warp >= 8) {
     // ================================================== cached rows into f16 tiles
@@ -442,15 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int ct = tid - 256, c = ct % kLanes, row0 = ct / kLanes;
     const int64_t vstep = (int64_t)rq.Hkv * rq.block_len * D;
     // The largest V scale of the request's blocks.
-    auto largest = [&](const PSeg& sg) {
-      const int32_t* table = rq.block_table + (int64_t)sg.r * rq.W;
+    auto largest = [&](int r, int g, int kv) {
+      const int32_t* table = rq.block_table + (int64_t)r * rq.W;
       float top = 0.f;
-      const int blocks = (max(sg.kv, 0) + rq.block_len - 1) / rq.block_len;
+      const int blocks = (kv + rq.block_len - 1) / rq.block_len;
 #pragma unroll 4
       for (int b = ct; b < blocks; b += 128) {
         const int blk = table[b];
         const bool ok = blk >= 0 && blk < prm.num_blocks;
-        const float s = prm.scale[(((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 + 1) * rq.Hkv + sg.g];
+        const float s = prm.scale[(((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 + 1) * rq.Hkv + g];
         top = fmaxf(top, ok ? s : 0.f);
       }
 #pragma unroll
@@ -493,43 +524,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       sts16(base + swz128(row, ch + odd), odd ? hi : lo);
       sts16(base + swz128(row, ch + 1 - odd), odd ? lo : hi);
     };
-    PSeg sg, ahead;  // this segment, the next one
-    auto find = [&](PSeg& s) {
-      while (wk.more())
-        if (wk.get(prm, s)) return true;
-        else wk.next(prm);
-      return false;
-    };
-    bool have = find(sg), have2 = false;
-    int seg = 0, i = 0, last_r = -1, last_g = -1;
+    int last_r = -1, last_g = -1;
     float vref = 0.f, rvref = 0.f;
-    if (have && sg.nt > 0 && looked_up(0)) {
-      fetch(0, sg.kend - sg.kt0 * kKT, kx, 0);
-      fetch(0, sg.kend - sg.kt0 * kKT, vx, vstep);
+    if (looked_up(0)) {
+      fetch(0, ms.tile[0].left, kx, 0);
+      fetch(0, ms.tile[0].left, vx, vstep);
     }
-    for (; have && !failed; seg += sg.nt > 0, sg = ahead, have = have2) {
-      wk.next(prm);
-      have2 = find(ahead);
-      if (sg.nt == 0) {  // nothing to convert; the next segment's first tile
-        if (have2 && ahead.nt > 0 && looked_up(i)) {
-          fetch(i, ahead.kend - ahead.kt0 * kKT, kx, 0);
-          fetch(i, ahead.kend - ahead.kt0 * kKT, vx, vstep);
-        }
-        continue;
-      }
-      if (sg.r != last_r || sg.g != last_g) {
-        vref = largest(sg);
+    for (int i = 0; !failed; ++i) {
+      const Tile& tl = ms.tile[i & (kRing - 1)];
+      if (tl.left == INT32_MIN) break;
+      const int b = i & 1, sl = tl.sl;
+      if (tl.r != last_r || tl.g != last_g) {
+        last_r = tl.r;
+        last_g = tl.g;
+        vref = largest(last_r, last_g, tl.kv);
         rvref = 1.f / vref;
-        last_r = sg.r;
-        last_g = sg.g;
       }
-      const int sl = seg & 3;
       if (ct == 0) ms.vref[sl] = vref;
-    for (int e = 0; e < sg.nt && !failed; ++e, ++i) {
-      const int kt = sg.kt0 + e, b = i & 1;
-      // the tile after this one, in this segment or the next
-      const bool more = e + 1 < sg.nt || (have2 && ahead.nt > 0);
-      const int left1 = e + 1 < sg.nt ? sg.kend - (kt + 1) * kKT : ahead.kend - ahead.kt0 * kKT;
       if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
@@ -538,30 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int p = 0; p < kPass; ++p) put(sbase + C::offK + b * C::kTile, p * kRows + row0, kx[p], 0, false);
       fence_proxy_async_smem();
       mbar_arrive(&ms.kready[b]);
-      if (more && looked_up(i + 1)) fetch(i + 1, left1, kx, 0);
+      if (looked_up(i + 1)) fetch(i + 1, ms.tile[(i + 1) & (kRing - 1)].left, kx, 0);
       if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
       }
-      if (kt * kKT + kKT > sg.pos0 + 1) {
-        // keys that not every row sees: a NaN would reach the others (0 x NaN), so it
-        // is noted for the rows that see it and cleared
+      // keys that not every row sees: a NaN would reach the others (0 x NaN)
+      const int all = tl.all;
+      bool nan = false;
+      if (all < kKT) {
 #pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-          const int key = kt * kKT + p * kRows + row0;
-          const uint32_t any = e4m3_nan(vx[p].x) | e4m3_nan(vx[p].y) | e4m3_nan(vx[p].z) | e4m3_nan(vx[p].w);
-          if (key > sg.pos0 && any) {
-            uint32_t w[4] = {vx[p].x, vx[p].y, vx[p].z, vx[p].w};
-            ms.any_nan[sl] = 1;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (((w[e >> 2] >> (8 * (e & 3))) & 0x7fu) == 0x7fu) {
-                w[e >> 2] &= ~(0xffu << (8 * (e & 3)));
-                atomicMin(&ms.nankey[sl][c * 16 + e], key);
-              }
-            vx[p] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        for (int p = 0; p < kPass; ++p)
+          nan |= p * kRows + row0 >= all && (e4m3_nan(vx[p].x) | e4m3_nan(vx[p].y) | e4m3_nan(vx[p].z) | e4m3_nan(vx[p].w));
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
@@ -569,10 +568,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (vs < 0.f) ms.bad[sl] = 1;
         put(sbase + C::offV + b * C::kTile, p * kRows + row0, vx[p], to_f16x2(f, f), true);
       }
+      if (nan) {  // noted for the rows that see it, and cleared
+        ms.any_nan[sl] = 1;
+#pragma unroll 1
+        for (int k = 0; k < kPass * 16; ++k) {
+          const int row = (k >> 4) * kRows + row0, e = k & 15;
+          const uint32_t a = sbase + C::offV + b * C::kTile + (c / 4) * C::kPanel + swz128(row, 2 * (c % 4) + (e >> 3)) + (e & 7) * 2;
+          if (row >= all && (lds_u16(a) & 0x7fffu) > 0x7c00u) {
+            sts_u16(a, 0);
+            atomicMin(&ms.nankey[sl][c * 16 + e], tl.key0 + row);
+          }
+        }
+      }
       fence_proxy_async_smem();
       mbar_arrive(&ms.vready[b]);
-      if (more && !failed) fetch(i + 1, left1, vx, vstep);
-    }
+      if (!failed) fetch(i + 1, ms.tile[(i + 1) & (kRing - 1)].left, vx, vstep);
     }
   } else {
     // ================================================== q rows, softmax, output
@@ -585,17 +595,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     int seg = 0, i0 = 0;
     uint32_t ns = 0;  // S tiles (and last P V's) so far of this row tile
-    for (; wk.more(); wk.next(prm)) {
-    PSeg sg;
-    if (!wk.get(prm, sg)) continue;
-    // (both row tiles together, so that nothing of a segment before is still read; the
-    // slots of `seg` count the segments with key tiles)
+    // One thread walks; the others read its segment from shared memory (their registers
+    // are the scores').  The slots of `seg` count the segments with key tiles.
+    const PSeg& sg = ms.seg;
+    for (;;) {
+    named_bar_sync(3, 256);  // nothing of the segment before is still read
+    if (tid == 0) {
+      PWalk k = ms.walk;
+      PSeg s;
+      bool any = false;
+      while (k.more() && !any) {
+        any = k.get(prm, s);
+        k.next(prm);
+      }
+      if (any) ms.seg = s;
+      ms.any_seg = any;
+      ms.walk = k;
+    }
     named_bar_sync(3, 256);
-    const int sl = seg & 3, toks = sg.toks, pos0 = sg.pos0, nt = sg.nt;
-    const bool valid = row < Tm * G && tok < toks;
-    const int lim = valid ? pos0 + tok + 1 : 0;         // keys the row sees
-    const int lim_all = pos0 + x * Tm + 1;              // keys every row of the tile sees
-    const int64_t at = ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
+    if (!ms.any_seg) break;
+    const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
+    const bool valid = row < Tm * G && tok < sg.toks;
+    const int lim = valid ? sg.pos0 + tok + 1 : 0;      // keys the row sees
+    const int lim_all = sg.pos0 + x * Tm + 1;           // keys every row of the tile sees
     if (nt > 0) {  // the next but one's
       if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
       if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // the row into its place, rounded to f16 there after the rotation
       const uint32_t tile = sbase + x * C::kTile;
       auto place = [&](int ch) { return tile + (ch >> 3) * C::kPanel + swz128(row, ch & 7); };
-      const bf16* src = prm.q + at;
+      const bf16* src = prm.q + ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
 #pragma unroll
       for (int ch = 0; ch < D / 8; ++ch) {
         if (valid) cp_async16(place(ch), src + ch * 8);
@@ -624,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
       const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
       rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
-      const int pos = max(pos0 + tok, 0);
+      const int pos = max(sg.pos0 + tok, 0);
       const uint64_t down2 = f2_make(down, down);
 #pragma unroll 1
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
@@ -655,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
     const bool live = x == 0 || sg.two;
     for (int e = 0; live && e < nt; ++e) {
-      const int i = i0 + e, key0 = (sg.kt0 + e) * kKT;
+      const int i = i0 + e, key0 = (kt0 + e) * kKT;
       const bool edge = key0 + kKT > lim_all;
       wait(&ms.sfull[x], ns++ & 1u);
       tc::fence_after_sync();
@@ -760,8 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const float vref = nt > 0 ? ms.vref[sl] : 0.f;
       if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
       const float inv = whole ? vref / sum : vref;
-      float* part = prm.parts + ((int64_t)(2 * me + sg.slot) * 256 + tid) * (D + 2);
-#pragma unroll 1
+      const int64_t at = ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
+      float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
+#pragma unroll 2
       for (int c = 0; c < D / 16; ++c) {
         float o[16];
         uint32_t ov[16];
@@ -782,12 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           stg16(prm.out + at + c * 16 + 8, make_uint4(w[4], w[5], w[6], w[7]));
         } else if (valid) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) *reinterpret_cast<float2*>(part + c * 16 + e) = make_float2(o[e], o[e + 1]);
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(part + tid * D + c * 16 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (valid && !whole) {
-        part[D] = m;
-        part[D + 1] = bad ? -1.f : sum;
+        part[256 * D + tid] = m;
+        part[256 * (D + 1) + tid] = bad ? -1.f : sum;
       }
       tc::fence_before_sync();
     }
@@ -824,13 +848,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Prefi
     const int k0 = (int)(u.tiles * o0 / u.cost), k1 = o1 >= u.cost ? u.tiles : (int)(u.tiles * o1 / u.cost);
     if (k0 == 0 && k1 == u.tiles) return;  // one CTA had all of its tiles
     if (k0 == k1) continue;
-    const float* p = prm.parts + ((int64_t)(2 * v + (o0 > 0 ? 0 : 1)) * 256 + row) * (D + 2);
-    const float pm = p[D], ps = p[D + 1], top = fmaxf(m, pm), f0 = exp2f(m - top), f1 = exp2f(pm - top);
+    const float* p = prm.parts + (int64_t)(2 * v + (o0 > 0 ? 0 : 1)) * 256 * (D + 2);
+    const float pm = p[256 * D + row], ps = p[256 * (D + 1) + row], top = fmaxf(m, pm), f0 = exp2f(m - top), f1 = exp2f(pm - top);
     bad |= ps < 0.f;
     m = top;
     sum = sum * f0 + ps * f1;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f0 + f1 * p[lane + 32 * e];
+    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f0 + f1 * p[row * D + lane + 32 * e];
   }
   const bool none = bad || u.pos0 + tok < 0;
   if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
