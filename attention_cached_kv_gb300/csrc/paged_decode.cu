@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
       }
       tc::fence_after_sync();
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t id = idesc_e4m3((KPR * 24 * nch + 15) & ~15, 1);
         const uint32_t vb = sbase + C::offV + vs * kStage, pp = sbase + C::offP + pb * C::PB;
 #pragma unroll
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         tc::fence_after_sync();
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint32_t kb = sbase + ks * kStage;
 #pragma unroll
           for (int p = 0; p < KPR; ++p)
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (pending && !failed) issue_pv();
-    if (lane == 0) tc::commit(smem_u32(&ms.drain));
+    if (tc::elect_one()) tc::commit(smem_u32(&ms.drain));
     __syncwarp();
     if (!mbar_wait(&ms.drain, 0)) failed = true;
   } else if (warp >= 6) {

@@ -173,35 +173,17 @@ struct PMisc {
   int64_t warp_sum[kThreads / 32], start_pre, total;
   int start_r;
   PWalk walk;  // the softmax warps' walk and segment
-  PSeg seg;
-  int any_seg;  // 0: there is no further one
+  PSeg seg[2];
+  int any_seg[2];  // 0: there is no further one
   // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
   // the pool (-1: no key that is seen, or a block outside the pool)
   alignas(16) float ksc[kRing][8], vsc[kRing][8];
   int64_t at[kRing][8];
   Tile tile[kRing];
-  int even[kRing];  // the groups' K scales are equal in pairs
   float vref[4], vpart[4];
   int nankey[4][D];  // first key past the first row's whose V is NaN, by element
 };
 
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// As ld32, waited for, the maximum only.
-__device__ __forceinline__ float ld32_max(uint32_t taddr) {
-  uint32_t r[32];
-  float m;
-  asm volatile(
-      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(m)::"memory");
-  return m;
-}
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -319,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       j = JoinRun{wk.unit(), total, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {}};
     }
     prm.join[me] = j;
-    ms.walk = wk;
   }
   bool failed = false;
 
@@ -331,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       return !failed;
     };
     auto issue_s = [&](int x, int i) {  // S of row tile x and the CTA's i-th key tile
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t qb = sbase + x * C::kTile, kb = sbase + C::offK + (i & 1) * C::kTile;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -343,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
     };
     auto issue_pv = [&](int x, int i, bool first) {
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t vb = sbase + C::offV + (i & 1) * C::kTile;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -353,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       __syncwarp();
     };
     auto arrive = [&](uint64_t* bar) {
-      if (lane == 0) tc::commit(smem_u32(bar));
+      if (tc::elect_one()) tc::commit(smem_u32(bar));
       __syncwarp();
     };
     int i0 = 0, seg = 0;       // tiles and segments so far
@@ -398,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       i0 += sg.nt;
     }
-    if (lane == 0) tc::commit(smem_u32(&ms.drain));
+    if (tc::elect_one()) tc::commit(smem_u32(&ms.drain));
     __syncwarp();
     if (!mbar_wait(&ms.drain, 0)) failed = true;
   } else if (warp == 13) {
@@ -456,11 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       ms.ksc[slot][gr] = ks;
       ms.vsc[slot][gr] = vs;  // (-1: the block id is outside the pool)
       ms.at[slot][gr] = at;
-      const uint32_t same = __ballot_sync(0xffffffffu, __shfl_xor_sync(0xffffffffu, ks, 1) == ks);
-      if (gr == 0) {
-        ms.even[slot] = ((same >> (8 * t)) & 0xffu) == 0xffu;
-        ms.tile[slot] = now;
-      }
+      if (gr == 0) ms.tile[slot] = now;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.gready[half]);
       if (last) break;
@@ -595,25 +572,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     int seg = 0, i0 = 0;
     uint32_t ns = 0;  // S tiles (and last P V's) so far of this row tile
-    // One thread walks; the others read its segment from shared memory (their registers
-    // are the scores').  The slots of `seg` count the segments with key tiles.
-    const PSeg& sg = ms.seg;
-    for (;;) {
-    named_bar_sync(3, 256);  // nothing of the segment before is still read
-    if (tid == 0) {
-      PWalk k = ms.walk;
+    // One thread walks, a segment ahead; the others read from shared memory (their
+    // registers are the scores').  The slots of `seg` count the segments with key tiles.
+    auto find = [&](int k) {
+      PWalk w = ms.walk;
       PSeg s;
       bool any = false;
-      while (k.more() && !any) {
-        any = k.get(prm, s);
-        k.next(prm);
+      while (w.more() && !any) {
+        any = w.get(prm, s);
+        w.next(prm);
       }
-      if (any) ms.seg = s;
-      ms.any_seg = any;
-      ms.walk = k;
+      if (any) ms.seg[k] = s;
+      ms.any_seg[k] = any;
+      ms.walk = w;
+    };
+    if (tid == 0) {
+      ms.walk = wk;
+      find(0);
     }
-    named_bar_sync(3, 256);
-    if (!ms.any_seg) break;
+    for (int now = 0;; now ^= 1) {
+    named_bar_sync(3, 256);  // nothing of the segment before is still read
+    if (!ms.any_seg[now]) break;
+    const PSeg& sg = ms.seg[now];
     const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
     const bool valid = row < Tm * G && tok < sg.toks;
     const int lim = valid ? sg.pos0 + tok + 1 : 0;      // keys the row sees
@@ -648,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
       const int pos = max(sg.pos0 + tok, 0);
       const uint64_t down2 = f2_make(down, down);
-#pragma unroll 1
+#pragma unroll 2
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
         const uint32_t pa = place(ch), pb = place(ch + D / 16);
         const uint4 va = lds16(pa), vb = lds16(pb);
@@ -673,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       fence_proxy_async_smem();
       mbar_arrive(&ms.qready);
     }
+    if (tid == 0) find(now ^ 1);
     float m = kNone;
     uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
     const bool live = x == 0 || sg.two;
@@ -682,89 +663,95 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       wait(&ms.sfull[x], ns++ & 1u);
       tc::fence_after_sync();
       const float* ksc = ms.ksc[i & (kRing - 1)];
-      float mx = kNone;
-      if (!edge && ms.even[i & (kRing - 1)]) {
+      // 16 scores v of chunk c (16 keys) as weights exp2(f v - m), packed; their sum into
+      // acc; returns their largest exponent
+      auto weights = [&](int c, const uint32_t (&v)[16], uint32_t* pk, int left) {
+        const float f = ksc[c] * rs;
+        const uint64_t g2 = f2_make(f, f), nm2 = f2_make(-m, -m);
+        float top = kNone;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) mx = fmaxf(mx, ld32_max(ts + c * 32) * (ksc[2 * c] * rs));
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          ld32(ts + c * 32, v);
-          tc::wait_ld();
-          const int left = lim - key0 - c * 32;  // columns of these that the row sees
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float t = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) t = fmaxf(t, h * 16 + e < left || !edge ? __uint_as_float(v[h * 16 + e]) : -INFINITY);
-            mx = fmaxf(mx, t * (ksc[2 * c + h] * rs));
-          }
-        }
-      }
-      // a row whose maximum jumps scales its O and sum down first; the TMEM load and
-      // store are warp-collective, so the warp does it for any of its rows
-      const bool move = mx - m > kSlack;
-      if (__any_sync(0xffffffffu, move)) {
-        const float fm = move ? ex2_approx(m - mx) : 1.f;
-        if (move) m = mx;
-        const uint64_t f2 = f2_make(fm, fm);
-        acc = f2_mul(acc, f2);
-        acc2 = f2_mul(acc2, f2);
-        if (e > 0) {
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t ov[16];
-            tc::ld16(to + c * 16, ov);
-            tc::wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * fm);
-            st16(to + c * 16, ov);
-          }
-        }
-      }
-      // 32 scores in registers, the next 32 on their way
-      const uint64_t nm2 = f2_make(-m, -m);
-      uint32_t va[32], vb[32];
-      auto weights = [&](int c, uint32_t (&v)[32], auto masked) {
-        uint32_t pk[16];
-        const float2 k2 = *reinterpret_cast<const float2*>(ksc + 2 * c);
-        const float f0 = k2.x * rs, f1 = k2.y * rs;
-        const uint64_t g0 = f2_make(f0, f0), g1 = f2_make(f1, f1);
-        const int left = lim - key0 - c * 32;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int k = 0; k < 8; ++k) {
           float a, b;
-          f2_split(f2_fma(f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), e < 8 ? g0 : g1, nm2), a, b);
-          if (masked) {
-            if (2 * e >= left) a = -INFINITY;
-            if (2 * e + 1 >= left) b = -INFINITY;
-          }
+          f2_split(f2_fma(f2_make(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), g2, nm2), a, b);
+          if (2 * k >= left) a = -INFINITY;
+          if (2 * k + 1 >= left) b = -INFINITY;
+          top = max3f(top, a, b);
           const float pa = ex2_approx(a), pb = ex2_approx(b);
-          if (e & 1) acc = f2_add(acc, f2_make(pa, pb));
+          if (k & 1) acc = f2_add(acc, f2_make(pa, pb));
           else acc2 = f2_add(acc2, f2_make(pa, pb));
-          pk[e] = to_f16x2(pa, pb);
+          pk[k] = to_f16x2(pa, pb);
         }
-        st16(ts + c * 16, pk);
+        return top;
       };
-      if (!edge) {
-        ld32(ts, va);
+      // One pass with the maximum as it is; P stays in registers until it is known that
+      // no row's scores passed it by too much.
+      bool done = false;
+      if (!edge && e > 0) {
+        const uint64_t keep = acc, keep2 = acc2;
+        uint32_t va[16], vb[16], pk[64];
+        float top = kNone;
+        tc::ld16(ts, va);
         tc::wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          ld32(ts + c * 32 + 32, vb);
-          weights(c, va, std::false_type{});
+        for (int c = 0; c < 8; c += 2) {
+          tc::ld16(ts + c * 16 + 16, vb);
+          top = fmaxf(top, weights(c, va, pk + c * 8, 16));
           tc::wait_ld();
-          if (c + 2 < 4) ld32(ts + c * 32 + 64, va);
-          weights(c + 1, vb, std::false_type{});
+          if (c + 2 < 8) tc::ld16(ts + c * 16 + 32, va);
+          top = fmaxf(top, weights(c + 1, vb, pk + c * 8 + 8, 16));
           tc::wait_ld();
         }
-      } else {
+        done = !__any_sync(0xffffffffu, top > kSlack);
+        if (done) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st16(ts + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
+        } else {
+          acc = keep;
+          acc2 = keep2;
+        }
+      }
+      if (!done) {
+        // the tile's maximum first.  A row whose maximum jumps scales its O and sum down;
+        // the TMEM load and store are warp-collective, so the warp does it for any of its
+        // rows
+        float mx = kNone;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          ld32(ts + c * 32, va);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[16];
+          tc::ld16(ts + c * 16, v);
           tc::wait_ld();
-          weights(c, va, std::true_type{});
+          const int left = edge ? lim - key0 - c * 16 : 16;  // columns of these that the row sees
+          float t = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) t = fmaxf(t, k < left ? __uint_as_float(v[k]) : -INFINITY);
+          mx = fmaxf(mx, t * (ksc[c] * rs));
+        }
+        const bool move = mx - m > kSlack;
+        if (__any_sync(0xffffffffu, move)) {
+          const float fm = move ? ex2_approx(m - mx) : 1.f;
+          if (move) m = mx;
+          const uint64_t f2 = f2_make(fm, fm);
+          acc = f2_mul(acc, f2);
+          acc2 = f2_mul(acc2, f2);
+          if (e > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t ov[16];
+              tc::ld16(to + c * 16, ov);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * fm);
+              st16(to + c * 16, ov);
+            }
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[16], pk[8];
+          tc::ld16(ts + c * 16, v);
+          tc::wait_ld();
+          weights(c, v, pk, edge ? lim - key0 - c * 16 : 16);
+          tc::st8(ts + c * 8, pk);
         }
       }
       tc::wait_st();

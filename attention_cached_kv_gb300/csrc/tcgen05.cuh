@@ -35,6 +35,16 @@ __device__ __forceinline__ void fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp, the same one every time.  The compiler knows the code
+// under it to be a single thread's and keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ---- descriptors ----
 // Shared-memory matrix descriptor: start address, leading / stride byte
 // offsets (all >> 4), version 1 (bits 46-47), 128-byte swizzle (layout 2 in
