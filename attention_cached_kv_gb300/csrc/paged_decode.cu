@@ -118,18 +118,6 @@ constexpr uint32_t smem_bytes() {
   return Cfg<D, CH>::offMisc + (uint32_t)sizeof(Misc<D, CH>);
 }
 
-// S = f8 x f8 -> f32
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t N, uint32_t a_mn_major) {
-  return (1u << 4) | (a_mn_major << 15) | ((N >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int c0,
                                             int c1, int c2) {
   asm volatile(
@@ -387,11 +375,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc::fence_after_sync();
       if (tc::elect_one()) {
-        const uint32_t id = idesc_e4m3((KPR * 24 * nch + 15) & ~15, 1);
+        const uint32_t id = tc::idesc_e4m3_f32(128, (KPR * 24 * nch + 15) & ~15, 1);
         const uint32_t vb = sbase + C::offV + vs * kStage, pp = sbase + C::offP + pb * C::PB;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_f8(tmem + C::kO, tc::smem_desc_sw128(vb + k * 4096, kStage, 1024),
+          tc::mma_ss_f8(tmem + C::kO, tc::smem_desc_sw128(vb + k * 4096, kStage, 1024),
                  tc::smem_desc_sw128(pp + k * 32, 16, 1024), id, !first || k > 0);
         tc::commit(smem_u32(&ms.pfree[pb]));
         tc::commit(smem_u32(&ms.vfree[vs]));
@@ -409,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         break;
       }
       nch = (ms.seg[qs].rows + 7) >> 3;
-      const uint32_t id = idesc_e4m3((24 * nch + 15) & ~15, 0);
+      const uint32_t id = tc::idesc_e4m3_f32(128, (24 * nch + 15) & ~15, 0);
       const uint32_t qb = sbase + C::offQ + qs * C::QB;
       for (int kt = kt0; kt < kt1; ++kt) {
         const int ks = i % NK, sb = i % SB;
@@ -425,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int p = 0; p < KPR; ++p)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              mma_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
+              tc::mma_ss_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
                      tc::smem_desc_sw128(qb + k * 32, 16, 1024), id, k > 0);
           tc::commit(smem_u32(&ms.sfull[sb]));
           tc::commit(smem_u32(&ms.kfree[ks]));

@@ -3,21 +3,23 @@
 //
 // A CTA takes one KV head and up to 256 query rows of a request: two row tiles of
 // floor(128 / G) tokens x G heads.  Its keys stream by in tiles of 128, one pass,
-//     S = q K^T, P = exp2(S - m), O += P V       (tcgen05 kind::f16, TMEM)
+//     S = q K^T        tcgen05 kind::f8f6f4: cached bytes as they are, q as the sum of
+//                      three E4M3 terms (11 bits and more), one product after the other
+//     P = exp2(S - m), O += P V       tcgen05 kind::f16, P back in TMEM
 // with m the row's running maximum, moved only when a tile's maximum passes it by
 // more than 8 (log2 units).  The warps:
 //   * 0-3, 4-7: a thread a row of each row tile, softmax and output; P goes back
 //     into S's columns as f16 (11 bits), A operand of the second product;
-//   * 8-11: cached rows from global memory through registers into f16 tiles.  E4M3
-//     to f16 is exact; values are also divided by the largest V scale of the
-//     request (exact for powers of two), K's block scales multiply the fp32 scores;
+//   * 8-11: cached rows into shared memory, keys by cp.async, values through registers
+//     as f16: E4M3 is exact there, and they are divided by the largest V scale of the
+//     request (exact for powers of two); K's block scales multiply the fp32 scores;
 //   * 12: the MMAs, alternating between the row tiles, so that one's products run
 //     while the other's softmax does;
 //   * 13: block ids and scales, four tiles at a time, ahead of the copies.
-// One conversion of a key serves 256 rows, against 256 exponentials for it: that is
-// why rows are taken in pairs of tiles here and cached bytes are used as they are
-// where there are few rows (paged_decode.cu).  q is scaled by a power of two a row
-// before its one rounding to f16.
+// One conversion of a value serves 256 rows: that is why rows are taken in pairs of
+// tiles.  Converting is slow here (about 16 cycles a warp's instruction): with the keys
+// converted too it was what bound the loop, which three products of keys as they are,
+// at twice the f16 rate, do not.  q is scaled by a power of two a row first.
 //
 // Work is the sequence of (request, KV head, row-tile pair) units, each worth the keys
 // it sees and a constant for its start; each SM's CTA takes an equal run of it, cut
@@ -67,14 +69,17 @@ struct PrefillParams {
   Requests rq;
   int Hq, L, layer, num_blocks, min_new, Tm;
   float scale_log2;
+  uint32_t per_g;  // 2^16 / G rounded up: j / G = j per_g >> 16 for j < 128
   uint64_t turn[64];
 };
 
 template <int D>
 struct PCfg {
-  static constexpr uint32_t kTile = 128 * D * 2;        // bytes of a 128-row f16 tile
-  static constexpr uint32_t kPanel = 128 * 128;
-  static constexpr uint32_t offK = 2 * kTile, offV = 4 * kTile, offMisc = 6 * kTile;
+  static constexpr uint32_t kCodes = 128 * 128;         // bytes of a 128-row E4M3 tile (rows of 128 bytes)
+  static constexpr uint32_t kQ = 3 * kCodes;            // a row tile of q: three terms
+  static constexpr uint32_t kPanel = 128 * 128;         // 64 columns of f16
+  static constexpr uint32_t kV = 128 * D * 2;           // a V tile, f16
+  static constexpr uint32_t offK = 2 * kQ, offV = offK + 3 * kCodes, offMisc = offV + 2 * kV;
   static constexpr int kS = 0, kO = 256;  // TMEM columns: S (P) of the row tiles, O
 };
 
@@ -167,7 +172,7 @@ struct Tile {
 
 template <int D>
 struct PMisc {
-  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
+  uint64_t kready[3], kfree[3], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
   uint32_t tmem;
   int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
   int64_t warp_sum[kThreads / 32], start_pre, total;
@@ -196,6 +201,13 @@ __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// cp.async of 16 bytes where `ok`, else 16 zeros.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   uint16_t v;
@@ -251,14 +263,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ms.kready[s], 128);
-      mbar_init(&ms.kfree[s], 1);
       mbar_init(&ms.vready[s], 128);
       mbar_init(&ms.vfree[s], 1);
       mbar_init(&ms.sfull[s], 1);
       mbar_init(&ms.pfull[s], 128);
       mbar_init(&ms.gready[s], 1);
       mbar_init(&ms.gfree[s], 1);
+    }
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&ms.kready[s], 128);
+      mbar_init(&ms.kfree[s], 1);
     }
     mbar_init(&ms.qready, 256);
     mbar_init(&ms.drain, 1);
@@ -313,19 +327,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     auto issue_s = [&](int x, int i) {  // S of row tile x and the CTA's i-th key tile
       if (tc::elect_one()) {
-        const uint32_t qb = sbase + x * C::kTile, kb = sbase + C::offK + (i & 1) * C::kTile;
+        const uint32_t qb = sbase + x * C::kQ, kb = sbase + C::offK + (i % 3) * C::kCodes;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_ss(tmem + C::kS + x * 128, tc::smem_desc_sw128(qb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
-                     tc::smem_desc_sw128(kb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
-                     tc::idesc_f16_f32(128, 128, 0), k > 0);
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            tc::mma_ss_f8(tmem + C::kS + x * 128, tc::smem_desc_sw128(qb + t * C::kCodes + k * 32, 16, 1024),
+                          tc::smem_desc_sw128(kb + k * 32, 16, 1024), tc::idesc_e4m3_f32(128, 128, 0), t > 0 || k > 0);
         tc::commit(smem_u32(&ms.sfull[x]));
       }
       __syncwarp();
     };
     auto issue_pv = [&](int x, int i, bool first) {
       if (tc::elect_one()) {
-        const uint32_t vb = sbase + C::offV + (i & 1) * C::kTile;
+        const uint32_t vb = sbase + C::offV + (i & 1) * C::kV;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc::mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
@@ -343,11 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       PSeg sg;
       if (!wk.get(prm, sg)) continue;
       if (!wait(&ms.qready, (uint32_t)seg++ & 1u)) break;
-      if (sg.nt == 0 || !wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
+      if (sg.nt == 0 || !wait(&ms.kready[i0 % 3], (uint32_t)(i0 / 3) & 1u)) continue;
       const bool two = sg.two;
       issue_s(0, i0);
       if (two) issue_s(1, i0);
-      arrive(&ms.kfree[i0 & 1]);
+      arrive(&ms.kfree[i0 % 3]);
       for (int e = 0; e < sg.nt; ++e) {
         const int i = i0 + e;
         const bool more = e + 1 < sg.nt;
@@ -359,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         issue_pv(0, i, e == 0);
         if (!two) free_v();
         if (more) {
-          if (!wait(&ms.kready[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
+          if (!wait(&ms.kready[(i + 1) % 3], (uint32_t)((i + 1) / 3) & 1u)) break;
           issue_s(0, i + 1);
-          if (!two) arrive(&ms.kfree[(i + 1) & 1]);
+          if (!two) arrive(&ms.kfree[(i + 1) % 3]);
         } else {
           arrive(&ms.sfull[0]);  // the last P V is done
         }
@@ -371,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           free_v();
           if (more) {
             issue_s(1, i + 1);
-            arrive(&ms.kfree[(i + 1) & 1]);
+            arrive(&ms.kfree[(i + 1) % 3]);
           } else {
             arrive(&ms.sfull[1]);
           }
@@ -468,14 +483,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       named_bar_sync(2, 128);
       return fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
     };
-    uint4 kx[kPass], vx[kPass];
-    auto fetch = [&](int i, int left, uint4 (&x)[kPass], int64_t more) {  // `left`: rows of the tile that are seen
+    uint4 vx[kPass];
+    auto fetch_v = [&](int i) {
+      const int left = ms.tile[i & (kRing - 1)].left;  // rows of the tile that are seen
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int row = p * kRows + row0;
         const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
-        x[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + more, at >= 0 && row < left);
+        vx[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + vstep, at >= 0 && row < left);
       }
+    };
+    auto fetch_k = [&](int i) {  // (a group of cp.async, empty past the last tile)
+      const int left = ms.tile[i & (kRing - 1)].left;
+      if (left != INT32_MIN) {
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+          const int row = p * kRows + row0;
+          const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
+          const bool ok = at >= 0 && row < left;
+          cp_async16_if(sbase + C::offK + (i % 3) * C::kCodes + swz128(row, c),
+                        prm.pool + (ok ? at + (row & 15) * D + c * 16 : 0), ok);
+        }
+      }
+      cp_async_commit();
+      return left != INT32_MIN;
     };
     auto looked_up = [&](int i) {
       if ((i & 3) == 0 && !mbar_wait(&ms.gready[(i >> 2) & 1], (uint32_t)(i >> 3) & 1u)) failed = true;
@@ -483,17 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     // 16 codes as two 16-byte chunks of f16 of tile row `row`; the second half of a
     // row's threads stores its chunks in the other order (bank conflicts)
-    auto put = [&](uint32_t tile, int row, uint4 x, uint32_t mul, bool scaled) {
+    auto put = [&](uint32_t tile, int row, uint4 x, uint32_t mul) {
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       uint32_t h[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        h[2 * e] = e4m3x2_to_f16x2((uint16_t)w[e]);
-        h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
-        if (scaled) {
-          h[2 * e] = mul_f16x2(h[2 * e], mul);
-          h[2 * e + 1] = mul_f16x2(h[2 * e + 1], mul);
-        }
+        h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul);
+        h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul);
       }
       const uint32_t base = tile + (c / 4) * C::kPanel;
       const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
@@ -503,9 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     int last_r = -1, last_g = -1;
     float vref = 0.f, rvref = 0.f;
-    if (looked_up(0)) {
-      fetch(0, ms.tile[0].left, kx, 0);
-      fetch(0, ms.tile[0].left, vx, vstep);
+    if (looked_up(0)) {  // keys two tiles ahead, values one
+      if (fetch_k(0)) fetch_k(1);
+      fetch_v(0);
     }
     for (int i = 0; !failed; ++i) {
       const Tile& tl = ms.tile[i & (kRing - 1)];
@@ -518,15 +545,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         rvref = 1.f / vref;
       }
       if (ct == 0) ms.vref[sl] = vref;
-      if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
-        failed = true;
-        break;
-      }
-#pragma unroll
-      for (int p = 0; p < kPass; ++p) put(sbase + C::offK + b * C::kTile, p * kRows + row0, kx[p], 0, false);
+      cp_async_wait_group<1>();
       fence_proxy_async_smem();
-      mbar_arrive(&ms.kready[b]);
-      if (looked_up(i + 1)) fetch(i + 1, ms.tile[(i + 1) & (kRing - 1)].left, kx, 0);
+      mbar_arrive(&ms.kready[i % 3]);
+      const bool more = ms.tile[(i + 1) & (kRing - 1)].left != INT32_MIN;
+      if (more) {  // (past the last tile nothing is looked up)
+        if (!looked_up(i + 2)) break;
+        if (i >= 1 && !mbar_wait(&ms.kfree[(i + 2) % 3], (uint32_t)((i - 1) / 3) & 1u)) {
+          failed = true;
+          break;
+        }
+        fetch_k(i + 2);
+      } else {
+        cp_async_commit();
+      }
       if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
@@ -543,14 +575,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int p = 0; p < kPass; ++p) {
         const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
         if (vs < 0.f) ms.bad[sl] = 1;
-        put(sbase + C::offV + b * C::kTile, p * kRows + row0, vx[p], to_f16x2(f, f), true);
+        put(sbase + C::offV + b * C::kV, p * kRows + row0, vx[p], to_f16x2(f, f));
       }
       if (nan) {  // noted for the rows that see it, and cleared
         ms.any_nan[sl] = 1;
 #pragma unroll 1
         for (int k = 0; k < kPass * 16; ++k) {
           const int row = (k >> 4) * kRows + row0, e = k & 15;
-          const uint32_t a = sbase + C::offV + b * C::kTile + (c / 4) * C::kPanel + swz128(row, 2 * (c % 4) + (e >> 3)) + (e & 7) * 2;
+          const uint32_t a = sbase + C::offV + b * C::kV + (c / 4) * C::kPanel + swz128(row, 2 * (c % 4) + (e >> 3)) + (e & 7) * 2;
           if (row >= all && (lds_u16(a) & 0x7fffu) > 0x7c00u) {
             sts_u16(a, 0);
             atomicMin(&ms.nankey[sl][c * 16 + e], tl.key0 + row);
@@ -559,14 +591,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.vready[b]);
-      if (!failed) fetch(i + 1, ms.tile[(i + 1) & (kRing - 1)].left, vx, vstep);
+      if (more) fetch_v(i + 1);
     }
+    cp_async_wait_all();
   } else {
     // ================================================== q rows, softmax, output
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::kS + x * 128, to = tmem + lane_base + C::kO + x * D;
-    const int tok = x * Tm + row / G, head = row % G;
+    auto token_of = [&](int r) { return (int)((uint32_t)r * prm.per_g >> 16); };
+    const int tok = x * Tm + token_of(row);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!failed && !mbar_wait(bar, parity)) failed = true;
     };
@@ -604,36 +638,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     float rs;  // softmax scale (log2) x the row's power of two
     {
-      // the row into its place, rounded to f16 there after the rotation
-      const uint32_t tile = sbase + x * C::kTile;
-      auto place = [&](int ch) { return tile + (ch >> 3) * C::kPanel + swz128(row, ch & 7); };
-      const bf16* src = prm.q + ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
+      // Rows into the room of the first two terms, a warp its own 32, D / 8 lanes a row:
+      // 16-byte chunk c at chunk c / 2 of term c mod 2.  The terms of chunks ch and
+      // ch + D / 16 then fall where chunks that were read lie (the next are read first).
+      const uint32_t tile = sbase + x * C::kQ;
+      auto raw = [&](int r, int c) { return tile + (c & 1) * C::kCodes + swz128(r, c >> 1); };
+      constexpr int RW = 256 / D;  // rows of a step
 #pragma unroll
-      for (int ch = 0; ch < D / 8; ++ch) {
-        if (valid) cp_async16(place(ch), src + ch * 8);
-        else sts16(place(ch), make_uint4(0, 0, 0, 0));
+      for (int k = 0; k < 32 / RW; ++k) {
+        const int rr = (row & ~31) + k * RW + lane / (D / 8), ch = lane % (D / 8), in = token_of(rr), tk = x * Tm + in;
+        const bf16* src = prm.q + ((int64_t)(sg.q0 + tk) * prm.Hq + sg.g * G + rr - in * G) * D + ch * 8;
+        if (rr < Tm * G && tk < sg.toks) cp_async16(raw(rr, ch), src);
+        else sts16(raw(rr, ch), make_uint4(0, 0, 0, 0));
       }
       cp_async_wait_all();
+      __syncwarp();
       // the largest magnitude bounds the rotated ones by sqrt 2, which the power of two
       // leaves room for
       uint32_t big = 0;
 #pragma unroll 4
       for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = lds16(place(ch));
+        const uint4 v = lds16(raw(row, ch));
         big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
       }
       const uint32_t tb = max(big & 0xffffu, big >> 16) << 16;
-      const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
-      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
-      rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
+      const int ex = max((int)(tb >> 23) - 127 - 7, -119);  // largest to [128, 256), rotated below 363
+      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+      rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
       const int pos = max(sg.pos0 + tok, 0);
       const uint64_t down2 = f2_make(down, down);
+      uint4 na = lds16(raw(row, 0)), nb = lds16(raw(row, D / 16));
 #pragma unroll 2
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
-        const uint32_t pa = place(ch), pb = place(ch + D / 16);
-        const uint4 va = lds16(pa), vb = lds16(pb);
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        uint32_t a[4], b[4];
+        const uint32_t wa[4] = {na.x, na.y, na.z, na.w}, wb[4] = {nb.x, nb.y, nb.z, nb.w};
+        if (ch + 1 < D / 16) {
+          na = lds16(raw(row, ch + 1));
+          nb = lds16(raw(row, ch + 1 + D / 16));
+        }
+        uint16_t a[3][4], b[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float s0, c0, s1, c1;
@@ -643,12 +685,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
           float r0, r1;
           f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
-          a[e] = to_f16x2(r0, r1);
+          terms3(to_f16x2(r0, r1), a[0][e], a[1][e], a[2][e]);
           f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
-          b[e] = to_f16x2(r0, r1);
+          terms3(to_f16x2(r0, r1), b[0][e], b[1][e], b[2][e]);
         }
-        sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
-        sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {  // 8 bytes each, half of a chunk
+          const uint32_t base = tile + t * C::kCodes;
+          sts64(base + swz128(row, ch >> 1) + (ch & 1) * 8, (uint32_t)a[t][0] | (uint32_t)a[t][1] << 16,
+                (uint32_t)a[t][2] | (uint32_t)a[t][3] << 16);
+          sts64(base + swz128(row, D / 32 + (ch >> 1)) + (ch & 1) * 8, (uint32_t)b[t][0] | (uint32_t)b[t][1] << 16,
+                (uint32_t)b[t][2] | (uint32_t)b[t][3] << 16);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.qready);
@@ -769,32 +817,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const float vref = nt > 0 ? ms.vref[sl] : 0.f;
       if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
       const float inv = whole ? vref / sum : vref;
-      const int64_t at = ((int64_t)(sg.q0 + tok) * prm.Hq + sg.g * G + head) * D;
       float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
+      // through the row's place in q's room, so that a warp stores whole rows: all columns
+      // as bf16, or one half after the other as fp32
+      const uint32_t tile = sbase + x * C::kQ;
+      auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
+      constexpr int RW = 256 / D;
+#pragma unroll 1
+      for (int half = 0; half < (whole ? 1 : 2); ++half) {
 #pragma unroll 2
-      for (int c = 0; c < D / 16; ++c) {
-        float o[16];
-        uint32_t ov[16];
-        tc::ld16(to + c * 16, ov);  // (without a tile: whatever is there, not used)
-        tc::wait_ld();
+        for (int c = 0; c < (whole ? D / 16 : D / 32); ++c) {
+          const int col = half * (D / 2) + c * 16;
+          float o[16];
+          uint32_t ov[16];
+          tc::ld16(to + col, ov);  // (without a tile: whatever is there, not used)
+          tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = none || nt == 0 ? 0.f : __uint_as_float(ov[e]) * inv;
-        if (nan && !none) {
+          for (int e = 0; e < 16; ++e) o[e] = none || nt == 0 ? 0.f : __uint_as_float(ov[e]) * inv;
+          if (nan && !none) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (ms.nankey[sl][c * 16 + e] < lim) o[e] = __int_as_float(0x7fc00000);
+            for (int e = 0; e < 16; ++e)
+              if (ms.nankey[sl][col + e] < lim) o[e] = __int_as_float(0x7fc00000);
+          }
+          if (whole) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = float2_to_bf16x2(o[2 * e], o[2 * e + 1]);
+            sts16(place(row, 2 * c), make_uint4(w[0], w[1], w[2], w[3]));
+            sts16(place(row, 2 * c + 1), make_uint4(w[4], w[5], w[6], w[7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sts16(place(row, 4 * c + e), make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                                      __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
+          }
         }
-        if (valid && whole) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = float2_to_bf16x2(o[2 * e], o[2 * e + 1]);
-          stg16(prm.out + at + c * 16, make_uint4(w[0], w[1], w[2], w[3]));
-          stg16(prm.out + at + c * 16 + 8, make_uint4(w[4], w[5], w[6], w[7]));
-        } else if (valid) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(part + tid * D + c * 16 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < 32 / RW; ++k) {
+          const int rr = (row & ~31) + k * RW + lane / (D / 8), ch = lane % (D / 8), in = token_of(rr), tk = x * Tm + in;
+          const uint4 v = lds16(place(rr, ch));
+          if (rr < Tm * G && tk < sg.toks) {
+            if (whole) stg16(prm.out + ((int64_t)(sg.q0 + tk) * prm.Hq + sg.g * G + rr - in * G) * D + ch * 8, v);
+            else stg16(part + (x * 128 + rr) * D + half * (D / 2) + ch * 4, v);
+          }
         }
+        __syncwarp();
       }
       if (valid && !whole) {
         part[256 * D + tid] = m;
@@ -880,6 +948,7 @@ int launch(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaSt
   prm.min_new = min_new;
   prm.Tm = 128 / pb.G;
   prm.scale_log2 = pb.scale_log2;
+  prm.per_g = (65536u + pb.G - 1) / pb.G;
   for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
   constexpr int smem = (int)(PCfg<D>::offMisc + sizeof(PMisc<D>));
   static_assert(smem <= 227 * 1024, "shared memory");
