@@ -3,23 +3,24 @@
 //
 // A CTA takes one KV head and up to 256 query rows of a request: two row tiles of
 // floor(128 / G) tokens x G heads.  Its keys stream by in tiles of 128, one pass,
-//     S = q K^T        tcgen05 kind::f8f6f4: cached bytes as they are, q as the sum of
-//                      three E4M3 terms (11 bits and more), one product after the other
-//     P = exp2(S - m), O += P V       tcgen05 kind::f16, P back in TMEM
+//     S = q K^T, P = exp2(S - m), O += P V       (tcgen05 kind::f16, TMEM)
 // with m the row's running maximum, moved only when a tile's maximum passes it by
 // more than 8 (log2 units).  The warps:
 //   * 0-3, 4-7: a thread a row of each row tile, softmax and output; P goes back
 //     into S's columns as f16 (11 bits), A operand of the second product;
-//   * 8-11: cached rows into shared memory, keys by cp.async, values through registers
-//     as f16: E4M3 is exact there, and they are divided by the largest V scale of the
-//     request (exact for powers of two); K's block scales multiply the fp32 scores;
+//   * 8-11: cached rows from global memory through registers into f16 tiles, exactly;
+//     values are also divided by the largest V scale of the request (exact for powers of
+//     two), K's block scales multiply the fp32 scores;
 //   * 12: the MMAs, alternating between the row tiles, so that one's products run
 //     while the other's softmax does;
 //   * 13: block ids and scales, four tiles at a time, ahead of the copies.
-// One conversion of a value serves 256 rows: that is why rows are taken in pairs of
-// tiles.  Converting is slow here (about 16 cycles a warp's instruction): with the keys
-// converted too it was what bound the loop, which three products of keys as they are,
-// at twice the f16 rate, do not.  q is scaled by a power of two a row first.
+// One conversion of a key serves 256 rows: that is why rows are taken in pairs of tiles
+// here and cached bytes are used as they are where there are few rows (paged_decode.cu).
+// It is still most of what the loop waits for: the conversion instruction takes about
+// 16 cycles a warp, 2.0 of 2.3 us a key tile.  (Tried, chunks of 700-1024 tokens behind
+// 1000-6000: keys unconverted with q as three E4M3 terms, more tensor work, 320 us for
+// 309; keys widened by integer operations, 349 us; a warp a row tile for the MMAs,
+// 344 us.)  q is scaled by a power of two a row before its one rounding to f16.
 //
 // Work is the sequence of (request, KV head, row-tile pair) units, each worth the keys
 // it sees and a constant for its start; each SM's CTA takes an equal run of it, cut
@@ -75,11 +76,9 @@ struct PrefillParams {
 
 template <int D>
 struct PCfg {
-  static constexpr uint32_t kCodes = 128 * 128;         // bytes of a 128-row E4M3 tile (rows of 128 bytes)
-  static constexpr uint32_t kQ = 3 * kCodes;            // a row tile of q: three terms
-  static constexpr uint32_t kPanel = 128 * 128;         // 64 columns of f16
-  static constexpr uint32_t kV = 128 * D * 2;           // a V tile, f16
-  static constexpr uint32_t offK = 2 * kQ, offV = offK + 3 * kCodes, offMisc = offV + 2 * kV;
+  static constexpr uint32_t kTile = 128 * D * 2;        // bytes of a 128-row f16 tile
+  static constexpr uint32_t kPanel = 128 * 128;         // 64 columns of it
+  static constexpr uint32_t offK = 2 * kTile, offV = 4 * kTile, offMisc = 6 * kTile;
   static constexpr int kS = 0, kO = 256;  // TMEM columns: S (P) of the row tiles, O
 };
 
@@ -172,7 +171,7 @@ struct Tile {
 
 template <int D>
 struct PMisc {
-  uint64_t kready[3], kfree[3], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
+  uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
   uint32_t tmem;
   int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
   int64_t warp_sum[kThreads / 32], start_pre, total;
@@ -201,13 +200,6 @@ __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-// cp.async of 16 bytes where `ok`, else 16 zeros.
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   uint16_t v;
@@ -263,16 +255,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&ms.kready[s], 128);
+      mbar_init(&ms.kfree[s], 1);
       mbar_init(&ms.vready[s], 128);
       mbar_init(&ms.vfree[s], 1);
       mbar_init(&ms.sfull[s], 1);
       mbar_init(&ms.pfull[s], 128);
       mbar_init(&ms.gready[s], 1);
       mbar_init(&ms.gfree[s], 1);
-    }
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(&ms.kready[s], 128);
-      mbar_init(&ms.kfree[s], 1);
     }
     mbar_init(&ms.qready, 256);
     mbar_init(&ms.drain, 1);
@@ -327,20 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     auto issue_s = [&](int x, int i) {  // S of row tile x and the CTA's i-th key tile
       if (tc::elect_one()) {
-        const uint32_t qb = sbase + x * C::kQ, kb = sbase + C::offK + (i % 3) * C::kCodes;
+        const uint32_t qb = sbase + x * C::kTile, kb = sbase + C::offK + (i & 1) * C::kTile;
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            tc::mma_ss_f8(tmem + C::kS + x * 128, tc::smem_desc_sw128(qb + t * C::kCodes + k * 32, 16, 1024),
-                          tc::smem_desc_sw128(kb + k * 32, 16, 1024), tc::idesc_e4m3_f32(128, 128, 0), t > 0 || k > 0);
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ss(tmem + C::kS + x * 128, tc::smem_desc_sw128(qb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
+                     tc::smem_desc_sw128(kb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
+                     tc::idesc_f16_f32(128, 128, 0), k > 0);
         tc::commit(smem_u32(&ms.sfull[x]));
       }
       __syncwarp();
     };
     auto issue_pv = [&](int x, int i, bool first) {
       if (tc::elect_one()) {
-        const uint32_t vb = sbase + C::offV + (i & 1) * C::kV;
+        const uint32_t vb = sbase + C::offV + (i & 1) * C::kTile;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc::mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
@@ -358,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       PSeg sg;
       if (!wk.get(prm, sg)) continue;
       if (!wait(&ms.qready, (uint32_t)seg++ & 1u)) break;
-      if (sg.nt == 0 || !wait(&ms.kready[i0 % 3], (uint32_t)(i0 / 3) & 1u)) continue;
+      if (sg.nt == 0 || !wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
       const bool two = sg.two;
       issue_s(0, i0);
       if (two) issue_s(1, i0);
-      arrive(&ms.kfree[i0 % 3]);
+      arrive(&ms.kfree[i0 & 1]);
       for (int e = 0; e < sg.nt; ++e) {
         const int i = i0 + e;
         const bool more = e + 1 < sg.nt;
@@ -374,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         issue_pv(0, i, e == 0);
         if (!two) free_v();
         if (more) {
-          if (!wait(&ms.kready[(i + 1) % 3], (uint32_t)((i + 1) / 3) & 1u)) break;
+          if (!wait(&ms.kready[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
           issue_s(0, i + 1);
-          if (!two) arrive(&ms.kfree[(i + 1) % 3]);
+          if (!two) arrive(&ms.kfree[(i + 1) & 1]);
         } else {
           arrive(&ms.sfull[0]);  // the last P V is done
         }
@@ -386,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           free_v();
           if (more) {
             issue_s(1, i + 1);
-            arrive(&ms.kfree[(i + 1) % 3]);
+            arrive(&ms.kfree[(i + 1) & 1]);
           } else {
             arrive(&ms.sfull[1]);
           }
@@ -483,56 +472,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       named_bar_sync(2, 128);
       return fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
     };
-    uint4 vx[kPass];
-    auto fetch_v = [&](int i) {
+    uint4 kx[kPass], vx[kPass];
+    auto fetch = [&](int i, uint4 (&x)[kPass], int64_t more) {
       const int left = ms.tile[i & (kRing - 1)].left;  // rows of the tile that are seen
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int row = p * kRows + row0;
         const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
-        vx[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + vstep, at >= 0 && row < left);
+        x[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + more, at >= 0 && row < left);
       }
-    };
-    auto fetch_k = [&](int i) {  // (a group of cp.async, empty past the last tile)
-      const int left = ms.tile[i & (kRing - 1)].left;
-      if (left != INT32_MIN) {
-#pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-          const int row = p * kRows + row0;
-          const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
-          const bool ok = at >= 0 && row < left;
-          cp_async16_if(sbase + C::offK + (i % 3) * C::kCodes + swz128(row, c),
-                        prm.pool + (ok ? at + (row & 15) * D + c * 16 : 0), ok);
-        }
-      }
-      cp_async_commit();
-      return left != INT32_MIN;
     };
     auto looked_up = [&](int i) {
       if ((i & 3) == 0 && !mbar_wait(&ms.gready[(i >> 2) & 1], (uint32_t)(i >> 3) & 1u)) failed = true;
       return !failed;
     };
-    // 16 codes as two 16-byte chunks of f16 of tile row `row`; the second half of a
+    // 16 elements as two 16-byte chunks of f16 of tile row `row`; the second half of a
     // row's threads stores its chunks in the other order (bank conflicts)
-    auto put = [&](uint32_t tile, int row, uint4 x, uint32_t mul) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t h[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul);
-        h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul);
-      }
+    auto put = [&](uint32_t tile, int row, const uint32_t (&h)[8]) {
       const uint32_t base = tile + (c / 4) * C::kPanel;
       const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
       const int odd = (c >> 2) & 1, ch = 2 * (c % 4);
       sts16(base + swz128(row, ch + odd), odd ? hi : lo);
       sts16(base + swz128(row, ch + 1 - odd), odd ? lo : hi);
     };
+    // address of f16 element k % 16 of this thread's row of pass k / 16
+    auto element = [&](uint32_t tile, int k) {
+      return tile + (c / 4) * C::kPanel + swz128((k >> 4) * kRows + row0, 2 * (c % 4) + ((k >> 3) & 1)) + (k & 7) * 2;
+    };
     int last_r = -1, last_g = -1;
     float vref = 0.f, rvref = 0.f;
-    if (looked_up(0)) {  // keys two tiles ahead, values one
-      if (fetch_k(0)) fetch_k(1);
-      fetch_v(0);
+    if (looked_up(0)) {
+      fetch(0, kx, 0);
+      fetch(0, vx, vstep);
     }
     for (int i = 0; !failed; ++i) {
       const Tile& tl = ms.tile[i & (kRing - 1)];
@@ -545,20 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         rvref = 1.f / vref;
       }
       if (ct == 0) ms.vref[sl] = vref;
-      cp_async_wait_group<1>();
-      fence_proxy_async_smem();
-      mbar_arrive(&ms.kready[i % 3]);
-      const bool more = ms.tile[(i + 1) & (kRing - 1)].left != INT32_MIN;
-      if (more) {  // (past the last tile nothing is looked up)
-        if (!looked_up(i + 2)) break;
-        if (i >= 1 && !mbar_wait(&ms.kfree[(i + 2) % 3], (uint32_t)((i - 1) / 3) & 1u)) {
-          failed = true;
-          break;
-        }
-        fetch_k(i + 2);
-      } else {
-        cp_async_commit();
+      if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+        failed = true;
+        break;
       }
+      const uint32_t ktile = sbase + C::offK + b * C::kTile, vtile = sbase + C::offV + b * C::kTile;
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        const uint32_t w[4] = {kx[p].x, kx[p].y, kx[p].z, kx[p].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[2 * e] = e4m3x2_to_f16x2((uint16_t)w[e]);
+          h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
+        }
+        put(ktile, p * kRows + row0, h);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ms.kready[b]);
+      if (looked_up(i + 1)) fetch(i + 1, kx, 0);
       if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
@@ -575,14 +551,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int p = 0; p < kPass; ++p) {
         const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
         if (vs < 0.f) ms.bad[sl] = 1;
-        put(sbase + C::offV + b * C::kV, p * kRows + row0, vx[p], to_f16x2(f, f));
+        const uint32_t w[4] = {vx[p].x, vx[p].y, vx[p].z, vx[p].w}, mul = to_f16x2(f, f);
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul);
+          h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul);
+        }
+        put(vtile, p * kRows + row0, h);
       }
       if (nan) {  // noted for the rows that see it, and cleared
         ms.any_nan[sl] = 1;
 #pragma unroll 1
         for (int k = 0; k < kPass * 16; ++k) {
           const int row = (k >> 4) * kRows + row0, e = k & 15;
-          const uint32_t a = sbase + C::offV + b * C::kV + (c / 4) * C::kPanel + swz128(row, 2 * (c % 4) + (e >> 3)) + (e & 7) * 2;
+          const uint32_t a = element(vtile, k);
           if (row >= all && (lds_u16(a) & 0x7fffu) > 0x7c00u) {
             sts_u16(a, 0);
             atomicMin(&ms.nankey[sl][c * 16 + e], tl.key0 + row);
@@ -591,9 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.vready[b]);
-      if (more) fetch_v(i + 1);
+      if (!failed) fetch(i + 1, vx, vstep);
     }
-    cp_async_wait_all();
   } else {
     // ================================================== q rows, softmax, output
     const int x = warp >> 2, row = tid & 127;
@@ -638,18 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     float rs;  // softmax scale (log2) x the row's power of two
     {
-      // Rows into the room of the first two terms, a warp its own 32, D / 8 lanes a row:
-      // 16-byte chunk c at chunk c / 2 of term c mod 2.  The terms of chunks ch and
-      // ch + D / 16 then fall where chunks that were read lie (the next are read first).
-      const uint32_t tile = sbase + x * C::kQ;
-      auto raw = [&](int r, int c) { return tile + (c & 1) * C::kCodes + swz128(r, c >> 1); };
+      // rows into their places, a warp its own 32, D / 8 lanes a row; rounded to f16
+      // there after the rotation
+      const uint32_t tile = sbase + x * C::kTile;
+      auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
       constexpr int RW = 256 / D;  // rows of a step
 #pragma unroll
       for (int k = 0; k < 32 / RW; ++k) {
         const int rr = (row & ~31) + k * RW + lane / (D / 8), ch = lane % (D / 8), in = token_of(rr), tk = x * Tm + in;
         const bf16* src = prm.q + ((int64_t)(sg.q0 + tk) * prm.Hq + sg.g * G + rr - in * G) * D + ch * 8;
-        if (rr < Tm * G && tk < sg.toks) cp_async16(raw(rr, ch), src);
-        else sts16(raw(rr, ch), make_uint4(0, 0, 0, 0));
+        if (rr < Tm * G && tk < sg.toks) cp_async16(place(rr, ch), src);
+        else sts16(place(rr, ch), make_uint4(0, 0, 0, 0));
       }
       cp_async_wait_all();
       __syncwarp();
@@ -658,24 +639,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       uint32_t big = 0;
 #pragma unroll 4
       for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = lds16(raw(row, ch));
+        const uint4 v = lds16(place(row, ch));
         big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
       }
       const uint32_t tb = max(big & 0xffffu, big >> 16) << 16;
-      const int ex = max((int)(tb >> 23) - 127 - 7, -119);  // largest to [128, 256), rotated below 363
-      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-      rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000) : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
+      const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
+      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
+      rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                             : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
       const int pos = max(sg.pos0 + tok, 0);
       const uint64_t down2 = f2_make(down, down);
-      uint4 na = lds16(raw(row, 0)), nb = lds16(raw(row, D / 16));
 #pragma unroll 2
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
-        const uint32_t wa[4] = {na.x, na.y, na.z, na.w}, wb[4] = {nb.x, nb.y, nb.z, nb.w};
-        if (ch + 1 < D / 16) {
-          na = lds16(raw(row, ch + 1));
-          nb = lds16(raw(row, ch + 1 + D / 16));
-        }
-        uint16_t a[3][4], b[3][4];
+        const uint32_t pa = place(row, ch), pb = place(row, ch + D / 16);
+        const uint4 va = lds16(pa), vb = lds16(pb);
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        uint32_t a[4], b[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float s0, c0, s1, c1;
@@ -685,18 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
           float r0, r1;
           f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
-          terms3(to_f16x2(r0, r1), a[0][e], a[1][e], a[2][e]);
+          a[e] = to_f16x2(r0, r1);
           f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
-          terms3(to_f16x2(r0, r1), b[0][e], b[1][e], b[2][e]);
+          b[e] = to_f16x2(r0, r1);
         }
-#pragma unroll
-        for (int t = 0; t < 3; ++t) {  // 8 bytes each, half of a chunk
-          const uint32_t base = tile + t * C::kCodes;
-          sts64(base + swz128(row, ch >> 1) + (ch & 1) * 8, (uint32_t)a[t][0] | (uint32_t)a[t][1] << 16,
-                (uint32_t)a[t][2] | (uint32_t)a[t][3] << 16);
-          sts64(base + swz128(row, D / 32 + (ch >> 1)) + (ch & 1) * 8, (uint32_t)b[t][0] | (uint32_t)b[t][1] << 16,
-                (uint32_t)b[t][2] | (uint32_t)b[t][3] << 16);
-        }
+        sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
+        sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
       }
       fence_proxy_async_smem();
       mbar_arrive(&ms.qready);
@@ -820,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
       // through the row's place in q's room, so that a warp stores whole rows: all columns
       // as bf16, or one half after the other as fp32
-      const uint32_t tile = sbase + x * C::kQ;
+      const uint32_t tile = sbase + x * C::kTile;
       auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
       constexpr int RW = 256 / D;
 #pragma unroll 1
