@@ -8,11 +8,13 @@
 //     S^T = K q^T      tcgen05 kind::f8f6f4, keys as M, the query rows as N
 //     O^T = V^T P^T    the V tile read transposed (M contiguous), P as N
 // so no cached element is ever converted.  q and P keep their precision as sums
-// of three E4M3 terms, x = x0 + x1 / 16 + x2 / 256 (each the rounded remainder of
-// the last, together 11 bits or more), side by side as columns of N: the few
-// query rows leave N room that costs nothing.  q is scaled by a power of two a
-// row, so its size does not matter; the K scale of a key's block multiplies its
-// fp32 scores, the V scale over the largest met so far its weights.
+// of three E4M3 terms, each the rounded remainder of the last, together 11 bits or
+// more.  q's are added in TMEM, one product after the other: q is scaled by a power
+// of two a row, its largest value to 128 and more, and the terms reach 2^-17 of that.
+// P's small weights matter more (they are many), so its terms are kept apart,
+// p0 + p1 / 16 + p2 / 256, side by side as columns of N: the few query rows leave N
+// room that costs nothing.  The K scale of a key's block multiplies its fp32 scores,
+// the V scale over the largest met so far its weights.
 //
 // A softmax thread owns one tile row (TMEM lane): its scores for all query rows,
 // the running maximum m of each (the same in all threads), its own part of the
@@ -72,10 +74,10 @@ struct Cfg {
   static constexpr int KT = 128 * KPR;          // keys a tile
   static constexpr int ROWS = 8 * CH;           // query rows at most
   static constexpr int NPB = CH <= 2 ? 2 : 1;   // P buffers (q tiles: two, one made ahead)
-  static constexpr int SP = (24 * CH + 15) & ~15;  // S columns a parity
+  static constexpr int SP = (8 * CH + 15) & ~15;   // S columns a parity
   static constexpr int OC = (KPR * 24 * CH + 15) & ~15;  // O columns
   static constexpr int SB = 2 * KPR * SP + OC <= 256 ? 2 : 1;  // S buffers
-  static constexpr uint32_t QB = 3072 * CH, PB = KPR * 3072 * CH;
+  static constexpr uint32_t QT = 1024 * CH, QB = 3 * QT, PB = KPR * 3072 * CH;
   static constexpr int NK = D == 128 && CH <= 2 ? 3 : D == 64 && CH == 1 ? 3 : 2;
   static constexpr int NV = D == 128 && CH == 1 ? 3 : 2;
   static constexpr uint32_t kO = SB * KPR * SP;  // O's first TMEM column
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         break;
       }
       nch = (ms.seg[qs].rows + 7) >> 3;
-      const uint32_t id = tc::idesc_e4m3_f32(128, (24 * nch + 15) & ~15, 0);
+      const uint32_t id = tc::idesc_e4m3_f32(128, (8 * nch + 15) & ~15, 0);
       const uint32_t qb = sbase + C::offQ + qs * C::QB;
       for (int kt = kt0; kt < kt1; ++kt) {
         const int ks = i % NK, sb = i % SB;
@@ -412,9 +414,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int p = 0; p < KPR; ++p)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              tc::mma_ss_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
-                     tc::smem_desc_sw128(qb + k * 32, 16, 1024), id, k > 0);
+            for (int t = 0; t < 3; ++t)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                tc::mma_ss_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
+                              tc::smem_desc_sw128(qb + t * C::QT + k * 32, 16, 1024), id, t > 0 || k > 0);
           tc::commit(smem_u32(&ms.sfull[sb]));
           tc::commit(smem_u32(&ms.kfree[ks]));
           if (kt == kt1 - 1) tc::commit(smem_u32(&ms.qfree[qs]));
@@ -490,18 +494,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           ms.rs[qs][row] = !real                ? 0.f
                            : tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
                                                : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
-        const uint32_t base = sbase + C::offQ + qs * C::QB + (row >> 3) * 3072 + (row & 7) * 128;
+        const uint32_t base = sbase + C::offQ + qs * C::QB + row * 128;
         const uint32_t at = (uint32_t)(l * 8) ^ ((row & 7) << 4), bt = (uint32_t)(D / 2 + l * 8) ^ ((row & 7) << 4);
         uint16_t ta[3][4], tb2[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          split3(to_f16x2(a[2 * e] * down, a[2 * e + 1] * down), ta[0][e], ta[1][e], ta[2][e]);
-          split3(to_f16x2(b[2 * e] * down, b[2 * e + 1] * down), tb2[0][e], tb2[1][e], tb2[2][e]);
+          terms3(to_f16x2(a[2 * e] * down, a[2 * e + 1] * down), ta[0][e], ta[1][e], ta[2][e]);
+          terms3(to_f16x2(b[2 * e] * down, b[2 * e + 1] * down), tb2[0][e], tb2[1][e], tb2[2][e]);
         }
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
-          sts64(base + s * 1024 + at, (uint32_t)ta[s][0] | (uint32_t)ta[s][1] << 16, (uint32_t)ta[s][2] | (uint32_t)ta[s][3] << 16);
-          sts64(base + s * 1024 + bt, (uint32_t)tb2[s][0] | (uint32_t)tb2[s][1] << 16, (uint32_t)tb2[s][2] | (uint32_t)tb2[s][3] << 16);
+          sts64(base + s * C::QT + at, (uint32_t)ta[s][0] | (uint32_t)ta[s][1] << 16, (uint32_t)ta[s][2] | (uint32_t)ta[s][3] << 16);
+          sts64(base + s * C::QT + bt, (uint32_t)tb2[s][0] | (uint32_t)tb2[s][1] << 16, (uint32_t)tb2[s][2] | (uint32_t)tb2[s][3] << 16);
         }
       }
       if (warp == 6 && lane == 0) ms.seg[qs] = Seg{wk.r, wk.g, rows, q0, pos0, max(kv, 0), kt0, kt1, wk.nt, 0};
@@ -550,11 +554,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (c < nch) {
-            uint32_t v[KPR][24];
+            uint32_t v[KPR][8];
 #pragma unroll
-            for (int p = 0; p < KPR; ++p)
-#pragma unroll
-              for (int k = 0; k < 3; ++k) ld8(tmem + lane_base + (sb * KPR + p) * C::SP + c * 24 + k * 8, v[p] + k * 8);
+            for (int p = 0; p < KPR; ++p) ld8(tmem + lane_base + (sb * KPR + p) * C::SP + c * 8, v[p]);
             tc::wait_ld();
             const float4* rp = reinterpret_cast<const float4*>(&ms.rs[qs][c * 8]);
             const float4 ra = rp[0], rb = rp[1];
@@ -563,10 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int p = 0; p < KPR; ++p)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                float x = __uint_as_float(v[p][j]);
-                x = fmaf(__uint_as_float(v[p][8 + j]), 0.0625f, x);
-                x = fmaf(__uint_as_float(v[p][16 + j]), 0.00390625f, x);
-                x *= ks * rs[j];
+                float x = __uint_as_float(v[p][j]) * (ks * rs[j]);
                 if (edge && key0 + p > sg.pos0 + token_of(c * 8 + j)) x = -INFINITY;
                 over |= x - m[c * 8 + j] > kSlack;
                 s[(c * KPR + p) * 8 + j] = x;
@@ -801,19 +800,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 // takes a row: all parts' maxima and sums at once, then their O with the final
 // weights, so that no load waits for another's result; the order of the sums is
 // fixed.
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kJoinHeld = 2048;
+constexpr int kJoinThreads = 1024, kJoinHeld = 2048;
 template <int D, int CH>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ DecodeParams prm) {
   constexpr int ROWS = Cfg<D, CH>::ROWS, E = D / 32;  // E elements a lane
   __shared__ float2 held[kJoinHeld];                  // [row][part]: maximum and sum
-  __shared__ float acc[kJoinWarps][D];
+  __shared__ float acc[kJoinThreads / 32][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x + 1;
-  const int G = prm.rq.G;
+  const int G = prm.rq.G, threads = blockDim.x, warps = threads / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinUnit u = prm.join[w];
   if (u.parts == 0) return;
-  int wpr = kJoinWarps;  // warps a row
-  while (wpr > 1 && kJoinWarps / wpr < u.rows) wpr >>= 1;
+  int wpr = warps;  // warps a row
+  while (wpr > 1 && warps / wpr < u.rows) wpr >>= 1;
   const int sub = warp % wpr, q = warp / wpr;
   const bool mine = q < u.rows;
   auto part = [&](int v) {
@@ -826,7 +825,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   const int most = kJoinHeld / u.rows;
   for (int v0 = 0; v0 < u.parts; v0 += most) {
     const int nv = min(most, u.parts - v0);
-    for (int i = tid; i < nv * u.rows; i += kJoinThreads) {
+    for (int i = tid; i < nv * u.rows; i += threads) {
       const int v = i / u.rows, row = i - v * u.rows;
       const float* p = part(v0 + v) + ROWS * D + row;
       held[row * most + v] = make_float2(p[0], p[ROWS]);
@@ -944,7 +943,9 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   // the combine's CTAs may start, and scan the lengths, while the last tiles run
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid - 1);
-  cfg.blockDim = dim3(kJoinThreads);
+  // a warp a row; all there may be where units are few and their parts many
+  const bool many = (int64_t)pb.B * pb.Hkv * 4 < grid;
+  cfg.blockDim = dim3(many ? kJoinThreads : 32 * Cfg<D, CH>::ROWS);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -53,9 +53,9 @@ constexpr int kStartCost = 256;       // keys that a unit's start is worth
 // What the join needs of a unit that crosses CTAs, left by the CTA whose run starts in
 // it first (cost 0: nothing to join there).
 struct JoinRun {
-  int64_t at, total;  // the unit's first place in the sequence of costs, the sequence's end
+  int64_t at, share, rest;  // the unit's first place in the sequence of costs; total / CTAs, total % CTAs
   int cost, tiles, q0, toks, pos0, g;
-  int pad[6];
+  int pad[4];
 };
 static_assert(sizeof(JoinRun) == 64, "the parts behind the headers are read 16 bytes at a time");
 
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (x0 > wk.unit() && cut(total, me - 1, W) <= wk.unit()) {
       PSeg s;
       wk.get(prm, s);
-      j = JoinRun{wk.unit(), total, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {}};
+      j = JoinRun{wk.unit(), total / W, total % W, wk.cost(), (s.kend + kKT - 1) / kKT, s.q0, s.toks, s.pos0, s.g, {}};
     }
     prm.join[me] = j;
   }
@@ -856,39 +856,71 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   }
 }
 
-// Adds up the parts of the units that cross CTAs, a warp a row: O, m and sum in key
-// order.  Block y takes 8 rows of the unit that CTA blockIdx.x + 1 left a header for.
+// Adds up the parts of the units that cross CTAs, a warp four rows at a time: O, m and
+// sum in key order.  Block y takes 32 rows of the unit that CTA blockIdx.x + 1 left a
+// header for.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ PrefillParams prm, int W) {
+  constexpr int R = 4, E = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = blockIdx.x + 1;
-  const int G = prm.rq.G, Tm = prm.Tm, row = blockIdx.y * 8 + warp, x = row >> 7, in = row & 127;
-  const int tok = x * Tm + in / G, head = in % G;
+  const int G = prm.rq.G, Tm = prm.Tm, row0 = blockIdx.y * 32 + warp * R, x = row0 >> 7;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinRun u = prm.join[w];
-  if (u.cost == 0 || in >= Tm * G || tok >= u.toks) return;
-  float m = kNone, sum = 0.f, o[D / 32];
-  bool bad = false;
+  if (u.cost == 0 || (row0 & 127) >= Tm * G) return;
+  float m[R], sum[R], o[R][E];
+  bool bad[R];  // (rows past the unit's hold anything: each by itself)
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  for (int v = w - 1; v < W; ++v) {
-    const int64_t o0 = max(cut(u.total, v, W) - u.at, (int64_t)0), o1 = cut(u.total, v + 1, W) - u.at;
-    if (o0 >= u.cost) break;
-    const int k0 = (int)(u.tiles * o0 / u.cost), k1 = o1 >= u.cost ? u.tiles : (int)(u.tiles * o1 / u.cost);
-    if (k0 == 0 && k1 == u.tiles) return;  // one CTA had all of its tiles
-    if (k0 == k1) continue;
-    const float* p = prm.parts + (int64_t)(2 * v + (o0 > 0 ? 0 : 1)) * 256 * (D + 2);
-    const float pm = p[256 * D + row], ps = p[256 * (D + 1) + row], top = fmaxf(m, pm), f0 = exp2f(m - top), f1 = exp2f(pm - top);
-    bad |= ps < 0.f;
-    m = top;
-    sum = sum * f0 + ps * f1;
+  for (int k = 0; k < R; ++k) {
+    bad[k] = false;
+    m[k] = kNone;
+    sum[k] = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f0 + f1 * p[row * D + lane + 32 * e];
+    for (int e = 0; e < E; ++e) o[k][e] = 0.f;
   }
-  const bool none = bad || u.pos0 + tok < 0;
-  if (lane == 0 && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-  bf16* dst = prm.out + ((int64_t)(u.q0 + tok) * prm.Hq + u.g * G + head) * D + lane;
+  auto first = [&](int v) { return u.share * v + min((int64_t)v, u.rest) - u.at; };  // CTA v's, from the unit's
+  auto tile = [&](int64_t at) { return at >= u.cost ? u.tiles : (int)(u.tiles * max(at, (int64_t)0) / u.cost); };
+  int k0 = 0;
+  for (int v = w - 1; v < W && first(v) < u.cost; ++v) {
+    const int k1 = tile(first(v + 1));
+    if (k0 == 0 && k1 == u.tiles) return;  // one CTA had all of its tiles
+    if (k0 < k1) {
+      const float* p = prm.parts + (int64_t)(2 * v + (first(v) > 0 ? 0 : 1)) * 256 * (D + 2);
+      float pm[R], ps[R], po[R][E];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) dst[32 * e] = __float2bfloat16(none ? 0.f : o[e] / sum);
+      for (int k = 0; k < R; ++k) {
+        pm[k] = p[256 * D + row0 + k];
+        ps[k] = p[256 * (D + 1) + row0 + k];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(p + (row0 + k) * D + lane * E + e);
+          po[k][e] = y.x;
+          po[k][e + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float top = fmaxf(m[k], pm[k]), f0 = exp2f(m[k] - top), f1 = exp2f(pm[k] - top);
+        bad[k] |= ps[k] < 0.f;
+        m[k] = top;
+        sum[k] = sum[k] * f0 + ps[k] * f1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[k][e] = o[k][e] * f0 + f1 * po[k][e];
+      }
+    }
+    k0 = k1;
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int in = (row0 & 127) + k, tok = x * Tm + in / G;
+    if (in >= Tm * G || tok >= u.toks) continue;
+    const bool none = bad[k] || u.pos0 + tok < 0;
+    if (lane == 0 && !none && !(sum[k] <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+    const float inv = 1.f / sum[k];
+    bf16* dst = prm.out + ((int64_t)(u.q0 + tok) * prm.Hq + u.g * G + in % G) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = none ? 0u : float2_to_bf16x2(o[k][e] * inv, o[k][e + 1] * inv);
+  }
 }
 
 // CTAs: one an SM, fewer where the token rows and the table cannot hold that many key
@@ -931,7 +963,7 @@ int launch(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaSt
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
   if (grid == 1) return GIST_ATTN_OK;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid - 1, 32);
+  cfg.gridDim = dim3((unsigned)grid - 1, 8);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
