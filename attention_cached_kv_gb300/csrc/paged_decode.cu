@@ -101,7 +101,7 @@ struct Misc {
   Seg seg[2];
   alignas(16) float rs[2][C::ROWS];  // softmax scale (log2) x q's power of two, by row
   alignas(16) float wmax[4][C::ROWS];  // by warp: a tile's maxima, a segment's sums
-  alignas(16) float mrow[C::ROWS];
+  alignas(16) float mrow[4][C::ROWS];  // running maxima, a copy a warp
   float ksc[3][16], vsc[3][16];  // scales of a tile's boxes
   float wv[4];
   alignas(16)
@@ -536,10 +536,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const Seg sg = ms.seg[qs];
       const int nch = (sg.rows + 7) >> 3;
-      float m[ROWS], l[ROWS];
+      // running maxima: registers, or, where scores and sums fill those, a warp's own
+      // copy in shared memory
+      constexpr bool kHeld = CH * KPR < 4;
+      float m[kHeld ? ROWS : 1], l[ROWS];
+      auto maxima = [&](int c, float (&v)[8]) {
+        if constexpr (kHeld) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = m[c * 8 + j];
+        } else {
+          const float4* at = reinterpret_cast<const float4*>(&ms.mrow[warp][c * 8]);
+          const float4 a = at[0], b = at[1];
+          v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+      };
       float vref = 0.f, vmul = 0.f;
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j) m[j] = kNone, l[j] = 0.f;
+      for (int j = 0; j < ROWS; ++j) l[j] = 0.f;
+      if constexpr (kHeld) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) m[j] = kNone;
+      } else {
+        if (lane < ROWS) ms.mrow[warp][lane] = kNone;
+        __syncwarp();
+      }
       for (int kt = kt0; kt < kt1; ++kt, ++i) {
         const int sb = i % SB, vs = i % NV, pb = i % NPB;
         const int key0 = kt * KT + t * KPR;  // this thread's first key
@@ -561,13 +581,15 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float4* rp = reinterpret_cast<const float4*>(&ms.rs[qs][c * 8]);
             const float4 ra = rp[0], rb = rp[1];
             const float rs[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+            float mv[8];
+            maxima(c, mv);
 #pragma unroll
             for (int p = 0; p < KPR; ++p)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 float x = __uint_as_float(v[p][j]) * (ks * rs[j]);
                 if (edge && key0 + p > sg.pos0 + token_of(c * 8 + j)) x = -INFINITY;
-                over |= x - m[c * 8 + j] > kSlack;
+                over |= x - mv[j] > kSlack;
                 s[(c * KPR + p) * 8 + j] = x;
               }
           }
@@ -602,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int c = 0; c < CH; ++c)
             if (c < nch) {
-              float f[8];
+              float f[8], mv[8];
+              maxima(c, mv);
 #pragma unroll
               for (int j = 0; j < 8; j += 4) {
                 float4 w[4];
@@ -615,12 +638,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int q = c * 8 + j + k;
-                  const float mn = fmaxf(m[q], top[k]);
-                  f[j + k] = ex2_approx(m[q] - mn);
+                  const float mn = fmaxf(mv[j + k], top[k]);
+                  f[j + k] = ex2_approx(mv[j + k] - mn);
                   l[q] *= f[j + k];
-                  m[q] = mn;
+                  mv[j + k] = mn;
                   f[j + k] *= fv;
                 }
+              }
+              if constexpr (kHeld) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[c * 8 + j] = mv[j];
+              } else {
+                __syncwarp();  // (all lanes have read the old ones)
+                if (lane == 0) {
+                  float4* at = reinterpret_cast<float4*>(&ms.mrow[warp][c * 8]);
+                  at[0] = make_float4(mv[0], mv[1], mv[2], mv[3]);
+                  at[1] = make_float4(mv[4], mv[5], mv[6], mv[7]);
+                }
+                __syncwarp();
               }
               if (kt > kt0) {
 #pragma unroll
@@ -646,14 +681,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int c = 0; c < CH; ++c)
           if (c < nch) {
+            float mv[8];
+            maxima(c, mv);
 #pragma unroll
             for (int p = 0; p < KPR; ++p) {
               const uint32_t at = pb * C::PB + (p * 3 * nch + c * 3) * 1024;
 #pragma unroll
               for (int j = 0; j < 8; j += 2) {
                 const int q = c * 8 + j;
-                const float p0 = ex2_approx(s[(c * KPR + p) * 8 + j] - m[q]);
-                const float p1 = ex2_approx(s[(c * KPR + p) * 8 + j + 1] - m[q + 1]);
+                const float p0 = ex2_approx(s[(c * KPR + p) * 8 + j] - mv[j]);
+                const float p1 = ex2_approx(s[(c * KPR + p) * 8 + j + 1] - mv[j + 1]);
                 l[q] += p0;
                 l[q + 1] += p1;
                 uint16_t u[3];
@@ -734,10 +771,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           y += __shfl_xor_sync(0xffffffffu, y, 2);
           y += __shfl_xor_sync(0xffffffffu, y, 1);
           if ((lane & 3) == 0) ms.wmax[warp][c * 8 + (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1)] = y;
-          if (t == 0) {
-            float4* at = reinterpret_cast<float4*>(&ms.mrow[c * 8]);
-            at[0] = make_float4(m[c * 8], m[c * 8 + 1], m[c * 8 + 2], m[c * 8 + 3]);
-            at[1] = make_float4(m[c * 8 + 4], m[c * 8 + 5], m[c * 8 + 6], m[c * 8 + 7]);
+          if (kHeld && t == 0) {
+            float mv[8];
+            maxima(c, mv);
+            float4* at = reinterpret_cast<float4*>(&ms.mrow[0][c * 8]);
+            at[0] = make_float4(mv[0], mv[1], mv[2], mv[3]);
+            at[1] = make_float4(mv[4], mv[5], mv[6], mv[7]);
           }
         }
       tc::fence_before_sync();
@@ -776,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(part + q * D + lane * E + e) = make_float2(x[e], x[e + 1]);
           if (lane == 0) {
-            part[ROWS * D + q] = ms.mrow[q];
+            part[ROWS * D + q] = ms.mrow[0][q];
             part[ROWS * D + ROWS + q] = bad ? -1.f : sum;
           }
         }
