@@ -65,6 +65,7 @@ struct DecodeParams {
   int box_rows, box_shift;  // tile rows of one TMA box: 2^box_shift
   float scale_log2;
   uint32_t per_g;  // 2^16 / G rounded up: j / G = j per_g >> 16 for the rows there are
+  int join_rows;   // rows that a block of the join takes
   uint64_t turn[64];
 };
 
@@ -657,7 +658,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 __syncwarp();
               }
-              if (kt > kt0) {
+              bool moved = false;  // (the same in all threads)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) moved |= f[j] != 1.f;
+              if (kt > kt0 && moved) {
 #pragma unroll
                 for (int p = 0; p < KPR; ++p) {
                   const uint32_t a = tmem + lane_base + C::kO + p * 24 * nch + c * 24;
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // takes a row: all parts' maxima and sums at once, then their O with the final
 // weights, so that no load waits for another's result; the order of the sums is
 // fixed.
-constexpr int kJoinThreads = 1024, kJoinHeld = 2048;
+constexpr int kJoinThreads = 32 * 32, kJoinHeld = 2048;
 template <int D, int CH>
 __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ DecodeParams prm) {
   constexpr int ROWS = Cfg<D, CH>::ROWS, E = D / 32;  // E elements a lane
@@ -847,13 +851,15 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   __shared__ float acc[kJoinThreads / 32][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = blockIdx.x + 1;
   const int G = prm.rq.G, threads = blockDim.x, warps = threads / 32;
+  const int row0 = blockIdx.y * prm.join_rows;  // this block's rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinUnit u = prm.join[w];
-  if (u.parts == 0) return;
+  const int rows = min(u.rows - row0, prm.join_rows);
+  if (u.parts == 0 || rows <= 0) return;
   int wpr = warps;  // warps a row
-  while (wpr > 1 && warps / wpr < u.rows) wpr >>= 1;
-  const int sub = warp % wpr, q = warp / wpr;
-  const bool mine = q < u.rows;
+  while (wpr > 1 && warps / wpr < rows) wpr >>= 1;
+  const int sub = warp % wpr, local = warp / wpr, q = row0 + local;
+  const bool mine = local < rows;
   auto part = [&](int v) {
     return prm.parts + (int64_t)(2 * (w - 1 + v) + (v == 0 ? u.second : 0)) * ROWS * (D + 2);
   };
@@ -861,17 +867,17 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
   bool bad = false;
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const int most = kJoinHeld / u.rows;
+  const int most = kJoinHeld / rows;
   for (int v0 = 0; v0 < u.parts; v0 += most) {
     const int nv = min(most, u.parts - v0);
-    for (int i = tid; i < nv * u.rows; i += threads) {
-      const int v = i / u.rows, row = i - v * u.rows;
-      const float* p = part(v0 + v) + ROWS * D + row;
+    for (int i = tid; i < nv * rows; i += threads) {
+      const int v = i / rows, row = i - v * rows;
+      const float* p = part(v0 + v) + ROWS * D + row0 + row;
       held[row * most + v] = make_float2(p[0], p[ROWS]);
     }
     __syncthreads();
     if (mine) {
-      const float2* h = held + q * most;
+      const float2* h = held + local * most;
       float top = kNone;
       for (int v = lane; v < nv; v += 32) top = fmaxf(top, h[v].x);
 #pragma unroll
@@ -969,6 +975,10 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   prm.box_shift = 7;
   while (plane_rows & ((1 << prm.box_shift) - 1)) --prm.box_shift;
   prm.box_rows = 1 << prm.box_shift;
+  // The join: a block a unit, a warp a row; where units are few their parts are many, and
+  // several warps take a row, blocks of eight warps a row or four.
+  const bool many = (int64_t)pb.B * pb.Hkv * 4 < grid;
+  prm.join_rows = !many ? Cfg<D, CH>::ROWS : CH == 1 ? 1 : 4;
   alignas(64) CUtensorMap tm;
   const int rc = encode_pool(&tm, pb, prm.box_rows);
   if (rc != GIST_ATTN_OK) return rc;
@@ -981,10 +991,8 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   if (grid == 1) return GIST_ATTN_OK;
   // the combine's CTAs may start, and scan the lengths, while the last tiles run
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid - 1);
-  // a warp a row; all there may be where units are few and their parts many
-  const bool many = (int64_t)pb.B * pb.Hkv * 4 < grid;
-  cfg.blockDim = dim3(many ? kJoinThreads : 32 * Cfg<D, CH>::ROWS);
+  cfg.gridDim = dim3((unsigned)grid - 1, many ? (Cfg<D, CH>::ROWS + prm.join_rows - 1) / prm.join_rows : 1);
+  cfg.blockDim = dim3(many ? 256 : 32 * Cfg<D, CH>::ROWS);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
