@@ -46,6 +46,9 @@ constexpr uint32_t kStage = 128 * 128;  // bytes of a K or V tile
 constexpr float kNone = -3.0e38f;       // running maximum before any key
 constexpr float kSlack = 2.f;           // log2 units a score may pass it by
 constexpr float kPUnit = 64.f;          // P's scale into E4M3
+// Short caches: two to four tiles one after the other (about 1.5 us each) against a
+// second launch and its loads (2 us on the GPU, 3 to 4 on the host).
+constexpr int kWhole = 4;
 
 // What the join needs of a unit that crosses CTAs, left by the CTA in whose run the
 // unit's second part begins (parts 0: nothing to join there).
@@ -66,6 +69,7 @@ struct DecodeParams {
   float scale_log2;
   uint32_t per_g;  // 2^16 / G rounded up: j / G = j per_g >> 16 for the rows there are
   int join_rows;   // rows that a block of the join takes
+  int whole;       // runs are of whole units
   uint64_t turn[64];
 };
 
@@ -175,31 +179,33 @@ __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
   return r;
 }
 
-// The walk over a CTA's segments; every role makes it for itself.
+// The walk over a CTA's segments; every role makes it for itself.  A unit counts for
+// its tiles, or for one where runs are of whole units.
 template <int KT>
 struct Walk {
-  int x, x_end, r, pre, g, nt;
-  __device__ void init(const Requests& rq, int x0, int x1, int r0, int pre0) {
+  int x, x_end, r, pre, g, nt, whole;
+  __device__ int count() const { return whole ? 1 : nt; }
+  __device__ int unit(const Requests& rq) const { return rq.Hkv * pre + g * count(); }
+  __device__ void init(const Requests& rq, int x0, int x1, int r0, int pre0, int whole_units) {
     x = x0;
     x_end = x1;
     r = r0;
     pre = pre0;
+    whole = whole_units;
     nt = rq.tiles<KT>(r);
-    g = (x - rq.Hkv * pre) / nt;
+    g = (x - rq.Hkv * pre) / count();
   }
   __device__ bool more() const { return x < x_end; }
   __device__ void get(int& kt0, int& kt1, const Requests& rq) const {
-    const int a = rq.Hkv * pre + g * nt;
-    kt0 = x - a;
-    kt1 = min(nt, x_end - a);
+    kt0 = whole ? 0 : x - unit(rq);
+    kt1 = whole ? nt : min(nt, x_end - unit(rq));
   }
   __device__ void next(const Requests& rq) {
-    const int a = rq.Hkv * pre + g * nt;
-    x = min(a + nt, x_end);
+    x = min(unit(rq) + count(), x_end);
     if (x >= x_end) return;
     if (++g == rq.Hkv) {
       g = 0;
-      pre += nt;
+      pre += count();
       do nt = ++r < rq.B ? rq.tiles<KT>(r) : 0;
       while (nt == 0 && r < rq.B);
       if (r >= rq.B) x = x_end;  // (lengths that changed under the kernel)
@@ -262,7 +268,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc::fence_before_sync();
   bool odd = false;
   scan_requests<kThreads>(  // (its barriers publish the above too)
-      rq.B, [&](int r) { return rq.tiles<KT>(r, &odd); }, ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
+      rq.B,
+      [&](int r) {
+        const int n = rq.tiles<KT>(r, &odd);
+        return prm.whole ? min(n, 1) : n;
+      },
+      ms.warp_sum, &ms.start_r, &ms.start_pre, &ms.total,
       [&](int all) { return Share(all * rq.Hkv, W).first(me) / rq.Hkv; });
   if (me == 0 && odd) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
   tc::fence_after_sync();
@@ -275,9 +286,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   Walk<KT> wk;
-  wk.init(rq, x0, x1, ms.start_r, ms.start_pre);
-  if (tid == 0) {
-    const int a = rq.Hkv * wk.pre + wk.g * wk.nt;  // the unit of this run's first tile
+  wk.init(rq, x0, x1, ms.start_r, ms.start_pre, prm.whole);
+  if (tid == 0 && !prm.whole) {
+    const int a = wk.unit(rq);  // the unit of this run's first tile
     JoinUnit u{};
     if (x0 > a && sh.first(me - 1) <= a) {
       const int q0 = rq.q_start[wk.r], n = rq.q_start[wk.r + 1] - q0;
@@ -959,6 +970,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   prm.out = static_cast<bf16*>(pb.out);
   prm.scale = pb.scale;
   const int grid = grid_of(pb, sms);
+  prm.whole = ((int64_t)pb.W * pb.block_len + Cfg<D, CH>::KT - 1) / Cfg<D, CH>::KT <= kWhole;
   prm.join = static_cast<JoinUnit*>(workspace);
   prm.parts = reinterpret_cast<float*>(prm.join + grid);
   prm.status = pb.status;
@@ -988,7 +1000,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
     return GIST_ATTN_ERR_LAUNCH;
   decode_kernel<D, CH><<<grid, kThreads, smem, stream>>>(tm, prm);
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
-  if (grid == 1) return GIST_ATTN_OK;
+  if (grid == 1 || prm.whole) return GIST_ATTN_OK;
   // the combine's CTAs may start, and scan the lengths, while the last tiles run
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid - 1, many ? (Cfg<D, CH>::ROWS + prm.join_rows - 1) / prm.join_rows : 1);
