@@ -24,10 +24,15 @@
 // Work is the sequence of tiles of all (request, KV head) units; each of at most
 // two CTAs an SM takes an equal run of it, so one long request spreads over the
 // machine.  A unit that crosses CTAs leaves parts (O, m, sum) in the workspace;
-// combine_kernel joins them in key order, the same way every time.
+// combine_kernel joins them in key order, the same way every time.  Where no unit can
+// have more than four tiles the runs are of whole units, and that launch falls away.
 //
-// Bound: HBM (a byte a cached element).  Eight warps: 0-3 softmax, 4 TMA and
-// scales, 5 tcgen05, 6-7 q rows.
+// Bound: HBM (a byte a cached element) where the contexts are long: 32 x ~4050 keys,
+// 32 heads of 128 with a KV head each, 171 us = 6.3 TB/s; in groups of four, 54 us =
+// 5.1 TB/s, of which about 10 us start, tail and join.  Few tiles a CTA: the chain
+// copy - scores - softmax - output, 1 to 3 us a tile; 16 requests of 2-5 tokens behind
+// 500-3000 keys 39 us, one of 131000 keys 21 us, four of 20-200 keys 8.2 us.
+// Eight warps: 0-3 softmax, 4 TMA and scales, 5 tcgen05, 6-7 q rows.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.
@@ -36,7 +41,7 @@
 
 #include "kernels.h"
 #include "paged.cuh"
-#include "tcgen05.cuh"
+#include "paged_tc.cuh"
 
 namespace gattn {
 namespace {
