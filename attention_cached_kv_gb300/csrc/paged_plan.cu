@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, a.B), r1 = min(r0 + per, a.B);
-  const int begin = max(a.free_range[0], 0), end = min(a.free_range[1], a.num_free);
+  const int begin = max(a.free_range[0], 0), end = max(min(a.free_range[1], a.num_free), 0);
   const long long avail = max(end - begin, 0);
 
   Sums own = {0, 0};

@@ -77,3 +77,11 @@ def test_nothing_to_do():
     check([], [], 16, [1, 2], [0, 2], 5, 4, 9)
     check([7, 0], [0, 0], 16, [1, 2], [0, 2], 0, 4, 9)
     check([7, 0], [0, 0], 16, [1, 2], [0, 2], 3, 4, 9)
+
+
+@pytest.mark.parametrize("free_range", [[5, -2 ** 31], [2 ** 31 - 1, 3], [-4, 2], [3, 3], [2 ** 31 - 1, -2 ** 31]])
+def test_free_ranges_without_a_block(free_range):
+    """Ends before the list, before their begin, or far outside give no blocks but
+    those in both the range and the list."""
+    ref = check([0, 15, 16], [4, 1, 4], 16, [6, 7, 8, 9, 5, 4], free_range, 9, 4, 12)
+    assert ref["status"] == 8 and list(ref["kv_len"])[1] == 16
