@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
   if (blockIdx.x == 0 && refused) report(a.status, GIST_ATTN_STATUS_NOT_SERVED);
   __syncthreads();
   if (blockIdx.x == 0 && tid == 0) {
-    a.free_range_out[0] = a.free_range[0] + (int)taken_all;
+    a.free_range_out[0] = max(a.free_range[0], 0) + (int)taken_all;
     a.free_range_out[1] = a.free_range[1];
   }
 

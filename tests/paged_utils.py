@@ -76,7 +76,7 @@ def plan(cached, new, table, free, free_range, T, bl, num_blocks):
         row += m
     q_start.append(min(row, T))
     return dict(block_table=table, q_start=np.array(q_start), kv_len=np.array(kv_len), slot=slot, position=position,
-                free_range=np.array([free_range[0] + taken, free_range[1]]), status=status)
+                free_range=np.array([max(free_range[0], 0) + taken, free_range[1]]), status=status)
 
 
 def pow2_scale(top: float, limit: float) -> float:

@@ -84,4 +84,7 @@ def test_free_ranges_without_a_block(free_range):
     """Ends before the list, before their begin, or far outside give no blocks but
     those in both the range and the list."""
     ref = check([0, 15, 16], [4, 1, 4], 16, [6, 7, 8, 9, 5, 4], free_range, 9, 4, 12)
-    assert ref["status"] == 8 and list(ref["kv_len"])[1] == 16
+    if free_range == [-4, 2]:
+        assert ref["status"] == 0 and ref["free_range"][0] == 2  # never handed out again
+    else:
+        assert ref["status"] == 8 and list(ref["kv_len"]) == [0, 16, 0]
