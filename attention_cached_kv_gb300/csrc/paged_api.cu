@@ -14,6 +14,7 @@ namespace gattn {
 namespace {
 
 constexpr int kMaxRequests = 16384;  // gist_paged_plan keeps 8 bytes a request in shared memory
+constexpr int kMaxAppendBlock = 1 << 20;  // a block's rows and bytes are counted in 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -113,6 +114,7 @@ extern "C" int gist_kv_append_fp8(const void* k_new, const void* v_new, void* kv
   PagedProblem pb{};
   const int rc = gattn::check_dims(dims, &pb);
   if (rc != GIST_ATTN_OK) return rc;
+  if (pb.block_len > gattn::kMaxAppendBlock) return GIST_ATTN_ERR_UNSUPPORTED;
   if (pb.T == 0) return GIST_ATTN_OK;
   if (!k_new || !v_new || !kv_pool_e4m3 || !kv_scale || !slot ||
       (!position && !(pb.flags & GIST_ATTN_FLAG_PREROTATED)))

@@ -78,6 +78,13 @@ def test_append_refuses(lib, kw, code):
     assert append(lib, **kw) == code
 
 
+def test_append_refuses_blocks_past_its_32_bit_counts(lib):
+    """Refused before any work (no device here), the largest one allowed is not."""
+    big = dict(BASE, num_blocks=1, max_blocks=1)
+    assert append(lib, d=dict(big, block_len=(1 << 20) + 1)) == binding.ERR_UNSUPPORTED
+    assert append(lib, d=dict(big, block_len=1 << 20, num_tokens=0)) == binding.OK
+
+
 def test_append_of_nothing(lib):
     assert append(lib, d=dict(BASE, num_tokens=0), k=0, v=0, slot=0, position=0) == binding.OK
 
