@@ -450,7 +450,8 @@ typedef struct {
  *   slot        int32 [T], written: block * block_len + row of each token's place
  *               in the cache, -1 for padding
  *   position    int32 [T], written: cached_len + index of each token, -1 for padding
- *   free_range_out int32 [2], written: free_range after the step
+ *   free_range_out int32 [2], written: free_range after the step (a begin below
+ *               zero counts as zero; the end is passed on as it is)
  * A request is not served when its lengths are negative or pass W * block_len,
  * when it ends past row T, or when it needs blocks and the needs summed in
  * request order up to and including its own (those of requests not served for
@@ -490,7 +491,7 @@ int gist_paged_plan(const int32_t* cached_len, const int32_t* new_len, int32_t* 
  * A block's new tokens must be consecutive in t with consecutive slots (skipped
  * ones keeping their place), as gist_paged_plan gives them, and no block may get
  * tokens of two requests: otherwise the block's rows and scale are unspecified
- * (the writes stay in it).
+ * (the writes stay in it).  block_len at most 2^20 (GIST_ATTN_ERR_UNSUPPORTED).
  * num_requests, max_new, max_blocks and Hq are not used.
  */
 int gist_kv_append_fp8(const void* k_new, const void* v_new, void* kv_pool_e4m3, float* kv_scale,
@@ -518,10 +519,12 @@ size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims);
  *               otherwise): scratch, overwritten by every call; two calls that may
  *               overlap on the GPU need one each
  * A token that sees no key (kv_len[r] < n) gets zeros.  Cached bytes that no token
- * sees (rows past kv_len in the last block) may hold anything.  A block id outside
- * the pool zeroes its request's rows and sets GIST_ATTN_STATUS_BAD_BLOCK, as does a
- * kv_len past W * block_len; a q_start pair outside [0, T], out of order or more
- * than max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
+ * sees (rows past kv_len in the last block) may hold anything.  out must not overlap
+ * what the call reads.  A block id outside the pool zeroes the rows that see keys of
+ * that block (earlier new tokens of the request may become zeros with them) and sets
+ * GIST_ATTN_STATUS_BAD_BLOCK; a kv_len past W * block_len zeroes all of the request's
+ * rows and sets it too; a q_start pair outside [0, T], out of order or more than
+ * max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
  * elsewhere.  block_len must be a multiple of 16, Hq / Hkv at most 128 and
  * W * block_len at most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).
  */

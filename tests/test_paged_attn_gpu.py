@@ -79,6 +79,34 @@ def test_chunks_and_decoding_requests_together(Hq, Hkv, d):
     close(run(pb), pb.expected(), f"{Hq}/{Hkv}/{d}")
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", HEADS)
+@pytest.mark.parametrize("new", [1, 2, 5])
+def test_few_tiles_of_requests_that_the_table_leaves_room_for(Hq, Hkv, d, new):
+    """The same short sequences with room for long ones in the table: a sequence's
+    tiles then go to several blocks of the grid and are joined."""
+    lens = [0, 1, 126, 127, 128, 129, 255, 256, 383, 700]
+    pb = pu.Problem(lens, [new] * len(lens), Hq, Hkv, d, 32, seed=d + Hq + new, pad=1, extra_width=300)
+    close(run(pb), pb.expected(), f"{Hq}/{Hkv}/{d} new={new}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_joined_parts_with_bad_blocks_and_nan(d):
+    """A block outside the pool in one part of a sequence zeroes its rows; a NaN in one
+    part reaches the element it stands in."""
+    pb = pu.Problem([500, 700, 900], [2, 2, 2], 4, 2, d, 16, seed=3, extra_width=300)
+    ref = pb.expected()
+    args = list(pb.args())
+    t = pb.table.copy()
+    t[1, 30] = pb.dims["num_blocks"]
+    args[3] = pb.i32(t)
+    args[1][int(t[2, 40]), pb.layer, 1, 1, 5, 7] = 0x7F  # V, KV head 1, element 7
+    got = run(pb, args, status=binding.STATUS_BAD_BLOCK)
+    assert (got[2:4] == 0).all() and np.isnan(got[4:6, 2:, 7]).all()
+    got[2:4] = ref[2:4]
+    got[4:6, 2:, 7] = ref[4:6, 2:, 7]
+    close(got, ref, "others")
+
+
 def test_wide_groups():
     """Groups wider than 16 heads, up to 128."""
     for Hq, Hkv, d in ((40, 1, 64), (128, 1, 128), (66, 2, 128)):
