@@ -13,7 +13,8 @@
 //     two), K's block scales multiply the fp32 scores;
 //   * 12: the MMAs, alternating between the row tiles, so that one's products run
 //     while the other's softmax does;
-//   * 13: block ids and scales, four tiles at a time, ahead of the copies.
+//   * 13: block ids and scales, four tiles at a time, ahead of the copies;
+//   * 14: the softmax warps' segments, one ahead.
 // One conversion of a key serves 256 rows: that is why rows are taken in pairs of tiles
 // here and cached bytes are used as they are where there are few rows (paged_decode.cu).
 // It is still most of what the loop waits for: the conversion instruction takes about
@@ -44,7 +45,7 @@
 namespace gattn {
 namespace {
 
-constexpr int kThreads = 448;         // 8 softmax, 4 converting, 1 MMA, 1 look-up warp
+constexpr int kThreads = 480;         // 8 softmax, 4 converting, MMA, look-up, segment warp
 constexpr int kRing = 8;              // tiles whose look-ups are held, in two halves
 constexpr int kKT = 128;              // keys a tile
 constexpr float kNone = -3.0e38f;     // running maximum before any key
@@ -178,8 +179,7 @@ struct PMisc {
   int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
   int64_t warp_sum[kThreads / 32], start_pre, total;
   int start_r;
-  PWalk walk;  // the softmax warps' walk and segment
-  PSeg seg[2];
+  PSeg seg[2];  // the softmax warps' segments
   int any_seg[2];  // 0: there is no further one
   // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
   // the pool (-1: no key that is seen, or a block outside the pool)
@@ -448,6 +448,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (lane == 0) mbar_arrive(&ms.gready[half]);
       if (last) break;
     }
+  } else if (warp == 14) {
+    // ================================================== the softmax warps' segments
+    for (int now = 0;; now ^= 1) {
+      bool any = false;
+      if (lane == 0) {
+        PSeg s;
+        while (wk.more() && !any) {
+          any = wk.get(prm, s);
+          wk.next(prm);
+        }
+        if (any) ms.seg[now] = s;
+        ms.any_seg[now] = any;
+      }
+      named_bar_sync(3, 288);  // nothing of the segment before is still read
+      if (!__shfl_sync(0xffffffffu, any, 0)) break;
+    }
   } else if (warp >= 8) {
     // ================================================== cached rows into f16 tiles
     constexpr int kLanes = D / 16;             // threads of a row (16 bytes each)
@@ -590,26 +606,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     int seg = 0, i0 = 0;
     uint32_t ns = 0;  // S tiles (and last P V's) so far of this row tile
-    // One thread walks, a segment ahead; the others read from shared memory (their
-    // registers are the scores').  The slots of `seg` count the segments with key tiles.
-    auto find = [&](int k) {
-      PWalk w = ms.walk;
-      PSeg s;
-      bool any = false;
-      while (w.more() && !any) {
-        any = w.get(prm, s);
-        w.next(prm);
-      }
-      if (any) ms.seg[k] = s;
-      ms.any_seg[k] = any;
-      ms.walk = w;
-    };
-    if (tid == 0) {
-      ms.walk = wk;
-      find(0);
-    }
+    // The slots of `seg` count the segments with key tiles.
     for (int now = 0;; now ^= 1) {
-    named_bar_sync(3, 256);  // nothing of the segment before is still read
+    named_bar_sync(3, 288);  // the segment is there (nothing of the one before it is still read)
     if (!ms.any_seg[now]) break;
     const PSeg& sg = ms.seg[now];
     const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
@@ -620,19 +619,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
       if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
     }
+    // rows of q and out, a warp its own 32, D / 8 lanes a row
+    constexpr int RW = 256 / D;  // rows of a step
+    const int rr0 = (row & ~31) + lane / (D / 8), rr1 = (row & ~31) + 32, rch = lane % (D / 8);
+    const int toks = sg.toks;
+    const int64_t at0 = ((int64_t)(sg.q0 + x * Tm) * prm.Hq + sg.g * G) * D + rch * 8;
+    auto row_ok = [&](int rr) { return rr < Tm * G && x * Tm + token_of(rr) < toks; };
+    auto at_row = [&](int rr) {
+      const int in = token_of(rr);
+      return at0 + ((int64_t)in * (prm.Hq - G) + rr) * D;
+    };
     float rs;  // softmax scale (log2) x the row's power of two
     {
-      // rows into their places, a warp its own 32, D / 8 lanes a row; rounded to f16
-      // there after the rotation
+      // rows into their places, rounded to f16 there after the rotation
       const uint32_t tile = sbase + x * C::kTile;
       auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
-      constexpr int RW = 256 / D;  // rows of a step
-#pragma unroll
-      for (int k = 0; k < 32 / RW; ++k) {
-        const int rr = (row & ~31) + k * RW + lane / (D / 8), ch = lane % (D / 8), in = token_of(rr), tk = x * Tm + in;
-        const bf16* src = prm.q + ((int64_t)(sg.q0 + tk) * prm.Hq + sg.g * G + rr - in * G) * D + ch * 8;
-        if (rr < Tm * G && tk < sg.toks) cp_async16(place(rr, ch), src);
-        else sts16(place(rr, ch), make_uint4(0, 0, 0, 0));
+#pragma unroll 1
+      for (int rr = rr0; rr < rr1; rr += RW) {
+        if (row_ok(rr)) cp_async16(place(rr, rch), prm.q + at_row(rr));
+        else sts16(place(rr, rch), make_uint4(0, 0, 0, 0));
       }
       cp_async_wait_all();
       __syncwarp();
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                              : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
       const int pos = max(sg.pos0 + tok, 0);
       const uint64_t down2 = f2_make(down, down);
-#pragma unroll 2
+#pragma unroll 1
       for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
         const uint32_t pa = place(row, ch), pb = place(row, ch + D / 16);
         const uint4 va = lds16(pa), vb = lds16(pb);
@@ -676,7 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       fence_proxy_async_smem();
       mbar_arrive(&ms.qready);
     }
-    if (tid == 0) find(now ^ 1);
     float m = kNone;
     uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
     const bool live = x == 0 || sg.two;
@@ -797,10 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // as bf16, or one half after the other as fp32
       const uint32_t tile = sbase + x * C::kTile;
       auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
-      constexpr int RW = 256 / D;
 #pragma unroll 1
       for (int half = 0; half < (whole ? 1 : 2); ++half) {
-#pragma unroll 2
+#pragma unroll 1
         for (int c = 0; c < (whole ? D / 16 : D / 32); ++c) {
           const int col = half * (D / 2) + c * 16;
           float o[16];
@@ -828,13 +831,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
         __syncwarp();
-#pragma unroll 4
-        for (int k = 0; k < 32 / RW; ++k) {
-          const int rr = (row & ~31) + k * RW + lane / (D / 8), ch = lane % (D / 8), in = token_of(rr), tk = x * Tm + in;
-          const uint4 v = lds16(place(rr, ch));
-          if (rr < Tm * G && tk < sg.toks) {
-            if (whole) stg16(prm.out + ((int64_t)(sg.q0 + tk) * prm.Hq + sg.g * G + rr - in * G) * D + ch * 8, v);
-            else stg16(part + (x * 128 + rr) * D + half * (D / 2) + ch * 4, v);
+#pragma unroll 1
+        for (int rr = rr0; rr < rr1; rr += RW) {
+          const uint4 v = lds16(place(rr, rch));
+          if (row_ok(rr)) {
+            if (whole) stg16(prm.out + at_row(rr), v);
+            else stg16(part + (x * 128 + rr) * D + half * (D / 2) + rch * 4, v);
           }
         }
         __syncwarp();
