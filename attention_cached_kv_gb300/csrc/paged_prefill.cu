@@ -538,6 +538,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         failed = true;
         break;
       }
+      // the values' factors (read before the tiles are written: the loads cannot pass those)
+      uint32_t mul[kPass];
+      bool lost = false;
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
+        lost |= vs < 0.f;
+        mul[p] = to_f16x2(f, f);
+      }
       const uint32_t ktile = sbase + C::offK + b * C::kTile, vtile = sbase + C::offV + b * C::kTile;
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
@@ -567,17 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
-        const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
-        if (vs < 0.f) ms.bad[sl] = 1;
-        const uint32_t w[4] = {vx[p].x, vx[p].y, vx[p].z, vx[p].w}, mul = to_f16x2(f, f);
+        const uint32_t w[4] = {vx[p].x, vx[p].y, vx[p].z, vx[p].w};
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul);
-          h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul);
+          h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul[p]);
+          h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul[p]);
         }
         put(vtile, p * kRows + row0, h);
       }
+      if (lost) ms.bad[sl] = 1;
       if (nan) {  // noted for the rows that see it, and cleared
         ms.any_nan[sl] = 1;
 #pragma unroll 1
