@@ -51,7 +51,7 @@ constexpr int kKT = 128;              // keys a tile
 constexpr float kNone = -3.0e38f;     // running maximum before any key
 constexpr float kSlack = 8.f;         // log2 units a score may pass it by
 
-constexpr int kStartCost = 256;       // keys that a unit's start is worth
+constexpr int kStartCost = 512;       // keys that a unit's start is worth
 
 // What the join needs of a unit that crosses CTAs, left by the CTA whose run starts in
 // it first (cost 0: nothing to join there).
@@ -170,6 +170,7 @@ struct Tile {
   int key0;  // its first key
   int sl;    // its segment's slot
   int r, g, kv;
+  int full;  // all of its rows are seen, and all in the pool
 };
 
 template <int D>
@@ -414,11 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       settle();
       want = false;
       blk = -1;
-      tl = Tile{INT32_MIN, 0, 0, 0, 0, 0, 0};
+      tl = Tile{INT32_MIN, 0, 0, 0, 0, 0, 0, 0};
       if (have) {
         const int key0 = (sg.kt0 + e) * kKT;
         key = key0 + gr * 16;
-        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, sg.r, sg.g, sg.kv};
+        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, sg.r, sg.g, sg.kv, 0};
         want = key < sg.kend;
         if (want) blk = rq.block_table[(int64_t)sg.r * rq.W + key / rq.block_len];
         e += 4;
@@ -427,10 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     look_up();
     for (int i = 0;; i += 4) {
       const bool last = __any_sync(0xffffffffu, !have);  // this half ends the sequence
-      const Tile now = tl;
+      Tile now = tl;
       const int half = (i >> 2) & 1;
       const bool ok = want && blk >= 0 && blk < prm.num_blocks, lost = want && !ok;
       if (lost) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
+      now.full = (__ballot_sync(0xffffffffu, ok) >> (8 * t) & 0xffu) == 0xffu && now.left >= kKT;
       const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + now.g;
       const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : -1;
       const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : lost ? -1.f : 0.f;
@@ -493,11 +495,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     uint4 kx[kPass], vx[kPass];
     auto fetch = [&](int i, uint4 (&x)[kPass], int64_t more) {
       const int left = ms.tile[i & (kRing - 1)].left;  // rows of the tile that are seen
+      const uint8_t* src = prm.pool + (row0 & 15) * D + c * 16 + more;
+      if (ms.tile[i & (kRing - 1)].full) {
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) x[p] = ldg16(src + ms.at[i & (kRing - 1)][(p * kRows + row0) >> 4]);
+        return;
+      }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int row = p * kRows + row0;
         const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
-        x[p] = ldg16_if(prm.pool + at + (row & 15) * D + c * 16 + more, at >= 0 && row < left);
+        x[p] = ldg16_if(src + at, at >= 0 && row < left);
       }
     };
     auto looked_up = [&](int i) {
