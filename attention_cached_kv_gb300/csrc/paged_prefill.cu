@@ -17,20 +17,23 @@
 //   * 14: the softmax warps' segments, one ahead.
 // One conversion of a key serves 256 rows: that is why rows are taken in pairs of tiles
 // here and cached bytes are used as they are where there are few rows (paged_decode.cu).
-// It is still most of what the loop waits for: the conversion instruction takes about
-// 16 cycles a warp, 2.0 of 2.3 us a key tile.  (Tried, chunks of 700-1024 tokens behind
-// 1000-6000: keys unconverted with q as three E4M3 terms, more tensor work, 320 us for
-// 309; keys widened by integer operations, 349 us; a warp a row tile for the MMAs,
-// 344 us.)  q is scaled by a power of two a row before its one rounding to f16.
+// q is scaled by a power of two a row before its one rounding to f16.
 //
 // Work is the sequence of (request, KV head, row-tile pair) units, each worth the keys
 // it sees and a constant for its start; each SM's CTA takes an equal run of it, cut
 // inside a unit between key tiles.  Units that cross CTAs leave parts (O, m, sum) in
 // the workspace and join_kernel adds them up in key order: chunks of unlike lengths,
-// or one short chunk behind a long context, spread evenly.
-// Bound: the converting warps, then the chain scores - softmax - output of a row tile:
-// four chunks of 700-1024 tokens behind 1000-6000 cached ones, 32 / 8 heads of 128:
-// 306 us = 764 TFLOP/s, tensor pipe 39 % busy.
+// or one short chunk behind a long context, spread evenly.  A start and an end (rows of q
+// in and rotated, rows of O out) run a few times a CTA, mostly out of a cold instruction
+// cache, so their loops stay rolled: unrolled they took 11 us together, rolled 9.
+// Bound: per key tile (2.2 us) the chain scores - softmax - output of a row tile, the
+// converting warps (1.8 us) and the products (1.5 us) are near one another.  Four
+// chunks of 700-1024 tokens behind 1000-6000 cached ones, 32 / 8 heads of 128:
+// 267 us = 877 TFLOP/s.  (Without any conversion it would be 250, with an eighth of
+// the products 220, without exponentials the same.  Tried: keys unconverted with q as
+// three E4M3 terms; a warp a row tile for the products; a warpgroup each for keys and
+// values with a register split; half the keys widened by integer operations; the
+// copies ahead into L2.  None gained, some lost up to a tenth.)
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.
@@ -624,247 +627,247 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     uint32_t ns = 0;  // S tiles (and last P V's) so far of this row tile
     // The slots of `seg` count the segments with key tiles.
     for (int now = 0;; now ^= 1) {
-    named_bar_sync(3, 288);  // the segment is there (nothing of the one before it is still read)
-    if (!ms.any_seg[now]) break;
-    const PSeg& sg = ms.seg[now];
-    const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
-    const bool valid = row < Tm * G && tok < sg.toks;
-    const int lim = valid ? sg.pos0 + tok + 1 : 0;      // keys the row sees
-    const int lim_all = sg.pos0 + x * Tm + 1;           // keys every row of the tile sees
-    if (nt > 0) {  // the next but one's
-      if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
-      if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
-    }
-    // rows of q and out, a warp its own 32, D / 8 lanes a row
-    constexpr int RW = 256 / D;  // rows of a step
-    const int rr0 = (row & ~31) + lane / (D / 8), rr1 = (row & ~31) + 32, rch = lane % (D / 8);
-    const int toks = sg.toks;
-    const int64_t at0 = ((int64_t)(sg.q0 + x * Tm) * prm.Hq + sg.g * G) * D + rch * 8;
-    auto row_ok = [&](int rr) { return rr < Tm * G && x * Tm + token_of(rr) < toks; };
-    auto at_row = [&](int rr) {
-      const int in = token_of(rr);
-      return at0 + ((int64_t)in * (prm.Hq - G) + rr) * D;
-    };
-    float rs;  // softmax scale (log2) x the row's power of two
-    {
-      // rows into their places, rounded to f16 there after the rotation
-      const uint32_t tile = sbase + x * C::kTile;
-      auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
-#pragma unroll 1
-      for (int rr = rr0; rr < rr1; rr += RW) {
-        if (row_ok(rr)) cp_async16(place(rr, rch), prm.q + at_row(rr));
-        else sts16(place(rr, rch), make_uint4(0, 0, 0, 0));
+      named_bar_sync(3, 288);  // the segment is there (nothing of the one before it is still read)
+      if (!ms.any_seg[now]) break;
+      const PSeg& sg = ms.seg[now];
+      const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
+      const bool valid = row < Tm * G && tok < sg.toks;
+      const int lim = valid ? sg.pos0 + tok + 1 : 0;      // keys the row sees
+      const int lim_all = sg.pos0 + x * Tm + 1;           // keys every row of the tile sees
+      if (nt > 0) {  // the next but one's
+        if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
+        if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
       }
-      cp_async_wait_all();
-      __syncwarp();
-      // the largest magnitude bounds the rotated ones by sqrt 2, which the power of two
-      // leaves room for
-      uint32_t big = 0;
-#pragma unroll 4
-      for (int ch = 0; ch < D / 8; ++ch) {
-        const uint4 v = lds16(place(row, ch));
-        big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-      }
-      const uint32_t tb = max(big & 0xffffu, big >> 16) << 16;
-      const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
-      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
-      rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
-                             : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
-      const int pos = max(sg.pos0 + tok, 0);
-      const uint64_t down2 = f2_make(down, down);
-#pragma unroll 1
-      for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
-        const uint32_t pa = place(row, ch), pb = place(row, ch + D / 16);
-        const uint4 va = lds16(pa), vb = lds16(pb);
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        uint32_t a[4], b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float s0, c0, s1, c1;
-          __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e]), &s0, &c0);
-          __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e + 1]), &s1, &c1);
-          const uint64_t u = f2_mul(bf16x2_to_f2(wa[e]), down2), y = f2_mul(bf16x2_to_f2(wb[e]), down2);
-          const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
-          float r0, r1;
-          f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
-          a[e] = to_f16x2(r0, r1);
-          f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
-          b[e] = to_f16x2(r0, r1);
-        }
-        sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
-        sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&ms.qready);
-    }
-    float m = kNone;
-    uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
-    const bool live = x == 0 || sg.two;
-    for (int e = 0; live && e < nt; ++e) {
-      const int i = i0 + e, key0 = (kt0 + e) * kKT;
-      const bool edge = key0 + kKT > lim_all;
-      wait(&ms.sfull[x], ns++ & 1u);
-      tc::fence_after_sync();
-      const float* ksc = ms.ksc[i & (kRing - 1)];
-      // 16 scores v of chunk c (16 keys) as weights exp2(f v - m), packed; their sum into
-      // acc; returns their largest exponent
-      auto weights = [&](int c, const uint32_t (&v)[16], uint32_t* pk, int left) {
-        const float f = ksc[c] * rs;
-        const uint64_t g2 = f2_make(f, f), nm2 = f2_make(-m, -m);
-        float top = kNone;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float a, b;
-          f2_split(f2_fma(f2_make(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), g2, nm2), a, b);
-          if (2 * k >= left) a = -INFINITY;
-          if (2 * k + 1 >= left) b = -INFINITY;
-          top = max3f(top, a, b);
-          const float pa = ex2_approx(a), pb = ex2_approx(b);
-          if (k & 1) acc = f2_add(acc, f2_make(pa, pb));
-          else acc2 = f2_add(acc2, f2_make(pa, pb));
-          pk[k] = to_f16x2(pa, pb);
-        }
-        return top;
+      // rows of q and out, a warp its own 32, D / 8 lanes a row
+      constexpr int RW = 256 / D;  // rows of a step
+      const int rr0 = (row & ~31) + lane / (D / 8), rr1 = (row & ~31) + 32, rch = lane % (D / 8);
+      const int toks = sg.toks;
+      const int64_t at0 = ((int64_t)(sg.q0 + x * Tm) * prm.Hq + sg.g * G) * D + rch * 8;
+      auto row_ok = [&](int rr) { return rr < Tm * G && x * Tm + token_of(rr) < toks; };
+      auto at_row = [&](int rr) {
+        const int in = token_of(rr);
+        return at0 + ((int64_t)in * (prm.Hq - G) + rr) * D;
       };
-      // One pass with the maximum as it is; P stays in registers until it is known that
-      // no row's scores passed it by too much.
-      bool done = false;
-      if (!edge && e > 0) {
-        const uint64_t keep = acc, keep2 = acc2;
-        uint32_t va[16], vb[16], pk[64];
-        float top = kNone;
-        tc::ld16(ts, va);
-        tc::wait_ld();
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          tc::ld16(ts + c * 16 + 16, vb);
-          top = fmaxf(top, weights(c, va, pk + c * 8, 16));
-          tc::wait_ld();
-          if (c + 2 < 8) tc::ld16(ts + c * 16 + 32, va);
-          top = fmaxf(top, weights(c + 1, vb, pk + c * 8 + 8, 16));
-          tc::wait_ld();
-        }
-        done = !__any_sync(0xffffffffu, top > kSlack);
-        if (done) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) st16(ts + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
-        } else {
-          acc = keep;
-          acc2 = keep2;
-        }
-      }
-      if (!done) {
-        // the tile's maximum first.  A row whose maximum jumps scales its O and sum down;
-        // the TMEM load and store are warp-collective, so the warp does it for any of its
-        // rows
-        float mx = kNone;
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t v[16];
-          tc::ld16(ts + c * 16, v);
-          tc::wait_ld();
-          const int left = edge ? lim - key0 - c * 16 : 16;  // columns of these that the row sees
-          float t = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) t = fmaxf(t, k < left ? __uint_as_float(v[k]) : -INFINITY);
-          mx = fmaxf(mx, t * (ksc[c] * rs));
-        }
-        const bool move = mx - m > kSlack;
-        if (__any_sync(0xffffffffu, move)) {
-          const float fm = move ? ex2_approx(m - mx) : 1.f;
-          if (move) m = mx;
-          const uint64_t f2 = f2_make(fm, fm);
-          acc = f2_mul(acc, f2);
-          acc2 = f2_mul(acc2, f2);
-          if (e > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t ov[16];
-              tc::ld16(to + c * 16, ov);
-              tc::wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * fm);
-              st16(to + c * 16, ov);
-            }
-          }
-        }
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t v[16], pk[8];
-          tc::ld16(ts + c * 16, v);
-          tc::wait_ld();
-          weights(c, v, pk, edge ? lim - key0 - c * 16 : 16);
-          tc::st8(ts + c * 8, pk);
-        }
-      }
-      tc::wait_st();
-      tc::fence_before_sync();
-      mbar_arrive(&ms.pfull[x]);
-    }
-    if (live) {
-      if (nt > 0) wait(&ms.sfull[x], ns++ & 1u);
-      tc::fence_after_sync();
-      float a0, a1, b0, b1;
-      f2_split(acc, a0, a1);
-      f2_split(acc2, b0, b1);
-      const float sum = (a0 + a1) + (b0 + b1);
-      const bool bad = nt > 0 && ms.bad[sl], none = lim <= 0 || bad, whole = sg.whole, nan = nt > 0 && ms.any_nan[sl];
-      const float vref = nt > 0 ? ms.vref[sl] : 0.f;
-      if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-      const float inv = whole ? vref / sum : vref;
-      float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
-      // through the row's place in q's room, so that a warp stores whole rows: all columns
-      // as bf16, or one half after the other as fp32
-      const uint32_t tile = sbase + x * C::kTile;
-      auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
-#pragma unroll 1
-      for (int half = 0; half < (whole ? 1 : 2); ++half) {
-#pragma unroll 1
-        for (int c = 0; c < (whole ? D / 16 : D / 32); ++c) {
-          const int col = half * (D / 2) + c * 16;
-          float o[16];
-          uint32_t ov[16];
-          tc::ld16(to + col, ov);  // (without a tile: whatever is there, not used)
-          tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = none || nt == 0 ? 0.f : __uint_as_float(ov[e]) * inv;
-          if (nan && !none) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (ms.nankey[sl][col + e] < lim) o[e] = __int_as_float(0x7fc00000);
-          }
-          if (whole) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = float2_to_bf16x2(o[2 * e], o[2 * e + 1]);
-            sts16(place(row, 2 * c), make_uint4(w[0], w[1], w[2], w[3]));
-            sts16(place(row, 2 * c + 1), make_uint4(w[4], w[5], w[6], w[7]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sts16(place(row, 4 * c + e), make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                                                      __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
-          }
-        }
-        __syncwarp();
+      float rs;  // softmax scale (log2) x the row's power of two
+      {
+        // rows into their places, rounded to f16 there after the rotation
+        const uint32_t tile = sbase + x * C::kTile;
+        auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
 #pragma unroll 1
         for (int rr = rr0; rr < rr1; rr += RW) {
-          const uint4 v = lds16(place(rr, rch));
-          if (row_ok(rr)) {
-            if (whole) stg16(prm.out + at_row(rr), v);
-            else stg16(part + (x * 128 + rr) * D + half * (D / 2) + rch * 4, v);
+          if (row_ok(rr)) cp_async16(place(rr, rch), prm.q + at_row(rr));
+          else sts16(place(rr, rch), make_uint4(0, 0, 0, 0));
+        }
+        cp_async_wait_all();
+        __syncwarp();
+        // the largest magnitude bounds the rotated ones by sqrt 2, which the power of two
+        // leaves room for
+        uint32_t big = 0;
+#pragma unroll 4
+        for (int ch = 0; ch < D / 8; ++ch) {
+          const uint4 v = lds16(place(row, ch));
+          big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+        const uint32_t tb = max(big & 0xffffu, big >> 16) << 16;
+        const int ex = min(max((int)(tb >> 23) - 127, -119), 126);
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // largest to [1, 2)
+        rs = tb >= 0x7f800000u ? __int_as_float(0x7fc00000)
+                               : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
+        const int pos = max(sg.pos0 + tok, 0);
+        const uint64_t down2 = f2_make(down, down);
+#pragma unroll 1
+        for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
+          const uint32_t pa = place(row, ch), pb = place(row, ch + D / 16);
+          const uint4 va = lds16(pa), vb = lds16(pb);
+          const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+          uint32_t a[4], b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float s0, c0, s1, c1;
+            __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e]), &s0, &c0);
+            __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e + 1]), &s1, &c1);
+            const uint64_t u = f2_mul(bf16x2_to_f2(wa[e]), down2), y = f2_mul(bf16x2_to_f2(wb[e]), down2);
+            const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
+            float r0, r1;
+            f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
+            a[e] = to_f16x2(r0, r1);
+            f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
+            b[e] = to_f16x2(r0, r1);
+          }
+          sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
+          sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&ms.qready);
+      }
+      float m = kNone;
+      uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
+      const bool live = x == 0 || sg.two;
+      for (int e = 0; live && e < nt; ++e) {
+        const int i = i0 + e, key0 = (kt0 + e) * kKT;
+        const bool edge = key0 + kKT > lim_all;
+        wait(&ms.sfull[x], ns++ & 1u);
+        tc::fence_after_sync();
+        const float* ksc = ms.ksc[i & (kRing - 1)];
+        // 16 scores v of chunk c (16 keys) as weights exp2(f v - m), packed; their sum into
+        // acc; returns their largest exponent
+        auto weights = [&](int c, const uint32_t (&v)[16], uint32_t* pk, int left) {
+          const float f = ksc[c] * rs;
+          const uint64_t g2 = f2_make(f, f), nm2 = f2_make(-m, -m);
+          float top = kNone;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float a, b;
+            f2_split(f2_fma(f2_make(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), g2, nm2), a, b);
+            if (2 * k >= left) a = -INFINITY;
+            if (2 * k + 1 >= left) b = -INFINITY;
+            top = max3f(top, a, b);
+            const float pa = ex2_approx(a), pb = ex2_approx(b);
+            if (k & 1) acc = f2_add(acc, f2_make(pa, pb));
+            else acc2 = f2_add(acc2, f2_make(pa, pb));
+            pk[k] = to_f16x2(pa, pb);
+          }
+          return top;
+        };
+        // One pass with the maximum as it is; P stays in registers until it is known that
+        // no row's scores passed it by too much.
+        bool done = false;
+        if (!edge && e > 0) {
+          const uint64_t keep = acc, keep2 = acc2;
+          uint32_t va[16], vb[16], pk[64];
+          float top = kNone;
+          tc::ld16(ts, va);
+          tc::wait_ld();
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            tc::ld16(ts + c * 16 + 16, vb);
+            top = fmaxf(top, weights(c, va, pk + c * 8, 16));
+            tc::wait_ld();
+            if (c + 2 < 8) tc::ld16(ts + c * 16 + 32, va);
+            top = fmaxf(top, weights(c + 1, vb, pk + c * 8 + 8, 16));
+            tc::wait_ld();
+          }
+          done = !__any_sync(0xffffffffu, top > kSlack);
+          if (done) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st16(ts + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
+          } else {
+            acc = keep;
+            acc2 = keep2;
           }
         }
-        __syncwarp();
+        if (!done) {
+          // the tile's maximum first.  A row whose maximum jumps scales its O and sum down;
+          // the TMEM load and store are warp-collective, so the warp does it for any of its
+          // rows
+          float mx = kNone;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[16];
+            tc::ld16(ts + c * 16, v);
+            tc::wait_ld();
+            const int left = edge ? lim - key0 - c * 16 : 16;  // columns of these that the row sees
+            float t = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) t = fmaxf(t, k < left ? __uint_as_float(v[k]) : -INFINITY);
+            mx = fmaxf(mx, t * (ksc[c] * rs));
+          }
+          const bool move = mx - m > kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float fm = move ? ex2_approx(m - mx) : 1.f;
+            if (move) m = mx;
+            const uint64_t f2 = f2_make(fm, fm);
+            acc = f2_mul(acc, f2);
+            acc2 = f2_mul(acc2, f2);
+            if (e > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t ov[16];
+                tc::ld16(to + c * 16, ov);
+                tc::wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * fm);
+                st16(to + c * 16, ov);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[16], pk[8];
+            tc::ld16(ts + c * 16, v);
+            tc::wait_ld();
+            weights(c, v, pk, edge ? lim - key0 - c * 16 : 16);
+            tc::st8(ts + c * 8, pk);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&ms.pfull[x]);
       }
-      if (valid && !whole) {
-        part[256 * D + tid] = m;
-        part[256 * (D + 1) + tid] = bad ? -1.f : sum;
+      if (live) {
+        if (nt > 0) wait(&ms.sfull[x], ns++ & 1u);
+        tc::fence_after_sync();
+        float a0, a1, b0, b1;
+        f2_split(acc, a0, a1);
+        f2_split(acc2, b0, b1);
+        const float sum = (a0 + a1) + (b0 + b1);
+        const bool bad = nt > 0 && ms.bad[sl], none = lim <= 0 || bad, whole = sg.whole, nan = nt > 0 && ms.any_nan[sl];
+        const float vref = nt > 0 ? ms.vref[sl] : 0.f;
+        if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
+        const float inv = whole ? vref / sum : vref;
+        float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
+        // through the row's place in q's room, so that a warp stores whole rows: all columns
+        // as bf16, or one half after the other as fp32
+        const uint32_t tile = sbase + x * C::kTile;
+        auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };
+#pragma unroll 1
+        for (int half = 0; half < (whole ? 1 : 2); ++half) {
+#pragma unroll 1
+          for (int c = 0; c < (whole ? D / 16 : D / 32); ++c) {
+            const int col = half * (D / 2) + c * 16;
+            float o[16];
+            uint32_t ov[16];
+            tc::ld16(to + col, ov);  // (without a tile: whatever is there, not used)
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = none || nt == 0 ? 0.f : __uint_as_float(ov[e]) * inv;
+            if (nan && !none) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (ms.nankey[sl][col + e] < lim) o[e] = __int_as_float(0x7fc00000);
+            }
+            if (whole) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = float2_to_bf16x2(o[2 * e], o[2 * e + 1]);
+              sts16(place(row, 2 * c), make_uint4(w[0], w[1], w[2], w[3]));
+              sts16(place(row, 2 * c + 1), make_uint4(w[4], w[5], w[6], w[7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                sts16(place(row, 4 * c + e), make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                                        __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3])));
+            }
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int rr = rr0; rr < rr1; rr += RW) {
+            const uint4 v = lds16(place(rr, rch));
+            if (row_ok(rr)) {
+              if (whole) stg16(prm.out + at_row(rr), v);
+              else stg16(part + (x * 128 + rr) * D + half * (D / 2) + rch * 4, v);
+            }
+          }
+          __syncwarp();
+        }
+        if (valid && !whole) {
+          part[256 * D + tid] = m;
+          part[256 * (D + 1) + tid] = bad ? -1.f : sum;
+        }
+        tc::fence_before_sync();
       }
-      tc::fence_before_sync();
-    }
-    i0 += nt;
-    seg += nt > 0;
+      i0 += nt;
+      seg += nt > 0;
     }
   }
   if (failed) report(prm.status, GIST_ATTN_STATUS_TIMEOUT);
