@@ -10,10 +10,42 @@ namespace gattn {
 // Angle of position `pos` (not negative) at frequency `turn` (theta / 2 pi modulo 1,
 // in units of 2^-64): the product modulo 2^64 is the angle modulo a whole turn, so
 // nothing is lost at far positions (off by at most pos 2^-53 turns, the double that
-// `turn` came from) and no range reduction is left.  In [-pi, pi).
+// `turn` came from) and no range reduction is left.  In units of 2^-32 turns.
+__device__ __forceinline__ uint32_t turn_part(int pos, uint64_t turn) {
+  return (uint32_t)pos * (uint32_t)(turn >> 32) + __umulhi((uint32_t)pos, (uint32_t)turn);
+}
+constexpr float kTurnUnit = 1.4629180792671596e-09f;  // 2 pi / 2^32
+// The same in radians, in [-pi, pi).
 __device__ __forceinline__ float turn_angle(int pos, uint64_t turn) {
-  const uint32_t a = (uint32_t)pos * (uint32_t)(turn >> 32) + __umulhi((uint32_t)pos, (uint32_t)turn);
-  return (float)(int32_t)a * 1.4629180792671596e-09f;  // 2 pi / 2^32
+  return (float)(int32_t)turn_part(pos, turn) * kTurnUnit;
+}
+
+// Sines and cosines of two angles in units of 2^-32 turns, off by about 2^-24: an angle
+// is brought within an eighth of a turn of a quarter's multiple (exact, in integers), x;
+// there sin x = x + x z S(z) and cos x = 1 - z / 2 + z^2 C(z), z = x^2, with S and C the
+// polynomials of degree 2 that interpolate at Chebyshev's nodes.
+__device__ __forceinline__ void sincos_turns(uint32_t a0, uint32_t a1, uint64_t& sn, uint64_t& cs) {
+  const uint32_t b[2] = {a0 + 0x20000000u, a1 + 0x20000000u};  // upper two bits: quarters
+  auto rest = [](uint32_t v) { return (float)((int)(v & 0x3fffffffu) - 0x20000000); };
+  auto both = [](float v) { return f2_make(v, v); };
+  const uint64_t x = f2_mul(f2_make(rest(b[0]), rest(b[1])), both(kTurnUnit)), z = f2_mul(x, x);
+  uint64_t s = f2_fma(both(-0.00019587890880412386f), z, both(0.008332748270629749f));
+  s = f2_fma(s, z, both(-0.1666666466231438f));
+  s = f2_fma(f2_mul(s, z), x, x);
+  uint64_t c = f2_fma(both(2.4547942085071572e-05f), z, both(-0.0013888303035894866f));
+  c = f2_fma(c, z, both(0.04166666465950221f));
+  c = f2_fma(f2_fma(c, z, both(-0.5f)), z, both(1.f));
+  float sv[2], cv[2], so[2], co[2];
+  f2_split(s, sv[0], sv[1]);
+  f2_split(c, cv[0], cv[1]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const bool odd = b[e] & 0x40000000u;
+    so[e] = __uint_as_float(__float_as_uint(odd ? cv[e] : sv[e]) ^ (b[e] & 0x80000000u));
+    co[e] = __uint_as_float(__float_as_uint(odd ? sv[e] : cv[e]) ^ ((b[e] ^ (b[e] << 1)) & 0x80000000u));
+  }
+  sn = f2_make(so[0], so[1]);
+  cs = f2_make(co[0], co[1]);
 }
 
 // Two floats to two E4M3 codes (nearest even, saturating at 448; `lo` in the low byte).

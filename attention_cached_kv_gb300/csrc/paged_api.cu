@@ -64,10 +64,17 @@ int check_dims(const gist_paged_dims* dm, PagedProblem* pb) {
   const double scale = d.softmax_scale > 0.f ? (double)d.softmax_scale : 1.0 / sqrt((double)d.head_dim);
   pb->scale_log2 = (float)(scale * 1.4426950408889634);  // log2(e)
   const bool rotate = !(d.flags & GIST_ATTN_FLAG_PREROTATED);
+  // theta^(-2j/d) as a product of two powers, of j's upper and lower three bits: 14 calls of
+  // pow for 64 (0.8 us of these checks for 1.4), off by a unit or two of the last place more
+  double low[8] = {1.0}, high[8] = {1.0};
+  for (int k = 1; rotate && k < 8; ++k) {
+    low[k] = pow((double)d.rope_theta, -2.0 * k / (double)d.head_dim);
+    if (8 * k < d.head_dim / 2) high[k] = pow((double)d.rope_theta, -16.0 * k / (double)d.head_dim);
+  }
   for (int j = 0; j < 64; ++j) {
     double turns = 0.0;  // theta_j / (2 pi) modulo 1
     if (rotate && j < d.head_dim / 2) {
-      turns = pow((double)d.rope_theta, -2.0 * j / (double)d.head_dim) * 0.15915494309189535;
+      turns = high[j >> 3] * low[j & 7] * 0.15915494309189535;
       turns -= floor(turns);
     }
     pb->turn[j] = turns < 1.0 ? (uint64_t)ldexp(turns, 64) : 0;

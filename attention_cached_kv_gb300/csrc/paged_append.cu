@@ -13,8 +13,12 @@
 // tokens (all of a prompt's block, a single token of a decoding step).  A thread holds elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row,
 // so it rotates its own pairs with four sines, and the rows stay in registers
 // between the pass for the largest magnitude and the one that converts.
+// Sine and cosine are carried to fp32's last place, though E4M3 keeps four bits: what
+// they are off by moves values that lie next to the middle of two codes.  Of 1.8 million
+// values 1.5 differ from the definition's (rotated in fp32 by torch: 0.8); by __sincosf,
+// off by 2^-21, 7.5 did, in 26 us where this takes 29.
 // Bound: issue, then HBM (three bytes an element: bf16 in, E4M3 out): 14.2 k tokens of
-// 8 heads of 128 in 26 us = 3.5 TB/s; few tokens: latency, 64 tokens in 6.3 us.
+// 8 heads of 128 in 29 us = 3.1 TB/s; few tokens: latency, 64 tokens in 6.4 us.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.
@@ -213,11 +217,13 @@ __global__ void __launch_bounds__(kThreads, 7)
       uint64_t f0 = bf16x2_to_f2(a.x), f1 = bf16x2_to_f2(a.y), h0 = bf16x2_to_f2(b.x), h1 = bf16x2_to_f2(b.y);
       if (rotate) {
         const int pos = i < kThreads ? pos_of[i] : prm.position[t + i];
-        float sn[4], cs[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) __sincosf(turn_angle(pos, turn[q]), &sn[q], &cs[q]);
-        const uint64_t c0 = f2_mul(f2_make(cs[0], cs[1]), inv2), c1 = f2_mul(f2_make(cs[2], cs[3]), inv2);
-        const uint64_t s0 = f2_mul(f2_make(sn[0], sn[1]), inv2), s1 = f2_mul(f2_make(sn[2], sn[3]), inv2);
+        uint64_t s0, s1, c0, c1;
+        sincos_turns(turn_part(pos, turn[0]), turn_part(pos, turn[1]), s0, c0);
+        sincos_turns(turn_part(pos, turn[2]), turn_part(pos, turn[3]), s1, c1);
+        s0 = f2_mul(s0, inv2);
+        s1 = f2_mul(s1, inv2);
+        c0 = f2_mul(c0, inv2);
+        c1 = f2_mul(c1, inv2);
         const uint64_t x0 = f0, x1 = f1;
         f0 = f2_sub(f2_mul(x0, c0), f2_mul(h0, s0));
         f1 = f2_sub(f2_mul(x1, c1), f2_mul(h1, s1));
