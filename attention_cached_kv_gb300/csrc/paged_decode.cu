@@ -87,7 +87,7 @@ struct Cfg {
   static constexpr int SP = (8 * CH + 15) & ~15;   // S columns a parity
   static constexpr int OC = (KPR * 24 * CH + 15) & ~15;  // O columns
   static constexpr int SB = 2 * KPR * SP + OC <= 256 ? 2 : 1;  // S buffers
-  static constexpr uint32_t QT = 1024 * CH, QB = 3 * QT, PB = KPR * 3072 * CH;
+  static constexpr uint32_t QT = 1024 * CH, QB = 3 * QT, PB = KPR * QB;
   static constexpr int NK = D == 128 && CH <= 2 ? 3 : D == 64 && CH == 1 ? 3 : 2;
   static constexpr int NV = D == 128 && CH == 1 ? 3 : 2;
   static constexpr uint32_t kO = SB * KPR * SP;  // O's first TMEM column
