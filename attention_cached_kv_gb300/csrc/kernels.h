@@ -98,6 +98,7 @@ struct PlanArgs {
   int32_t* status;
   int B, T, block_len, W, num_blocks, num_free;
 };
+constexpr int kPlanRequests = 16384;  // at most: the plan keeps 8 bytes a request in shared memory
 int launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
 int launch_paged_append(const PagedProblem& pb, const void* k_new, const void* v_new, void* pool,
                         float* scale, const int32_t* slot, const int32_t* position,

@@ -13,7 +13,6 @@
 namespace gattn {
 namespace {
 
-constexpr int kMaxRequests = 16384;  // gist_paged_plan keeps 8 bytes a request in shared memory
 constexpr int kMaxAppendBlock = 1 << 20;  // a block's rows and bytes are counted in 32 bits
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -97,7 +96,7 @@ extern "C" int gist_paged_plan(const int32_t* cached_len, const int32_t* new_len
   const int rc = gattn::check_sizes(*dims);
   if (rc != GIST_ATTN_OK) return rc;
   if (num_free < 0) return GIST_ATTN_ERR_DIMS;
-  if (dims->num_requests > gattn::kMaxRequests) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (dims->num_requests > gattn::kPlanRequests) return GIST_ATTN_ERR_UNSUPPORTED;
   const bool some = dims->num_requests > 0, tokens = dims->num_tokens > 0;
   if (!q_start || !free_range || !free_range_out ||
       (some && (!cached_len || !new_len || !block_table || !kv_len)) ||

@@ -167,8 +167,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 
 int launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   const int smem = (2 * a.B + 1) * (int)sizeof(int);
+  // the limit holds for all threads of the process: always the same one, so that no call
+  // lowers it between another's two lines here
+  constexpr int kMost = (2 * kPlanRequests + 1) * (int)sizeof(int);
   if (smem > 32 * 1024 &&
-      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
   const int want = (a.T + kThreads - 1) / kThreads;
   const int grid = want < 1 ? 1 : want > 128 ? 128 : want;
