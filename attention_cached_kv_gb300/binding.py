@@ -484,6 +484,18 @@ def _pool_ptr(pool, dims, dev):
     return _sized(pool, pool.dtype, "kv_pool_e4m3", n * dims["block_len"] * dims["head_dim"], dev), n
 
 
+def _allocating_for(stream, dev):
+    """Allocations under this belong to the stream that the call on device `dev` runs on (a
+    torch stream, a raw handle, or None for the current one): memory of another stream's
+    may still be in use there, and freed memory goes back to it while the call runs."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", dev))
+    return torch.cuda.stream(stream)
+
+
 def _call(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current, on `stream` or the device's current one."""
     if torch.cuda.current_device() != dev:
@@ -499,12 +511,14 @@ def gist_paged_plan(cached_len, new_len, block_table, free_blocks, free_range, o
     """Blocks, slots and positions of one step from the requests' lengths (int32
     CUDA tensors throughout); writes the entries of newly taken blocks into
     block_table and returns a PagedPlan.  `out`: five int32 tensors in PagedPlan's
-    order to write into (allocated if None), so that a captured step keeps its
-    buffers."""
+    order to write into (allocated on the call's stream if None), so that a captured
+    step keeps its buffers."""
     lib = load_library()
     B, T, i32, dev = dims["num_requests"], dims["num_tokens"], torch.int32, _index(new_len, "new_len")
-    plan = PagedPlan(*(out if out is not None else
-                       (torch.empty(n, dtype=i32, device=new_len.device) for n in (B + 1, B, T, T, 2))))
+    if out is None:
+        with _allocating_for(stream, dev):
+            out = [torch.empty(n, dtype=i32, device=new_len.device) for n in (B + 1, B, T, T, 2)]
+    plan = PagedPlan(*out)
     D = make_paged_dims(dims, status)
     _call(dev, stream, lib.gist_paged_plan, _sized(cached_len, i32, "cached_len", B, dev),
           _sized(new_len, i32, "new_len", B, dev),
@@ -543,23 +557,21 @@ def gist_attn_paged_fp8kv(q, kv_pool_e4m3, kv_scale, block_table, q_start, kv_le
                           workspace=None, *, dims: dict, status: torch.Tensor | None = None,
                           stream=None):
     """Causal attention of every request's new tokens over its cached sequence,
-    which already holds them; returns `out` [T][Hq][d] (allocated if None; rows of
-    padding tokens are not written).  `workspace`: a uint8 tensor of at least
-    paged_workspace_bytes(dims) bytes, one per call in flight (allocated if None,
-    on the current stream)."""
+    which already holds them; returns `out` [T][Hq][d] (rows of padding tokens are
+    not written).  `workspace`: a uint8 tensor of at least paged_workspace_bytes(dims)
+    bytes, one per call in flight.  Both are allocated on the call's stream if None."""
     lib = load_library()
     B, dev, bf, i32 = dims["num_requests"], _index(q, "q"), torch.bfloat16, torch.int32
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream, dev):
+            out = torch.empty_like(q)
     n = dims["num_tokens"] * dims["num_q_heads"] * dims["head_dim"]
     pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
     D = make_paged_dims(dims, status)
     if workspace is None:
-        with torch.cuda.device(dev):
+        with _allocating_for(stream, dev), torch.cuda.device(dev):
             need = int(lib.gist_attn_paged_workspace_bytes(ctypes.byref(D)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None and hasattr(stream, "cuda_stream"):
-            workspace.record_stream(stream)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _call(dev, stream, lib.gist_attn_paged_fp8kv, _sized(q, bf, "q", n, dev), pool,
           _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
           _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),

@@ -7,6 +7,7 @@ import threading
 import pytest
 import torch
 
+import paged_utils as pu
 from attention_cached_kv_gb300 import binding
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,64 @@ def test_plans_of_unlike_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+STREAMS = ["stream", "handle"]
+
+
+def problem():
+    pb = pu.Problem([3000, 700, 20], [1, 40, 3], 8, 2, 64, 16, seed=1)
+    return pb, pb.args()
+
+
+@pytest.mark.parametrize("kind", STREAMS)
+def test_what_a_call_allocates_belongs_to_its_stream(kind, monkeypatch):
+    """Workspace, output and plan buffers come from the memory of the stream that the call
+    runs on, so that no other stream's work can still be using them, or get them while
+    the call runs."""
+    pb, args = problem()
+    s = torch.cuda.Stream()
+    given = s if kind == "stream" else s.cuda_stream
+    seen = []
+    for name in ("empty", "empty_like"):
+        def alloc(*a, _f=getattr(torch, name), **kw):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return _f(*a, **kw)
+        monkeypatch.setattr(torch, name, alloc)
+    torch.cuda.synchronize()
+    binding.gist_attn_paged_fp8kv(*args, dims=pb.dims, stream=given)
+    assert seen == [s.cuda_stream] * 2
+    i = pb.i32([0, 5])
+    dims = dict(pb.dims, num_requests=1, num_tokens=4)
+    binding.gist_paged_plan(i[:1], i[1:], pb.i32(pb.table), i, pb.i32([0, 0]), dims=dims, stream=given)
+    assert seen == [s.cuda_stream] * 7
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", STREAMS)
+def test_memory_that_other_streams_use_is_not_taken(kind):
+    """Calls on two streams without workspaces, the memory between them freed and used
+    again on the current one: every answer is the one of a call alone."""
+    pb, args = problem()
+    want = binding.gist_attn_paged_fp8kv(*args, dims=pb.dims)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    need = binding.paged_workspace_bytes(pb.dims)
+    outs = []
+    for i in range(20):
+        here = torch.zeros(need, dtype=torch.uint8, device=DEV)  # current stream: work on memory of that size,
+        here.fill_(0x7F)
+        del here                                                   # then free while the work may be under way
+        s = streams[i % 2]
+        outs.append(binding.gist_attn_paged_fp8kv(*args, dims=pb.dims, stream=s if kind == "stream" else s.cuda_stream))
+        outs.append(binding.gist_attn_paged_fp8kv(*args, dims=pb.dims))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_a_raw_handle_of_the_default_stream():
+    pb, args = problem()
+    want = binding.gist_attn_paged_fp8kv(*args, dims=pb.dims)
+    got = binding.gist_attn_paged_fp8kv(*args, dims=pb.dims, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
