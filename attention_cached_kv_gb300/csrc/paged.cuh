@@ -83,6 +83,15 @@ __device__ __forceinline__ void terms3(uint32_t x, uint16_t& t0, uint16_t& t1, u
       : "r"(x));
 }
 
+// The attention kernels hold exp2(s + log2 |v| - m), v the V scale of a key's block and m the
+// running maximum of s + log2 |v|, and sum exp2(s - m) apart: with |v| in [2^-100, 2^119],
+// as gist_kv_append_fp8 writes it, neither leaves fp32's range.  Smaller ones count as zero.
+constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100
+__device__ __forceinline__ float scale_log2(float v) {
+  const float a = fabsf(v);
+  return a < kLeastScale ? -100.f : log2f(a);
+}
+
 // The requests of a step, as the attention kernels walk them.
 struct Requests {
   const int32_t* q_start;

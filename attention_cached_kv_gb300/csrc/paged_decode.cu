@@ -13,13 +13,17 @@
 // of two a row, its largest value to 128 and more, and the terms reach 2^-17 of that.
 // P's small weights matter more (they are many), so its terms are kept apart,
 // p0 + p1 / 16 + p2 / 256, side by side as columns of N: the few query rows leave N
-// room that costs nothing.  The K scale of a key's block multiplies its fp32 scores,
-// the V scale over the largest met so far its weights.
+// room that costs nothing.  The K scale of a key's block multiplies its fp32 scores s,
+// the logarithm of its V scale is added to them: a weight with its V scale is
+// P = exp2(s + log2 v - m), without it exp2(s - m), and a row's output is the quotient of
+// the two sums (over P x V codes, and over the second).  So P's bits go by what a key adds
+// to the row, and a large V scale of a key that the row hardly weighs, or does not see,
+// takes none away.
 //
 // A softmax thread owns one tile row (TMEM lane): its scores for all query rows,
-// the running maximum m of each (the same in all threads), its own part of the
-// sums.  m moves only when a score passes it by more than 2 (log2 units), all
-// threads together; then O in TMEM is rescaled.  P is at most 2^2 x 64 of 448.
+// the running maximum (of s + log2 v, less kPUnit) m of each (the same in all threads),
+// its own part of the sums.  m moves only when a score passes it by more than 2 (log2
+// units), all threads together; then O in TMEM is rescaled.  P is at most 2^2 x 64 of 448.
 //
 // Work is the sequence of tiles of all (request, KV head) units; each of at most
 // two CTAs an SM takes an equal run of it, so one long request spreads over the
@@ -50,7 +54,7 @@ constexpr int kThreads = 256;
 constexpr uint32_t kStage = 128 * 128;  // bytes of a K or V tile
 constexpr float kNone = -3.0e38f;       // running maximum before any key
 constexpr float kSlack = 2.f;           // log2 units a score may pass it by
-constexpr float kPUnit = 64.f;          // P's scale into E4M3
+constexpr float kPUnit = 6.f;           // log2 of P's scale into E4M3
 // Short caches: two to four tiles one after the other (about 1.5 us each) against a
 // second launch and its loads (2 us on the GPU, 3 to 4 on the host).
 constexpr int kWhole = 4;
@@ -112,8 +116,7 @@ struct Misc {
   alignas(16) float rs[2][C::ROWS];  // softmax scale (log2) x q's power of two, by row
   alignas(16) float wmax[4][C::ROWS];  // by warp: a tile's maxima, a segment's sums
   alignas(16) float mrow[4][C::ROWS];  // running maxima, a copy a warp
-  float ksc[3][16], vsc[3][16];  // scales of a tile's boxes
-  float wv[4];
+  float ksc[3][16], vsc[3][16], vlog[3][16];  // scales of a tile's boxes, log2 of V's
   alignas(16)
   int nankey[D];  // first key past the first row's whose V is NaN, by element
   // the scan
@@ -177,6 +180,11 @@ __device__ __forceinline__ void split3(uint32_t x, uint16_t& t0, uint16_t& t1, u
       "cvt.rn.satfinite.e4m3x2.f16x2 %2, r;\n\t}"
       : "=&h"(t0), "=&h"(t1), "=&h"(t2)
       : "r"(x));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
   uint32_t r;
@@ -366,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane < 16) {
           ms.ksc[vs][lane] = ok ? k_scale : 0.f;
           ms.vsc[vs][lane] = ok ? v_scale : 0.f;
+          ms.vlog[vs][lane] = ok ? scale_log2(v_scale) : 0.f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.scfull[vs]);
@@ -567,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         }
       };
-      float vref = 0.f, vmul = 0.f;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) l[j] = 0.f;
       if constexpr (kHeld) {
@@ -584,10 +592,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         float s[ROWS * KPR];
         wait(&ms.scfull[vs], (uint32_t)(i / NV) & 1u);
         const int box = t >> prm.box_shift;
-        const float ks = ms.ksc[vs][box], vsc = ms.vsc[vs][box];
+        const float ks = ms.ksc[vs][box], vlog = ms.vlog[vs][box];
         wait(&ms.sfull[sb], (uint32_t)(i / SB) & 1u);
         tc::fence_after_sync();
-        bool over = vsc > vref;
+        bool over = false;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if (c < nch) {
@@ -604,9 +612,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int p = 0; p < KPR; ++p)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                float x = __uint_as_float(v[p][j]) * (ks * rs[j]);
+                float x = fmaf(__uint_as_float(v[p][j]), ks * rs[j], vlog);
                 if (edge && key0 + p > sg.pos0 + token_of(c * 8 + j)) x = -INFINITY;
-                over |= x - mv[j] > kSlack;
+                over |= x - mv[j] > kSlack + kPUnit;
                 s[(c * KPR + p) * 8 + j] = x;
               }
           }
@@ -628,14 +636,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 at[1] = make_float4(w[4], w[5], w[6], w[7]);
               }
             }
-          float vm = warp_max(vsc);
-          if (lane == 0) ms.wv[warp] = vm;
           named_bar_sync(1, 128);
-          vm = fmaxf(fmaxf(ms.wv[0], ms.wv[1]), fmaxf(ms.wv[2], ms.wv[3]));
-          const float vnew = fmaxf(vref, fmaxf(vm, 7.5e-37f));
-          const float fv = vref / vnew;
-          vref = vnew;
-          vmul = kPUnit / vnew;
           if (kt > kt0) wait(&ms.pfree[(i - 1) % NPB], (uint32_t)((i - 1) / NPB) & 1u);
           tc::fence_after_sync();
 #pragma unroll
@@ -655,11 +656,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int q = c * 8 + j + k;
-                  const float mn = fmaxf(mv[j + k], top[k]);
+                  const float mn = fmaxf(mv[j + k], top[k] - kPUnit);
                   f[j + k] = ex2_approx(mv[j + k] - mn);
                   l[q] *= f[j + k];
                   mv[j + k] = mn;
-                  f[j + k] *= fv;
                 }
               }
               if constexpr (kHeld) {
@@ -697,7 +697,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           tc::wait_st();
         }
         if (i >= NPB) wait(&ms.pfree[pb], (uint32_t)(i / NPB - 1) & 1u);
-        const float vr = vsc * vmul;
+        // the V scale's sign goes to P, and a scale of zero makes P zero
+        const float vsc = ms.vsc[vs][box];
+        const uint32_t sign = fabsf(vsc) < kLeastScale ? 0u : vsc < 0.f ? 0xbc00bc00u : 0x3c003c00u;  // 0, -1 or 1, twice
 #pragma unroll
         for (int c = 0; c < CH; ++c)
           if (c < nch) {
@@ -709,12 +711,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
               for (int j = 0; j < 8; j += 2) {
                 const int q = c * 8 + j;
-                const float p0 = ex2_approx(s[(c * KPR + p) * 8 + j] - mv[j]);
-                const float p1 = ex2_approx(s[(c * KPR + p) * 8 + j + 1] - mv[j + 1]);
-                l[q] += p0;
-                l[q + 1] += p1;
+                const float x0 = s[(c * KPR + p) * 8 + j] - mv[j], x1 = s[(c * KPR + p) * 8 + j + 1] - mv[j + 1];
+                l[q] += ex2_approx(x0 - vlog);
+                l[q + 1] += ex2_approx(x1 - vlog);
                 uint16_t u[3];
-                split3(to_f16x2(p0 * vr, p1 * vr), u[0], u[1], u[2]);
+                split3(mul_f16x2(to_f16x2(ex2_approx(x0), ex2_approx(x1)), sign), u[0], u[1], u[2]);
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                   sts8(pof[j] + at + k * 1024, u[k]);
@@ -758,7 +759,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       wait(&ms.pfree[(i - 1) % NPB], (uint32_t)((i - 1) / NPB) & 1u);
       tc::fence_after_sync();
       // through shared memory (P's room), a warp a row then
-      const float od = vref * (1.f / kPUnit);
       float* stage = reinterpret_cast<float*>(smem + C::offP);  // [ROWS][128]
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float x = __uint_as_float(v[j]);
             x = fmaf(__uint_as_float(v[8 + j]), 0.0625f, x);
             x = fmaf(__uint_as_float(v[16 + j]), 0.00390625f, x);
-            stage[(c * 8 + j) * 128 + t] = x * od;
+            stage[(c * 8 + j) * 128 + t] = x;
           }
           // the warp's sums of 8 rows: halves, quarters, eighths of the rows a lane
           float h[4];

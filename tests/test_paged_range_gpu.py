@@ -1,0 +1,141 @@
+"""gist_attn_paged_fp8kv over its whole range: V scales of one sequence far apart, q
+of large logits, far positions.  Every element has a tolerance of its own, summed
+from the roundings of one token and head:
+
+  output    2^-8 |out|, its rounding to bf16
+  weights   each off by 2^-10 of itself at most (11 bits and the sums), and by
+            2^-24 of the largest weight x scale where they are smaller than that:
+            2^-10 sum_j p_j |v_j| + keys 2^-24 448 max_j(p_j scale_j)
+  scores    q element i carried to 2^-15.8 of itself and 2^-17 of the row's largest,
+            the errors independent and uniform: six deviations of their sum over
+            i; and 2^-20 of the products' magnitudes for sums and angles in fp32.
+            An error e_j of score j moves the output by sum_j p_j |v_j| (e_j + sum p e)
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_utils as pu
+from attention_cached_kv_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SENTINEL = -77.0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    binding.load_library()
+    yield
+    torch.cuda.empty_cache()
+
+
+def expected(pb, rotated):
+    """The definition in 64 bits and the tolerance of each element."""
+    q, d = pb.q.double().numpy(), pb.dims["head_dim"]
+    scale = pb.scale.astype(np.float32).astype(np.float64)
+    sc = 1 / math.sqrt(d)
+    out, tol = np.full(q.shape, np.nan), np.full(q.shape, np.nan)
+    for r, C in enumerate(pb.kv_len):
+        a, b = pb.q_start[r], pb.q_start[r + 1]
+        ids = pb.table[r, :-(-C // pb.bl)]
+        pos = C - (b - a) + np.arange(b - a)
+        x = q[a:b] if rotated else pu.rotate(q[a:b], pos)
+        for h in range(q.shape[1]):
+            g = h // pb.G
+            kk, vv = ((pu.E4M3[pb.codes[ids, pb.layer, kv, g]] * scale[ids, pb.layer, kv, g][:, None, None]).reshape(-1, d)[:C]
+                      for kv in (0, 1))
+            vs = np.repeat(np.abs(scale[ids, pb.layer, 1, g]), pb.bl)[:C]
+            for i, p in enumerate(pos):
+                k, v, y, s_v = kk[:p + 1], vv[:p + 1], x[i, h], vs[:p + 1]
+                s = k @ y * sc
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                dq = 2.0 ** -15.8 * np.abs(y) + 2.0 ** -17 * np.abs(y).max()
+                e = sc * (6 / math.sqrt(3) * np.sqrt((k * k) @ (dq * dq)) + 2.0 ** -20 * (np.abs(k) @ np.abs(y)))
+                o = w @ v
+                mag = np.abs(v) * w[:, None]
+                out[a + i, h] = o
+                tol[a + i, h] = (2.0 ** -8 * np.abs(o) + 2.0 ** -10 * mag.sum(0) + len(s) * 2.0 ** -24 * 448 * (w * s_v).max()
+                                 + (mag * (e + w @ e)[:, None]).sum(0))
+    return out, tol
+
+
+def check(pb, what, rotated=False, status=0):
+    args = pb.args()
+    out = torch.full_like(args[0], SENTINEL)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    binding.gist_attn_paged_fp8kv(*args, out, dims=dict(pb.dims, flags=binding.FLAG_PREROTATED if rotated else 0), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == status, what
+    got = out.float().cpu().numpy().astype(np.float64)
+    ref, tol = expected(pb, rotated)
+    written = ~np.isnan(ref)
+    assert (got[~written] == SENTINEL).all(), f"{what}: padding rows were written"
+    assert np.isfinite(got[written]).all(), what
+    worst = (np.abs(got - ref)[written] / np.maximum(tol[written], 1e-37)).max()
+    assert worst <= 1.0, f"{what}: worst error / tolerance {worst:.3f}"
+
+
+def outlier(pb, r, block, k, low):
+    """Block `block` of request r gets V scales 2^k, and keys that score about -2 low (in
+    a head whose q has 4 as its first element, prerotated)."""
+    blk = pb.table[r, block]
+    d = pb.dims["head_dim"]
+    pb.scale[blk, pb.layer, 1] = 2.0 ** k
+    pb.codes[blk, pb.layer, 0] = 0
+    pb.codes[blk, pb.layer, 0, ..., 0] = pu.encode(np.array(-448.0))
+    pb.scale[blk, pb.layer, 0] = 2.0 * low * math.sqrt(d) / (4 * 448.0)
+
+
+# new tokens, heads, d: 4, 12, 1 and 32 rows (of which d = 64 takes 16 at most)
+FEW = [(n, Hq, Hkv, d) for n, Hq, Hkv in ((1, 8, 2), (3, 8, 2), (1, 4, 4)) for d in (64, 128)] + [(2, 32, 2, 128), (1, 32, 2, 64)]
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,d", FEW)
+@pytest.mark.parametrize("k", [4, 10, 16, 24, 60])
+@pytest.mark.parametrize("block", [0, 7, -1])
+def test_few_rows_beside_a_block_of_large_v_scale(new, Hq, Hkv, d, k, block):
+    """A block of hardly any weight, met first, in the middle or last, takes no bits from
+    the others; in the last block it is one that earlier drafted tokens do not see."""
+    pb = pu.Problem([300, 40], [new] * 2, Hq, Hkv, d, 16, seed=k + new)
+    pb.q[..., 0] = 4.0
+    n = -(-int(pb.kv_len[0]) // 16)
+    outlier(pb, 0, block % n, k - 7, k)
+    check(pb, f"k={k} block={block}", rotated=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_with_v_scales_in_every_order(d):
+    """Scales that fall, rise and alternate by 2^30 along the sequence, weights alike; a
+    sequence long enough to be joined from parts."""
+    for kind in range(3):
+        pb = pu.Problem([3000, 90], [1, 2], 8, 2, d, 16, seed=kind)
+        n = -(-int(pb.kv_len[0]) // 16)
+        ramp = np.linspace(-15, 15, n).round()
+        e = [ramp, -ramp, np.where(np.arange(n) % 2, 15.0, -15.0)][kind]
+        pb.scale[pb.table[0, :n], pb.layer, 1] = (2.0 ** e)[:, None]
+        check(pb, f"kind {kind}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_with_v_scales_at_the_ends_of_their_range(d):
+    """Blocks of zeros at append's smallest scale, blocks of scale zero and of negative
+    scale among ordinary ones; sequences of nothing else."""
+    pb = pu.Problem([100, 50, 33, 20], [1, 2, 1, 1], 4, 2, d, 16, seed=4)
+    t, V = pb.table, (pb.layer, 1)
+    for r, blocks in ((0, [0, 3]), (2, [0, 1, 2])):
+        for b in blocks:
+            pb.codes[t[r, b]][V] = 0
+            pb.scale[t[r, b]][V] = 2.0 ** -100
+    pb.scale[t[0, 1]][V] = 0.0
+    pb.scale[t[0, 4]][V] *= -1
+    pb.scale[t[1, :4], pb.layer, 1] = 0.0
+    pb.scale[t[3, :2], pb.layer, 1] = 2.0 ** 100
+    check(pb, "ends")
