@@ -84,12 +84,14 @@ __device__ __forceinline__ void terms3(uint32_t x, uint16_t& t0, uint16_t& t1, u
 }
 
 // The attention kernels hold exp2(s + log2 |v| - m), v the V scale of a key's block and m the
-// running maximum of s + log2 |v|, and sum exp2(s - m) apart: with |v| in [2^-100, 2^119],
-// as gist_kv_append_fp8 writes it, neither leaves fp32's range.  Smaller ones count as zero.
-constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100
+// running maximum of s + log2 |v| (up to 8 of it are slack, 6 a unit), and sum exp2(s - m)
+// apart.  With |v| from 2^-96 to 2^100 that sum stays in fp32's range: 2^20 keys of the
+// least scale come to 2^(96 + 8 + 20), and beside a key of the largest all of at least
+// 2^-26 of its weight count.  Smaller scales count as zero, larger ones are reported.
+constexpr float kLeastScale = 1.262177448353619e-29f, kMostScale = 1.2676506002282294e+30f;
 __device__ __forceinline__ float scale_log2(float v) {
   const float a = fabsf(v);
-  return a < kLeastScale ? -100.f : log2f(a);
+  return a < kLeastScale ? -96.f : log2f(a);
 }
 
 // The requests of a step, as the attention kernels walk them.

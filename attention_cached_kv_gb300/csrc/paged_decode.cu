@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           ms.bad[seg & 7] = 1;
           report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
         }
+        if (ok && fabsf(v_scale) > kMostScale) report(prm.status, GIST_ATTN_STATUS_RANGE);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * br * 128;
         const int inner = row % vbl;
         if (__any_sync(0xffffffffu, (i >= NK && !mbar_wait(&ms.kfree[ks], ((uint32_t)(i / NK) & 1u) ^ 1u)))) {
@@ -656,9 +657,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const int q = c * 8 + j + k;
-                  const float mn = fmaxf(mv[j + k], top[k] - kPUnit);
-                  f[j + k] = ex2_approx(mv[j + k] - mn);
-                  l[q] *= f[j + k];
+                  // (in two steps: where the maximum moves by V scales the sum may be far from 1)
+                  const float mn = fmaxf(mv[j + k], top[k] - kPUnit), half = ex2_approx(0.5f * (mv[j + k] - mn));
+                  f[j + k] = half * half;
+                  l[q] = l[q] * half * half;
                   mv[j + k] = mn;
                 }
               }
@@ -899,14 +901,15 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
 #pragma unroll
       for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
       top = fmaxf(top, m);
-      const float f = exp2f(m - top);
+      const float half = exp2f(0.5f * (m - top)), f = half * half;
       m = top;
-      sum *= f;
+      sum = sum * half * half;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] *= f;
       for (int v = lane; v < nv; v += 32) {
         const float2 x = h[v];
-        sum += x.y * exp2f(x.x - m);
+        const float half = exp2f(0.5f * (x.x - m));
+        sum += x.y * half * half;
         bad |= x.y < 0.f;
       }
 #pragma unroll 8

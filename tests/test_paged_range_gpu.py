@@ -139,3 +139,37 @@ def test_few_rows_with_v_scales_at_the_ends_of_their_range(d):
     pb.scale[t[1, :4], pb.layer, 1] = 0.0
     pb.scale[t[3, :2], pb.layer, 1] = 2.0 ** 100
     check(pb, "ends")
+
+
+def spread(pb, r, e, rng):
+    """Request r's V scales 2^e (repeated along its blocks), and a fifth of the blocks zeros
+    at the smallest scale."""
+    n = -(-int(pb.kv_len[r]) // pb.bl)
+    e = np.resize(np.asarray(e, dtype=np.float64), n)
+    for b in range(n):
+        at = (pb.table[r, b], pb.layer, 1)
+        pb.scale[at] = 2.0 ** e[b]
+        if rng.random() < 0.2:
+            pb.codes[at] = 0
+            pb.scale[at] = 2.0 ** -100
+
+
+SPREADS = [[-90, 0, 90], [90, -90], [60, 20, -20, -60, -95], [-95, -90, -60, 0, 60, 99], [-95] * 3 + [50]]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", SPREADS)
+def test_few_rows_with_v_scales_over_their_whole_range(d, e):
+    """From 2^-95 to 2^99 in one sequence, rising, falling and alternating along it."""
+    pb = pu.Problem([330, 2000, 100], [1, 2, 1], 4, 2, d, 16, seed=len(e))
+    rng = np.random.default_rng(2)
+    for r in range(3):
+        spread(pb, r, e if r != 1 else np.repeat(e, 126 // len(e) + 1), rng)
+    check(pb, f"{e}")
+
+
+@pytest.mark.parametrize("new", [1, 2])
+def test_few_rows_report_v_scales_past_the_range(new):
+    pb = pu.Problem([100, 50], [new, new], 4, 2, 64, 16, seed=4)
+    pb.scale[pb.table[1, 1], pb.layer, 1] = 2.0 ** 110
+    check(pb, "past", status=binding.STATUS_RANGE)
