@@ -84,10 +84,10 @@ __device__ __forceinline__ void terms3(uint32_t x, uint16_t& t0, uint16_t& t1, u
 }
 
 // The attention kernels hold exp2(s + log2 |v| - m), v the V scale of a key's block and m the
-// running maximum of s + log2 |v| (up to 8 of it are slack, 6 a unit), and sum exp2(s - m)
-// apart.  With |v| from 2^-96 to 2^100 that sum stays in fp32's range: 2^20 keys of the
-// least scale come to 2^(96 + 8 + 20), and beside a key of the largest all of at least
-// 2^-26 of its weight count.  Smaller scales count as zero, larger ones are reported.
+// running maximum of s + log2 |v| (which may stay 12 behind), and sum exp2(s - m) apart.
+// With |v| from 2^-96 to 2^100 that sum stays in fp32's range: 2^19 keys of the least scale
+// come to 2^(96 + 12 + 19) at most, and beside a key of the largest all of at least 2^-26 of
+// its weight count.  Smaller scales count as zero, larger ones are reported.
 constexpr float kLeastScale = 1.262177448353619e-29f, kMostScale = 1.2676506002282294e+30f;
 __device__ __forceinline__ float scale_log2(float v) {
   const float a = fabsf(v);

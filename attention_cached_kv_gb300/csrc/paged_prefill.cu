@@ -3,14 +3,15 @@
 //
 // A CTA takes one KV head and up to 256 query rows of a request: two row tiles of
 // floor(128 / G) tokens x G heads.  Its keys stream by in tiles of 128, one pass,
-//     S = q K^T, P = exp2(S - m), O += P V       (tcgen05 kind::f16, TMEM)
-// with m the row's running maximum, moved only when a tile's maximum passes it by
-// more than 8 (log2 units).  The warps:
+//     S = q K^T, P = exp2(S + log2 v - m), O += P V       (tcgen05 kind::f16, TMEM)
+// with v the V scale of a key's block, V its codes, and m the row's running maximum of
+// S + log2 v, moved only when a tile's maximum passes it by more than 12 (log2 units).
+// The sum of weights is of P / v.  So P's bits go by what a key adds to the row, and the
+// values are exact.  The warps:
 //   * 0-3, 4-7: a thread a row of each row tile, softmax and output; P goes back
 //     into S's columns as f16 (11 bits), A operand of the second product;
-//   * 8-11: cached rows from global memory through registers into f16 tiles, exactly;
-//     values are also divided by the largest V scale of the request (exact for powers of
-//     two), K's block scales multiply the fp32 scores;
+//   * 8-11: cached rows from global memory through registers into f16 tiles, exactly
+//     (K's block scales multiply the fp32 scores);
 //   * 12: the MMAs, alternating between the row tiles, so that one's products run
 //     while the other's softmax does;
 //   * 13: block ids and scales, four tiles at a time, ahead of the copies;
@@ -52,7 +53,12 @@ constexpr int kThreads = 480;         // 8 softmax, 4 converting, MMA, look-up, 
 constexpr int kRing = 8;              // tiles whose look-ups are held, in two halves
 constexpr int kKT = 128;              // keys a tile
 constexpr float kNone = -3.0e38f;     // running maximum before any key
-constexpr float kSlack = 8.f;         // log2 units a score may pass it by
+// Log2 units that a score may pass it by (P stays below f16's 2^16).  A tile that passes it
+// is done twice: with 8, where V scales differ by 2^2, the chunks below took 295 us for 252.
+constexpr float kSlack = 12.f;
+// While no V scale is outside 2^+-45 the sum's terms are P / v: P is at least 2^-126 for all
+// keys of 2^-36 of the largest weight and more.  Otherwise they are exponentials of their own.
+constexpr float kPlain = 45.f;
 
 constexpr int kStartCost = 512;       // keys that a unit's start is worth
 
@@ -90,7 +96,7 @@ struct PCfg {
 
 // One unit's share of a CTA.
 struct PSeg {
-  int r, g, q0, toks, pos0, kend, kv, kt0, nt, slot;
+  int r, g, q0, toks, pos0, kend, kt0, nt, slot;
   bool two, whole;
 };
 
@@ -136,7 +142,6 @@ struct PWalk {
     const int c = cost(), tok0 = p * w;
     s.r = r;
     s.g = g;
-    s.kv = kv;
     s.toks = min(w, n - tok0);
     s.q0 = prm.rq.q_start[r] + tok0;         // first token row
     s.pos0 = max(kv, 0) - n + tok0;          // position of the first token
@@ -172,25 +177,31 @@ struct Tile {
   int all;   // rows that every query row sees
   int key0;  // its first key
   int sl;    // its segment's slot
-  int r, g, kv;
   int full;  // all of its rows are seen, and all in the pool
+  int odd;   // some are in a block outside the pool, or of V scale zero or negative
+};
+
+// Of a 16-key group.
+struct alignas(16) Scales {
+  float k, vlog;  // K scale, log2 of the V scale
+  float vinv;     // the V scale's inverse (infinite: a scale that counts as zero)
+  int wide;       // (of the tile)
 };
 
 template <int D>
 struct PMisc {
   uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
   uint32_t tmem;
-  int bad[4], any_nan[4];  // by segment (modulo 4), as vref and nankey
+  int bad[4], any_nan[4];  // by segment (modulo 4), as nankey
   int64_t warp_sum[kThreads / 32], start_pre, total;
   int start_r;
   PSeg seg[2];  // the softmax warps' segments
   int any_seg[2];  // 0: there is no further one
-  // by tile (modulo kRing) and 16-key group: K and V scale, first byte of the K rows in
-  // the pool (-1: no key that is seen, or a block outside the pool)
-  alignas(16) float ksc[kRing][8], vsc[kRing][8];
+  // by tile (modulo kRing) and 16-key group: scales; first byte of the K rows in the pool
+  // (-1: no key that is seen, -2: a block outside the pool)
+  Scales scales[kRing][8];
   int64_t at[kRing][8];
   Tile tile[kRing];
-  float vref[4], vpart[4];
   int nankey[4][D];  // first key past the first row's whose V is NaN, by element
 };
 
@@ -214,11 +225,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
 }
 __device__ __forceinline__ void sts_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -412,17 +418,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       have = false;
     };
-    int blk = -1, key = 0;
+    int blk = -1, key = 0, g = 0;
     Tile tl;
     auto look_up = [&]() {
       settle();
       want = false;
       blk = -1;
-      tl = Tile{INT32_MIN, 0, 0, 0, 0, 0, 0, 0};
+      tl = Tile{INT32_MIN, 0, 0, 0, 0, 0};
       if (have) {
         const int key0 = (sg.kt0 + e) * kKT;
         key = key0 + gr * 16;
-        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, sg.r, sg.g, sg.kv, 0};
+        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, 0, 0};
+        g = sg.g;
         want = key < sg.kend;
         if (want) blk = rq.block_table[(int64_t)sg.r * rq.W + key / rq.block_len];
         e += 4;
@@ -435,18 +442,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int half = (i >> 2) & 1;
       const bool ok = want && blk >= 0 && blk < prm.num_blocks, lost = want && !ok;
       if (lost) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
-      now.full = (__ballot_sync(0xffffffffu, ok) >> (8 * t) & 0xffu) == 0xffu && now.left >= kKT;
-      const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + now.g;
-      const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : -1;
-      const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : lost ? -1.f : 0.f;
+      const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + g;
+      const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : lost ? -2 : -1;
+      const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : 1.f;
+      const float vlog = scale_log2(vs), vinv = fabsf(vs) < kLeastScale ? INFINITY : 1.f / vs;
+      if (fabsf(vs) > kMostScale) report(prm.status, GIST_ATTN_STATUS_RANGE);
+      auto in_tile = [&](bool p) { return __ballot_sync(0xffffffffu, p) >> (8 * t) & 0xffu; };
+      now.full = in_tile(ok) == 0xffu && now.left >= kKT;
+      now.odd = in_tile(lost || vs < kLeastScale) != 0;
+      const uint32_t above = in_tile(vlog > kPlain), below = in_tile(vlog < -kPlain);
+      const int wide = above ? 2 : below ? 1 : 0;  // some V scale is outside 2^+-kPlain (2: above)
       if (!last) look_up();  // its load runs while this half is waited for
       if (__any_sync(0xffffffffu, i >= kRing && !mbar_wait(&ms.gfree[half], ((uint32_t)(i >> 3) & 1u) ^ 1u))) {
         failed = true;
         break;
       }
       const int slot = (i + t) & (kRing - 1);
-      ms.ksc[slot][gr] = ks;
-      ms.vsc[slot][gr] = vs;  // (-1: the block id is outside the pool)
+      ms.scales[slot][gr] = Scales{ks, vlog, vinv, wide};
       ms.at[slot][gr] = at;
       if (gr == 0) ms.tile[slot] = now;
       __syncwarp();
@@ -476,25 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr int kPass = 128 / kRows;
     const int ct = tid - 256, c = ct % kLanes, row0 = ct / kLanes;
     const int64_t vstep = (int64_t)rq.Hkv * rq.block_len * D;
-    // The largest V scale of the request's blocks.
-    auto largest = [&](int r, int g, int kv) {
-      const int32_t* table = rq.block_table + (int64_t)r * rq.W;
-      float top = 0.f;
-      const int blocks = (kv + rq.block_len - 1) / rq.block_len;
-#pragma unroll 4
-      for (int b = ct; b < blocks; b += 128) {
-        const int blk = table[b];
-        const bool ok = blk >= 0 && blk < prm.num_blocks;
-        const float s = prm.scale[(((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 + 1) * rq.Hkv + g];
-        top = fmaxf(top, ok ? s : 0.f);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      named_bar_sync(2, 128);
-      if (lane == 0) ms.vpart[warp - 8] = top;
-      named_bar_sync(2, 128);
-      return fmaxf(fmaxf(fmaxf(ms.vpart[0], ms.vpart[1]), fmaxf(ms.vpart[2], ms.vpart[3])), 7.5e-37f);
-    };
     uint4 kx[kPass], vx[kPass];
     auto fetch = [&](int i, uint4 (&x)[kPass], int64_t more) {
       const int left = ms.tile[i & (kRing - 1)].left;  // rows of the tile that are seen
@@ -528,8 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto element = [&](uint32_t tile, int k) {
       return tile + (c / 4) * C::kPanel + swz128((k >> 4) * kRows + row0, 2 * (c % 4) + ((k >> 3) & 1)) + (k & 7) * 2;
     };
-    int last_r = -1, last_g = -1;
-    float vref = 0.f, rvref = 0.f;
     if (looked_up(0)) {
       fetch(0, kx, 0);
       fetch(0, vx, vstep);
@@ -538,25 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const Tile& tl = ms.tile[i & (kRing - 1)];
       if (tl.left == INT32_MIN) break;
       const int b = i & 1, sl = tl.sl;
-      if (tl.r != last_r || tl.g != last_g) {
-        last_r = tl.r;
-        last_g = tl.g;
-        vref = largest(last_r, last_g, tl.kv);
-        rvref = 1.f / vref;
-      }
-      if (ct == 0) ms.vref[sl] = vref;
       if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
         break;
-      }
-      // the values' factors (read before the tiles are written: the loads cannot pass those)
-      uint32_t mul[kPass];
-      bool lost = false;
-#pragma unroll
-      for (int p = 0; p < kPass; ++p) {
-        const float vs = ms.vsc[i & (kRing - 1)][(p * kRows + row0) >> 4], f = vs * rvref;
-        lost |= vs < 0.f;
-        mul[p] = to_f16x2(f, f);
       }
       const uint32_t ktile = sbase + C::offK + b * C::kTile, vtile = sbase + C::offV + b * C::kTile;
 #pragma unroll
@@ -577,6 +552,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         failed = true;
         break;
       }
+      if (tl.odd) {
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+          const int gr = (p * kRows + row0) >> 4;
+          if (ms.at[i & (kRing - 1)][gr] == -2) ms.bad[sl] = 1;
+          const float inv = ms.scales[i & (kRing - 1)][gr].vinv;
+          auto turn = [&](uint32_t w) {  // the scale's sign; zeros but for NaN
+            const uint32_t nan = e4m3_nan(w);
+            return isinf(inv) ? nan - (nan >> 7) : signbit(inv) ? w ^ 0x80808080u : w;
+          };
+          vx[p] = make_uint4(turn(vx[p].x), turn(vx[p].y), turn(vx[p].z), turn(vx[p].w));
+        }
+      }
       // keys that not every row sees: a NaN would reach the others (0 x NaN)
       const int all = tl.all;
       bool nan = false;
@@ -591,12 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          h[2 * e] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)w[e]), mul[p]);
-          h[2 * e + 1] = mul_f16x2(e4m3x2_to_f16x2((uint16_t)(w[e] >> 16)), mul[p]);
+          h[2 * e] = e4m3x2_to_f16x2((uint16_t)w[e]);
+          h[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(w[e] >> 16));
         }
         put(vtile, p * kRows + row0, h);
       }
-      if (lost) ms.bad[sl] = 1;
       if (nan) {  // noted for the rows that see it, and cleared
         ms.any_nan[sl] = 1;
 #pragma unroll 1
@@ -701,19 +688,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_arrive(&ms.qready);
       }
       float m = kNone;
-      uint64_t acc = f2_make(0.f, 0.f), acc2 = acc;
+      bool far = false;  // some V scale of the segment is above 2^kPlain
+      uint64_t acc = f2_make(0.f, 0.f);
       const bool live = x == 0 || sg.two;
       for (int e = 0; live && e < nt; ++e) {
         const int i = i0 + e, key0 = (kt0 + e) * kKT;
         const bool edge = key0 + kKT > lim_all;
         wait(&ms.sfull[x], ns++ & 1u);
         tc::fence_after_sync();
-        const float* ksc = ms.ksc[i & (kRing - 1)];
-        // 16 scores v of chunk c (16 keys) as weights exp2(f v - m), packed; their sum into
-        // acc; returns their largest exponent
-        auto weights = [&](int c, const uint32_t (&v)[16], uint32_t* pk, int left) {
-          const float f = ksc[c] * rs;
-          const uint64_t g2 = f2_make(f, f), nm2 = f2_make(-m, -m);
+        const Scales* scales = ms.scales[i & (kRing - 1)];
+        const uint32_t sca = smem_u32(scales);
+        uint4 s0 = lds16(sca), s1;
+        far |= s0.w == 2;  // (the maximum is above all sums from here on)
+        const bool own = far || s0.w != 0;
+        // 16 scores v of a group with scales sw as weights exp2(f v + log2 scale - m), packed;
+        // their sum without the scale into acc; returns their largest exponent
+        auto weights = [&](auto own_sum, uint4 sw, const uint32_t (&v)[16], uint32_t* pk, int left) {
+          const float f = __uint_as_float(sw.x) * rs, lg = __uint_as_float(sw.y);
+          const float w = decltype(own_sum)::value ? 1.f : fabsf(__uint_as_float(sw.z));
+          const uint64_t g2 = f2_make(f, f), nm2 = f2_make(lg - m, lg - m);
+          uint64_t sum = 0;
           float top = kNone;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -723,17 +717,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (2 * k + 1 >= left) b = -INFINITY;
             top = max3f(top, a, b);
             const float pa = ex2_approx(a), pb = ex2_approx(b);
-            if (k & 1) acc = f2_add(acc, f2_make(pa, pb));
-            else acc2 = f2_add(acc2, f2_make(pa, pb));
+            const uint64_t p = decltype(own_sum)::value ? f2_make(ex2_approx(a - lg), ex2_approx(b - lg)) : f2_make(pa, pb);
+            sum = k == 0 ? p : f2_add(sum, p);
             pk[k] = to_f16x2(pa, pb);
           }
+          acc = f2_fma(sum, f2_make(w, w), acc);
           return top;
         };
         // One pass with the maximum as it is; P stays in registers until it is known that
         // no row's scores passed it by too much.
         bool done = false;
         if (!edge && e > 0) {
-          const uint64_t keep = acc, keep2 = acc2;
+          const uint64_t keep = acc;
           uint32_t va[16], vb[16], pk[64];
           float top = kNone;
           tc::ld16(ts, va);
@@ -741,19 +736,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 8; c += 2) {
             tc::ld16(ts + c * 16 + 16, vb);
-            top = fmaxf(top, weights(c, va, pk + c * 8, 16));
+            s1 = lds16(sca + c * 16 + 16);
+            top = fmaxf(top, weights(std::false_type{}, s0, va, pk + c * 8, 16));
             tc::wait_ld();
-            if (c + 2 < 8) tc::ld16(ts + c * 16 + 32, va);
-            top = fmaxf(top, weights(c + 1, vb, pk + c * 8 + 8, 16));
+            if (c + 2 < 8) {
+              tc::ld16(ts + c * 16 + 32, va);
+              s0 = lds16(sca + c * 16 + 32);
+            }
+            top = fmaxf(top, weights(std::false_type{}, s1, vb, pk + c * 8 + 8, 16));
             tc::wait_ld();
           }
-          done = !__any_sync(0xffffffffu, top > kSlack);
+          done = !__any_sync(0xffffffffu, top > kSlack || own);
           if (done) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) st16(ts + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + c * 16));
           } else {
             acc = keep;
-            acc2 = keep2;
           }
         }
         if (!done) {
@@ -767,18 +765,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             tc::ld16(ts + c * 16, v);
             tc::wait_ld();
             const int left = edge ? lim - key0 - c * 16 : 16;  // columns of these that the row sees
+            const float f = scales[c].k * rs;
             float t = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) t = fmaxf(t, k < left ? __uint_as_float(v[k]) : -INFINITY);
-            mx = fmaxf(mx, t * (ksc[c] * rs));
+            for (int k = 0; k < 16; ++k) t = fmaxf(t, k < left ? __uint_as_float(v[k]) * f : -INFINITY);
+            mx = fmaxf(mx, t + scales[c].vlog);
           }
           const bool move = mx - m > kSlack;
           if (__any_sync(0xffffffffu, move)) {
-            const float fm = move ? ex2_approx(m - mx) : 1.f;
+            // (in two steps: where the maximum moves by V scales the sum may be far from 1)
+            const float half = move ? ex2_approx(0.5f * (m - mx)) : 1.f, fm = half * half;
             if (move) m = mx;
-            const uint64_t f2 = f2_make(fm, fm);
-            acc = f2_mul(acc, f2);
-            acc2 = f2_mul(acc2, f2);
+            const uint64_t half2 = f2_make(half, half);
+            acc = f2_mul(f2_mul(acc, half2), half2);
             if (e > 0) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
@@ -796,7 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             uint32_t v[16], pk[8];
             tc::ld16(ts + c * 16, v);
             tc::wait_ld();
-            weights(c, v, pk, edge ? lim - key0 - c * 16 : 16);
+            const int left = edge ? lim - key0 - c * 16 : 16;
+            s0 = lds16(sca + c * 16);
+            if (own) weights(std::true_type{}, s0, v, pk, left);
+            else weights(std::false_type{}, s0, v, pk, left);
             tc::st8(ts + c * 8, pk);
           }
         }
@@ -807,14 +809,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (live) {
         if (nt > 0) wait(&ms.sfull[x], ns++ & 1u);
         tc::fence_after_sync();
-        float a0, a1, b0, b1;
+        float a0, a1;
         f2_split(acc, a0, a1);
-        f2_split(acc2, b0, b1);
-        const float sum = (a0 + a1) + (b0 + b1);
+        const float sum = a0 + a1;
         const bool bad = nt > 0 && ms.bad[sl], none = lim <= 0 || bad, whole = sg.whole, nan = nt > 0 && ms.any_nan[sl];
-        const float vref = nt > 0 ? ms.vref[sl] : 0.f;
         if (valid && whole && !none && !(sum <= 3.0e38f)) report(prm.status, GIST_ATTN_STATUS_RANGE);
-        const float inv = whole ? vref / sum : vref;
+        const float inv = whole ? 1.f / sum : 1.f;
         float* part = prm.parts + (int64_t)(2 * me + sg.slot) * 256 * (D + 2);  // [256][D], then maxima, sums
         // through the row's place in q's room, so that a warp stores whole rows: all columns
         // as bf16, or one half after the other as fp32
@@ -922,10 +922,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Prefi
       }
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        const float top = fmaxf(m[k], pm[k]), f0 = exp2f(m[k] - top), f1 = exp2f(pm[k] - top);
+        const float top = fmaxf(m[k], pm[k]), h0 = exp2f(0.5f * (m[k] - top)), h1 = exp2f(0.5f * (pm[k] - top));
+        const float f0 = h0 * h0, f1 = h1 * h1;
         bad[k] |= ps[k] < 0.f;
         m[k] = top;
-        sum[k] = sum[k] * f0 + ps[k] * f1;
+        sum[k] = sum[k] * h0 * h0 + ps[k] * h1 * h1;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[k][e] = o[k][e] * f0 + f1 * po[k][e];
       }

@@ -525,8 +525,11 @@ size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims);
  * GIST_ATTN_STATUS_BAD_BLOCK; a kv_len past W * block_len zeroes all of the request's
  * rows and sets it too; a q_start pair outside [0, T], out of order or more than
  * max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
- * elsewhere.  block_len must be a multiple of 16, Hq / Hkv at most 128 and
- * W * block_len at most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).
+ * elsewhere, and where a V scale's magnitude is above 2^100; one below 2^-96 counts
+ * as zero.  The scales of a sequence's blocks may lie as far apart as that: a row's
+ * precision goes by its largest weight times V scale.  block_len must be a multiple
+ * of 16, Hq / Hkv at most 128 and W * block_len at most 2^30
+ * (GIST_ATTN_ERR_UNSUPPORTED).
  */
 int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3, const float* kv_scale,
                           const int32_t* block_table, const int32_t* q_start,

@@ -173,3 +173,61 @@ def test_few_rows_report_v_scales_past_the_range(new):
     pb = pu.Problem([100, 50], [new, new], 4, 2, 64, 16, seed=4)
     pb.scale[pb.table[1, 1], pb.layer, 1] = 2.0 ** 110
     check(pb, "past", status=binding.STATUS_RANGE)
+
+
+MANY = [(n, Hq, Hkv, d) for n, Hq, Hkv in ((40, 8, 2), (35, 4, 4), (150, 16, 2), (9, 40, 1)) for d in (64, 128)] + [(2, 32, 2, 64)]
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,d", MANY)
+@pytest.mark.parametrize("k", [4, 16, 24, 30, 60])
+@pytest.mark.parametrize("block", [0, 7, -1])
+def test_many_rows_beside_a_block_of_large_v_scale(new, Hq, Hkv, d, k, block):
+    """As with few rows; in the last block it is one that most new tokens do not see."""
+    pb = pu.Problem([300, 40], [new] * 2, Hq, Hkv, d, 16, seed=k + new)
+    pb.q[..., 0] = 4.0
+    n = -(-int(pb.kv_len[0]) // 16)
+    outlier(pb, 0, block % n, k - 7, k)
+    check(pb, f"k={k} block={block}", rotated=True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_with_v_scales_in_every_order(d):
+    for kind in range(3):
+        pb = pu.Problem([1500, 90], [33, 70], 4, 2, d, 16, seed=kind)
+        n = -(-int(pb.kv_len[0]) // 16)
+        ramp = np.linspace(-15, 15, n).round()
+        e = [ramp, -ramp, np.where(np.arange(n) % 2, 15.0, -15.0)][kind]
+        pb.scale[pb.table[0, :n], pb.layer, 1] = (2.0 ** e)[:, None]
+        check(pb, f"kind {kind}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_with_v_scales_at_the_ends_of_their_range(d):
+    pb = pu.Problem([100, 50, 33, 20, 300], [40, 39, 65, 38, 40], 4, 2, d, 16, seed=4)
+    t, V = pb.table, (pb.layer, 1)
+    for r, blocks in ((0, [0, 3]), (2, range(7)), (4, [2, 17])):
+        for b in blocks:
+            pb.codes[t[r, b]][V] = 0
+            pb.scale[t[r, b]][V] = 2.0 ** -100
+    pb.scale[t[0, 1]][V] = 0.0
+    for r, b in ((0, 4), (4, 3), (4, 10)):
+        pb.scale[t[r, b]] *= -1  # keys too
+    pb.scale[t[1, :6], pb.layer, 1] = 0.0
+    pb.scale[t[3, :4], pb.layer, 1] = 2.0 ** 100
+    check(pb, "ends")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", SPREADS)
+def test_many_rows_with_v_scales_over_their_whole_range(d, e):
+    pb = pu.Problem([330, 1500, 100], [40, 33, 70], 2, 1, d, 16, seed=len(e))
+    rng = np.random.default_rng(2)
+    for r in range(3):
+        spread(pb, r, e if r != 1 else np.repeat(e, 96 // len(e) + 1), rng)
+    check(pb, f"{e}")
+
+
+def test_many_rows_report_v_scales_past_the_range():
+    pb = pu.Problem([100, 50], [40, 39], 4, 2, 64, 16, seed=4)
+    pb.scale[pb.table[1, 1], pb.layer, 1] = 2.0 ** 110
+    check(pb, "past", status=binding.STATUS_RANGE)
