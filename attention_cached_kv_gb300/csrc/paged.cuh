@@ -68,19 +68,27 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) {
   return f;
 }
 
-// An f16 pair (magnitudes below 448) as the sum of three E4M3 pairs, each the rounded
-// remainder of the ones before: off by at most 2^-12 of a value or 2^-10.
-__device__ __forceinline__ void terms3(uint32_t x, uint16_t& t0, uint16_t& t1, uint16_t& t2) {
-  asm("{\n\t.reg .b32 f, r;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %0, %3;\n\t"
+// Two floats (magnitudes below 448) as the sums of four E4M3 pairs, each the rounded
+// remainder of the ones before: off by at most 2^-16 of a value or 2^-10, and 2^-19 of a
+// value where the second remainder goes on in f16.
+__device__ __forceinline__ void terms4(float lo, float hi, uint16_t& t0, uint16_t& t1, uint16_t& t2, uint16_t& t3) {
+  auto rest = [&](uint16_t t) {  // exact
+    const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(t));
+    lo -= f.x;
+    hi -= f.y;
+  };
+  t0 = e4m3x2(lo, hi);
+  rest(t0);
+  t1 = e4m3x2(lo, hi);
+  rest(t1);
+  asm("{\n\t.reg .b32 x, f;\n\t"
+      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, x;\n\t"
       "cvt.rn.f16x2.e4m3x2 f, %0;\n\t"
-      "sub.rn.f16x2 r, %3, f;\n\t"  // exact
-      "cvt.rn.satfinite.e4m3x2.f16x2 %1, r;\n\t"
-      "cvt.rn.f16x2.e4m3x2 f, %1;\n\t"
-      "sub.rn.f16x2 r, r, f;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 %2, r;\n\t}"
-      : "=&h"(t0), "=&h"(t1), "=&h"(t2)
-      : "r"(x));
+      "sub.rn.f16x2 x, x, f;\n\t"  // exact
+      "cvt.rn.satfinite.e4m3x2.f16x2 %1, x;\n\t}"
+      : "=&h"(t2), "=&h"(t3)
+      : "f"(lo), "f"(hi));
 }
 
 // The attention kernels hold exp2(s + log2 |v| - m), v the V scale of a key's block and m the

@@ -8,12 +8,14 @@
 //     S^T = K q^T      tcgen05 kind::f8f6f4, keys as M, the query rows as N
 //     O^T = V^T P^T    the V tile read transposed (M contiguous), P as N
 // so no cached element is ever converted.  q and P keep their precision as sums
-// of three E4M3 terms, each the rounded remainder of the last, together 11 bits or
-// more.  q's are added in TMEM, one product after the other: q is scaled by a power
-// of two a row, its largest value to 128 and more, and the terms reach 2^-17 of that.
-// P's small weights matter more (they are many), so its terms are kept apart,
-// p0 + p1 / 16 + p2 / 256, side by side as columns of N: the few query rows leave N
-// room that costs nothing.  The K scale of a key's block multiplies its fp32 scores s,
+// of E4M3 terms, each the rounded remainder of the last.  q has four, added in TMEM, one
+// product after the other: it is scaled by a power of two a row, its largest value to 128
+// and more, and the terms leave 2^-16 of a value or 2^-17 of that (a score is off by as
+// much of |q| |k|: after a rounding to f16, 2^-11, outputs of logits in the tens were off by
+// more than their rounding to bf16).  P, whose
+// rounding moves an output by as little of itself, has three of 11 bits or more; its small
+// weights matter (they are many), so they are kept apart, p0 + p1 / 16 + p2 / 256, side by
+// side as columns of N: the few query rows leave N room that costs nothing.  The K scale of a key's block multiplies its fp32 scores s,
 // the logarithm of its V scale is added to them: a weight with its V scale is
 // P = exp2(s + log2 v - m), without it exp2(s - m), and a row's output is the quotient of
 // the two sums (over P x V codes, and over the second).  So P's bits go by what a key adds
@@ -91,13 +93,13 @@ struct Cfg {
   static constexpr int SP = (8 * CH + 15) & ~15;   // S columns a parity
   static constexpr int OC = (KPR * 24 * CH + 15) & ~15;  // O columns
   static constexpr int SB = 2 * KPR * SP + OC <= 256 ? 2 : 1;  // S buffers
-  static constexpr uint32_t QT = 1024 * CH, QB = 3 * QT, PB = KPR * QB;
+  static constexpr uint32_t QT = 1024 * CH, QB = 4 * QT, PB = KPR * 3 * QT;
   static constexpr int NK = D == 128 && CH <= 2 ? 3 : D == 64 && CH == 1 ? 3 : 2;
   static constexpr int NV = D == 128 && CH == 1 ? 3 : 2;
   static constexpr uint32_t kO = SB * KPR * SP;  // O's first TMEM column
   static constexpr uint32_t offV = NK * kStage, offQ = offV + NV * kStage, offP = offQ + 2 * QB,
-                            kP = NPB * PB + 1024,  // (an MMA's N may run 8 rows past a tile)
-                            offMisc = offP + (kP > ROWS * 512 ? kP : ROWS * 512);
+                            offMisc = offP + NPB * PB + 1024;  // (an MMA's N may run 8 rows past a tile)
+  static_assert(QB >= ROWS * 512, "a segment's outputs leave through its q");
   static_assert(kO + OC <= 256, "TMEM columns");
 };
 
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int p = 0; p < KPR; ++p)
 #pragma unroll
-            for (int t = 0; t < 3; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
               for (int k = 0; k < D / 32; ++k)
                 tc::mma_ss_f8(tmem + (sb * KPR + p) * C::SP, tc::smem_desc_sw128(kb + p * 64 + k * 32, 16, 1024),
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float x = real ? __uint_as_float(e & 1 ? uw[e >> 1] & 0xffff0000u : uw[e >> 1] << 16) : 0.f;
           const float y = real ? __uint_as_float(e & 1 ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16) : 0.f;
           float sn, cs;
-          __sincosf(turn_angle(pos, turn[e]), &sn, &cs);
+          __sincosf(turn_angle(pos, turn[e]), &sn, &cs);  // off by 2^-21: under the terms' rounding
           a[e] = x * cs - y * sn;
           b[e] = y * cs + x * sn;
           top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
@@ -523,14 +525,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                : prm.scale_log2 * __uint_as_float((uint32_t)max(ex + 127, 1) << 23);
         const uint32_t base = sbase + C::offQ + qs * C::QB + row * 128;
         const uint32_t at = (uint32_t)(l * 8) ^ ((row & 7) << 4), bt = (uint32_t)(D / 2 + l * 8) ^ ((row & 7) << 4);
-        uint16_t ta[3][4], tb2[3][4];
+        uint16_t ta[4][4], tb2[4][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          terms3(to_f16x2(a[2 * e] * down, a[2 * e + 1] * down), ta[0][e], ta[1][e], ta[2][e]);
-          terms3(to_f16x2(b[2 * e] * down, b[2 * e + 1] * down), tb2[0][e], tb2[1][e], tb2[2][e]);
+          terms4(a[2 * e] * down, a[2 * e + 1] * down, ta[0][e], ta[1][e], ta[2][e], ta[3][e]);
+          terms4(b[2 * e] * down, b[2 * e + 1] * down, tb2[0][e], tb2[1][e], tb2[2][e], tb2[3][e]);
         }
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
+        for (int s = 0; s < 4; ++s) {
           sts64(base + s * C::QT + at, (uint32_t)ta[s][0] | (uint32_t)ta[s][1] << 16, (uint32_t)ta[s][2] | (uint32_t)ta[s][3] << 16);
           sts64(base + s * C::QT + bt, (uint32_t)tb2[s][0] | (uint32_t)tb2[s][1] << 16, (uint32_t)tb2[s][2] | (uint32_t)tb2[s][3] << 16);
         }
@@ -760,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- the segment's O, m and sums
       wait(&ms.pfree[(i - 1) % NPB], (uint32_t)((i - 1) / NPB) & 1u);
       tc::fence_after_sync();
-      // through shared memory (P's room), a warp a row then
-      float* stage = reinterpret_cast<float*>(smem + C::offP);  // [ROWS][128]
+      // through shared memory (the segment's q is used no more), a warp a row then
+      float* stage = reinterpret_cast<float*>(smem + C::offQ + qs * C::QB);  // [ROWS][128]
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         if (c < nch) {

@@ -231,3 +231,19 @@ def test_many_rows_report_v_scales_past_the_range():
     pb = pu.Problem([100, 50], [40, 39], 4, 2, 64, 16, seed=4)
     pb.scale[pb.table[1, 1], pb.layer, 1] = 2.0 ** 110
     check(pb, "past", status=binding.STATUS_RANGE)
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,d", FEW)
+@pytest.mark.parametrize("times", [1, 4, 16, 64])
+def test_few_rows_of_large_logits(new, Hq, Hkv, d, times):
+    """q whose logits are up to hundreds, rotated here."""
+    pb = pu.Problem([300, 77], [new] * 2, Hq, Hkv, d, 16, seed=times)
+    pb.q.mul_(float(times))
+    check(pb, f"x {times}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_far_from_the_start(d):
+    pb = pu.Problem([30011, 20000], [1, 3], 4, 2, d, 64, seed=5)
+    pb.q.mul_(8.0)
+    check(pb, "far")
