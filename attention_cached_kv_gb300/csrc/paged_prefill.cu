@@ -18,7 +18,12 @@
 //   * 14: the softmax warps' segments, one ahead.
 // One conversion of a key serves 256 rows: that is why rows are taken in pairs of tiles
 // here and cached bytes are used as they are where there are few rows (paged_decode.cu).
-// q is scaled by a power of two a row before its one rounding to f16.
+// q is scaled by a power of two a row and rounded to f16, and what that leaves of it to f16
+// again: the low part, which takes part only in tiles where scores may be so large that the
+// first rounding shows (kFine).  Its room is why values have one buffer if D = 128: they are
+// converted a tile behind the keys.  All that costs 10 us of the chunks below, the low
+// products, where scores are large, 30 more (as four E4M3 terms against unconverted keys,
+// with two buffers for values, they were always there and cost 54).
 //
 // Work is the sequence of (request, KV head, row-tile pair) units, each worth the keys
 // it sees and a constant for its start; each SM's CTA takes an equal run of it, cut
@@ -56,6 +61,11 @@ constexpr float kNone = -3.0e38f;     // running maximum before any key
 // Log2 units that a score may pass it by (P stays below f16's 2^16).  A tile that passes it
 // is done twice: with 8, where V scales differ by 2^2, the chunks below took 295 us for 252.
 constexpr float kSlack = 12.f;
+// Where |q| |k| (log2 units, k all of 448) is above this, q's scores take its low part as well.
+// Below it what f16 rounds off q, 2^-11 at most of an element, moves a score by 160 2^-11 /
+// sqrt(3 d) rms even then, a weight by no more than an output's half step in bf16.
+constexpr float kFine = 160.f;
+
 // While no V scale is outside 2^+-45 the sum's terms are P / v: P is at least 2^-126 for all
 // keys of 2^-36 of the largest weight and more.  Otherwise they are exponentials of their own.
 constexpr float kPlain = 45.f;
@@ -82,6 +92,7 @@ struct PrefillParams {
   Requests rq;
   int Hq, L, layer, num_blocks, min_new, Tm;
   float scale_log2;
+  float largest;  // |k| of codes all 448 (0 where q has no low parts)
   uint32_t per_g;  // 2^16 / G rounded up: j / G = j per_g >> 16 for j < 128
   uint64_t turn[64];
 };
@@ -90,7 +101,9 @@ template <int D>
 struct PCfg {
   static constexpr uint32_t kTile = 128 * D * 2;        // bytes of a 128-row f16 tile
   static constexpr uint32_t kPanel = 128 * 128;         // 64 columns of it
-  static constexpr uint32_t offK = 2 * kTile, offV = 4 * kTile, offMisc = 6 * kTile;
+  static constexpr int NV = D == 64 ? 2 : 1;            // V buffers
+  static constexpr int kSlots = 2 * NV;                 // segments that are apart: see nankey
+  static constexpr uint32_t offL = 2 * kTile, offK = 4 * kTile, offV = 6 * kTile, offMisc = (6 + NV) * kTile;
   static constexpr int kS = 0, kO = 256;  // TMEM columns: S (P) of the row tiles, O
 };
 
@@ -185,24 +198,29 @@ struct Tile {
 struct alignas(16) Scales {
   float k, vlog;  // K scale, log2 of the V scale
   float vinv;     // the V scale's inverse (infinite: a scale that counts as zero)
-  int wide;       // (of the tile)
-};
+  uint32_t tile;  // of the tile: in its first group 1 or 2 where a V scale is outside
+};                // 2^+-kPlain (2: above), in the others the largest magnitude of a K scale
 
 template <int D>
 struct PMisc {
+  static constexpr int kSlots = PCfg<D>::kSlots;
   uint64_t kready[2], kfree[2], vready[2], vfree[2], sfull[2], pfull[2], gready[2], gfree[2], qready, drain;
   uint32_t tmem;
-  int bad[4], any_nan[4];  // by segment (modulo 4), as nankey
+  float qpart[8];  // the largest bound on a row's scores by a key of scale 1, by warp
+  int bad[kSlots], any_nan[kSlots];  // by segment (modulo kSlots), as nankey
   int64_t warp_sum[kThreads / 32], start_pre, total;
   int start_r;
   PSeg seg[2];  // the softmax warps' segments
   int any_seg[2];  // 0: there is no further one
-  // by tile (modulo kRing) and 16-key group: scales; first byte of the K rows in the pool
-  // (-1: no key that is seen, -2: a block outside the pool)
+  // by tile (modulo kRing) and 16-key group: scales; the K rows' place in the pool, counted
+  // in groups (32 bits: 2 TB or more; -1: no key that is seen, -2: a block outside the pool)
   Scales scales[kRing][8];
-  int64_t at[kRing][8];
+  int at[kRing][8];
   Tile tile[kRing];
-  int nankey[4][D];  // first key past the first row's whose V is NaN, by element
+  // First key past the first row's whose V is NaN, by element.  Values of a segment's tile are
+  // written when the softmax of NV tiles before is done, so at most NV segments ahead of it;
+  // a segment's start clears the slot of the NV-th after it.
+  int nankey[kSlots][D];
 };
 
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -217,6 +235,12 @@ __device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// Two floats as f16 pairs: rounded, and what that leaves.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = to_f16x2(a, b);
+  const float2 f = f16x2_to_float2(hi);
+  lo = to_f16x2(a - f.x, b - f.y);
 }
 __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   uint16_t v;
@@ -279,9 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     mbar_init(&ms.qready, 256);
     mbar_init(&ms.drain, 1);
     fence_mbar_init();
-    for (int s = 0; s < 4; ++s) ms.bad[s] = ms.any_nan[s] = 0;
+    for (int s = 0; s < C::kSlots; ++s) ms.bad[s] = ms.any_nan[s] = 0;
   }
-  for (int i = tid; i < 4 * D; i += kThreads) ms.nankey[i / D][i % D] = INT32_MAX;
+  for (int i = tid; i < C::kSlots * D; i += kThreads) ms.nankey[i / D][i % D] = INT32_MAX;
   tc::fence_before_sync();
   // ---- this CTA's run of the sequence (the scan's barriers publish the above too)
   bool odd = false;
@@ -327,7 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       tc::fence_after_sync();
       return !failed;
     };
-    auto issue_s = [&](int x, int i) {  // S of row tile x and the CTA's i-th key tile
+    // S of row tile x and the CTA's i-th key tile; q's low parts where scores may be large
+    auto issue_s = [&](int x, int i, float bound) {
+      const bool low = bound * __uint_as_float(ms.scales[i & (kRing - 1)][1].tile) > kFine;
       if (tc::elect_one()) {
         const uint32_t qb = sbase + x * C::kTile, kb = sbase + C::offK + (i & 1) * C::kTile;
 #pragma unroll
@@ -335,13 +361,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           tc::mma_ss(tmem + C::kS + x * 128, tc::smem_desc_sw128(qb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
                      tc::smem_desc_sw128(kb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
                      tc::idesc_f16_f32(128, 128, 0), k > 0);
+        if (low) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_ss(tmem + C::kS + x * 128,
+                       tc::smem_desc_sw128(qb + C::offL + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
+                       tc::smem_desc_sw128(kb + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024),
+                       tc::idesc_f16_f32(128, 128, 0), 1);
+        }
         tc::commit(smem_u32(&ms.sfull[x]));
       }
       __syncwarp();
     };
     auto issue_pv = [&](int x, int i, bool first) {
       if (tc::elect_one()) {
-        const uint32_t vb = sbase + C::offV + (i & 1) * C::kTile;
+        const uint32_t vb = sbase + C::offV + i % C::NV * C::kTile;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           tc::mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
@@ -359,24 +393,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       PSeg sg;
       if (!wk.get(prm, sg)) continue;
       if (!wait(&ms.qready, (uint32_t)seg++ & 1u)) break;
+      float qnorm[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        qnorm[x] = fmaxf(fmaxf(ms.qpart[4 * x], ms.qpart[4 * x + 1]), fmaxf(ms.qpart[4 * x + 2], ms.qpart[4 * x + 3]));
       if (sg.nt == 0 || !wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
       const bool two = sg.two;
-      issue_s(0, i0);
-      if (two) issue_s(1, i0);
+      issue_s(0, i0, qnorm[0]);
+      if (two) issue_s(1, i0, qnorm[1]);
       arrive(&ms.kfree[i0 & 1]);
       for (int e = 0; e < sg.nt; ++e) {
         const int i = i0 + e;
         const bool more = e + 1 < sg.nt;
         auto free_v = [&]() {
-          arrive(&ms.vfree[i & 1]);
+          arrive(&ms.vfree[i % C::NV]);
           if ((i & 3) == 3) arrive(&ms.gfree[(i >> 2) & 1]);  // (the tile's softmax is done too)
         };
-        if (!wait(&ms.vready[i & 1], (uint32_t)(i >> 1) & 1u) || !wait(&ms.pfull[0], np0++ & 1u)) break;
+        if (!wait(&ms.vready[i % C::NV], (uint32_t)(i / C::NV) & 1u) || !wait(&ms.pfull[0], np0++ & 1u)) break;
         issue_pv(0, i, e == 0);
         if (!two) free_v();
         if (more) {
           if (!wait(&ms.kready[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
-          issue_s(0, i + 1);
+          issue_s(0, i + 1, qnorm[0]);
           if (!two) arrive(&ms.kfree[(i + 1) & 1]);
         } else {
           arrive(&ms.sfull[0]);  // the last P V is done
@@ -386,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           issue_pv(1, i, e == 0);
           free_v();
           if (more) {
-            issue_s(1, i + 1);
+            issue_s(1, i + 1, qnorm[1]);
             arrive(&ms.kfree[(i + 1) & 1]);
           } else {
             arrive(&ms.sfull[1]);
@@ -428,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (have) {
         const int key0 = (sg.kt0 + e) * kKT;
         key = key0 + gr * 16;
-        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & 3, 0, 0};
+        tl = Tile{sg.kend - key0, sg.pos0 + 1 - key0, key0, passed & (C::kSlots - 1), 0, 0};
         g = sg.g;
         want = key < sg.kend;
         if (want) blk = rq.block_table[(int64_t)sg.r * rq.W + key / rq.block_len];
@@ -443,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool ok = want && blk >= 0 && blk < prm.num_blocks, lost = want && !ok;
       if (lost) report(prm.status, GIST_ATTN_STATUS_BAD_BLOCK);
       const int64_t plane = ((int64_t)(ok ? blk : 0) * prm.L + prm.layer) * 2 * rq.Hkv + g;
-      const int64_t at = ok ? (plane * rq.block_len + key % rq.block_len) * D : lost ? -2 : -1;
+      const int at = ok ? (int)((plane * rq.block_len + key % rq.block_len) >> 4) : lost ? -2 : -1;
       const float ks = ok ? prm.scale[plane] : 0.f, vs = ok ? prm.scale[plane + rq.Hkv] : 1.f;
       const float vlog = scale_log2(vs), vinv = fabsf(vs) < kLeastScale ? INFINITY : 1.f / vs;
       if (fabsf(vs) > kMostScale) report(prm.status, GIST_ATTN_STATUS_RANGE);
@@ -451,14 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       now.full = in_tile(ok) == 0xffu && now.left >= kKT;
       now.odd = in_tile(lost || vs < kLeastScale) != 0;
       const uint32_t above = in_tile(vlog > kPlain), below = in_tile(vlog < -kPlain);
-      const int wide = above ? 2 : below ? 1 : 0;  // some V scale is outside 2^+-kPlain (2: above)
+      float kmax = fabsf(ks);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) kmax = fmaxf(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
+      const uint32_t of_tile = gr > 0 ? __float_as_uint(kmax) : above ? 2u : below ? 1u : 0u;
       if (!last) look_up();  // its load runs while this half is waited for
       if (__any_sync(0xffffffffu, i >= kRing && !mbar_wait(&ms.gfree[half], ((uint32_t)(i >> 3) & 1u) ^ 1u))) {
         failed = true;
         break;
       }
       const int slot = (i + t) & (kRing - 1);
-      ms.scales[slot][gr] = Scales{ks, vlog, vinv, wide};
+      ms.scales[slot][gr] = Scales{ks, vlog, vinv, of_tile};
       ms.at[slot][gr] = at;
       if (gr == 0) ms.tile[slot] = now;
       __syncwarp();
@@ -494,14 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint8_t* src = prm.pool + (row0 & 15) * D + c * 16 + more;
       if (ms.tile[i & (kRing - 1)].full) {
 #pragma unroll
-        for (int p = 0; p < kPass; ++p) x[p] = ldg16(src + ms.at[i & (kRing - 1)][(p * kRows + row0) >> 4]);
+        for (int p = 0; p < kPass; ++p) x[p] = ldg16(src + (int64_t)ms.at[i & (kRing - 1)][(p * kRows + row0) >> 4] * (16 * D));
         return;
       }
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const int row = p * kRows + row0;
-        const int64_t at = ms.at[i & (kRing - 1)][row >> 4];
-        x[p] = ldg16_if(src + at, at >= 0 && row < left);
+        const int at = ms.at[i & (kRing - 1)][row >> 4];
+        x[p] = ldg16_if(src + (int64_t)at * (16 * D), at >= 0 && row < left);
       }
     };
     auto looked_up = [&](int i) {
@@ -521,19 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto element = [&](uint32_t tile, int k) {
       return tile + (c / 4) * C::kPanel + swz128((k >> 4) * kRows + row0, 2 * (c % 4) + ((k >> 3) & 1)) + (k & 7) * 2;
     };
-    if (looked_up(0)) {
-      fetch(0, kx, 0);
-      fetch(0, vx, vstep);
-    }
-    for (int i = 0; !failed; ++i) {
-      const Tile& tl = ms.tile[i & (kRing - 1)];
-      if (tl.left == INT32_MIN) break;
-      const int b = i & 1, sl = tl.sl;
+    // Keys go a tile ahead of values: those have one buffer (two if D = 64), free only when
+    // the tile before is done.
+    auto keys = [&](int i) {  // tile i's into their buffer, the next one's from memory
+      const int b = i & 1;
       if (i >= 2 && !mbar_wait(&ms.kfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
         failed = true;
-        break;
+        return;
       }
-      const uint32_t ktile = sbase + C::offK + b * C::kTile, vtile = sbase + C::offV + b * C::kTile;
+      const uint32_t ktile = sbase + C::offK + b * C::kTile;
 #pragma unroll
       for (int p = 0; p < kPass; ++p) {
         const uint32_t w[4] = {kx[p].x, kx[p].y, kx[p].z, kx[p].w};
@@ -548,7 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       fence_proxy_async_smem();
       mbar_arrive(&ms.kready[b]);
       if (looked_up(i + 1)) fetch(i + 1, kx, 0);
-      if (i >= 2 && !mbar_wait(&ms.vfree[b], ((uint32_t)(i >> 1) & 1u) ^ 1u)) {
+    };
+    auto past = [&](int i) { return ms.tile[i & (kRing - 1)].left == INT32_MIN; };
+    if (looked_up(0)) {
+      fetch(0, kx, 0);
+      fetch(0, vx, vstep);
+      if (!past(0)) keys(0);
+    }
+#pragma unroll 1
+    for (int i = 0; !failed && !past(i); ++i) {
+      if (!past(i + 1)) keys(i + 1);
+      if (failed) break;
+      const Tile& tl = ms.tile[i & (kRing - 1)];
+      const int sl = tl.sl;
+      const uint32_t vtile = sbase + C::offV + i % C::NV * C::kTile;
+      if (i >= C::NV && !mbar_wait(&ms.vfree[i % C::NV], ((uint32_t)(i / C::NV) & 1u) ^ 1u)) {
         failed = true;
         break;
       }
@@ -597,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&ms.vready[b]);
+      mbar_arrive(&ms.vready[i % C::NV]);
       if (!failed) fetch(i + 1, vx, vstep);
     }
   } else {
@@ -617,13 +668,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       named_bar_sync(3, 288);  // the segment is there (nothing of the one before it is still read)
       if (!ms.any_seg[now]) break;
       const PSeg& sg = ms.seg[now];
-      const int sl = seg & 3, nt = sg.nt, kt0 = sg.kt0;
+      const int sl = seg & (C::kSlots - 1), nt = sg.nt, kt0 = sg.kt0;
       const bool valid = row < Tm * G && tok < sg.toks;
       const int lim = valid ? sg.pos0 + tok + 1 : 0;      // keys the row sees
       const int lim_all = sg.pos0 + x * Tm + 1;           // keys every row of the tile sees
-      if (nt > 0) {  // the next but one's
-        if (tid < D) ms.nankey[(sl + 2) & 3][tid] = INT32_MAX;
-        if (tid == 0) ms.any_nan[(sl + 2) & 3] = ms.bad[(sl + 2) & 3] = 0;
+      if (nt > 0) {
+        const int ahead = (sl + C::NV) & (C::kSlots - 1);
+        if (tid < D) ms.nankey[ahead][tid] = INT32_MAX;
+        if (tid == 0) ms.any_nan[ahead] = ms.bad[ahead] = 0;
       }
       // rows of q and out, a warp its own 32, D / 8 lanes a row
       constexpr int RW = 256 / D;  // rows of a step
@@ -662,28 +714,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                : prm.scale_log2 * __uint_as_float((uint32_t)(ex + 127) << 23);
         const int pos = max(sg.pos0 + tok, 0);
         const uint64_t down2 = f2_make(down, down);
+        uint64_t squares = f2_make(0.f, 0.f);
 #pragma unroll 1
         for (int ch = 0; ch < D / 16; ++ch) {  // 8 pairs: elements 8 ch .. and D/2 + 8 ch ..
           const uint32_t pa = place(row, ch), pb = place(row, ch + D / 16);
           const uint4 va = lds16(pa), vb = lds16(pb);
           const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-          uint32_t a[4], b[4];
+          uint32_t a[4], b[4], al[4], bl[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float s0, c0, s1, c1;
             __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e]), &s0, &c0);
             __sincosf(turn_angle(pos, prm.turn[ch * 8 + 2 * e + 1]), &s1, &c1);
             const uint64_t u = f2_mul(bf16x2_to_f2(wa[e]), down2), y = f2_mul(bf16x2_to_f2(wb[e]), down2);
+            squares = f2_fma(u, u, f2_fma(y, y, squares));
             const uint64_t cs = f2_make(c0, c1), sn = f2_make(s0, s1);
             float r0, r1;
             f2_split(f2_sub(f2_mul(u, cs), f2_mul(y, sn)), r0, r1);
-            a[e] = to_f16x2(r0, r1);
+            split2(r0, r1, a[e], al[e]);
             f2_split(f2_fma(y, cs, f2_mul(u, sn)), r0, r1);
-            b[e] = to_f16x2(r0, r1);
+            split2(r0, r1, b[e], bl[e]);
           }
+          sts16(pa + C::offL, make_uint4(al[0], al[1], al[2], al[3]));
+          sts16(pb + C::offL, make_uint4(bl[0], bl[1], bl[2], bl[3]));
           sts16(pa, make_uint4(a[0], a[1], a[2], a[3]));
           sts16(pb, make_uint4(b[0], b[1], b[2], b[3]));
         }
+        float sq0, sq1;
+        f2_split(squares, sq0, sq1);
+        float bound = sqrtf(sq0 + sq1) * rs * prm.largest;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
+        if (lane == 0) ms.qpart[warp] = bound;
         fence_proxy_async_smem();
         mbar_arrive(&ms.qready);
       }
@@ -699,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const Scales* scales = ms.scales[i & (kRing - 1)];
         const uint32_t sca = smem_u32(scales);
         uint4 s0 = lds16(sca), s1;
-        far |= s0.w == 2;  // (the maximum is above all sums from here on)
+        far |= s0.w == 2u;  // (the maximum is above all sums from here on)
         const bool own = far || s0.w != 0;
         // 16 scores v of a group with scales sw as weights exp2(f v + log2 scale - m), packed;
         // their sum without the scale into acc; returns their largest exponent
@@ -978,6 +1040,7 @@ int launch(const PagedProblem& pb, void* workspace, int min_new, int sms, cudaSt
   prm.Tm = 128 / pb.G;
   prm.scale_log2 = pb.scale_log2;
   prm.per_g = (65536u + pb.G - 1) / pb.G;
+  prm.largest = pb.flags & GIST_ATTN_FLAG_PREROTATED ? 0.f : 448.f * sqrtf((float)D);  // (bf16 fits f16)
   for (int j = 0; j < 64; ++j) prm.turn[j] = pb.turn[j];
   constexpr int smem = (int)(PCfg<D>::offMisc + sizeof(PMisc<D>));
   static_assert(smem <= 227 * 1024, "shared memory");

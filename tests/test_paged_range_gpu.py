@@ -10,6 +10,8 @@ from the roundings of one token and head:
             the errors independent and uniform: six deviations of their sum over
             i; and 2^-20 of the products' magnitudes for sums and angles in fp32.
             An error e_j of score j moves the output by sum_j p_j |v_j| (e_j + sum p e)
+            (with many rows q is carried to 2^-11 where scores stay below 160 in any
+            case: six deviations of that are below the other terms)
 """
 from __future__ import annotations
 
@@ -245,5 +247,20 @@ def test_few_rows_of_large_logits(new, Hq, Hkv, d, times):
 @pytest.mark.parametrize("d", [64, 128])
 def test_few_rows_far_from_the_start(d):
     pb = pu.Problem([30011, 20000], [1, 3], 4, 2, d, 64, seed=5)
+    pb.q.mul_(8.0)
+    check(pb, "far")
+
+
+@pytest.mark.parametrize("new,Hq,Hkv,d", MANY)
+@pytest.mark.parametrize("times", [1, 1.25, 2, 4, 16, 64])
+def test_many_rows_of_large_logits(new, Hq, Hkv, d, times):
+    pb = pu.Problem([300, 77], [new] * 2, Hq, Hkv, d, 16, seed=int(times))
+    pb.q.mul_(float(times))
+    check(pb, f"x {times}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_far_from_the_start(d):
+    pb = pu.Problem([30011], [35], 2, 1, d, 64, seed=5)
     pb.q.mul_(8.0)
     check(pb, "far")
