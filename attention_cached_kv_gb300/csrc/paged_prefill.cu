@@ -391,13 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     uint32_t np0 = 0, np1 = 0;  // P tiles so far of each row tile
     for (; wk.more() && !failed; wk.next(prm)) {
       PSeg sg;
-      if (!wk.get(prm, sg)) continue;
+      if (!wk.get(prm, sg) || sg.nt == 0) continue;  // (without tiles there is no q either)
       if (!wait(&ms.qready, (uint32_t)seg++ & 1u)) break;
       float qnorm[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         qnorm[x] = fmaxf(fmaxf(ms.qpart[4 * x], ms.qpart[4 * x + 1]), fmaxf(ms.qpart[4 * x + 2], ms.qpart[4 * x + 3]));
-      if (sg.nt == 0 || !wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
+      if (!wait(&ms.kready[i0 & 1], (uint32_t)(i0 >> 1) & 1u)) continue;
       const bool two = sg.two;
       issue_s(0, i0, qnorm[0]);
       if (two) issue_s(1, i0, qnorm[1]);
@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int in = token_of(rr);
         return at0 + ((int64_t)in * (prm.Hq - G) + rr) * D;
       };
-      float rs;  // softmax scale (log2) x the row's power of two
-      {
+      float rs = 0.f;  // softmax scale (log2) x the row's power of two
+      if (nt > 0) {
         // rows into their places, rounded to f16 there after the rotation
         const uint32_t tile = sbase + x * C::kTile;
         auto place = [&](int r, int ch) { return tile + (ch >> 3) * C::kPanel + swz128(r, ch & 7); };

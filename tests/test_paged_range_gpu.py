@@ -55,6 +55,9 @@ def expected(pb, rotated):
                       for kv in (0, 1))
             vs = np.repeat(np.abs(scale[ids, pb.layer, 1, g]), pb.bl)[:C]
             for i, p in enumerate(pos):
+                if p < 0:  # sees no key
+                    out[a + i, h] = tol[a + i, h] = 0.0
+                    continue
                 k, v, y, s_v = kk[:p + 1], vv[:p + 1], x[i, h], vs[:p + 1]
                 s = k @ y * sc
                 w = np.exp(s - s.max())
