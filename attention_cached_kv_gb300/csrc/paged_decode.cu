@@ -702,7 +702,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (i >= NPB) wait(&ms.pfree[pb], (uint32_t)(i / NPB - 1) & 1u);
         // the V scale's sign goes to P, and a scale of zero makes P zero
-        const float vsc = ms.vsc[vs][box];
+        // (a NaN logarithm is in the scores of the rows that see the key; the others' weights
+        // stay 0)
+        const float vsc = ms.vsc[vs][box], vback = vlog == vlog ? vlog : 0.f;
         const uint32_t sign = fabsf(vsc) < kLeastScale ? 0u : vsc < 0.f ? 0xbc00bc00u : 0x3c003c00u;  // 0, -1 or 1, twice
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -716,8 +718,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int j = 0; j < 8; j += 2) {
                 const int q = c * 8 + j;
                 const float x0 = s[(c * KPR + p) * 8 + j] - mv[j], x1 = s[(c * KPR + p) * 8 + j + 1] - mv[j + 1];
-                l[q] += ex2_approx(x0 - vlog);
-                l[q + 1] += ex2_approx(x1 - vlog);
+                l[q] += ex2_approx(x0 - vback);
+                l[q + 1] += ex2_approx(x1 - vback);
                 uint16_t u[3];
                 split3(mul_f16x2(to_f16x2(ex2_approx(x0), ex2_approx(x1)), sign), u[0], u[1], u[2]);
 #pragma unroll

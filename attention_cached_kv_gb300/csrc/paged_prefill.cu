@@ -766,8 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         // 16 scores v of a group with scales sw as weights exp2(f v + log2 scale - m), packed;
         // their sum without the scale into acc; returns their largest exponent
         auto weights = [&](auto own_sum, uint4 sw, const uint32_t (&v)[16], uint32_t* pk, int left) {
-          const float f = __uint_as_float(sw.x) * rs, lg = __uint_as_float(sw.y);
-          const float w = decltype(own_sum)::value ? 1.f : fabsf(__uint_as_float(sw.z));
+          const bool seen = left > 0;  // (a scale that the row does not see may be NaN)
+          const float f = __uint_as_float(sw.x) * rs, lg = seen ? __uint_as_float(sw.y) : 0.f;
+          const float w = decltype(own_sum)::value ? 1.f : seen ? fabsf(__uint_as_float(sw.z)) : 0.f;
           const uint64_t g2 = f2_make(f, f), nm2 = f2_make(lg - m, lg - m);
           uint64_t sum = 0;
           float top = kNone;

@@ -7,7 +7,7 @@ import torch
 
 import paged_utils as pu
 from attention_cached_kv_gb300 import binding
-from test_paged_range_gpu import check
+from test_paged_range_gpu import check, expected
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -29,3 +29,23 @@ def test_many_chunks_that_see_no_key():
     pb = pu.Problem([30 if r in served else 0 for r in range(400)], [17] * 400, 2, 1, 64, 16, seed=3)
     pb.kv_len = np.array([47 if r in served else 0 for r in range(400)])
     check(pb, "unserved")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [3, 33])
+@pytest.mark.parametrize("which,value", [("K", float("nan")), ("V", float("nan")), ("V", float("inf")), ("V", float("-inf"))])
+def test_scales_that_are_not_finite_reach_the_tokens_that_see_them(d, new, which, value):
+    """The last block's scale, which only the last token of one request sees: that token's
+    rows are not finite and reported, all others are what they would be."""
+    pb = pu.Problem([48 - new + 1, 200], [new, new], 4, 2, d, 16, seed=6)
+    assert pb.kv_len[0] == 49
+    ref, tol = expected(pb, False)
+    args = list(pb.args())
+    args[2][int(pb.table[0, 3]), pb.layer, "KV".index(which)] = value
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = binding.gist_attn_paged_fp8kv(*args, dims=pb.dims, status=st).float().cpu().numpy().astype(np.float64)
+    last = new - 1
+    assert int(st.item()) == binding.STATUS_RANGE
+    assert not np.isfinite(got[last]).any()
+    rest = np.arange(len(got)) != last
+    assert (np.abs(got - ref) <= tol)[rest].all()
