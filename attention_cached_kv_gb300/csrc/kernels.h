@@ -82,7 +82,8 @@ struct PagedProblem {
   int32_t* status;
   int B, T, max_new, Hq, Hkv, G, d, block_len, W, num_blocks, L, layer, flags;
   float scale_log2;      // softmax scale * log2(e)
-  uint64_t turn[64];     // RoPE: theta_j / 2 pi modulo 1, in units of 2^-64 (0: no rotation)
+  uint64_t turn[64];     // RoPE: theta_j / 2 pi modulo 1, in units of 2^-64, the lower half
+                         // signed (0: no rotation)
 };
 struct PlanArgs {
   const int32_t* cached_len;

@@ -7,12 +7,13 @@
 
 namespace gattn {
 
-// Angle of position `pos` (not negative) at frequency `turn` (theta / 2 pi modulo 1,
-// in units of 2^-64): the product modulo 2^64 is the angle modulo a whole turn, so
-// nothing is lost at far positions (off by at most pos 2^-53 turns, the double that
-// `turn` came from) and no range reduction is left.  In units of 2^-32 turns.
+// Angle of position `pos` at frequency `turn` (theta / 2 pi modulo 1, in units of 2^-64,
+// its lower half signed: the upper one is one more where that is negative): the product
+// modulo 2^64 is the angle modulo a whole turn, so nothing is lost at far positions (off by
+// at most pos 2^-53 turns, the double that `turn` came from) and no range reduction is left.
+// In units of 2^-32 turns.
 __device__ __forceinline__ uint32_t turn_part(int pos, uint64_t turn) {
-  return (uint32_t)pos * (uint32_t)(turn >> 32) + __umulhi((uint32_t)pos, (uint32_t)turn);
+  return (uint32_t)pos * (uint32_t)(turn >> 32) + (uint32_t)__mulhi(pos, (int)(uint32_t)turn);
 }
 constexpr float kTurnUnit = 1.4629180792671596e-09f;  // 2 pi / 2^32
 // The same in radians, in [-pi, pi).

@@ -76,7 +76,8 @@ int check_dims(const gist_paged_dims* dm, PagedProblem* pb) {
       turns = high[j >> 3] * low[j & 7] * 0.15915494309189535;
       turns -= floor(turns);
     }
-    pb->turn[j] = turns < 1.0 ? (uint64_t)ldexp(turns, 64) : 0;
+    const uint64_t turn = turns < 1.0 ? (uint64_t)ldexp(turns, 64) : 0;
+    pb->turn[j] = turn + ((turn & 0x80000000u) << 1);  // the lower half as a signed number
   }
   return GIST_ATTN_OK;
 }

@@ -49,3 +49,14 @@ def test_scales_that_are_not_finite_reach_the_tokens_that_see_them(d, new, which
     assert not np.isfinite(got[last]).any()
     rest = np.arange(len(got)) != last
     assert (np.abs(got - ref) <= tol)[rest].all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("start", [-5, -4096, -2 ** 31])
+def test_append_turns_keys_at_negative_positions(d, start):
+    """Backwards, as far as forwards."""
+    from test_paged_append_gpu import check as check_append, fresh, places
+    pb = pu.Problem([3, 9], [9, 2], 2, 2, d, 16, seed=4)
+    k, v = fresh(pb, 7)
+    slot, position = places(pb)
+    check_append(pb, k, v, slot, [p - 3 + start for p in position])
