@@ -125,9 +125,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 
   bool bad = false;
   const int total = start[a.B];
-  for (int base = blockIdx.x * kThreads; base < a.T; base += gridDim.x * kThreads) {
-    const int t = base + tid;
-    if (t >= a.T) break;
+  for (int64_t row = blockIdx.x * kThreads + tid; row < a.T; row += gridDim.x * kThreads) {
+    const int t = (int)row;
     if (t >= total) {
       a.slot[t] = -1;
       a.position[t] = -1;
@@ -173,8 +172,8 @@ int launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
   if (smem > 32 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  const int want = (a.T + kThreads - 1) / kThreads;
-  const int grid = want < 1 ? 1 : want > 128 ? 128 : want;
+  const int64_t want = ((int64_t)a.T + kThreads - 1) / kThreads;
+  const int grid = want < 1 ? 1 : want > 128 ? 128 : (int)want;
   plan_kernel<<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }

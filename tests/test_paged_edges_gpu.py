@@ -60,3 +60,21 @@ def test_append_turns_keys_at_negative_positions(d, start):
     k, v = fresh(pb, 7)
     slot, position = places(pb)
     check_append(pb, k, v, slot, [p - 3 + start for p in position])
+
+
+def test_plan_of_the_largest_number_of_token_rows():
+    """2^31 - 1 rows, nearly all of them padding: counted past the last without a wrap."""
+    T = 2 ** 31 - 1
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out = [torch.zeros(n, **i32) for n in (3, 2, T, T, 2)]
+    dims = dict(num_requests=2, num_tokens=T, max_new=8, num_q_heads=1, num_kv_heads=1, head_dim=64, block_len=16, max_blocks=2,
+                num_blocks=9, num_layers=1, layer=0, rope_theta=1e4, softmax_scale=0.0)
+    table = torch.tensor([[5, -1], [-1, -1]], **i32)
+    st = torch.zeros(1, **i32)
+    p = binding.gist_paged_plan(torch.tensor([14, 0], **i32), torch.tensor([4, 3], **i32), table, torch.tensor([7, 8], **i32),
+                                torch.tensor([0, 2], **i32), out, dims=dims, status=st)
+    assert int(st.item()) == 0 and p.kv_len.tolist() == [18, 3] and p.free_range.tolist() == [2, 2]
+    assert p.slot[:8].tolist() == [94, 95, 112, 113, 128, 129, 130, -1]
+    for x in (p.slot, p.position):
+        for a in range(7, T, 1 << 29):
+            assert int(x[a:a + (1 << 29)].max()) == -1 == int(x[a:a + (1 << 29)].min())
