@@ -199,6 +199,33 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _allocating_for(stream, dev):
+    """Allocations under this belong to the stream that the call on device `dev` runs on (a
+    torch stream, a raw handle, or None for the current one): memory of another stream's
+    may still be in use there, and freed memory goes back to it while the call runs."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", dev))
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, like, stream):
+    """An output on the device of `like`, of the call's stream."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _allocating_for(stream, like.get_device()):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _like(t, stream):
+    """An output like tensor `t`, of the call's stream."""
+    if stream is None or not isinstance(t, torch.Tensor):
+        return torch.empty_like(t)
+    return _new(t.shape, t.dtype, t, stream)
+
+
 def _raise(rc):
     if rc != OK:
         raise GistAttnError(rc, status_string(rc))
@@ -209,7 +236,7 @@ def gist_attn_fwd(q, k_new, v_new, kv_pool, item_ids=None, block_table=None, pos
     """One layer of cached-KV attention; returns `out` (allocated if None)."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     bf, i32 = torch.bfloat16, torch.int32
     D = make_dims(dims, status)
     rc = lib.gist_attn_fwd(_ptr(q, bf, "q"), _ptr(k_new, bf, "k_new"), _ptr(v_new, bf, "v_new"),
@@ -245,7 +272,7 @@ def gist_attn_fwd_ws(q, k_new, v_new, kv_pool, item_ids=None, block_table=None, 
     least workspace_bytes(dims) bytes, or None); returns `out`."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     bf, i32 = torch.bfloat16, torch.int32
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
@@ -270,7 +297,7 @@ def gist_attn_fwd_noalloc(q, k_new, v_new, kv_pool, item_ids=None, block_table=N
     convenience only).  Returns `out`."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     bf, i32 = torch.bfloat16, torch.int32
     D = make_dims(dims, status)
     rc = lib.gist_attn_fwd_noalloc(_ptr(q, bf, "q"), _ptr(k_new, bf, "k_new"),
@@ -290,7 +317,7 @@ def gist_attn_fwd_fp8kv(q, k_new, v_new, kv_pool_e4m3, kv_scale, item_ids=None, 
     [num_blocks][L][2][Hkv]; returns `out` (allocated if None)."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     bf, i32 = torch.bfloat16, torch.int32
     if kv_pool_e4m3 is not None and kv_pool_e4m3.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise TypeError("kv_pool_e4m3 must be float8_e4m3fn or uint8")
@@ -313,10 +340,10 @@ def gist_attn_fwd_block_mass(q, k_new, v_new, kv_pool, block_table, pos_offset=N
     """Decode step plus per-block attention mass [P][Hq][blocks_per_pair]; returns (out, mass)."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     if block_mass is None:
-        block_mass = torch.empty((dims["num_pairs"], dims["num_q_heads"], dims["blocks_per_pair"]),
-                                 dtype=torch.float32, device=q.device)
+        block_mass = _new((dims["num_pairs"], dims["num_q_heads"], dims["blocks_per_pair"]), torch.float32, q,
+                          stream)
     bf, i32 = torch.bfloat16, torch.int32
     D = make_dims(dims, status)
     rc = lib.gist_attn_fwd_block_mass(_ptr(q, bf, "q"), _ptr(k_new, bf, "k_new"), _ptr(v_new, bf, "v_new"),
@@ -347,7 +374,7 @@ def gist_attn_fwd_gist_mask(q, k_new, v_new, kv_pool=None, item_ids=None, block_
     """gist_attn_fwd under the gist mask (gist_start int32 [P] required); returns `out`."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream)
     bf, i32 = torch.bfloat16, torch.int32
     D = make_dims(dims, status)
     rc = lib.gist_attn_fwd_gist_mask(_ptr(q, bf, "q"), _ptr(k_new, bf, "k_new"), _ptr(v_new, bf, "v_new"),
@@ -380,13 +407,12 @@ def gist_qkv_rope(x, w_qkv, pos_offset=None, q=None, k_new=None, v_new=None, *, 
     lib = load_library()
     P, l, Hq, Hkv, d = (dims["num_pairs"], dims["n_new"], dims["num_q_heads"], dims["num_kv_heads"],
                         dims["head_dim"])
-    dev = x.device
     if q is None:
-        q = torch.empty((P, l, Hq, d), dtype=torch.bfloat16, device=dev)
+        q = _new((P, l, Hq, d), torch.bfloat16, x, stream)
     if k_new is None:
-        k_new = torch.empty((P, l, Hkv, d), dtype=torch.bfloat16, device=dev)
+        k_new = _new((P, l, Hkv, d), torch.bfloat16, x, stream)
     if v_new is None:
-        v_new = torch.empty((P, l, Hkv, d), dtype=torch.bfloat16, device=dev)
+        v_new = _new((P, l, Hkv, d), torch.bfloat16, x, stream)
     bf, i32 = torch.bfloat16, torch.int32
     D = make_dims(dims, status)
     rc = lib.gist_qkv_rope(_ptr(x, bf, "x"), _ptr(w_qkv, bf, "w_qkv"), _ptr(pos_offset, i32, "pos_offset"),
@@ -401,8 +427,7 @@ def gist_out_proj(attn_out, w_o, y=None, *, dims: dict, status=None, stream=None
     lib = load_library()
     d_model = int(w_o.shape[0])
     if y is None:
-        y = torch.empty((dims["num_pairs"], dims["n_new"], d_model), dtype=torch.bfloat16,
-                        device=attn_out.device)
+        y = _new((dims["num_pairs"], dims["n_new"], d_model), torch.bfloat16, attn_out, stream)
     D = make_dims(dims, status)
     rc = lib.gist_out_proj(_ptr(attn_out, torch.bfloat16, "attn_out"), _ptr(w_o, torch.bfloat16, "w_o"),
                            _ptr(y, torch.bfloat16, "y"), d_model, ctypes.byref(D), _stream(stream))
@@ -416,8 +441,8 @@ def gist_attn_gather_debug(kv_pool, item_ids=None, block_table=None, dst=None, *
     lib = load_library()
     C = dims["block_len"] * dims["blocks_per_pair"]
     if dst is None:
-        dst = torch.empty((dims["num_pairs"], dims["num_kv_heads"], 2, C, dims["head_dim"]),
-                          dtype=torch.bfloat16, device=kv_pool.device)
+        dst = _new((dims["num_pairs"], dims["num_kv_heads"], 2, C, dims["head_dim"]), torch.bfloat16, kv_pool,
+                   stream)
     D = make_dims(dims, status)
     rc = lib.gist_attn_gather_debug(_ptr(kv_pool, torch.bfloat16, "kv_pool"),
                                     _ptr(item_ids, torch.int32, "item_ids"),
@@ -482,18 +507,6 @@ def _pool_ptr(pool, dims, dev):
         raise TypeError("kv_pool_e4m3 must be float8_e4m3fn or uint8")
     n = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
     return _sized(pool, pool.dtype, "kv_pool_e4m3", n * dims["block_len"] * dims["head_dim"], dev), n
-
-
-def _allocating_for(stream, dev):
-    """Allocations under this belong to the stream that the call on device `dev` runs on (a
-    torch stream, a raw handle, or None for the current one): memory of another stream's
-    may still be in use there, and freed memory goes back to it while the call runs."""
-    if stream is None:
-        return torch.cuda.device(dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=torch.device("cuda", dev))
-    return torch.cuda.stream(stream)
 
 
 def _call(dev, stream, fn, *args):
@@ -563,8 +576,7 @@ def gist_attn_paged_fp8kv(q, kv_pool_e4m3, kv_scale, block_table, q_start, kv_le
     lib = load_library()
     B, dev, bf, i32 = dims["num_requests"], _index(q, "q"), torch.bfloat16, torch.int32
     if out is None:
-        with _allocating_for(stream, dev):
-            out = torch.empty_like(q)
+        out = _like(q, stream)
     n = dims["num_tokens"] * dims["num_q_heads"] * dims["head_dim"]
     pool, planes = _pool_ptr(kv_pool_e4m3, dims, dev)
     D = make_paged_dims(dims, status)

@@ -110,3 +110,40 @@ def test_a_raw_handle_of_the_default_stream():
     got = binding.gist_attn_paged_fp8kv(*args, dims=pb.dims, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", STREAMS)
+def test_outputs_of_the_other_calls_belong_to_their_stream(kind, monkeypatch):
+    """Attention over bf16 and E4M3 pools, block mass, gather and projections."""
+    P, Hq, Hkv, d, bl, nblk = 2, 4, 2, 64, 16, 9
+    dims = dict(num_pairs=P, n_new=1, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=d, block_len=bl, blocks_per_pair=nblk,
+                num_blocks=P * nblk, num_layers=1, layer=0, rope_theta=1e4, softmax_scale=0.0, flags=0)
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    q, k, v = (torch.randn((P, 1, h, d), **bf) for h in (Hq, Hkv, Hkv))
+    pool = torch.randn((P * nblk, 1, 2, Hkv, bl, d), **bf)
+    codes, scale = pool.to(torch.float8_e4m3fn), torch.ones((P * nblk, 1, 2, Hkv), device=DEV)
+    table = torch.arange(P * nblk, dtype=torch.int32, device=DEV).view(P, nblk)
+    rows = dict(dims, num_pairs=3, n_new=64, num_q_heads=14, block_len=8, blocks_per_pair=1, num_blocks=1)
+    x, w = torch.randn((3, 64, 256), **bf), torch.randn(((14 + 2 * Hkv) * d, 256), **bf)
+    wo, attn = torch.randn((256, 14 * d), **bf), torch.randn((3, 64, 14, d), **bf)
+    s = torch.cuda.Stream()
+    given = s if kind == "stream" else s.cuda_stream
+    calls = [lambda **kw: binding.gist_attn_fwd(q, k, v, pool, None, table, dims=dims, **kw),
+             lambda **kw: binding.gist_attn_fwd_fp8kv(q, k, v, codes, scale, None, table, dims=dims, **kw),
+             lambda **kw: binding.gist_attn_fwd_block_mass(q, k, v, pool, table, dims=dims, **kw),
+             lambda **kw: binding.gist_attn_gather_debug(pool, None, table, dims=dims, **kw),
+             lambda **kw: binding.gist_qkv_rope(x, w, dims=rows, **kw),
+             lambda **kw: binding.gist_out_proj(attn, wo, dims=rows, **kw)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    seen = []
+    for name in ("empty", "empty_like"):
+        def alloc(*a, _f=getattr(torch, name), **kw):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return _f(*a, **kw)
+        monkeypatch.setattr(torch, name, alloc)
+    got = [call(stream=given) for call in calls]
+    torch.cuda.synchronize()
+    assert seen == [s.cuda_stream] * 9
+    flat = lambda xs: [t for x in xs for t in (x if isinstance(x, tuple) else (x,))]  # noqa: E731
+    assert all(torch.equal(a, b) for a, b in zip(flat(got), flat(want)))
