@@ -267,3 +267,23 @@ def test_many_rows_far_from_the_start(d):
     pb = pu.Problem([30011], [35], 2, 1, d, 64, seed=5)
     pb.q.mul_(8.0)
     check(pb, "far")
+
+
+HEADS = [(14, 2, 64), (32, 8, 128), (8, 8, 128), (16, 1, 64), (16, 1, 128), (6, 2, 128)]
+BATCHES = {"decode": ([0, 1, 15, 63, 64, 127, 128, 255, 256, 700], [1] * 10, 0),
+           "room for long ones": ([0, 126, 129, 383, 700], [1, 2, 5, 3, 2], 300),
+           "mixed": ([0, 77, 400, 0, 130, 20], [130, 1, 65, 33, 1, 150], 0),
+           "one chunk behind many keys": ([3000, 5], [37, 2], 0)}
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", HEADS)
+@pytest.mark.parametrize("name", BATCHES)
+def test_every_request_and_head_by_itself(Hq, Hkv, d, name):
+    """Heads and requests whose values lie 2^12 apart and more: each by its own measure."""
+    cached, new, room = BATCHES[name]
+    pb = pu.Problem(cached, new, Hq, Hkv, d, 16, seed=d + Hq, pad=3, extra_width=room)
+    for r in range(len(cached)):
+        n = -(-int(pb.kv_len[r]) // 16)
+        for g in range(Hkv):
+            pb.scale[pb.table[r, :n], pb.layer, 1, g] *= 2.0 ** (12 * ((r + g) % 4) - 20)
+    check(pb, name)
