@@ -10,15 +10,18 @@
 //
 // A unit is the new tokens of one block (consecutive rows, some perhaps skipped), a
 // KV head and K or V; one CTA takes the units whose first token lies in its `chunk`
-// tokens (all of a prompt's block, a single token of a decoding step).  A thread holds elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row,
-// so it rotates its own pairs with four sines, and the rows stay in registers
-// between the pass for the largest magnitude and the one that converts.
+// tokens (all of a prompt's block, a single token of a decoding step).  A thread holds
+// elements j .. j + 3 and j + d/2 .. j + d/2 + 3 of a row, so it rotates its own pairs with
+// four sines, and the rows stay in registers between the pass for the largest magnitude and
+// the one that converts.
 // Sine and cosine are carried to fp32's last place, though E4M3 keeps four bits: what
 // they are off by moves values that lie next to the middle of two codes.  Of 1.8 million
 // values 1.5 differ from the definition's (rotated in fp32 by torch: 0.8); by __sincosf,
 // off by 2^-21, 7.5 did, in 26 us where this takes 29.
-// Bound: issue, then HBM (three bytes an element: bf16 in, E4M3 out): 14.2 k tokens of
-// 8 heads of 128 in 29 us = 3.1 TB/s; few tokens: latency, 64 tokens in 6.4 us.
+// Bound: a unit's chain of load, largest magnitude, sines, conversion and store, with
+// barriers between and nothing of the next unit under way (issue is at 50 %, DRAM at 25 %;
+// three bytes an element: bf16 in, E4M3 out): 14.2 k tokens of 8 heads of 128 in 29.5 us =
+// 3.1 TB/s; few tokens: latency, 64 tokens in 6.7 us.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.

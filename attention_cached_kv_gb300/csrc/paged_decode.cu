@@ -11,16 +11,17 @@
 // of E4M3 terms, each the rounded remainder of the last.  q has four, added in TMEM, one
 // product after the other: it is scaled by a power of two a row, its largest value to 128
 // and more, and the terms leave 2^-16 of a value or 2^-17 of that (a score is off by as
-// much of |q| |k|: after a rounding to f16, 2^-11, outputs of logits in the tens were off by
-// more than their rounding to bf16).  P, whose
-// rounding moves an output by as little of itself, has three of 11 bits or more; its small
-// weights matter (they are many), so they are kept apart, p0 + p1 / 16 + p2 / 256, side by
-// side as columns of N: the few query rows leave N room that costs nothing.  The K scale of a key's block multiplies its fp32 scores s,
-// the logarithm of its V scale is added to them: a weight with its V scale is
-// P = exp2(s + log2 v - m), without it exp2(s - m), and a row's output is the quotient of
-// the two sums (over P x V codes, and over the second).  So P's bits go by what a key adds
-// to the row, and a large V scale of a key that the row hardly weighs, or does not see,
-// takes none away.
+// much of |q| |k|: after a rounding to f16, 2^-11, outputs of logits in the tens were off
+// by more than their rounding to bf16).  P, whose rounding moves an output by as little of
+// itself, has three of 11 bits or more; its small weights matter (they are many), so they
+// are kept apart, p0 + p1 / 16 + p2 / 256, side by side as columns of N: the few query rows
+// leave N room that costs nothing.
+//
+// The K scale of a key's block multiplies its fp32 scores s, the logarithm of its V scale is
+// added to them: a weight with its V scale is P = exp2(s + log2 v - m), without it
+// exp2(s - m), and a row's output is the quotient of the two sums (over P x V codes, and
+// over the second).  So P's bits go by what a key adds to the row, and a large V scale of a
+// key that the row hardly weighs, or does not see, takes none away.
 //
 // A softmax thread owns one tile row (TMEM lane): its scores for all query rows,
 // the running maximum (of s + log2 v, less kPUnit) m of each (the same in all threads),
@@ -34,10 +35,10 @@
 // have more than four tiles the runs are of whole units, and that launch falls away.
 //
 // Bound: HBM (a byte a cached element) where the contexts are long: 32 x ~4050 keys,
-// 32 heads of 128 with a KV head each, 171 us = 6.3 TB/s; in groups of four, 54 us =
+// 32 heads of 128 with a KV head each, 167 us = 6.4 TB/s; in groups of four, 54 us =
 // 5.1 TB/s, of which about 10 us start, tail and join.  Few tiles a CTA: the chain
-// copy - scores - softmax - output, 1 to 3 us a tile; 16 requests of 2-5 tokens behind
-// 500-3000 keys 39 us, one of 131000 keys 21 us, four of 20-200 keys 8.2 us.
+// copy - scores - softmax - output, 1 to 6 us a tile; 16 requests of 2-5 tokens behind
+// 500-3000 keys 40 us, one of 131000 keys 21 us, four of 20-200 keys 8.3 us.
 // Eight warps: 0-3 softmax, 4 TMA and scales, 5 tcgen05, 6-7 q rows.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
@@ -1013,7 +1014,7 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   decode_kernel<D, CH><<<grid, kThreads, smem, stream>>>(tm, prm);
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
   if (grid == 1 || prm.whole) return GIST_ATTN_OK;
-  // the combine's CTAs may start, and scan the lengths, while the last tiles run
+  // the combine's CTAs may start while the last tiles run (and then wait for them)
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid - 1, many ? (Cfg<D, CH>::ROWS + prm.join_rows - 1) / prm.join_rows : 1);
   cfg.blockDim = dim3(many ? 256 : 32 * Cfg<D, CH>::ROWS);

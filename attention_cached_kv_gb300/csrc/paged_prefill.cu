@@ -32,14 +32,12 @@
 // or one short chunk behind a long context, spread evenly.  A start and an end (rows of q
 // in and rotated, rows of O out) run a few times a CTA, mostly out of a cold instruction
 // cache, so their loops stay rolled: unrolled they took 11 us together, rolled 9.
-// Bound: per key tile (2.2 us) the chain scores - softmax - output of a row tile, the
-// converting warps (1.8 us) and the products (1.5 us) are near one another.  Four
-// chunks of 700-1024 tokens behind 1000-6000 cached ones, 32 / 8 heads of 128:
-// 267 us = 877 TFLOP/s.  (Without any conversion it would be 250, with an eighth of
-// the products 220, without exponentials the same.  Tried: keys unconverted with q as
-// three E4M3 terms; a warp a row tile for the products; a warpgroup each for keys and
-// values with a register split; half the keys widened by integer operations; the
-// copies ahead into L2.  None gained, some lost up to a tenth.)
+// Bound: per key tile (2.1 us) the chain scores - softmax - output of a row tile; the
+// converting warps (1.6 us) and the products (1.5 us) are not far below.  Four chunks of
+// 700-1024 tokens behind 1000-6000 cached ones, 32 / 8 heads of 128: 264 us = 884 TFLOP/s;
+// 293 us where every tile needs q's low part.  (Tried: a warp a row tile for the products;
+// a warpgroup each for keys and values with a register split; half the keys widened by
+// integer operations; the copies ahead into L2.  None gained, some lost up to a tenth.)
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.

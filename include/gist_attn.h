@@ -492,7 +492,8 @@ int gist_paged_plan(const int32_t* cached_len, const int32_t* new_len, int32_t* 
  * ones keeping their place), as gist_paged_plan gives them, and no block may get
  * tokens of two requests: otherwise the block's rows and scale are unspecified
  * (the writes stay in it).  block_len at most 2^20 (GIST_ATTN_ERR_UNSUPPORTED).
- * num_requests, max_new, max_blocks and Hq are not used.
+ * num_requests, max_new, max_blocks and Hq are checked, but not used.  Values past
+ * 448 times the largest scale are stored as that.
  */
 int gist_kv_append_fp8(const void* k_new, const void* v_new, void* kv_pool_e4m3, float* kv_scale,
                        const int32_t* slot, const int32_t* position, const gist_paged_dims* dims,
