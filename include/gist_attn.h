@@ -528,7 +528,8 @@ size_t gist_attn_paged_workspace_bytes(const gist_paged_dims* dims);
  * max_new apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as
  * elsewhere, and where a V scale's magnitude is above 2^100; one below 2^-96 counts
  * as zero.  The scales of a sequence's blocks may lie as far apart as that: a row's
- * precision goes by its largest weight times V scale.  block_len must be a multiple
+ * precision goes by its largest weight times V scale (2^-96 for one that counts as
+ * zero: what other keys add is lost below 2^-120 or so).  block_len must be a multiple
  * of 16, Hq / Hkv at most 128 and W * block_len at most 2^30
  * (GIST_ATTN_ERR_UNSUPPORTED).
  */
