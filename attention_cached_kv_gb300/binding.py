@@ -33,7 +33,9 @@ EXPORTS = ("gist_attn_fwd", "gist_attn_workspace_bytes", "gist_attn_fwd_ws", "gi
            "gist_attn_gather_debug", "gist_kv_bytes_per_position", "gist_kv_bytes_per_item",
            "gist_kv_bytes_batch", "gist_attn_status_string", "gist_attn_route",
            "gist_paged_plan", "gist_kv_append_fp8", "gist_attn_paged_workspace_bytes",
-           "gist_attn_paged_fp8kv")
+           "gist_attn_paged_fp8kv", "gist_attn_paged_decode_workspace_bytes", "gist_attn_paged_decode",
+           "gist_pages_free", "gist_pages_compact", "gist_pages_fork", "gist_pages_copy",
+           "gist_qkv_rope_w4", "gist_out_proj_w4")
 
 
 class GistAttnError(RuntimeError):
@@ -90,6 +92,36 @@ class PagedPlan(NamedTuple):
     kv_len: torch.Tensor
     slot: torch.Tensor
     position: torch.Tensor
+    free_range: torch.Tensor
+
+
+class PagesFree(NamedTuple):
+    """What gist_pages_free writes (int32): ref_count [num_blocks], free_blocks [num_blocks], free_range [2]."""
+    ref_count: torch.Tensor
+    free_blocks: torch.Tensor
+    free_range: torch.Tensor
+
+
+class PagesCompact(NamedTuple):
+    """What gist_pages_compact writes (int32): block_table [B][W], new_id [num_blocks], copy_src and
+    copy_dst [num_blocks // 2], num_copies [1], free_blocks [num_blocks], free_range [2]."""
+    block_table: torch.Tensor
+    new_id: torch.Tensor
+    copy_src: torch.Tensor
+    copy_dst: torch.Tensor
+    num_copies: torch.Tensor
+    free_blocks: torch.Tensor
+    free_range: torch.Tensor
+
+
+class PagesFork(NamedTuple):
+    """What gist_pages_fork writes beside the block table (int32): cached_len, copy_src, copy_dst and
+    copy_rows [B], num_copies [1], free_range [2]."""
+    cached_len: torch.Tensor
+    copy_src: torch.Tensor
+    copy_dst: torch.Tensor
+    copy_rows: torch.Tensor
+    num_copies: torch.Tensor
     free_range: torch.Tensor
 
 
@@ -155,6 +187,22 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             lib.gist_attn_paged_workspace_bytes.argtypes = [PD]
             lib.gist_attn_paged_fp8kv.restype = ctypes.c_int
             lib.gist_attn_paged_fp8kv.argtypes = [V, V, V, V, V, V, V, V, ctypes.c_size_t, PD, V]
+            lib.gist_attn_paged_decode_workspace_bytes.restype = ctypes.c_size_t
+            lib.gist_attn_paged_decode_workspace_bytes.argtypes = [PD]
+            lib.gist_attn_paged_decode.restype = ctypes.c_int
+            lib.gist_attn_paged_decode.argtypes = [V, V, V, V, V, V, V, ctypes.c_size_t, PD, V]
+            lib.gist_pages_free.restype = ctypes.c_int
+            lib.gist_pages_free.argtypes = [V, V, V, V, V, PD, V]
+            lib.gist_pages_compact.restype = ctypes.c_int
+            lib.gist_pages_compact.argtypes = [V, V, V, V, V, V, V, V, V, PD, V]
+            lib.gist_pages_fork.restype = ctypes.c_int
+            lib.gist_pages_fork.argtypes = [V, V, V, V, ctypes.c_int32, V, V, V, V, V, V, V, PD, V]
+            lib.gist_pages_copy.restype = ctypes.c_int
+            lib.gist_pages_copy.argtypes = [V, V, ctypes.c_int32, V, V, V, V, ctypes.c_int32, PD, V]
+            lib.gist_qkv_rope_w4.restype = ctypes.c_int
+            lib.gist_qkv_rope_w4.argtypes = [V, V, V, V, V, V, V, ctypes.c_int, ctypes.c_int, PD, V]
+            lib.gist_out_proj_w4.restype = ctypes.c_int
+            lib.gist_out_proj_w4.argtypes = [V, V, V, V, ctypes.c_int, ctypes.c_int, PD, V]
             _lib = lib
     return _lib
 
@@ -591,3 +639,173 @@ def gist_attn_paged_fp8kv(q, kv_pool_e4m3, kv_scale, block_table, q_start, kv_le
           _sized(out, bf, "out", n, dev), _sized(workspace, torch.uint8, "workspace", 0, dev),
           workspace.numel(), ctypes.byref(D))
     return out
+
+
+# ------------------------------- single tokens over a bf16 paged cache, its blocks ---
+
+def paged_decode_workspace_bytes(dims: dict) -> int:
+    """Device bytes gist_attn_paged_decode needs for these dimensions on the current device."""
+    D = make_paged_dims(dims)
+    return int(load_library().gist_attn_paged_decode_workspace_bytes(ctypes.byref(D)))
+
+
+def gist_attn_paged_decode(q, kv_pool, block_table, kv_len, q_start=None, out=None, workspace=None, *,
+                           dims: dict, status: torch.Tensor | None = None, stream=None):
+    """Attention of one new token a request over a bf16 paged cache that already holds it;
+    returns `out` [T][Hq][d] (rows of no request are not written).  `q_start`: the plan's,
+    or None where request r's token is row r.  `workspace`: a uint8 tensor of at least
+    paged_decode_workspace_bytes(dims) bytes, one per call in flight.  Both are allocated on
+    the call's stream if None."""
+    lib = load_library()
+    B, dev, bf, i32 = dims["num_requests"], _index(q, "q"), torch.bfloat16, torch.int32
+    if out is None:
+        out = _like(q, stream)
+    n = dims["num_tokens"] * dims["num_q_heads"] * dims["head_dim"]
+    planes = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
+    D = make_paged_dims(dims, status)
+    if workspace is None:
+        with _allocating_for(stream, dev), torch.cuda.device(dev):
+            need = int(lib.gist_attn_paged_decode_workspace_bytes(ctypes.byref(D)))
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _call(dev, stream, lib.gist_attn_paged_decode, _sized(q, bf, "q", n, dev),
+          _sized(kv_pool, bf, "kv_pool", planes * dims["block_len"] * dims["head_dim"], dev),
+          _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
+          None if q_start is None else _sized(q_start, i32, "q_start", B + 1, dev),
+          _sized(kv_len, i32, "kv_len", B, dev), _sized(out, bf, "out", n, dev),
+          _sized(workspace, torch.uint8, "workspace", 0, dev), workspace.numel(), ctypes.byref(D))
+    return out
+
+
+def _outputs(kind, out, shapes, stream, dev):
+    """A NamedTuple `kind` of the int32 tensors `out`, allocated on the call's stream if None."""
+    if out is None:
+        with _allocating_for(stream, dev):
+            out = [torch.empty(s, dtype=torch.int32, device=torch.device("cuda", dev)) for s in shapes]
+    return kind(*out)
+
+
+def gist_pages_free(cached_len, block_table, out=None, *, dims: dict, status: torch.Tensor | None = None,
+                    stream=None) -> PagesFree:
+    """Reference counts and the free list from the tables of the requests alive.  `out`: three
+    int32 tensors in PagesFree's order to write into (allocated on the call's stream if None)."""
+    lib = load_library()
+    B, n, i32, dev = dims["num_requests"], dims["num_blocks"], torch.int32, _index(block_table, "block_table")
+    f = _outputs(PagesFree, out, (n, n, 2), stream, dev)
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_pages_free, _sized(cached_len, i32, "cached_len", B, dev),
+          _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
+          _sized(f.ref_count, i32, "ref_count", n, dev), _sized(f.free_blocks, i32, "free_blocks", n, dev),
+          _sized(f.free_range, i32, "free_range", 2, dev), ctypes.byref(D))
+    return f
+
+
+def gist_pages_compact(cached_len, block_table, out=None, *, dims: dict, status: torch.Tensor | None = None,
+                       stream=None) -> PagesCompact:
+    """Renames the blocks in use to 0, 1, ... and lists the copies that gist_pages_copy has to
+    make.  `out`: seven int32 tensors in PagesCompact's order to write into (its first may be
+    block_table), allocated on the call's stream if None."""
+    lib = load_library()
+    B, W, n, i32 = dims["num_requests"], dims["max_blocks"], dims["num_blocks"], torch.int32
+    dev = _index(block_table, "block_table")
+    f = _outputs(PagesCompact, out, ((B, W), n, n // 2, n // 2, 1, n, 2), stream, dev)
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_pages_compact, _sized(cached_len, i32, "cached_len", B, dev),
+          _sized(block_table, i32, "block_table", B * W, dev),
+          _sized(f.block_table, i32, "block_table (out)", B * W, dev), _sized(f.new_id, i32, "new_id", n, dev),
+          _sized(f.copy_src, i32, "copy_src", n // 2, dev), _sized(f.copy_dst, i32, "copy_dst", n // 2, dev),
+          _sized(f.num_copies, i32, "num_copies", 1, dev), _sized(f.free_blocks, i32, "free_blocks", n, dev),
+          _sized(f.free_range, i32, "free_range", 2, dev), ctypes.byref(D))
+    return f
+
+
+def gist_pages_fork(cached_len, parent, block_table, free_blocks, free_range, out=None, *, dims: dict,
+                    status: torch.Tensor | None = None, stream=None) -> PagesFork:
+    """Rows that go on from another row's cache (block_table in place); lists the copies that
+    gist_pages_copy has to make.  `out`: six int32 tensors in PagesFork's order to write into
+    (allocated on the call's stream if None)."""
+    lib = load_library()
+    B, i32, dev = dims["num_requests"], torch.int32, _index(block_table, "block_table")
+    f = _outputs(PagesFork, out, (B, B, B, B, 1, 2), stream, dev)
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_pages_fork, _sized(cached_len, i32, "cached_len", B, dev),
+          _sized(parent, i32, "parent", B, dev), _sized(block_table, i32, "block_table", B * dims["max_blocks"], dev),
+          _sized(free_blocks, i32, "free_blocks", 0, dev), free_blocks.numel(),
+          _sized(free_range, i32, "free_range", 2, dev), _sized(f.cached_len, i32, "cached_len (out)", B, dev),
+          _sized(f.copy_src, i32, "copy_src", B, dev), _sized(f.copy_dst, i32, "copy_dst", B, dev),
+          _sized(f.copy_rows, i32, "copy_rows", B, dev), _sized(f.num_copies, i32, "num_copies", 1, dev),
+          _sized(f.free_range, i32, "free_range (out)", 2, dev), ctypes.byref(D))
+    return f
+
+
+_POOL_BYTES = {torch.bfloat16: 2, torch.float8_e4m3fn: 1, torch.uint8: 1}
+
+
+def gist_pages_copy(kv_pool, kv_scale, copy_src, copy_dst, copy_rows=None, num_copies=None, *, dims: dict,
+                    status: torch.Tensor | None = None, stream=None):
+    """Copies blocks copy_src to copy_dst (their first copy_rows rows, or whole) within a pool
+    (bf16, float8_e4m3fn or uint8) and its scales, if not None; in place.  `num_copies`: how many
+    entries count, on the device (all if None)."""
+    lib = load_library()
+    dev, i32 = _index(kv_pool, "kv_pool"), torch.int32
+    _index(copy_src, "copy_src")
+    n = copy_src.numel()
+    if kv_pool.dtype not in _POOL_BYTES:
+        raise TypeError(f"kv_pool must be bfloat16, float8_e4m3fn or uint8, got {kv_pool.dtype}")
+    planes = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_pages_copy,
+          _sized(kv_pool, kv_pool.dtype, "kv_pool", planes * dims["block_len"] * dims["head_dim"], dev),
+          None if kv_scale is None else _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
+          _POOL_BYTES[kv_pool.dtype], _sized(copy_src, i32, "copy_src", n, dev), _sized(copy_dst, i32, "copy_dst", n, dev),
+          None if copy_rows is None else _sized(copy_rows, i32, "copy_rows", n, dev),
+          None if num_copies is None else _sized(num_copies, i32, "num_copies", 1, dev), n, ctypes.byref(D))
+    return kv_pool
+
+
+# ------------------------------------------- 4-bit projections of few tokens ---
+
+def _w4_sizes(group):
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+
+
+def gist_qkv_rope_w4(x, w, w_scale, position, q=None, k_new=None, v_new=None, *, group: int, dims: dict,
+                     status: torch.Tensor | None = None, stream=None):
+    """QKV projection of x [T][d_model] with 4-bit weights w (uint8 [N][d_model / 2]) and bf16
+    scales [N][d_model / group], q and k rotated at `position`; returns (q, k_new, v_new), which
+    go to the append and the attention with flags=FLAG_PREROTATED."""
+    lib = load_library()
+    T, Hq, Hkv, d = dims["num_tokens"], dims["num_q_heads"], dims["num_kv_heads"], dims["head_dim"]
+    dev, bf, K = _index(x, "x"), torch.bfloat16, int(x.shape[-1])
+    _w4_sizes(group)
+    if q is None:
+        q = _new((T, Hq, d), bf, x, stream)
+    if k_new is None:
+        k_new = _new((T, Hkv, d), bf, x, stream)
+    if v_new is None:
+        v_new = _new((T, Hkv, d), bf, x, stream)
+    N = (Hq + 2 * Hkv) * d
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_qkv_rope_w4, _sized(x, bf, "x", T * K, dev), _sized(w, torch.uint8, "w", N * K // 2, dev),
+          _sized(w_scale, bf, "w_scale", N * (K // group), dev), _sized(position, torch.int32, "position", T, dev),
+          _sized(q, bf, "q", T * Hq * d, dev), _sized(k_new, bf, "k_new", T * Hkv * d, dev),
+          _sized(v_new, bf, "v_new", T * Hkv * d, dev), K, group, ctypes.byref(D))
+    return q, k_new, v_new
+
+
+def gist_out_proj_w4(attn_out, w, w_scale, y=None, *, group: int, dims: dict, status: torch.Tensor | None = None,
+                     stream=None):
+    """y [T][d_model] = attn_out [T][Hq][d] . w^T with 4-bit weights w (uint8 [d_model][Hq d / 2])
+    and bf16 scales [d_model][Hq d / group]."""
+    lib = load_library()
+    T, K, dev, bf = dims["num_tokens"], dims["num_q_heads"] * dims["head_dim"], _index(attn_out, "attn_out"), torch.bfloat16
+    _w4_sizes(group)
+    _index(w, "w")
+    N = int(w.shape[0])
+    if y is None:
+        y = _new((T, N), bf, attn_out, stream)
+    D = make_paged_dims(dims, status)
+    _call(dev, stream, lib.gist_out_proj_w4, _sized(attn_out, bf, "attn_out", T * K, dev),
+          _sized(w, torch.uint8, "w", N * K // 2, dev), _sized(w_scale, bf, "w_scale", N * (K // group), dev),
+          _sized(y, bf, "y", T * N, dev), N, group, ctypes.byref(D))
+    return y

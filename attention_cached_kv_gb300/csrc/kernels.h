@@ -114,6 +114,60 @@ int launch_paged_prefill(const PagedProblem& pb, void* workspace, int min_new, i
                          cudaStream_t stream);
 size_t paged_prefill_workspace(const PagedProblem& pb, int min_new, int sms);
 
+// One token a request over a bf16 pool (paged_bf16.cu); pb.pool is the bf16 pool, pb.q_start may be null.
+int launch_paged_bf16(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream);
+size_t paged_bf16_workspace(const PagedProblem& pb, int sms);
+
+// The blocks of a paged cache between steps (paged_pages.cu).
+struct PagesArgs {
+  const int32_t* cached_len;
+  const int32_t* block_table;
+  int32_t* table_out;  // compact: may be block_table
+  int32_t* ids;        // [num_blocks]: reference counts, or new ids
+  int32_t* src;        // compact: [num_blocks / 2]
+  int32_t* dst;
+  int32_t* count;
+  int32_t* free_blocks;  // [num_blocks]
+  int32_t* free_range;
+  int32_t* status;
+  int B, W, block_len, num_blocks;
+};
+struct ForkArgs {
+  const int32_t* cached_len;
+  const int32_t* parent;
+  int32_t* block_table;
+  const int32_t* free_blocks;
+  const int32_t* free_range;
+  int32_t* cached_len_out;
+  int32_t* src;  // [B]
+  int32_t* dst;
+  int32_t* rows;
+  int32_t* count;
+  int32_t* free_range_out;
+  int32_t* status;
+  int B, W, block_len, num_blocks, num_free;
+};
+struct CopyArgs {
+  uint4* pool;
+  float* scale;  // or nullptr
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* rows;   // or nullptr: whole blocks
+  const int32_t* count;  // device; or nullptr: n
+  int32_t* status;
+  int n, num_blocks, block_len;
+  int planes, plane;  // of a block, and 16-byte pieces of a plane
+};
+int launch_pages_tables(const PagesArgs& a, bool compact, cudaStream_t stream);
+int launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
+int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream);
+
+// Projections of a few tokens with 4-bit weights (proj_w4.cu).
+int launch_qkv_rope_w4(const PagedProblem& pb, const void* x, const void* w, const void* scale, const int32_t* position,
+                       void* q, void* k_new, void* v_new, int d_model, int group, int sms, cudaStream_t stream);
+int launch_out_proj_w4(const PagedProblem& pb, const void* attn, const void* w, const void* scale, void* y, int d_model,
+                       int group, int sms, cudaStream_t stream);
+
 // Whether the prefill kernel can hold this problem's tiles in shared memory.
 bool prefill_fits(const Problem& pb);
 bool prefill_tc_fits(const Problem& pb);

@@ -1,0 +1,356 @@
+// paged_pages.cu -- the blocks ("pages") of a paged cache between steps: sharing
+// them with forked requests, giving them back, moving them together, copying them
+// ([Suffix page, §6 问题四]: a logical slot is found through the block table, so
+// a block moves by rewriting entries).
+//
+// free      ref[b] = number of live entries naming b; the free list is the ids
+//           with ref 0 in ascending order.  Nothing is counted up and down
+//           between calls, so a lost count cannot leak a block.
+// compact   n = blocks in use.  The k-th id in use from n on goes to the k-th unused
+//           id below n; there are as many of one as of the other, and no source is a
+//           destination, so the copies need no order.
+// fork      a child's row is its parent's; where the parent's last block is
+//           filled in part, the child gets a block of its own and a copy of it.
+// copy      the data, from the lists that fork and compact leave on the device.
+//
+// Bound: the tables are latency (few hundred KB, dependent passes), the copy is HBM.
+//
+// Pages: [Suffix page] icman.com.cn news 64898.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace gattn {
+namespace {
+
+// ------------------------------------------------------- free and compact ---
+//
+// One cluster does the whole of it, its barriers between the passes, so one launch
+// is enough and no counter has to be zeroed before.
+constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kSeg = 128;  // entries of one row that a warp takes at a time
+
+// Blocks of a request: the live entries of its row.
+__device__ __forceinline__ int blocks_of(int len, int block_len, int W, bool& bad) {
+  if (len <= 0) return 0;
+  const unsigned n = ((unsigned)len + block_len - 1) / block_len;
+  if (n > (unsigned)W) bad = true;
+  return min((int)n, W);
+}
+
+// Calls visit(r, j0, n) by whole warps for every segment [j0, j0 + kSeg) of every row of
+// the table, n the row's live entries.
+template <class Visit>
+__device__ __forceinline__ void each_segment(const PagesArgs& a, int warp, int warps, bool& bad, Visit visit) {
+  const int lane = threadIdx.x & 31;
+  const int per_row = (a.W + kSeg - 1) / kSeg;
+  const int64_t units = (int64_t)a.B * per_row;
+  const int64_t u0 = units * warp / warps, u1 = units * (warp + 1) / warps;
+  for (int64_t base = u0; base < u1; base += 32) {
+    const int64_t mine = base + lane;  // each lane reads the length of one of 32 units
+    int row = 0, seg = 0, n = 0;
+    if (mine < u1) {
+      row = (int)(mine / per_row);
+      seg = (int)(mine - (int64_t)row * per_row);
+      n = blocks_of(a.cached_len[row], a.block_len, a.W, bad);
+    }
+    const int m = (int)min((int64_t)32, u1 - base);
+    for (int i = 0; i < m; ++i)
+      visit(__shfl_sync(0xffffffffu, row, i), __shfl_sync(0xffffffffu, seg, i) * kSeg, __shfl_sync(0xffffffffu, n, i));
+  }
+}
+
+template <bool COMPACT>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ PagesArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int count[kWarps];                // ids in use in each warp's slice
+  __shared__ int below[kWarps];                // COMPACT: those of them below n
+  __shared__ int all[kCtas * kWarps], all_below;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x, gw = cta * kWarps + warp;
+  bool bad = false;
+
+  for (int b = cta * kThreads + tid; b < a.num_blocks; b += kCtas * kThreads) a.ids[b] = 0;
+  cluster.sync();
+
+  each_segment(a, gw, kCtas * kWarps, bad, [&](int r, int j0, int n) {
+    const int32_t* row = a.block_table + (int64_t)r * a.W;
+    int id[kSeg / 32];
+#pragma unroll
+    for (int k = 0; k < kSeg / 32; ++k) {
+      const int j = j0 + 32 * k + lane;
+      id[k] = j < n ? row[j] : -1;
+      if (j < n && (id[k] < 0 || id[k] >= a.num_blocks)) {
+        bad = true;
+        id[k] = -1;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSeg / 32; ++k) {
+      if (id[k] < 0) continue;
+      if constexpr (COMPACT) a.ids[id[k]] = 1;
+      else atomicAdd(&a.ids[id[k]], 1);
+    }
+  });
+  if (bad) report(a.status, GIST_ATTN_STATUS_BAD_BLOCK);
+  cluster.sync();
+
+  // each warp's slice of the ids: how many are in use
+  const int per = ((a.num_blocks + kCtas * kWarps - 1) / (kCtas * kWarps) + 31) & ~31;
+  const int b0 = (int)min((int64_t)gw * per, (int64_t)a.num_blocks), b1 = min(b0 + per, a.num_blocks);
+  int used = 0;
+  for (int b = b0; b < b1; b += 32) used += __popc(__ballot_sync(0xffffffffu, b + lane < b1 && __ldcg(a.ids + b + lane) != 0));
+  if (lane == 0) count[warp] = used;
+  cluster.sync();
+  if (tid < kCtas * kWarps) all[tid] = *cluster.map_shared_rank(&count[tid % kWarps], tid / kWarps);
+  __syncthreads();
+  int before = 0, n = 0;  // ids in use ahead of the slice, and in all
+  for (int w = lane; w < kCtas * kWarps; w += 32) {
+    n += all[w];
+    before += w < gw ? all[w] : 0;
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const uint32_t ahead = (1u << lane) - 1;
+
+  if constexpr (!COMPACT) {
+    const int free = a.num_blocks - n;
+    for (int b = b0; b < b1; b += 32) {
+      const bool in = b + lane < b1, use = in && __ldcg(a.ids + b + lane) != 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, use);
+      // the unused ids ahead of an id: the id itself less those in use ahead of it
+      if (in && !use) a.free_blocks[b + lane - before - __popc(m & ahead)] = b + lane;
+      before += __popc(m);
+    }
+    for (int i = free + cta * kThreads + tid; i < a.num_blocks; i += kCtas * kThreads) a.free_blocks[i] = -1;
+    if (cta == 0 && tid == 0) {
+      a.free_range[0] = 0;
+      a.free_range[1] = free;
+    }
+    cluster.sync();  // no CTA leaves while another reads its counts
+    return;
+  }
+
+  // ids in use below n, which say how many blocks move
+  int low = 0;
+  for (int b = b0; b < min(b1, n); b += 32) low += __popc(__ballot_sync(0xffffffffu, b + lane < min(b1, n) && __ldcg(a.ids + b + lane) != 0));
+  if (lane == 0) below[warp] = low;
+  cluster.sync();
+  if (tid == 0) all_below = 0;
+  __syncthreads();
+  if (tid < kCtas * kWarps) atomicAdd(&all_below, *cluster.map_shared_rank(&below[tid % kWarps], tid / kWarps));
+  __syncthreads();
+  const int stay = all_below, moves = n - stay;
+  for (int b = b0; b < b1; b += 32) {
+    const int id = b + lane;
+    const bool in = id < b1, use = in && __ldcg(a.ids + id) != 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, use);
+    const int rank = before + __popc(m & ahead);  // ids in use ahead of this one
+    if (use && id >= n) a.src[rank - stay] = id;
+    if (in && !use && id < n) a.dst[id - rank] = id;
+    if (in) a.ids[id] = use && id < n ? id : -1;
+    before += __popc(m);
+  }
+  for (int i = moves + cta * kThreads + tid; i < a.num_blocks / 2; i += kCtas * kThreads) a.src[i] = a.dst[i] = -1;
+  for (int i = cta * kThreads + tid; i < a.num_blocks; i += kCtas * kThreads) a.free_blocks[i] = i < a.num_blocks - n ? n + i : -1;
+  if (cta == 0 && tid == 0) {
+    a.count[0] = moves;
+    a.free_range[0] = 0;
+    a.free_range[1] = a.num_blocks - n;
+  }
+  cluster.sync();
+  for (int k = cta * kThreads + tid; k < moves; k += kCtas * kThreads) a.ids[__ldcg(a.src + k)] = __ldcg(a.dst + k);
+  cluster.sync();
+  each_segment(a, gw, kCtas * kWarps, bad, [&](int r, int j0, int live) {
+    const int64_t at = (int64_t)r * a.W;
+    int id[kSeg / 32];
+#pragma unroll
+    for (int k = 0; k < kSeg / 32; ++k) {
+      const int j = j0 + 32 * k + lane;
+      id[k] = j < a.W ? a.block_table[at + j] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kSeg / 32; ++k) {
+      const int j = j0 + 32 * k + lane;
+      if (j < live && id[k] >= 0 && id[k] < a.num_blocks) id[k] = __ldcg(a.ids + id[k]);
+      if (j < a.W) a.table_out[at + j] = id[k];
+    }
+  });
+}
+
+// ------------------------------------------------------------------- fork ---
+//
+// Every CTA sums over all requests by itself (as the plan does), then takes rows of its
+// own; the rows read are those of requests that are not forked, so none is written.
+__global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ ForkArgs a) {
+  extern __shared__ int take[];  // [B] index among the blocks taken; -1: none needed, -2: not served, -3: not forked
+  __shared__ int warp_sum[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, a.B), r1 = min(r0 + per, a.B);
+  const int begin = max(a.free_range[0], 0), end = max(min(a.free_range[1], a.num_free), 0);
+  const int avail = max(end - begin, 0);
+  // 1: a block is needed, 0: none, -2: cannot be forked, -3: is not
+  auto asked = [&](int r) {
+    const int p = a.parent[r];
+    if (p < 0 || p == r) return -3;
+    if (p >= a.B) return -2;
+    const int pp = a.parent[p];
+    if (pp >= 0 && pp != p) return -2;
+    const int c = a.cached_len[p];
+    if (c < 0 || (int64_t)c > (int64_t)a.W * a.block_len) return -2;
+    return c % a.block_len != 0 ? 1 : 0;
+  };
+  int own = 0;
+  for (int r = r0; r < r1; ++r) own += asked(r) == 1;
+  int inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int before = inc - own, needed = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    needed += warp_sum[w];
+  }
+  const int taken = min(needed, avail);
+  for (int r = r0; r < r1; ++r) {
+    const int n = asked(r);
+    take[r] = n < 0 ? n : n == 0 ? -1 : before < avail ? before : -2;
+    before += n == 1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.count[0] = taken;
+    a.free_range_out[0] = max(a.free_range[0], 0) + taken;
+    a.free_range_out[1] = a.free_range[1];
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int i = taken + tid; i < a.B; i += kThreads) a.src[i] = a.dst[i] = a.rows[i] = -1;
+
+  int bits = 0;
+  for (int r = blockIdx.x * kWarps + warp; r < a.B; r += gridDim.x * kWarps) {
+    const int k = take[r];
+    if (k == -3) {
+      if (lane == 0) a.cached_len_out[r] = a.cached_len[r];
+      continue;
+    }
+    if (k == -2) {
+      bits |= GIST_ATTN_STATUS_NOT_SERVED;
+      if (lane == 0) a.cached_len_out[r] = 0;
+      continue;
+    }
+    const int p = a.parent[r], c = a.cached_len[p], full = c / a.block_len, part = c - full * a.block_len;
+    const int32_t* from = a.block_table + (int64_t)p * a.W;
+    int32_t* to = a.block_table + (int64_t)r * a.W;
+    int src = -1, dst = -1;
+    if (k >= 0) {
+      src = from[full];
+      dst = a.free_blocks[begin + k];
+    }
+    const bool ok = k < 0 || (src >= 0 && src < a.num_blocks && dst >= 0 && dst < a.num_blocks);
+    if (lane == 0) {
+      if (k >= 0) {
+        a.src[k] = ok ? src : -1;
+        a.dst[k] = ok ? dst : -1;
+        a.rows[k] = ok ? part : -1;
+      }
+      a.cached_len_out[r] = ok ? c : 0;
+      if (ok && k >= 0) to[full] = dst;
+    }
+    if (ok) {
+      for (int j = lane; j < full; j += 32) to[j] = from[j];
+    } else {
+      bits |= GIST_ATTN_STATUS_BAD_BLOCK;
+    }
+  }
+  if (bits && lane == 0) report(a.status, bits);
+}
+
+// ------------------------------------------------------------------- copy ---
+//
+// Chunks of kCopyThreads x V 16-byte pieces, a thread's V loads in flight together; a
+// copy of `rows` rows of a block counts the pieces of those rows alone, plane after plane.
+constexpr int kCopyThreads = 256;
+
+template <int V>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+  const int n = a.count ? min(max(*a.count, 0), a.n) : a.n;
+  const int row = a.plane / a.block_len;  // pieces of a row
+  const int whole = a.planes * a.plane;
+  const int chunks = (whole + kCopyThreads * V - 1) / (kCopyThreads * V);
+  const int64_t total = (int64_t)n * chunks;
+  bool bad = false;
+  for (int64_t at = blockIdx.x; at < total; at += gridDim.x) {
+    const int i = (int)(at / chunks), first = (int)(at - (int64_t)i * chunks) * (kCopyThreads * V);
+    const int s = a.src[i], d = a.dst[i];
+    if (s < 0 || d < 0) continue;
+    const int rows = a.rows ? a.rows[i] : a.block_len;
+    if (s >= a.num_blocks || d >= a.num_blocks || rows < 0 || rows > a.block_len) {
+      bad = true;
+      continue;
+    }
+    if (s == d) continue;
+    const uint4* from = a.pool + (int64_t)s * whole;
+    uint4* to = a.pool + (int64_t)d * whole;
+    const int run = rows * row, pieces = run * a.planes;  // of the planes' parts that are copied
+    if (a.scale && first == 0)
+      for (int k = threadIdx.x; k < a.planes; k += kCopyThreads)
+        a.scale[(int64_t)d * a.planes + k] = a.scale[(int64_t)s * a.planes + k];
+    uint4 v[V];
+    int off[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int x = first + k * kCopyThreads + threadIdx.x;
+      off[k] = x < pieces ? x : -1;
+      if (rows != a.block_len && x < pieces) {
+        const int pl = x / run;
+        off[k] = pl * a.plane + (x - pl * run);
+      }
+      if (off[k] >= 0) v[k] = __ldcs(from + off[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (off[k] >= 0) __stcs(to + off[k], v[k]);
+  }
+  if (bad && threadIdx.x == 0) report(a.status, GIST_ATTN_STATUS_BAD_BLOCK);
+}
+
+}  // namespace
+
+int launch_pages_tables(const PagesArgs& a, bool compact, cudaStream_t stream) {
+  if (compact) tables_kernel<true><<<kCtas, kThreads, 0, stream>>>(a);
+  else tables_kernel<false><<<kCtas, kThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+int launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
+  const int smem = a.B * (int)sizeof(int);
+  // always the largest limit, so that no thread's call lowers it between another's two lines here
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanRequests * (int)sizeof(int)) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  const int want = (a.B + kWarps - 1) / kWarps, grid = want < 1 ? 1 : want > 64 ? 64 : want;
+  fork_kernel<<<grid, kThreads, smem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream) {
+  const int64_t pieces = (int64_t)a.n * a.planes * a.plane;
+  const int most = 8 * sms;
+  auto grid = [&](int V) {
+    const int64_t chunks = (int64_t)a.n * ((a.planes * (int64_t)a.plane + kCopyThreads * V - 1) / (kCopyThreads * V));
+    return (int)(chunks < most ? chunks : most);
+  };
+  if (pieces >= (int64_t)most * kCopyThreads * 8) copy_kernel<8><<<grid(8), kCopyThreads, 0, stream>>>(a);
+  else copy_kernel<2><<<grid(2), kCopyThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+}  // namespace gattn

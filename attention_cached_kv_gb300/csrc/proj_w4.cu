@@ -1,0 +1,333 @@
+// proj_w4.cu -- projections of a few tokens with 4-bit weights and a scale per group
+// of inputs: the QKV projection with RoPE in its epilogue and the output
+// projection around the attention of a decoding step ([Gist page, "在线的一次
+// attention"]: per layer X is projected to Q, K, V, then attends; the projections
+// of gemm.cu need at least 22 tokens a pair).
+//
+//   y[t][n] = sum over groups of  s[n][group] * sum_{k in group} (c[n][k] - 8) x[t][k]
+//
+// The weights are read once and dominate the bytes: HBM bound.  The codes less 8 are
+// exact in bf16, so the inner sums run on mma.sync m16n8k16 with the weights
+// as the 16 rows and the tokens as the N (even one token is cheaper there than on
+// the CUDA cores, which would spend an FMA and a conversion a weight); the scale
+// is applied in fp32 to each group's sum.
+//
+// Eight codes of a word become four bf16 pairs (k, k + 4): bits 4 j of both halves,
+// or'ed into 128.0, are 128 + c exactly; less 136.  x is staged in shared
+// memory with its elements in the same order.  A tile's 16 rows are 8 neighbours
+// and their 8 rotation partners (half a head on), so a thread holds both values
+// of a rotated pair.
+//
+// Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gattn {
+namespace {
+
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kStep = 128;   // inputs of a ring stage
+constexpr int kStages = 8;   // of a warp's ring, 1 KB a row tile each
+constexpr int kMaxX = 72 * 1024;  // staged x of a CTA, at most
+
+struct W4Params {
+  const bf16* x;
+  const uint8_t* w;
+  const bf16* scale;
+  bf16* out[3];           // q, k_new, v_new; or y
+  const int32_t* position;  // nullptr: output projection
+  int T, N, K, group, tiles, slice;  // slice: inputs of a CTA
+  int Hq, Hkv, d;
+  uint64_t turn[64];
+};
+
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// Two codes (bits 0..3 and 16..19) less 8, as bf16: 128 + c is exact, and so is the difference.
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t c) {
+  const uint32_t v = (c & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// First row of a tile, and its other eight rows' distance.
+__device__ __forceinline__ int tile_row(const W4Params& p, int tile, int& apart) {
+  if (!p.position) {
+    apart = 8;
+    return tile * 16;
+  }
+  const int per_head = p.d / 16, head = tile / per_head;
+  apart = p.d / 2;
+  return head * p.d + (tile - head * per_head) * 8;
+}
+
+// NT tiles of 8 tokens, MR row tiles a warp, WR warps along the rows (the others along K).
+template <int NT, int MR, int WR>
+__global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4Params p) {
+  constexpr int WK = kWarps / WR, TN = NT * 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+  const int wr = warp % WR, wk = warp / WR;
+  const int split = cluster.num_blocks(), part = cluster.block_rank();
+  const int tile0 = (blockIdx.x / split) * (MR * WR) + wr * MR;
+  const int k0 = part * p.slice, k1 = min(k0 + p.slice, p.K);
+  const int t0 = blockIdx.y * TN;
+  const int tokens = min(TN, p.T - t0);
+  const uint32_t pitch = p.slice * 2 + 64;  // of a token's staged row: 64 modulo 128
+  const uint32_t xs = smem_u32(smem);
+  const int staged = min(TN, p.T);  // rows of x in shared memory; MMA columns behind them repeat the last
+  const uint32_t ring = xs + staged * pitch + warp * (kStages * MR * 1024);
+
+  // ---- weights: rows of 64 bytes, 16 a row tile; chunk c of row r at c ^ (r / 2 mod 4)
+  int row[MR], apart;
+#pragma unroll
+  for (int m = 0; m < MR; ++m) row[m] = tile0 + m < p.tiles ? tile_row(p, tile0 + m, apart) : -1;
+  const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
+  const int mine = (steps - wk + WK - 1) / WK;  // steps wk, wk + WK, ...
+  auto issue = [&](int i) {
+    if (i < mine) {
+      const int k = k0 + (wk + i * WK) * kStep;
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = h * 8 + g8, kk = k + t4 * 32;
+          const bool in = row[m] >= 0 && kk < k1;
+          const int64_t at = in ? (int64_t)(row[m] + h * apart + g8) * (p.K / 2) + kk / 2 : 0;
+          cp_async16_or_zero(ring + ((i % kStages) * MR + m) * 1024 + r * 64 + ((t4 ^ ((r >> 1) & 3)) << 4), p.w + at, in);
+        }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+  // ---- x: eight inputs as the pairs (k, k + 4), zeros past the inputs
+  const int pieces = p.slice / 8;
+  for (int i = tid; i < staged * pieces; i += kThreads) {
+    const int t = i / pieces, c = i - t * pieces, k = k0 + c * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (t < tokens && k < k1) v = ldg16(p.x + (int64_t)(t0 + t) * p.K + k);
+    sts16(xs + t * pitch + c * 16, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
+  }
+  __syncthreads();
+
+  float acc[MR][NT][4];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+  const int groups = p.K / p.group, per32 = p.group / 32;
+
+  for (int i = 0; i < mine; ++i) {
+    const int k = k0 + (wk + i * WK) * kStep;
+    float sc[MR][4][2];
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kk = k + 32 * q;
+          sc[m][q][h] = row[m] >= 0 && kk < k1 ? __bfloat162float(p.scale[(int64_t)(row[m] + h * apart + g8) * groups + kk / p.group]) : 0.f;
+        }
+    cp_async_wait_group<kStages - 2>();
+    __syncwarp();
+    const uint32_t st = ring + (i % kStages) * MR * 1024;
+    float sum[MR][NT][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q % per32 == 0) {
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sum[m][n][0] = sum[m][n][1] = sum[m][n][2] = sum[m][n][3] = 0.f;
+      }
+      uint32_t a[MR][2][4];
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = h * 8 + g8;
+          const uint32_t u = lds32(st + m * 1024 + r * 64 + ((q ^ ((r >> 1) & 3)) << 4) + t4 * 4);
+          a[m][0][h] = codes_to_bf16x2(u);
+          a[m][0][2 + h] = codes_to_bf16x2(u >> 4);
+          a[m][1][h] = codes_to_bf16x2(u >> 8);
+          a[m][1][2 + h] = codes_to_bf16x2(u >> 12);
+        }
+      const uint32_t xa = xs + (k - k0 + 32 * q) * 2 + t4 * 16;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 b = lds16(xa + min(n * 8 + g8, staged - 1) * pitch);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+          mma_16816(sum[m][n], a[m][0], b.x, b.y);
+          mma_16816(sum[m][n], a[m][1], b.z, b.w);
+        }
+      }
+      if (q % per32 == per32 - 1) {
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(sum[m][n][e], sc[m][q][e >> 1], acc[m][n][e]);
+      }
+    }
+    __syncwarp();
+    issue(i + kStages - 1);
+  }
+
+  // ---- the warps along K and the CTAs of the cluster added up: [wk][row][token]
+  cp_async_wait_all();
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+  constexpr int RT = 16 * MR * WR, RP = TN + 1;
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        red[(wk * RT + (wr * MR + m) * 16 + (e >> 1) * 8 + g8) * RP + n * 8 + t4 * 2 + (e & 1)] = acc[m][n][e];
+  if (split > 1) cluster.sync();
+  else __syncthreads();
+  // pairs of rows; the cluster's CTAs share them out
+  constexpr int pairs = RT / 2 * TN;
+  for (int i = part * kThreads + tid; i < pairs; i += split * kThreads) {
+    const int t = i / (RT / 2), j = i - t * (RT / 2), tile = (blockIdx.x / split) * (MR * WR) + j / 8;
+    if (t >= tokens || tile >= p.tiles) continue;
+    const int at = ((j / 8) * 16 + (j & 7)) * RP + t;
+    float a = 0.f, b = 0.f;
+    for (int c = 0; c < split; ++c) {
+      const float* from = split > 1 ? cluster.map_shared_rank(red, c) : red;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        a += from[w * RT * RP + at];
+        b += from[w * RT * RP + at + 8 * RP];
+      }
+    }
+    int far;
+    const int n = tile_row(p, tile, far) + (j & 7);
+    if (!p.position) {
+      bf16* y = p.out[0] + (int64_t)(t0 + t) * p.N + n;
+      y[0] = __float2bfloat16(a);
+      y[8] = __float2bfloat16(b);
+      continue;
+    }
+    const int pos = p.position[t0 + t];
+    if (pos < 0) continue;
+    int head = n / p.d;
+    const int e = n - head * p.d;
+    if (head < p.Hq + p.Hkv) {
+      float sn, cs;
+      sincosf(turn_angle(pos, p.turn[e]), &sn, &cs);
+      const float x = a;
+      a = x * cs - b * sn;
+      b = b * cs + x * sn;
+    }
+    int which = 0, heads = p.Hq;
+    if (head >= p.Hq) which = 1, head -= p.Hq, heads = p.Hkv;
+    if (which == 1 && head >= p.Hkv) which = 2, head -= p.Hkv;
+    bf16* y = p.out[which] + ((int64_t)(t0 + t) * heads + head) * p.d + e;
+    y[0] = __float2bfloat16(a);
+    y[far] = __float2bfloat16(b);
+  }
+  if (split > 1) cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+template <int NT, int MR, int WR>
+int launch_as(W4Params p, int sms, cudaStream_t stream) {
+  constexpr int TN = NT * 8, RT = MR * WR;
+  const int blocks = (p.tiles + RT - 1) / RT, token_blocks = (p.T + TN - 1) / TN;
+  // K is split over the CTAs of a cluster until x fits and every SM has a CTA or two
+  int split = 1;
+  auto slice = [&](int s) { return ((p.K + s - 1) / s + kStep - 1) / kStep * kStep; };
+  const int staged = p.T < TN ? p.T : TN;
+  while (split < 8 && (staged * (slice(split) * 2 + 64) > kMaxX ||
+                       ((int64_t)blocks * token_blocks * split < 2 * sms && slice(split) >= 2 * kStep * (kWarps / WR))))
+    split *= 2;
+  p.slice = slice(split);
+  const int x_bytes = staged * (p.slice * 2 + 64), ring = kWarps * kStages * MR * 1024;
+  const int red = (kWarps / WR) * 16 * RT * (TN + 1) * 4;
+  const int smem = x_bytes + ring > red ? x_bytes + ring : red;
+  constexpr int kMostSmem = 227 * 1024;
+  if (smem > kMostSmem || token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(w4_kernel<NT, MR, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks * split, token_blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, w4_kernel<NT, MR, WR>, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+int launch(const W4Params& p, int sms, cudaStream_t stream) {
+  // the tokens in one pass where their part of x fits beside the rings, in more of fewer where not
+  int rc = GIST_ATTN_ERR_UNSUPPORTED;
+  if (p.T > 32) rc = launch_as<8, 1, 4>(p, sms, stream);
+  if (rc == GIST_ATTN_ERR_UNSUPPORTED && p.T > 16) rc = launch_as<4, 1, 4>(p, sms, stream);
+  if (rc == GIST_ATTN_ERR_UNSUPPORTED && p.T > 8) rc = launch_as<2, 1, 1>(p, sms, stream);
+  return rc == GIST_ATTN_ERR_UNSUPPORTED ? launch_as<1, 1, 1>(p, sms, stream) : rc;
+}
+
+}  // namespace
+
+int launch_qkv_rope_w4(const PagedProblem& pb, const void* x, const void* w, const void* scale, const int32_t* position,
+                       void* q, void* k_new, void* v_new, int d_model, int group, int sms, cudaStream_t stream) {
+  W4Params p = {};
+  p.x = static_cast<const bf16*>(x);
+  p.w = static_cast<const uint8_t*>(w);
+  p.scale = static_cast<const bf16*>(scale);
+  p.out[0] = static_cast<bf16*>(q);
+  p.out[1] = static_cast<bf16*>(k_new);
+  p.out[2] = static_cast<bf16*>(v_new);
+  p.position = position;
+  p.T = pb.T;
+  p.d = pb.d;
+  p.Hq = pb.Hq;
+  p.Hkv = pb.Hkv;
+  p.N = (pb.Hq + 2 * pb.Hkv) * pb.d;
+  p.K = d_model;
+  p.group = group;
+  p.tiles = p.N / 16;
+  for (int j = 0; j < 64; ++j) p.turn[j] = pb.turn[j];
+  return launch(p, sms, stream);
+}
+
+int launch_out_proj_w4(const PagedProblem& pb, const void* attn, const void* w, const void* scale, void* y, int d_model,
+                       int group, int sms, cudaStream_t stream) {
+  W4Params p = {};
+  p.x = static_cast<const bf16*>(attn);
+  p.w = static_cast<const uint8_t*>(w);
+  p.scale = static_cast<const bf16*>(scale);
+  p.out[0] = static_cast<bf16*>(y);
+  p.T = pb.T;
+  p.N = d_model;
+  p.K = pb.Hq * pb.d;
+  p.group = group;
+  p.tiles = d_model / 16;
+  return launch(p, sms, stream);
+}
+
+}  // namespace gattn

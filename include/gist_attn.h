@@ -56,8 +56,8 @@ extern "C" {
 #define GIST_ATTN_ERR_LAUNCH (-5)      /* the CUDA launch itself failed                 */
 #define GIST_ATTN_ERR_SCRATCH (-6)     /* gist_attn_fwd_noalloc: the call needs more
                                           scratch than the library's fixed array holds;
-                                          gist_attn_paged_fp8kv: the workspace is
-                                          missing, misaligned or too small             */
+                                          gist_attn_paged_fp8kv and _decode: the workspace
+                                          is missing, misaligned or too small          */
 
 /* Device status bits (OR-ed into *dims->status). */
 #define GIST_ATTN_STATUS_BAD_BLOCK 1 /* a block id was outside [0, num_blocks): that
@@ -71,7 +71,8 @@ extern "C" {
                                         the kernels that form q.K in f16 recompute the
                                         rows they reach in fp32.)                      */
 #define GIST_ATTN_STATUS_NOT_SERVED 8 /* gist_paged_plan: a request got no blocks or
-                                        tokens in this step (kv_len 0, slots -1)      */
+                                        tokens in this step (kv_len 0, slots -1);
+                                        gist_pages_fork: a fork got none (length 0)   */
 
 typedef struct {
   int32_t num_pairs;       /* P >= 0: pairs (or decode sequences) in this call          */
@@ -538,6 +539,165 @@ int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3, const float* 
                           const int32_t* kv_len, void* out, void* workspace,
                           size_t workspace_bytes, const gist_paged_dims* dims,
                           cudaStream_t stream);
+
+/*
+ * gist_attn_paged_decode -- one new token a request over a bf16 paged cache, each
+ * request with a cached length of its own ([KV page, "Reusable-state"]: the decode step,
+ * K_{<=t} = [K_{<t}; k_t], with the token's K/V already appended by gist_kv_append;
+ * [Suffix page, §6 问题四]: the block table):
+ *   out[row][h] = sum_j softmax_j(scale R(q[row]) . K_j) V_j,   j < kv_len[r],
+ * q rotated at kv_len[r] - 1 unless GIST_ATTN_FLAG_PREROTATED.  Lengths stay on the
+ * device, so one captured graph serves every step.
+ *   q, out      bf16 [T][Hq][d]
+ *   kv_pool     bf16 [num_blocks][L][2][Hkv][block_len][d], 16-byte aligned, read only
+ *   block_table int32 [B][W]; entries past ceil(kv_len / block_len) are not read
+ *   q_start     int32 [B + 1] (gist_paged_plan's): request r's token is row q_start[r],
+ *               and q_start[r + 1] == q_start[r] says that it has none in this step.
+ *               NULL: request r's token is row r (T >= B, GIST_ATTN_ERR_DIMS otherwise)
+ *   kv_len      int32 [B], the new token counted
+ *   workspace   device pointer, 256-byte aligned, at least
+ *               gist_attn_paged_decode_workspace_bytes(dims) bytes (GIST_ATTN_ERR_SCRATCH
+ *               otherwise): scratch, overwritten by every call; two calls that may
+ *               overlap on the GPU need one each
+ * max_new must be 1, block_len a multiple of 16, Hq / Hkv at most 128 and W * block_len at
+ * most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).  A request with kv_len <= 0 gets zeros.  Cached
+ * rows past kv_len may hold anything.  out must not overlap what the call reads; rows of
+ * no request are left as they were.  A block id outside the pool among those of the
+ * request's keys, or a kv_len past W * block_len, zeroes the request's row and sets
+ * GIST_ATTN_STATUS_BAD_BLOCK; a q_start pair outside [0, T], out of order or more than
+ * one apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as elsewhere.  The
+ * order of all sums is fixed: the same call gives the same bits.
+ */
+size_t gist_attn_paged_decode_workspace_bytes(const gist_paged_dims* dims);
+int gist_attn_paged_decode(const void* q, const void* kv_pool, const int32_t* block_table,
+                           const int32_t* q_start, const int32_t* kv_len, void* out,
+                           void* workspace, size_t workspace_bytes,
+                           const gist_paged_dims* dims, cudaStream_t stream);
+
+/*
+ * The blocks of a paged cache between steps.  The block table and the lengths say which
+ * blocks are in use: a request holds the first ceil(cached_len / block_len) entries of its
+ * row (none where cached_len <= 0, as for one that has ended), and several rows may name
+ * the same block.  gist_pages_fork and gist_pages_compact work on the tables and leave
+ * lists of the copies to make; gist_pages_copy makes them, in a pool of either type.
+ * All outputs are written whole; a list's entries past its count are -1.  No output may
+ * overlap an input or another output except where said.  These calls read
+ * num_requests, block_len, max_blocks, num_blocks and status of dims (gist_pages_copy:
+ * num_blocks, num_layers, num_kv_heads, block_len, head_dim and status).  num_blocks is at
+ * most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).
+ *
+ * gist_pages_free -- who holds what, and the free list, from the tables alone:
+ *   cached_len  int32 [B], block_table int32 [B][W], read only
+ *   ref_count   int32 [num_blocks], written: live entries that name the block
+ *   free_blocks int32 [num_blocks], written: the ids that no live entry names, ascending
+ *   free_range  int32 [2], written: {0, their number}
+ * free_blocks and free_range are what gist_paged_plan and gist_pages_fork take.  A block
+ * that a request took in a step which failed is free again.  A live entry outside
+ * [0, num_blocks) is passed over and sets GIST_ATTN_STATUS_BAD_BLOCK; so does a cached_len past
+ * W * block_len, which counts as that.
+ */
+int gist_pages_free(const int32_t* cached_len, const int32_t* block_table, int32_t* ref_count,
+                    int32_t* free_blocks, int32_t* free_range, const gist_paged_dims* dims,
+                    cudaStream_t stream);
+
+/*
+ * gist_pages_compact -- renames blocks so that the n in use are 0 .. n - 1: the ids in use
+ * from n on, ascending, take the unused ids below n, ascending.
+ *   cached_len, block_table as gist_pages_free
+ *   block_table_out int32 [B][W], written: live entries renamed, the others as they
+ *               are; may be block_table itself
+ *   new_id      int32 [num_blocks], written: the new id of a block in use, -1 of the others
+ *   copy_src, copy_dst int32 [num_blocks / 2], written: the blocks to copy (no destination is
+ *               a source), then -1; may be NULL where num_blocks is 1
+ *   num_copies  int32 [1], written: how many
+ *   free_blocks, free_range as gist_pages_free, after the renaming: n, n + 1, ...
+ * Call gist_pages_copy with the lists for each pool that the table indexes before anything
+ * else writes to it.  Entries outside the pool and lengths as gist_pages_free (such an entry
+ * is left as it is).
+ */
+int gist_pages_compact(const int32_t* cached_len, const int32_t* block_table,
+                       int32_t* block_table_out, int32_t* new_id, int32_t* copy_src,
+                       int32_t* copy_dst, int32_t* num_copies, int32_t* free_blocks,
+                       int32_t* free_range, const gist_paged_dims* dims, cudaStream_t stream);
+
+/*
+ * gist_pages_fork -- requests that go on from another one's cache.  Row r with
+ * p = parent[r] >= 0, p != r becomes a fork of row p: its first cached_len[p] / block_len entries
+ * are p's (shared), and where cached_len[p] is no multiple of block_len it takes a free
+ * block, to which the filled rows of p's last block are to be copied, so that both can
+ * append.  Other rows are left as they are.
+ *   cached_len  int32 [B], parent int32 [B], read only
+ *   block_table int32 [B][W], in and out: a fork's first ceil(cached_len[p] / block_len)
+ *               entries are written
+ *   free_blocks, num_free, free_range as gist_paged_plan: taken from the front in
+ *               request order
+ *   cached_len_out int32 [B], written: cached_len[p] of a fork, cached_len[r] of the others
+ *   copy_src, copy_dst, copy_rows int32 [B], written: the blocks to copy and the filled rows
+ *               of each, then -1
+ *   num_copies  int32 [1], written: how many
+ *   free_range_out int32 [2], written: free_range after the call (a begin below zero
+ *               counts as zero; the end is passed on as it is)
+ * A fork is not served where p is no row, is itself a fork in this call or has a cached_len
+ * outside [0, W * block_len], or where the free blocks do not last: cached_len_out 0, no
+ * entry written, GIST_ATTN_STATUS_NOT_SERVED.  A block id outside [0, num_blocks) as the
+ * source or destination of its copy gives cached_len_out 0, -1 in the lists and
+ * GIST_ATTN_STATUS_BAD_BLOCK.  What a row held before it became a fork is given back by
+ * the next gist_pages_free.  At most 16384 requests (GIST_ATTN_ERR_UNSUPPORTED).
+ */
+int gist_pages_fork(const int32_t* cached_len, const int32_t* parent, int32_t* block_table,
+                    const int32_t* free_blocks, int32_t num_free, const int32_t* free_range,
+                    int32_t* cached_len_out, int32_t* copy_src, int32_t* copy_dst,
+                    int32_t* copy_rows, int32_t* num_copies, int32_t* free_range_out,
+                    const gist_paged_dims* dims, cudaStream_t stream);
+
+/*
+ * gist_pages_copy -- copies blocks within a pool, all layers, K and V and heads of them.
+ *   kv_pool     [num_blocks][L][2][Hkv][block_len][d] of elem_bytes each (2: bf16,
+ *               1: E4M3), 16-byte aligned, written
+ *   kv_scale    float [num_blocks][L][2][Hkv], copied with the blocks, or NULL
+ *   copy_src, copy_dst int32 [max_copies]
+ *   copy_rows   int32 [max_copies]: the first so many rows of every plane are copied,
+ *               the others left as they are; NULL: whole blocks
+ *   num_copies  device int32 [1]: how many of the entries count (at most max_copies), or NULL: all
+ * An entry with a negative source or destination is passed over, as is one whose source is its
+ * destination; one with an id from num_blocks on, or rows outside [0, block_len], is passed
+ * over and sets GIST_ATTN_STATUS_BAD_BLOCK.  A block that is the destination of two
+ * entries, or the destination of one and the source of another, ends up unspecified.  A block
+ * has at most 2^30 16-byte pieces and d is 64 or 128 (GIST_ATTN_ERR_UNSUPPORTED).
+ */
+int gist_pages_copy(void* kv_pool, float* kv_scale, int32_t elem_bytes, const int32_t* copy_src,
+                    const int32_t* copy_dst, const int32_t* copy_rows, const int32_t* num_copies,
+                    int32_t max_copies, const gist_paged_dims* dims, cudaStream_t stream);
+
+/*
+ * gist_qkv_rope_w4, gist_out_proj_w4 -- gist_qkv_rope and gist_out_proj for few tokens (from one
+ * on), with 4-bit weights and a scale per group of inputs:
+ *   w[n][k] = (c[n][k] - 8) scale[n][k / group],  c = 0 .. 15
+ *   w        uint8 [N][K / 2]: c[n][2 i] in the low four bits of byte i, c[n][2 i + 1] in
+ *            the high ones, 16-byte aligned
+ *   w_scale  bf16 [N][K / group], 2-byte aligned;  group 32, 64 or 128, K a multiple of it
+ * gist_qkv_rope_w4: [q | k | v][t] = x[t] . w^T, q and k heads rotated at position[t] from
+ * the fp32 values and rounded once to bf16 (nearest even); N = (Hq + 2 Hkv) d rows, q
+ * heads, then k heads, then v heads, K = d_model.
+ *   x        bf16 [T][d_model], 16-byte aligned
+ *   position int32 [T] (gist_paged_plan's): a negative one leaves the token's rows of q,
+ *            k_new and v_new as they were
+ *   q        bf16 [T][Hq][d];  k_new, v_new bf16 [T][Hkv][d]  (written)
+ * Feed the results to the append and the attention with GIST_ATTN_FLAG_PREROTATED (the
+ * flag itself changes nothing here).
+ * gist_out_proj_w4: y[t] = attn_out[t] . w^T, N = d_model (a multiple of 16,
+ * GIST_ATTN_ERR_UNSUPPORTED otherwise), K = Hq d.
+ *   attn_out bf16 [T][Hq][d], y bf16 [T][d_model] (written)
+ * T is num_tokens; sums are fp32 in a fixed order.  More than 64 tokens run as several
+ * passes over the weights (use gist_qkv_rope and gist_out_proj for prompts).  Reads
+ * num_tokens, num_q_heads, num_kv_heads, head_dim and (QKV) rope_theta of dims.  d_model is at most
+ * 65536 and T at most 2^20 (GIST_ATTN_ERR_UNSUPPORTED); outputs must not overlap inputs.
+ */
+int gist_qkv_rope_w4(const void* x, const void* w, const void* w_scale, const int32_t* position,
+                     void* q, void* k_new, void* v_new, int d_model, int group,
+                     const gist_paged_dims* dims, cudaStream_t stream);
+int gist_out_proj_w4(const void* attn_out, const void* w, const void* w_scale, void* y,
+                     int d_model, int group, const gist_paged_dims* dims, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
