@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(LIB_DIR, "libgistattn.so")
 SOURCES = ["api.cu", "prefill.cu", "prefill_tc.cu", "prefill_long.cu", "decode.cu", "decode_long.cu",
            "decode_short.cu", "gather.cu", "append.cu", "gemm.cu", "stage.cu", "noalloc.cu",
            "decode_gqa.cu", "paged_api.cu", "paged_plan.cu", "paged_append.cu", "paged_decode.cu",
-           "paged_prefill.cu", "paged_bf16.cu", "paged_pages.cu", "proj_w4.cu"]
+           "paged_prefill.cu", "paged_bf16.cu", "paged_pages.cu", "proj_w4.cu",
+           "proj_w4_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

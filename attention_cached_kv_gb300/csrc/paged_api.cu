@@ -409,7 +409,7 @@ extern "C" int gist_qkv_rope_w4(const void* x, const void* w, const void* w_scal
   if (pb.T == 0) return GIST_ATTN_OK;
   if (!x || !w || !w_scale || !position || !q || !k_new || !v_new) return GIST_ATTN_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(w_scale, 2) || !aligned(position, 4) || !aligned(q, 16) ||
-      !aligned(k_new, 16) || !aligned(v_new, 16))
+      !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(pb.status, 4))
     return GIST_ATTN_ERR_ALIGN;
   int sms = 0;
   rc = gattn::device_sms(&sms);
@@ -426,7 +426,9 @@ extern "C" int gist_out_proj_w4(const void* attn_out, const void* w, const void*
   if (d_model % 16 != 0 || pb.Hq * pb.d % group != 0) return GIST_ATTN_ERR_UNSUPPORTED;
   if (pb.T == 0) return GIST_ATTN_OK;
   if (!attn_out || !w || !w_scale || !y) return GIST_ATTN_ERR_NULL;
-  if (!aligned(attn_out, 16) || !aligned(w, 16) || !aligned(w_scale, 2) || !aligned(y, 16)) return GIST_ATTN_ERR_ALIGN;
+  if (!aligned(attn_out, 16) || !aligned(w, 16) || !aligned(w_scale, 2) || !aligned(y, 16) ||
+      !aligned(pb.status, 4))
+    return GIST_ATTN_ERR_ALIGN;
   int sms = 0;
   rc = gattn::device_sms(&sms);
   if (rc != GIST_ATTN_OK) return rc;

@@ -21,9 +21,7 @@
 // Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
 #include <cooperative_groups.h>
 
-#include "common.cuh"
-#include "kernels.h"
-#include "paged.cuh"
+#include "proj_w4.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,33 +33,11 @@ constexpr int kStep = 128;   // inputs of a ring stage
 constexpr int kStages = 8;   // of a warp's ring, 1 KB a row tile each
 constexpr int kMaxX = 72 * 1024;  // staged x of a CTA, at most
 
-struct W4Params {
-  const bf16* x;
-  const uint8_t* w;
-  const bf16* scale;
-  bf16* out[3];           // q, k_new, v_new; or y
-  const int32_t* position;  // nullptr: output projection
-  int T, N, K, group, tiles, slice;  // slice: inputs of a CTA
-  int Hq, Hkv, d;
-  uint64_t turn[64];
-};
-
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-// Two codes (bits 0..3 and 16..19) less 8, as bf16: 128 + c is exact, and so is the difference.
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t c) {
-  const uint32_t v = (c & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // First row of a tile, and its other eight rows' distance.
 __device__ __forceinline__ int tile_row(const W4Params& p, int tile, int& apart) {
   if (!p.position) {
@@ -92,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   const uint32_t ring = xs + staged * pitch + warp * (kStages * MR * 1024);
 
   // ---- weights: rows of 64 bytes, 16 a row tile; chunk c of row r at c ^ (r / 2 mod 4)
-  int row[MR], apart;
+  int row[MR], apart = 8;
 #pragma unroll
   for (int m = 0; m < MR; ++m) row[m] = tile0 + m < p.tiles ? tile_row(p, tile0 + m, apart) : -1;
   const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
@@ -130,11 +106,17 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   for (int m = 0; m < MR; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  const int groups = p.K / p.group, per32 = p.group / 32;
+  const int shift = 31 - __clz(p.group), per32 = p.group / 32;
+  const uint16_t* scale[MR][2];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      scale[m][h] = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)(max(row[m], 0) + h * apart + g8) * (p.K >> shift);
 
   for (int i = 0; i < mine; ++i) {
     const int k = k0 + (wk + i * WK) * kStep;
-    float sc[MR][4][2];
+    uint16_t sc[MR][4][2];
 #pragma unroll
     for (int m = 0; m < MR; ++m)
 #pragma unroll
@@ -142,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int kk = k + 32 * q;
-          sc[m][q][h] = row[m] >= 0 && kk < k1 ? __bfloat162float(p.scale[(int64_t)(row[m] + h * apart + g8) * groups + kk / p.group]) : 0.f;
+          if (q % per32 == per32 - 1) sc[m][q][h] = row[m] >= 0 && kk < k1 ? __ldg(scale[m][h] + (kk >> shift)) : 0;
         }
     cp_async_wait_group<kStages - 2>();
     __syncwarp();
@@ -184,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(sum[m][n][e], sc[m][q][e >> 1], acc[m][n][e]);
+            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(sum[m][n][e], __uint_as_float((uint32_t)sc[m][q][e >> 1] << 16), acc[m][n][e]);
       }
     }
     __syncwarp();
@@ -222,29 +204,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
     }
     int far;
     const int n = tile_row(p, tile, far) + (j & 7);
-    if (!p.position) {
-      bf16* y = p.out[0] + (int64_t)(t0 + t) * p.N + n;
-      y[0] = __float2bfloat16(a);
-      y[8] = __float2bfloat16(b);
-      continue;
-    }
-    const int pos = p.position[t0 + t];
-    if (pos < 0) continue;
-    int head = n / p.d;
-    const int e = n - head * p.d;
-    if (head < p.Hq + p.Hkv) {
-      float sn, cs;
-      sincosf(turn_angle(pos, p.turn[e]), &sn, &cs);
-      const float x = a;
-      a = x * cs - b * sn;
-      b = b * cs + x * sn;
-    }
-    int which = 0, heads = p.Hq;
-    if (head >= p.Hq) which = 1, head -= p.Hq, heads = p.Hkv;
-    if (which == 1 && head >= p.Hkv) which = 2, head -= p.Hkv;
-    bf16* y = p.out[which] + ((int64_t)(t0 + t) * heads + head) * p.d + e;
-    y[0] = __float2bfloat16(a);
-    y[far] = __float2bfloat16(b);
+    finish_pair(p, t0 + t, n, far, a, b);
   }
   if (split > 1) cluster.sync();  // no CTA leaves while another reads its sums
 }
@@ -283,11 +243,9 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
 }
 
 int launch(const W4Params& p, int sms, cudaStream_t stream) {
-  // the tokens in one pass where their part of x fits beside the rings, in more of fewer where not
-  int rc = GIST_ATTN_ERR_UNSUPPORTED;
-  if (p.T > 32) rc = launch_as<8, 1, 4>(p, sms, stream);
-  if (rc == GIST_ATTN_ERR_UNSUPPORTED && p.T > 16) rc = launch_as<4, 1, 4>(p, sms, stream);
-  if (rc == GIST_ATTN_ERR_UNSUPPORTED && p.T > 8) rc = launch_as<2, 1, 1>(p, sms, stream);
+  if (p.T > 16) return launch_w4_tc(p, sms, stream);
+  // the tokens in one pass where their part of x fits beside the rings, in two where not
+  const int rc = p.T > 8 ? launch_as<2, 1, 1>(p, sms, stream) : GIST_ATTN_ERR_UNSUPPORTED;
   return rc == GIST_ATTN_ERR_UNSUPPORTED ? launch_as<1, 1, 1>(p, sms, stream) : rc;
 }
 
@@ -303,8 +261,10 @@ int launch_qkv_rope_w4(const PagedProblem& pb, const void* x, const void* w, con
   p.out[1] = static_cast<bf16*>(k_new);
   p.out[2] = static_cast<bf16*>(v_new);
   p.position = position;
+  p.status = pb.status;
   p.T = pb.T;
   p.d = pb.d;
+  p.shift = pb.d == 64 ? 6 : 7;
   p.Hq = pb.Hq;
   p.Hkv = pb.Hkv;
   p.N = (pb.Hq + 2 * pb.Hkv) * pb.d;
@@ -322,6 +282,7 @@ int launch_out_proj_w4(const PagedProblem& pb, const void* attn, const void* w, 
   p.w = static_cast<const uint8_t*>(w);
   p.scale = static_cast<const bf16*>(scale);
   p.out[0] = static_cast<bf16*>(y);
+  p.status = pb.status;
   p.T = pb.T;
   p.N = d_model;
   p.K = pb.Hq * pb.d;

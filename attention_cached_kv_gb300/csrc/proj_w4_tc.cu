@@ -1,0 +1,362 @@
+// proj_w4_tc.cu -- the 4-bit projections of 17 tokens and more on the 5th-generation
+// tensor core: 128 rows of weights are M, up to 64 tokens are N, so that the weights are
+// still read once.
+//
+//   D[n][t] = sum_{k in group} (c[n][k] - 8) x[t][k]     (tcgen05 kind::f16, A in TMEM)
+//   acc[n][t] += s[n][group] D[n][t]                     (fp32 registers)
+//
+// The codes less 8 are exact in bf16; the group's scale cannot go into them (the product
+// has up to twelve bits), so each group's sums are read out of TMEM and scaled.  The
+// converted weights go through TMEM and not through shared memory: writing and reading
+// them there would cost 32 bytes for each 4 of codes, more than its bandwidth.
+//
+// A CTA has a tile of 128 rows and a part of K; the CTAs of a cluster have the parts
+// of one tile, send each other the rows that the other adds up (bulk copies between
+// their shared memories) and write those.  Warps: 0-3 convert (a thread a row: codes by
+// cp.async into a ring of the warp's own, then into TMEM), the next four for each 32
+// tokens scale and add (a thread a row), one issues MMAs, one loads x by TMA.
+//
+// Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
+#include <cooperative_groups.h>
+
+#include "proj_w4.cuh"
+#include "tcgen05.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gattn {
+namespace {
+
+constexpr int kRows = 128, kPairs = 64, kThreads = 320, kMma = 8;  // kMma: the warp that issues MMAs
+constexpr int kChunk = 128;          // inputs of a stage of codes: 64 bytes a row
+constexpr int kRaw = 5;              // stages of a warp's ring of codes, 2 KB each
+constexpr int kSA = 2, kSB = 3;      // stages of converted weights in TMEM, of x in shared memory
+constexpr int kCols = 256;           // TMEM columns: kSA x 64, then two accumulators
+
+struct Bars {
+  uint64_t a_full[kSA], a_empty[kSA], b_full[kSB], b_empty[kSB], d_full[2], d_empty[2], sums;
+  uint32_t tmem;
+};
+
+template <int TN>
+struct Layout {
+  static constexpr uint32_t tile_b = 2 * TN * 128;  // two tiles of 64 inputs
+  static constexpr uint32_t raw = kSB * tile_b;
+  static constexpr uint32_t bars = raw + 4 * kRaw * 2048;
+  static constexpr uint32_t bytes = bars + 256 + 1024;  // + alignment
+  // over the rings: this CTA's sums [pair][2][TN], then the parts of the pairs that it adds up
+  static constexpr uint32_t sums = kRows * TN * 4;
+  static_assert(2 * sums <= bars, "sums");
+};
+
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // and waits
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// One lane of a warp that has converged.  Under elect.sync the compiler keeps the operands of
+// tcgen05.mma in uniform registers; behind `lane == 0` it moves them there for each MMA, which
+// takes 47 cycles an MMA in place of the 16 (32 tokens) or 32 (64) that the tensor core needs.
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+// TN tokens, groups of 16 PG inputs (PG MMAs).
+template <int TN, int PG>
+__global__ void __launch_bounds__(kThreads, 2)
+    w4_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ W4Params p) {
+  using L = Layout<TN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  Bars& bars = *reinterpret_cast<Bars*>(smem + L::bars);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int split = cluster.num_blocks(), part = cluster.block_rank();
+  const int n0 = (blockIdx.x / split) * kRows, t0 = blockIdx.y * TN;
+  const int k0 = part * p.slice, k1 = max(min(k0 + p.slice, p.K), k0);
+  const int chunks = (k1 - k0 + kChunk - 1) / kChunk;
+
+  // ---- warps 0-3: the first codes are asked for before anything else
+  const uint32_t ring = base + L::raw + (warp & 3) * (kRaw * 2048);
+  const int c4 = lane & 3, most = k1 - k0 - c4 * 32;  // this lane's 32 inputs of chunk i exist where i kChunk < most
+  const uint8_t* src[4];
+  uint32_t to[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = j * 8 + (lane >> 2);
+    src[j] = p.w + (int64_t)min(n0 + (warp & 3) * 32 + r, p.N - 1) * (p.K / 2) + (k0 + c4 * 32) / 2;  // rows past N are not written
+    to[j] = ring + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4);
+  }
+  int slot = 0;
+  auto issue = [&](int i) {
+    if (i < chunks) {
+      const bool in = i * kChunk < most;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cp_async16_or_zero(to[j] + slot * 2048, in ? src[j] : p.w, in);
+        src[j] += kChunk / 2;
+      }
+    }
+    slot = slot == kRaw - 1 ? 0 : slot + 1;
+    cp_async_commit();
+  };
+  if (warp < 4)
+    for (int i = 0; i < kRaw - 1; ++i) issue(i);
+  if (warp == kMma) {
+    tc::tmem_alloc(smem_u32(&bars.tmem), kCols);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kSA; ++s) mbar_init(&bars.a_full[s], 4), mbar_init(&bars.a_empty[s], 1);
+    for (int s = 0; s < kSB; ++s) mbar_init(&bars.b_full[s], 1), mbar_init(&bars.b_empty[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&bars.d_full[s], 1), mbar_init(&bars.d_empty[s], 4);
+    mbar_init(&bars.sums, 1);
+    fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bars.tmem, lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const int groups = (k1 - k0) / (16 * PG);
+  bool failed = false;
+  auto wait = [&](uint64_t* bar, int use) {  // the use-th completion of a barrier (0: the first)
+    if (__any_sync(0xffffffffu, !mbar_wait(bar, (uint32_t)use & 1u))) failed = true;
+    return !failed;
+  };
+  float acc[TN];
+
+  if (warp < 4) {
+    // ---------------------------------------------------------- codes to bf16
+    int at = 0;
+    for (int i = 0; i < chunks && !failed; ++i) {
+      cp_async_wait_group<kRaw - 2>();
+      __syncwarp();
+      const uint32_t from = ring + at * 2048 + lane * 64;
+      at = at == kRaw - 1 ? 0 : at + 1;
+      const int s = i % kSA;
+      if (i >= kSA && !wait(&bars.a_empty[s], i / kSA - 1)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t u[8], a[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 v = lds16(from + (((2 * h + c) ^ ((lane >> 1) & 3)) << 4));
+          u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) word_to_bf16(u[j], a + 4 * j);
+        st32(tmem + lanes + s * 64 + h * 32, a);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.a_full[s]);
+      issue(i + kRaw - 1);
+    }
+    cp_async_wait_all();
+  } else if (warp < kMma) {
+    // ------------------------------------------------- the groups' sums, scaled and added
+#pragma unroll
+    for (int e = 0; e < TN; ++e) acc[e] = 0.f;
+    const int n = n0 + (warp & 3) * 32 + lane;
+    const uint16_t* scale = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)min(n, p.N - 1) * (p.K / p.group) + k0 / p.group;
+    constexpr int kAhead = 4;  // scales are read so many groups ahead (and converted when used)
+    uint16_t next[kAhead];
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) next[g] = g < groups ? __ldg(scale + g) : 0;
+    for (int g0 = 0; g0 < groups && !failed; g0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int g = g0 + j;
+        if (g >= groups) break;
+        const float now = __uint_as_float((uint32_t)next[j] << 16);
+        next[j] = g + kAhead < groups ? __ldg(scale + g + kAhead) : 0;
+        if (!wait(&bars.d_full[g & 1], g >> 1)) break;
+        tc::fence_after_sync();
+        const uint32_t d = tmem + lanes + kSA * 64 + (g & 1) * TN;
+#pragma unroll
+        for (int h = 0; h < TN / 16; ++h) {
+          uint32_t v[16];
+          ld16(d + 16 * h, v);
+          if (h == TN / 16 - 1) {
+            tc::fence_before_sync();  // the accumulator is read: the next group but one may have it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.d_empty[g & 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[16 * h + e] = fmaf(__uint_as_float(v[e]), now, acc[16 * h + e]);
+        }
+      }
+    }
+  } else if (warp == kMma) {
+    // ------------------------------------------ MMAs, by one thread and with few instructions
+    if (elected()) {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, TN, 0);
+      const uint64_t x0 = tc::smem_desc_sw128(base, 16, 1024);  // addresses in units of 16 bytes
+      constexpr int kGroups = 8 / PG;  // of a chunk
+      int g = 0;
+      for (int i = 0; i < chunks && !failed; ++i) {
+        const int s = i % kSA, sb = i % kSB;
+        failed = !mbar_wait(&bars.a_full[s], i / kSA & 1) || !mbar_wait(&bars.b_full[sb], i / kSB & 1);
+        const uint64_t bd = x0 + sb * (L::tile_b / 16);
+        const uint32_t a = tmem + s * 64;
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+          if (failed || g >= groups) break;  // past K's end there is nothing left to add
+          if (g >= 2 && !mbar_wait(&bars.d_empty[g & 1], ((g >> 1) - 1) & 1)) failed = true;
+          tc::fence_after_sync();
+          const uint32_t d = tmem + kSA * 64 + (g & 1) * TN;
+#pragma unroll
+          for (int k = 0; k < PG; ++k) {
+            const int ks = j * PG + k;  // 16 inputs: 8 columns of A, 32 bytes of a row of x's tile
+            tc::mma_ts(d, a + ks * 8, bd + (ks >> 2) * (TN * 128 / 16) + (ks & 3) * 2, idesc, k == 0 ? 0u : 1u);
+          }
+          tc::commit(smem_u32(&bars.d_full[g & 1]));
+          ++g;
+        }
+        tc::commit(smem_u32(&bars.a_empty[s]));
+        tc::commit(smem_u32(&bars.b_empty[sb]));
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------- x
+    if (elected()) {
+      tma_prefetch_map(&tm_x);
+      for (int i = 0; i < chunks && !failed; ++i) {
+        const int s = i % kSB;
+        if (i >= kSB && !mbar_wait(&bars.b_empty[s], (i / kSB - 1) & 1)) {
+          failed = true;
+          break;
+        }
+        mbar_arrive_expect_tx(&bars.b_full[s], L::tile_b);
+        // inputs past K and tokens past T are zeros (and counted)
+        tma_load_2d(base + s * L::tile_b, &tm_x, &bars.b_full[s], k0 + i * kChunk, t0);
+        tma_load_2d(base + s * L::tile_b + TN * 128, &tm_x, &bars.b_full[s], k0 + i * kChunk + 64, t0);
+      }
+      // none of the copies is left in flight
+      for (int i = max(chunks - kSB, 0); i < chunks && !failed; ++i) failed = !mbar_wait(&bars.b_full[i % kSB], i / kSB & 1);
+    }
+    __syncwarp();
+  }
+  if (__any_sync(0xffffffffu, failed) && lane == 0) report(p.status, GIST_ATTN_STATUS_TIMEOUT);
+
+  // ---- the cluster's CTAs added up.  Pairs of rows that are rotated together lie next to
+  // each other; 16-byte chunk c of a row of sums at c ^ (pair mod 8)
+  tc::fence_before_sync();
+  __syncthreads();  // the rings are done with
+  if (warp == kMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kCols);
+  }
+  const int half = p.position ? p.shift - 1 : 6;  // rows of a pair are 1 << half apart
+  const int own = kPairs / split, q0 = part * own;  // the pairs that this CTA adds up
+  if (warp >= 4 && warp < kMma) {
+    const int r = (warp & 3) * 32 + lane, pair = r >> (half + 1) << half | (r & ((1 << half) - 1)), which = r >> half & 1;
+    const uint32_t row = base + (2 * pair + which) * (TN * 4);
+#pragma unroll
+    for (int c = 0; c < TN / 4; ++c)
+      sts16(row + ((c ^ (pair & 7)) << 4), make_uint4(__float_as_uint(acc[4 * c]), __float_as_uint(acc[4 * c + 1]),
+                                                      __float_as_uint(acc[4 * c + 2]), __float_as_uint(acc[4 * c + 3])));
+    fence_proxy_async_smem();
+  }
+  const int bytes = own * 2 * TN * 4;
+  if (tid == 0) mbar_arrive_expect_tx(&bars.sums, split * bytes);
+  cluster.sync();
+  if (tid < split) {
+    uint32_t dst, bar;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(base + L::sums + part * bytes), "r"(tid));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&bars.sums)), "r"(tid));
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(base + tid * bytes), "r"(bytes), "r"(bar)
+                 : "memory");
+  }
+  if (!mbar_wait(&bars.sums, 0)) {
+    if (lane == 0) report(p.status, GIST_ATTN_STATUS_TIMEOUT);
+  } else {
+    const int tokens = min(TN, p.T - t0);
+    for (int i = tid; i < own * (TN / 4); i += kThreads) {
+      const int q = i & (own - 1), c = i / own, pair = q0 + q;  // a pair of rows, four tokens
+      const int n = n0 + (pair >> half << (half + 1) | (pair & ((1 << half) - 1)));
+      if (c * 4 >= tokens || n >= p.N) continue;
+      const uint32_t from = base + L::sums + q * 2 * (TN * 4) + ((c ^ (pair & 7)) << 4);
+      float a[4] = {}, b[4] = {};
+      for (int s = 0; s < split; ++s) {
+        const uint4 x = lds16(from + s * bytes), y = lds16(from + s * bytes + TN * 4);
+        a[0] += __uint_as_float(x.x), a[1] += __uint_as_float(x.y), a[2] += __uint_as_float(x.z), a[3] += __uint_as_float(x.w);
+        b[0] += __uint_as_float(y.x), b[1] += __uint_as_float(y.y), b[2] += __uint_as_float(y.z), b[3] += __uint_as_float(y.w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c * 4 + e < tokens) finish_pair(p, t0 + c * 4 + e, n, 1 << half, a[e], b[e]);
+    }
+  }
+  cluster.sync();  // no CTA leaves while its sums are being sent
+}
+
+template <int TN, int PG>
+int launch_as(W4Params p, int sms, cudaStream_t stream) {
+  const EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return GIST_ATTN_ERR_LAUNCH;
+  alignas(64) CUtensorMap tm;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.K, (cuuint64_t)p.T}, strides[1] = {(cuuint64_t)p.K * 2};
+  const cuuint32_t box[2] = {64, TN}, estr[2] = {1, 1};
+  if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(p.x), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return GIST_ATTN_ERR_UNSUPPORTED;
+  const int tiles = (p.N + kRows - 1) / kRows, token_blocks = (p.T + TN - 1) / TN, chunks = (p.K + kChunk - 1) / kChunk;
+  // two CTAs an SM, where K has a few chunks for each
+  int split = 1;
+  while (split < 8 && (int64_t)tiles * token_blocks * split * 2 <= 2 * sms && split * 4 <= chunks) split *= 2;
+  p.slice = (chunks + split - 1) / split * kChunk;
+  constexpr int smem = Layout<TN>::bytes;
+  if (token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(w4_tc_kernel<TN, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return GIST_ATTN_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * split, token_blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, w4_tc_kernel<TN, PG>, tm, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_w4_tc(const W4Params& p, int sms, cudaStream_t stream) {
+  if (p.T <= 32)
+    return p.group == 32   ? launch_as<32, 2>(p, sms, stream)
+           : p.group == 64 ? launch_as<32, 4>(p, sms, stream)
+                           : launch_as<32, 8>(p, sms, stream);
+  return p.group == 32   ? launch_as<64, 2>(p, sms, stream)
+         : p.group == 64 ? launch_as<64, 4>(p, sms, stream)
+                         : launch_as<64, 8>(p, sms, stream);
+}
+
+}  // namespace gattn
