@@ -158,7 +158,7 @@ struct CopyArgs {
   int n, num_blocks, block_len;
   int planes, plane;  // of a block, and 16-byte pieces of a plane
 };
-int launch_pages_tables(const PagesArgs& a, bool compact, cudaStream_t stream);
+int launch_pages_tables(const PagesArgs& a, bool compact, int sms, cudaStream_t stream);
 int launch_pages_fork(const ForkArgs& a, cudaStream_t stream);
 int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream);
 

@@ -288,7 +288,9 @@ extern "C" int gist_pages_free(const int32_t* cached_len, const int32_t* block_t
   a.W = dims->max_blocks;
   a.block_len = dims->block_len;
   a.num_blocks = dims->num_blocks;
-  return gattn::launch_pages_tables(a, false, stream);
+  int sms = 0;
+  const int found = gattn::device_sms(&sms);
+  return found != GIST_ATTN_OK ? found : gattn::launch_pages_tables(a, false, sms, stream);
 }
 
 extern "C" int gist_pages_compact(const int32_t* cached_len, const int32_t* block_table,
@@ -308,7 +310,9 @@ extern "C" int gist_pages_compact(const int32_t* cached_len, const int32_t* bloc
   const gattn::PagesArgs a = {cached_len,  block_table, block_table_out,    new_id,           copy_src,
                               copy_dst,    num_copies,  free_blocks,        free_range,       dims->status,
                               dims->num_requests, dims->max_blocks, dims->block_len, dims->num_blocks};
-  return gattn::launch_pages_tables(a, true, stream);
+  int sms = 0;
+  const int found = gattn::device_sms(&sms);
+  return found != GIST_ATTN_OK ? found : gattn::launch_pages_tables(a, true, sms, stream);
 }
 
 extern "C" int gist_pages_fork(const int32_t* cached_len, const int32_t* parent, int32_t* block_table,

@@ -32,6 +32,14 @@ namespace {
 // is enough and no counter has to be zeroed before.
 constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kSeg = 128;  // entries of one row that a warp takes at a time
+constexpr int kAlone = 512, kAloneIds = 16384;  // segments and ids that one cluster does alone
+constexpr int kFew = 64, kFewIds = 4096;         // that one CTA does, whose barriers cost next to nothing
+
+// A kernel that follows another on its stream: may start early, waits here for its results.
+__device__ __forceinline__ void follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // Blocks of a request: the live entries of its row.
 __device__ __forceinline__ int blocks_of(int len, int block_len, int W, bool& bad) {
@@ -41,8 +49,10 @@ __device__ __forceinline__ int blocks_of(int len, int block_len, int W, bool& ba
   return min((int)n, W);
 }
 
-// Calls visit(r, j0, n) by whole warps for every segment [j0, j0 + kSeg) of every row of
-// the table, n the row's live entries.
+// Calls visit(r, j0, n) by whole warps for the segments [j0, j0 + kSeg) of every row of the
+// table, n the row's live entries; kAtOnce segments a call (n < 0: none), so that their loads
+// are in flight together.
+constexpr int kAtOnce = 4;
 template <class Visit>
 __device__ __forceinline__ void each_segment(const PagesArgs& a, int warp, int warps, bool& bad, Visit visit) {
   const int lane = threadIdx.x & 31;
@@ -51,64 +61,149 @@ __device__ __forceinline__ void each_segment(const PagesArgs& a, int warp, int w
   const int64_t u0 = units * warp / warps, u1 = units * (warp + 1) / warps;
   for (int64_t base = u0; base < u1; base += 32) {
     const int64_t mine = base + lane;  // each lane reads the length of one of 32 units
-    int row = 0, seg = 0, n = 0;
+    int row = 0, seg = 0, n = -1;
     if (mine < u1) {
       row = (int)(mine / per_row);
       seg = (int)(mine - (int64_t)row * per_row);
       n = blocks_of(a.cached_len[row], a.block_len, a.W, bad);
     }
     const int m = (int)min((int64_t)32, u1 - base);
-    for (int i = 0; i < m; ++i)
-      visit(__shfl_sync(0xffffffffu, row, i), __shfl_sync(0xffffffffu, seg, i) * kSeg, __shfl_sync(0xffffffffu, n, i));
+    for (int i = 0; i < m; i += kAtOnce) {
+      int r[kAtOnce], j0[kAtOnce], live[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {  // lanes past m have n = -1
+        r[k] = __shfl_sync(0xffffffffu, row, i + k);
+        j0[k] = __shfl_sync(0xffffffffu, seg, i + k) * kSeg;
+        live[k] = __shfl_sync(0xffffffffu, n, i + k);
+      }
+      visit(r, j0, live);
+    }
   }
 }
 
-template <bool COMPACT>
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ PagesArgs a) {
-  cg::cluster_group cluster = cg::this_cluster();
-  __shared__ int count[kWarps];                // ids in use in each warp's slice
-  __shared__ int below[kWarps];                // COMPACT: those of them below n
-  __shared__ int all[kCtas * kWarps], all_below;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = blockIdx.x, gw = cta * kWarps + warp;
-  bool bad = false;
+// A warp's slice [b0, b1) of the ids, 32 at a time: which of them are in use.  The masks of
+// up to 1024 ids stay with the lanes after the first pass, longer slices are read again.
+struct Slice {
+  const int32_t* ids;
+  int b0, b1;
+  uint32_t kept;  // lane i: the i-th mask
 
-  for (int b = cta * kThreads + tid; b < a.num_blocks; b += kCtas * kThreads) a.ids[b] = 0;
-  cluster.sync();
-
-  each_segment(a, gw, kCtas * kWarps, bad, [&](int r, int j0, int n) {
-    const int32_t* row = a.block_table + (int64_t)r * a.W;
-    int id[kSeg / 32];
+  // Calls visit(first id, mask) in order.
+  template <bool READ, class Visit>
+  __device__ __forceinline__ void each(Visit visit) {
+    const int lane = threadIdx.x & 31;
+    const bool read = READ || b1 - b0 > 1024;
+    for (int b = b0; b < b1; b += 8 * 32) {
+      uint32_t m[8];
+      if (read) {
+        int v[8];
 #pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) {
-      const int j = j0 + 32 * k + lane;
-      id[k] = j < n ? row[j] : -1;
-      if (j < n && (id[k] < 0 || id[k] >= a.num_blocks)) {
-        bad = true;
-        id[k] = -1;
+        for (int k = 0; k < 8; ++k) v[k] = b + 32 * k + lane < b1 ? __ldcg(ids + b + 32 * k + lane) : 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = __ballot_sync(0xffffffffu, v[k] != 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = __shfl_sync(0xffffffffu, kept, (b - b0) / 32 + k);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (READ && lane == (((b - b0) / 32 + k) & 31)) kept = m[k];
+        if (b + 32 * k < b1) visit(b + 32 * k, m[k]);
       }
     }
+  }
+};
+
+// Counts (or marks) the ids that live entries name.
+template <bool COMPACT>
+__device__ __forceinline__ void mark(const PagesArgs& a, int gw, int warps) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+  each_segment(a, gw, warps, bad, [&](const int (&r)[kAtOnce], const int (&j0)[kAtOnce], const int (&n)[kAtOnce]) {
+    int id[kAtOnce][kSeg / 32];
 #pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) {
-      if (id[k] < 0) continue;
-      if constexpr (COMPACT) a.ids[id[k]] = 1;
-      else atomicAdd(&a.ids[id[k]], 1);
-    }
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int k = 0; k < kSeg / 32; ++k) {
+        const int j = j0[u] + 32 * k + lane;
+        id[u][k] = j < n[u] ? a.block_table[(int64_t)r[u] * a.W + j] : -1;
+        bad |= j < n[u] && (id[u][k] < 0 || id[u][k] >= a.num_blocks);
+      }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int k = 0; k < kSeg / 32; ++k) {
+        if (id[u][k] < 0 || id[u][k] >= a.num_blocks) continue;
+        if constexpr (COMPACT) a.ids[id[u][k]] = 1;
+        else atomicAdd(&a.ids[id[u][k]], 1);
+      }
   });
   if (bad) report(a.status, GIST_ATTN_STATUS_BAD_BLOCK);
-  cluster.sync();
+}
+
+// The table with the new ids.
+__device__ __forceinline__ void rename(const PagesArgs& a, int gw, int warps) {
+  const int lane = threadIdx.x & 31;
+  bool bad = false;  // reported by mark
+  each_segment(a, gw, warps, bad, [&](const int (&r)[kAtOnce], const int (&j0)[kAtOnce], const int (&live)[kAtOnce]) {
+    int id[kAtOnce][kSeg / 32];
+    auto inside = [&](int u, int k) { return live[u] >= 0 && j0[u] + 32 * k + lane < a.W; };
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int k = 0; k < kSeg / 32; ++k) id[u][k] = inside(u, k) ? a.block_table[(int64_t)r[u] * a.W + j0[u] + 32 * k + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int k = 0; k < kSeg / 32; ++k)
+        if (j0[u] + 32 * k + lane < live[u] && id[u][k] >= 0 && id[u][k] < a.num_blocks) id[u][k] = __ldcg(a.ids + id[u][k]);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int k = 0; k < kSeg / 32; ++k)
+        if (inside(u, k)) a.table_out[(int64_t)r[u] * a.W + j0[u] + 32 * k + lane] = id[u][k];
+  });
+}
+
+// ALONE: the whole of the work; otherwise the passes over the table, which are wide, have
+// kernels of their own and this one has the passes over the ids, which depend on each other.
+template <bool COMPACT, bool ALONE, int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ PagesArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  auto sync = [&]() {
+    if (CTAS > 1) cluster.sync();
+    else __syncthreads();
+  };
+  __shared__ int count[kWarps];                // ids in use in each warp's slice
+  __shared__ int below[kWarps];                // COMPACT: those of them below n
+  __shared__ int all[CTAS * kWarps], all_below;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x, gw = cta * kWarps + warp;
+
+  if constexpr (ALONE) {
+    for (int b = cta * kThreads + tid; b < a.num_blocks; b += CTAS * kThreads) a.ids[b] = 0;
+    sync();
+    mark<COMPACT>(a, gw, CTAS * kWarps);
+    sync();
+  } else {
+    follow();
+  }
 
   // each warp's slice of the ids: how many are in use
-  const int per = ((a.num_blocks + kCtas * kWarps - 1) / (kCtas * kWarps) + 31) & ~31;
-  const int b0 = (int)min((int64_t)gw * per, (int64_t)a.num_blocks), b1 = min(b0 + per, a.num_blocks);
+  const int per = ((a.num_blocks + CTAS * kWarps - 1) / (CTAS * kWarps) + 31) & ~31;
+  Slice s;
+  s.ids = a.ids;
+  s.b0 = (int)min((int64_t)gw * per, (int64_t)a.num_blocks);
+  s.b1 = min(s.b0 + per, a.num_blocks);
+  s.kept = 0;
   int used = 0;
-  for (int b = b0; b < b1; b += 32) used += __popc(__ballot_sync(0xffffffffu, b + lane < b1 && __ldcg(a.ids + b + lane) != 0));
+  s.each<true>([&](int, uint32_t m) { used += __popc(m); });
   if (lane == 0) count[warp] = used;
-  cluster.sync();
-  if (tid < kCtas * kWarps) all[tid] = *cluster.map_shared_rank(&count[tid % kWarps], tid / kWarps);
+  sync();
+  if (tid < CTAS * kWarps) all[tid] = *cluster.map_shared_rank(&count[tid % kWarps], tid / kWarps);
   __syncthreads();
   int before = 0, n = 0;  // ids in use ahead of the slice, and in all
-  for (int w = lane; w < kCtas * kWarps; w += 32) {
+  for (int w = lane; w < CTAS * kWarps; w += 32) {
     n += all[w];
     before += w < gw ? all[w] : 0;
   }
@@ -117,68 +212,69 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) tables
   const uint32_t ahead = (1u << lane) - 1;
 
   if constexpr (!COMPACT) {
+    if (CTAS > 1) cluster.barrier_arrive();  // this CTA has read the others' counts
     const int free = a.num_blocks - n;
-    for (int b = b0; b < b1; b += 32) {
-      const bool in = b + lane < b1, use = in && __ldcg(a.ids + b + lane) != 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, use);
+    s.each<false>([&](int b, uint32_t m) {
+      const int id = b + lane;
       // the unused ids ahead of an id: the id itself less those in use ahead of it
-      if (in && !use) a.free_blocks[b + lane - before - __popc(m & ahead)] = b + lane;
+      if (id < s.b1 && !(m >> lane & 1)) a.free_blocks[id - before - __popc(m & ahead)] = id;
       before += __popc(m);
-    }
-    for (int i = free + cta * kThreads + tid; i < a.num_blocks; i += kCtas * kThreads) a.free_blocks[i] = -1;
+    });
+    for (int i = free + cta * kThreads + tid; i < a.num_blocks; i += CTAS * kThreads) a.free_blocks[i] = -1;
     if (cta == 0 && tid == 0) {
       a.free_range[0] = 0;
       a.free_range[1] = free;
     }
-    cluster.sync();  // no CTA leaves while another reads its counts
+    if (CTAS > 1) cluster.barrier_wait();  // and they have read this one's
     return;
   }
 
   // ids in use below n, which say how many blocks move
   int low = 0;
-  for (int b = b0; b < min(b1, n); b += 32) low += __popc(__ballot_sync(0xffffffffu, b + lane < min(b1, n) && __ldcg(a.ids + b + lane) != 0));
+  s.each<false>([&](int b, uint32_t m) { low += b + 32 <= n ? __popc(m) : b < n ? __popc(m & ((1u << (n - b)) - 1)) : 0; });
   if (lane == 0) below[warp] = low;
-  cluster.sync();
+  sync();
   if (tid == 0) all_below = 0;
   __syncthreads();
-  if (tid < kCtas * kWarps) atomicAdd(&all_below, *cluster.map_shared_rank(&below[tid % kWarps], tid / kWarps));
+  if (tid < CTAS * kWarps) atomicAdd(&all_below, *cluster.map_shared_rank(&below[tid % kWarps], tid / kWarps));
   __syncthreads();
   const int stay = all_below, moves = n - stay;
-  for (int b = b0; b < b1; b += 32) {
+  s.each<false>([&](int b, uint32_t m) {
     const int id = b + lane;
-    const bool in = id < b1, use = in && __ldcg(a.ids + id) != 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, use);
+    const bool use = m >> lane & 1;
     const int rank = before + __popc(m & ahead);  // ids in use ahead of this one
     if (use && id >= n) a.src[rank - stay] = id;
-    if (in && !use && id < n) a.dst[id - rank] = id;
-    if (in) a.ids[id] = use && id < n ? id : -1;
+    if (id < s.b1 && !use && id < n) a.dst[id - rank] = id;
+    if (id < s.b1) a.ids[id] = use && id < n ? id : -1;
     before += __popc(m);
-  }
-  for (int i = moves + cta * kThreads + tid; i < a.num_blocks / 2; i += kCtas * kThreads) a.src[i] = a.dst[i] = -1;
-  for (int i = cta * kThreads + tid; i < a.num_blocks; i += kCtas * kThreads) a.free_blocks[i] = i < a.num_blocks - n ? n + i : -1;
+  });
+  for (int i = moves + cta * kThreads + tid; i < a.num_blocks / 2; i += CTAS * kThreads) a.src[i] = a.dst[i] = -1;
+  for (int i = cta * kThreads + tid; i < a.num_blocks; i += CTAS * kThreads) a.free_blocks[i] = i < a.num_blocks - n ? n + i : -1;
   if (cta == 0 && tid == 0) {
     a.count[0] = moves;
     a.free_range[0] = 0;
     a.free_range[1] = a.num_blocks - n;
   }
-  cluster.sync();
-  for (int k = cta * kThreads + tid; k < moves; k += kCtas * kThreads) a.ids[__ldcg(a.src + k)] = __ldcg(a.dst + k);
-  cluster.sync();
-  each_segment(a, gw, kCtas * kWarps, bad, [&](int r, int j0, int live) {
-    const int64_t at = (int64_t)r * a.W;
-    int id[kSeg / 32];
-#pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) {
-      const int j = j0 + 32 * k + lane;
-      id[k] = j < a.W ? a.block_table[at + j] : -1;
-    }
-#pragma unroll
-    for (int k = 0; k < kSeg / 32; ++k) {
-      const int j = j0 + 32 * k + lane;
-      if (j < live && id[k] >= 0 && id[k] < a.num_blocks) id[k] = __ldcg(a.ids + id[k]);
-      if (j < a.W) a.table_out[at + j] = id[k];
-    }
-  });
+  sync();
+  for (int k = cta * kThreads + tid; k < moves; k += CTAS * kThreads) a.ids[__ldcg(a.src + k)] = __ldcg(a.dst + k);
+  if constexpr (ALONE) {
+    sync();
+    rename(a, gw, CTAS * kWarps);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) zero_kernel(const __grid_constant__ PagesArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.num_blocks; b += gridDim.x * kThreads) a.ids[b] = 0;
+}
+template <bool COMPACT>
+__global__ void __launch_bounds__(kThreads) mark_kernel(const __grid_constant__ PagesArgs a) {
+  follow();
+  mark<COMPACT>(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
+}
+__global__ void __launch_bounds__(kThreads) rename_kernel(const __grid_constant__ PagesArgs a) {
+  follow();
+  rename(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
 }
 
 // ------------------------------------------------------------------- fork ---
@@ -324,10 +420,37 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 }  // namespace
 
-int launch_pages_tables(const PagesArgs& a, bool compact, cudaStream_t stream) {
-  if (compact) tables_kernel<true><<<kCtas, kThreads, 0, stream>>>(a);
-  else tables_kernel<false><<<kCtas, kThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+int launch_pages_tables(const PagesArgs& a, bool compact, int sms, cudaStream_t stream) {
+  const int64_t segments = (int64_t)a.B * ((a.W + kSeg - 1) / kSeg);
+  if (segments <= kAlone && a.num_blocks <= kAloneIds) {
+    const bool few = segments <= kFew && a.num_blocks <= kFewIds;
+    if (few && compact) tables_kernel<true, true, 1><<<1, kThreads, 0, stream>>>(a);
+    else if (few) tables_kernel<false, true, 1><<<1, kThreads, 0, stream>>>(a);
+    else if (compact) tables_kernel<true, true, kCtas><<<kCtas, kThreads, 0, stream>>>(a);
+    else tables_kernel<false, true, kCtas><<<kCtas, kThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  }
+  const int64_t want = (segments + kWarps * kAtOnce - 1) / (kWarps * kAtOnce);
+  const int wide = want < 1 ? 1 : want > sms ? sms : (int)want;
+  const int zeros = (a.num_blocks - 1) / (4 * kThreads) + 1;
+  zero_kernel<<<zeros < sms ? zeros : sms, kThreads, 0, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
+  auto next = [&](void (*kernel)(PagesArgs), int grid) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
+  };
+  bool ok = next(compact ? mark_kernel<true> : mark_kernel<false>, wide) &&
+            next(compact ? tables_kernel<true, false, kCtas> : tables_kernel<false, false, kCtas>, kCtas);
+  if (compact) ok = ok && next(rename_kernel, wide);
+  return ok ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
 int launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
