@@ -34,7 +34,6 @@
 namespace gattn {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kKeys = 16;      // of a tile
 constexpr int kWindow = 64;    // tiles of a warp's run that are resolved ahead
 constexpr float kRise = 8.f;   // a maximum stays until a score is so much above it (log2)
@@ -51,7 +50,7 @@ struct Bf16Params {
   int4* head;    // [CTA] request and unit of its parts 0 and 1 (-1: none)
   float* parts;  // [CTA][2] of a unit that began in an earlier CTA; that begins here and goes on
   float* kept;   // [CTA][warp] of a unit that began in an earlier warp, while the warp goes on
-  int B, T, Hq, Hkv, G, chunks, block_len, W, num_blocks, L, layer, least;
+  int B, T, Hq, Hkv, G, chunks, block_len, W, num_blocks, L, layer, least, ctas;
   float scale_log2;
   uint64_t turn[64];
 
@@ -90,11 +89,12 @@ constexpr uint32_t kFirst = 32, kLast = 64;
 
 template <int D>
 struct Ring {
+  static constexpr int warps = 8, threads = warps * 32;
   static constexpr int stages = D == 128 ? 3 : 6;
   static constexpr uint32_t tile = kKeys * D * 2, stage = 2 * tile;
   static constexpr uint32_t warp = stages * stage;
-  static constexpr uint32_t windows = kWarps * warp;
-  static constexpr uint32_t bytes = windows + kWarps * kWindow * sizeof(Tile);
+  static constexpr uint32_t windows = warps * warp;
+  static constexpr uint32_t bytes = windows + warps * kWindow * sizeof(Tile);
 };
 // A part in shared memory or the workspace: O [H][D], m [H], l [H].
 template <int D, int H>
@@ -122,14 +122,21 @@ __device__ __forceinline__ float weight(float m, float top) { return m == top ? 
 
 // MODE 0: up to four heads, hi and lo side by side; 1: up to eight; 2: up to sixteen.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
+__global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
   constexpr int H = MODE == 0 ? 4 : MODE == 1 ? 8 : 16, NT = MODE == 2 ? 2 : 1, KS = D / 16, HK = KS / 2;
-  constexpr int S = Ring<D>::stages, PIECES = D / 8;  // 16-byte pieces of a row
+  constexpr int kWarps = Ring<D>::warps, kThreads = Ring<D>::threads, S = Ring<D>::stages, PIECES = D / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sum[kWarps], start_r, start_pre, total;
   __shared__ int4 piece[2 * kWarps];  // the warps' open parts: request, unit, whether it begins and ends there
+  __shared__ int4 unit_of[2 * kWarps];  // units of those parts: first part, end, whether another CTA has parts too, slot
+  __shared__ int units_here;
+  __shared__ float part_weight[2 * kWarps][H], unit_top[2 * kWarps][H], unit_sum[2 * kWarps][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the frequencies are read here, while nothing else can be done: each line of them is a miss
+  // of the constant cache, and a warp that waits for one issues nothing
+  __shared__ uint64_t turn[D / 2];
+  if (tid < D / 2) turn[tid] = p.turn[tid];
 
   // ---- this CTA's run of tiles, and the request that it begins in
   bool bad = false;
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   const int c16 = lane % PIECES, r16 = lane / PIECES;
   auto issue = [&](int x) {
     if (x < w1) {
-      if ((x - w0) % 32 == 0) resolve(x);
+      if (x > w0 && (x - w0) % 32 == 0) resolve(x);
       const Tile t = window[(x - w0) % kWindow];
       const int keys = t.at < 0 ? 0 : (int)(t.info & 31);
       const uint32_t st = ring + (x - w0) % S * Ring<D>::stage;
@@ -206,37 +213,73 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     cp_async_commit();
   };
+  // ---- q of a unit: fetched ahead, then rotated at the token's position, hi and lo
+  // (16 bytes a lane: a long sequence has every warp of the GPU read the same few rows at once)
+  constexpr int CQ = D / 32;  // 16-byte chunks of a head's row a lane: chunks 4 i + t4
+  uint4 raw[NT][CQ];
+  auto fetch_q = [&](const Tile& t) {
+    const int unit = t.info >> 8, g = unit / p.chunks, h0 = (unit - g * p.chunks) * 16;
+    const bf16* rows = p.q + ((int64_t)p.row(t.r) * p.Hq + g * p.G + h0) * D + t4 * 8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int col = MODE == 0 ? g8 & 3 : n * 8 + g8;
+#pragma unroll
+      for (int i = 0; i < CQ; ++i)
+        raw[n][i] = h0 + col < p.G ? *reinterpret_cast<const uint4*>(rows + col * D + i * 32) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (w0 < w1) {  // before the keys, which would be ahead of it in the memory's queues
+    resolve(w0);
+    fetch_q(window[0]);
+  }
   for (int x = w0; x < w0 + S - 1; ++x) issue(x);
 
   uint32_t qh[NT][KS][2], ql[NT][KS][2];
   float m[NT][2], l[NT][2], o[KS][NT][4];
-  // ---- q of a unit: rotated at the token's position, hi and lo
-  auto load_q = [&](const Tile& t) {
-    const int unit = t.info >> 8, g = unit / p.chunks, h0 = (unit - g * p.chunks) * 16;
+  auto turn_q = [&](const Tile& t) {
     const int pos = max(p.length(t.r) - 1, 0);
+    // the four lanes of a head have four chunks of four words; each wants its word of every chunk
+    uint32_t word[NT][KS][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int col = MODE == 0 ? g8 & 3 : n * 8 + g8;
-      const bool in = h0 + col < p.G;
-      const bf16* row = p.q + ((int64_t)p.row(t.r) * p.Hq + g * p.G + (in ? h0 + col : 0)) * D;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int ks = 0; ks < HK; ++ks)
+      for (int i = 0; i < CQ; ++i) {
+        const uint32_t v[4] = {raw[n][i].x, raw[n][i].y, raw[n][i].z, raw[n][i].w};
+        uint32_t got[4];  // from lane t4 ^ s: its chunk's word t4
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int j = ks * 16 + e * 8 + t4 * 2;
-          uint64_t x = bf16x2_to_f2(*reinterpret_cast<const uint32_t*>(row + j));
-          uint64_t y = bf16x2_to_f2(*reinterpret_cast<const uint32_t*>(row + j + D / 2));
-          uint64_t sn, cs;
-          sincos_turns(turn_part(pos, p.turn[j]), turn_part(pos, p.turn[j + 1]), sn, cs);
+        for (int s = 0; s < 4; ++s) {
+          const int w = t4 ^ s;  // the word that the lane asking wants
+          const uint32_t lo = w & 1 ? v[1] : v[0], hi = w & 1 ? v[3] : v[2];
+          got[s] = __shfl_xor_sync(0xffffffffu, w & 2 ? hi : lo, s);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // chunk 4 i + c came from lane c, in step c ^ t4
+          const uint32_t lo = t4 & 1 ? got[c ^ 1] : got[c], hi = t4 & 1 ? got[c ^ 3] : got[c ^ 2];
+          word[n][2 * i + c / 2][c & 1] = t4 & 2 ? hi : lo;
+        }
+      }
+#pragma unroll
+    for (int ks = 0; ks < HK; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = ks * 16 + e * 8 + t4 * 2;
+        uint64_t sn, cs;
+        sincos_turns(turn_part(pos, turn[j]), turn_part(pos, turn[j + 1]), sn, cs);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint64_t x = bf16x2_to_f2(word[n][ks][e]), y = bf16x2_to_f2(word[n][ks + HK][e]);
           const uint64_t a = f2_sub(f2_mul(x, cs), f2_mul(y, sn)), b = f2_fma(x, sn, f2_mul(y, cs));
           const uint32_t ah = f2_to_bf16x2(a), bh = f2_to_bf16x2(b);
           const uint32_t al = f2_to_bf16x2(f2_sub(a, bf16x2_to_f2(ah))), bl = f2_to_bf16x2(f2_sub(b, bf16x2_to_f2(bh)));
           const bool low = MODE == 0 && g8 >= 4;
-          qh[n][ks][e] = !in ? 0u : low ? al : ah;
-          qh[n][ks + HK][e] = !in ? 0u : low ? bl : bh;
-          ql[n][ks][e] = in ? al : 0u;
-          ql[n][ks + HK][e] = in ? bl : 0u;
+          qh[n][ks][e] = low ? al : ah;
+          qh[n][ks + HK][e] = low ? bl : bh;
+          ql[n][ks][e] = al;
+          ql[n][ks + HK][e] = bl;
         }
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
@@ -257,10 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     __syncwarp();
     const Tile t = window[(x - w0) % kWindow];
     if (x == w0 || (t.info & kFirst)) {
-      load_q(t);
+      turn_q(t);
       wrong = false;
       begins = t.info & kFirst;
     }
+    if (x + 1 < w1 && (window[(x + 1 - w0) % kWindow].info & kFirst)) fetch_q(window[(x + 1 - w0) % kWindow]);
     wrong |= t.at < 0;
     const int keys = t.info & 31;
     const uint32_t st = ring + (x - w0) % S * Ring<D>::stage;
@@ -407,121 +451,185 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
   }
   __syncthreads();
 
-  // ---- the warps' parts joined: whole units are written, the others left for the next kernel
-  int4 head = make_int4(-1, -1, -1, -1);
-  for (int i = 0; i < 2 * kWarps;) {
-    const int4 id = piece[i];
-    if (id.x < 0) {
-      ++i;
+  // ---- the warps' parts joined: whole units are written, the others left for the next kernel.
+  // First the weights, a warp a head and a lane a part; parts of one unit follow one another.
+  constexpr int kParts = 2 * kWarps;
+  static_assert(kParts <= 32, "a lane a part");
+  auto part = [&](int j) -> const float* {
+    return j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * Ring<D>::warp) : p.kept + ((int64_t)blockIdx.x * kWarps + (j >> 1)) * P;
+  };
+  {
+    const int4 id = lane < kParts ? piece[lane] : make_int4(-1, -1, 0, 0);
+    const bool valid = id.x >= 0;
+    const uint32_t upto = (2u << lane) - 1, valids = __ballot_sync(0xffffffffu, valid);
+    const int before = 31 - __clz(valids & (upto >> 1));  // the part before (-1: none)
+    const int px = __shfl_sync(0xffffffffu, id.x, max(before, 0)), py = __shfl_sync(0xffffffffu, id.y, max(before, 0));
+    const bool first = valid && (before < 0 || px != id.x || py != id.y);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first), later = firsts & ~upto;
+    const int begin = 31 - __clz(firsts & upto), end = later ? __ffs(later) - 1 : 32;  // of this lane's unit
+    const uint32_t members = valids & (upto | (end == 32 ? 0xffffffffu : (1u << end) - 1)) & (begin < 0 ? 0u : ~((1u << begin) - 1));
+    for (int h = warp; h < H; h += kWarps) {
+      const float mine = valid ? part(lane)[H * D + h] : -INFINITY, lj = valid ? part(lane)[H * D + H + h] : 0.f;
+      float top = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, top, s);
+        if (lane - s >= begin && lane >= s) top = fmaxf(top, v);
+      }
+      top = __shfl_sync(0xffffffffu, top, end - 1);
+      const float f = valid ? weight(mine, top) : 0.f;
+      float sum = valid ? f * lj : 0.f;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, sum, s);
+        if (lane - s >= begin && lane >= s) sum += v;
+      }
+      sum = __shfl_sync(0xffffffffu, sum, end - 1);
+      if (__ballot_sync(0xffffffffu, valid && lj == kBad) & members) sum = kBad;
+      if (lane < kParts) part_weight[lane][h] = f;
+      if (first) {
+        unit_top[lane][h] = top;
+        unit_sum[lane][h] = sum;
+      }
+    }
+    if (warp == 0) {
+      const int ends = __shfl_sync(0xffffffffu, id.w, 31 - __clz(members | 1u));
+      const int slot = id.z ? 1 : 0;
+      const bool open = first && !(id.z && ends);
+      if (first) unit_of[__popc(firsts & (upto >> 1))] = make_int4(lane, end, open, slot);
+      if (lane == 0) units_here = __popc(firsts);
+      // at most one unit began before this CTA, and at most one goes on behind it
+      int4 head = make_int4(-1, -1, -1, -1);
+      const uint32_t s0 = __ballot_sync(0xffffffffu, open && slot == 0), s1 = __ballot_sync(0xffffffffu, open && slot == 1);
+      head.x = __shfl_sync(0xffffffffu, id.x, s0 ? __ffs(s0) - 1 : 0);
+      head.y = __shfl_sync(0xffffffffu, id.y, s0 ? __ffs(s0) - 1 : 0);
+      head.z = __shfl_sync(0xffffffffu, id.x, s1 ? __ffs(s1) - 1 : 0);
+      head.w = __shfl_sync(0xffffffffu, id.y, s1 ? __ffs(s1) - 1 : 0);
+      if (lane == 0) p.head[blockIdx.x] = make_int4(s0 ? head.x : -1, s0 ? head.y : -1, s1 ? head.z : -1, s1 ? head.w : -1);
+    }
+  }
+  __syncthreads();
+  constexpr int QUADS = H * D / 4;  // four elements of a head a thread
+  for (int i = tid; i < units_here * QUADS; i += kThreads) {
+    const int4 u = unit_of[i / QUADS];
+    const int quad = i % QUADS, h = quad / (D / 4), e = quad % (D / 4) * 4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = u.x; j < min(u.y, kParts); ++j) {
+      if (piece[j].x < 0) continue;
+      const float f = part_weight[j][h];
+      const float4 v = *reinterpret_cast<const float4*>(part(j) + quad * 4);
+      a.x += f * v.x;
+      a.y += f * v.y;
+      a.z += f * v.z;
+      a.w += f * v.w;
+    }
+    const int4 id = piece[u.x];
+    if (!u.z) {
+      write_pair<D>(p, id.x, id.y, h, e, a.x, a.y, unit_sum[u.x][h]);
+      write_pair<D>(p, id.x, id.y, h, e + 2, a.z, a.w, unit_sum[u.x][h]);
       continue;
     }
-    int end = i, ends = 0;  // the unit's parts are i .. end - 1 (with gaps)
-    for (int j = i; j < 2 * kWarps; ++j) {
-      const int4 other = piece[j];
-      if (other.x < 0) continue;
-      if (other.x != id.x || other.y != id.y) break;
-      end = j + 1;
-      ends |= other.w;
+    float* to = p.parts + ((int64_t)blockIdx.x * 2 + u.w) * P;
+    *reinterpret_cast<float4*>(to + quad * 4) = a;
+    if (e == 0) {
+      to[H * D + h] = unit_top[u.x][h];
+      to[H * D + H + h] = unit_sum[u.x][h];
     }
-    auto part = [&](int j) -> const float* {
-      return j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * Ring<D>::warp)
-                   : p.kept + ((int64_t)blockIdx.x * kWarps + (j >> 1)) * P;
-    };
-    const int slot = id.z ? 1 : 0;
-    float* to = p.parts + ((int64_t)blockIdx.x * 2 + slot) * P;
-    if (!(id.z && ends)) {
-      if (slot == 0) head.x = id.x, head.y = id.y;
-      else head.z = id.x, head.w = id.y;
-    }
-    for (int k = tid; k < H * D / 2; k += kThreads) {
-      const int h = k / (D / 2), e = (k - h * (D / 2)) * 2;
-      float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
-      bool none = false;
-      for (int j = i; j < end; ++j)
-        if (piece[j].x >= 0) top = fmaxf(top, part(j)[H * D + h]);
-      for (int j = i; j < end; ++j) {
-        if (piece[j].x < 0) continue;
-        const float* from = part(j);
-        const float f = weight(from[H * D + h], top), lj = from[H * D + H + h];
-        none |= lj == kBad;
-        sum += f * lj;
-        a += f * from[h * D + e];
-        b += f * from[h * D + e + 1];
-      }
-      if (none) sum = kBad;
-      if (id.z && ends) {
-        write_pair<D>(p, id.x, id.y, h, e, a, b, sum);
-      } else {
-        *reinterpret_cast<float2*>(to + h * D + e) = make_float2(a, b);
-        if (e == 0) {
-          to[H * D + h] = top;
-          to[H * D + H + h] = sum;
-        }
-      }
-    }
-    i = end;
   }
-  if (tid == 0) p.head[blockIdx.x] = head;
 }
 
-// Joins the CTAs' parts of a unit: block (c, h) takes head h of the unit that begins in
-// CTA c and goes on in the next ones.
-template <int D, int H>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Bf16Params p) {
-  constexpr int P = kPart<D, H>, LANES = D / 2, GROUPS = kThreads / LANES;
-  __shared__ float2 red[GROUPS][LANES];
-  __shared__ float red_m[kWarps], red_l[kWarps];
-  const int tid = threadIdx.x, c = blockIdx.x, h = blockIdx.y, ctas = gridDim.x;
+// Joins the CTAs' parts of a unit: block c takes the one that begins in CTA c and goes on in the
+// next ones.  Four elements of a head a thread; where threads are left, groups of them share out
+// the parts, so that many parts are read at once.
+constexpr int kJoinThreads = 1024, kMostCtas = 192;
+template <int D, int H, int HB>  // HB < H: block (u, i) takes the u-th unit's i-th HB heads
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Bf16Params p) {
+  constexpr int P = kPart<D, H>, QUADS = HB * D / 4, GROUPS = kJoinThreads / QUADS, AHEAD = 4;
+  __shared__ float4 red[GROUPS > 1 ? kJoinThreads : 1];
+  __shared__ float part_top[kMostCtas][HB], part_sum[kMostCtas][HB], unit_sum[HB];
+  __shared__ int begins_in;
+  const int tid = threadIdx.x, h0 = blockIdx.y * HB, lane = tid & 31, warp = tid >> 5;
+  if (HB < H && tid == 0) begins_in = -1;
+  if (HB < H) __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 id = p.head[c];
-  if (id.z < 0) return;
-  int parts = 1;  // the CTAs that go on with a unit follow one another
-  for (int i = c + 1; i < ctas; i += kThreads) {
-    const int o = i + tid;
-    const int4 other = o < ctas ? p.head[o] : make_int4(-1, -1, -1, -1);
-    parts += __syncthreads_count(other.x == id.z && other.y == id.w);
+  const int4 other = tid < p.ctas ? p.head[tid] : make_int4(-1, -1, -1, -1);
+  int4 id;
+  if (HB < H) {
+    id.z = blockIdx.x / p.units();
+    id.w = blockIdx.x - id.z * p.units();
+    if (other.z == id.z && other.w == id.w) begins_in = tid;
+  } else {
+    id = p.head[blockIdx.x];
+    if (id.z < 0) return;
   }
+  // the CTAs that go on with a unit follow one another
+  const int parts = 1 + __syncthreads_count(other.x == id.z && other.y == id.w);
+  const int c = HB < H ? begins_in : blockIdx.x;
+  if (c < 0) return;
   auto part = [&](int j) { return p.parts + ((int64_t)(c + j) * 2 + (j == 0)) * P; };
-  float top = -INFINITY;
-  for (int j = tid; j < parts; j += kThreads) top = fmaxf(top, part(j)[H * D + h]);
+  const int quad = tid % QUADS, group = tid / QUADS, h = quad / (D / 4), e = quad % (D / 4) * 4;
+  float4 v[AHEAD];  // read beside the maxima, whose weights they wait for
 #pragma unroll
-  for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  if (tid % 32 == 0) red_m[tid / 32] = top;
+  for (int k = 0; k < AHEAD; ++k)
+    if (group + k * GROUPS < parts) v[k] = *reinterpret_cast<const float4*>(part(group + k * GROUPS) + h0 * D + quad * 4);
+  for (int i = tid; i < parts * HB; i += kJoinThreads) {
+    part_top[i / HB][i % HB] = part(i / HB)[H * D + h0 + i % HB];
+    part_sum[i / HB][i % HB] = part(i / HB)[H * D + H + h0 + i % HB];
+  }
   __syncthreads();
+  if (warp < HB) {  // a warp a head: the maximum, each part's weight, the sum
+    float top = -INFINITY, sum = 0.f;
+    bool none = false;
+    for (int j = lane; j < parts; j += 32) top = fmaxf(top, part_top[j][warp]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w]);
-  float sum = 0.f;
-  bool none = false;
-  for (int j = tid; j < parts; j += kThreads) {
-    const float lj = part(j)[H * D + H + h];
-    none |= lj == kBad;
-    sum += weight(part(j)[H * D + h], top) * lj;
-  }
-  none = __syncthreads_or(none);
+    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    for (int j = lane; j < parts; j += 32) {
+      const float lj = part_sum[j][warp], f = weight(part_top[j][warp], top);
+      none |= lj == kBad;
+      sum += f * lj;
+      part_top[j][warp] = f;
+    }
 #pragma unroll
-  for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  if (tid % 32 == 0) red_l[tid / 32] = sum;
-  const int e = tid % LANES, group = tid / LANES;
-  float2 o = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int j = group; j < parts; j += GROUPS) {
-    const float f = weight(part(j)[H * D + h], top);
-    const float2 v = *reinterpret_cast<const float2*>(part(j) + h * D + e * 2);
-    o.x += f * v.x;
-    o.y += f * v.y;
+    for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    none = __any_sync(0xffffffffu, none);
+    if (lane == 0) unit_sum[warp] = none ? kBad : sum;
   }
-  red[group][e] = o;
   __syncthreads();
-  if (group != 0) return;
-  sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = group; j0 < parts; j0 += AHEAD * GROUPS) {
+    float4 next[AHEAD];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += red_l[w];
+    for (int k = 0; k < AHEAD; ++k) {
+      const int j = j0 + (AHEAD + k) * GROUPS;
+      if (j < parts) next[k] = *reinterpret_cast<const float4*>(part(j) + h0 * D + quad * 4);
+    }
 #pragma unroll
-  for (int k = 1; k < GROUPS; ++k) {
-    o.x += red[k][e].x;
-    o.y += red[k][e].y;
+    for (int k = 0; k < AHEAD; ++k) {
+      if (j0 + k * GROUPS < parts) {
+        const float f = part_top[j0 + k * GROUPS][h];
+        o.x += f * v[k].x;
+        o.y += f * v[k].y;
+        o.z += f * v[k].z;
+        o.w += f * v[k].w;
+      }
+      v[k] = next[k];
+    }
   }
-  write_pair<D>(p, id.z, id.w, h, e * 2, o.x, o.y, none ? kBad : sum);
+  if constexpr (GROUPS > 1) {
+    red[tid] = o;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) {
+      const float4 v = red[k * QUADS + quad];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
+  }
+  write_pair<D>(p, id.z, id.w, h0 + h, e, o.x, o.y, unit_sum[h]);
+  write_pair<D>(p, id.z, id.w, h0 + h, e + 2, o.z, o.w, unit_sum[h]);
 }
 
 int heads_of(const PagedProblem& pb) { return pb.G <= 4 ? 4 : pb.G <= 8 ? 8 : 16; }
@@ -529,6 +637,7 @@ size_t part_bytes(const PagedProblem& pb) { return (size_t)heads_of(pb) * (pb.d 
 
 template <int D, int MODE>
 int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
+  const int ctas = sms < kMostCtas ? sms : kMostCtas;
   constexpr int H = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;
   Bf16Params p{};
   p.q = static_cast<const bf16*>(pb.q);
@@ -539,8 +648,8 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   p.kv_len = pb.kv_len;
   p.status = pb.status;
   p.head = static_cast<int4*>(workspace);
-  p.parts = reinterpret_cast<float*>(p.head + sms);
-  p.kept = p.parts + (size_t)sms * 2 * kPart<D, H>;
+  p.parts = reinterpret_cast<float*>(p.head + ctas);
+  p.kept = p.parts + (size_t)ctas * 2 * kPart<D, H>;
   p.B = pb.B;
   p.T = pb.T;
   p.Hq = pb.Hq;
@@ -552,31 +661,35 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   p.num_blocks = pb.num_blocks;
   p.L = pb.L;
   p.layer = pb.layer;
-  p.least = 2 * kWarps;
+  p.least = Ring<D>::warps;
+  p.ctas = ctas;
   p.scale_log2 = pb.scale_log2;
   for (int j = 0; j < 64; ++j) p.turn[j] = pb.turn[j];
   constexpr int smem = Ring<D>::bytes;
   if (cudaFuncSetAttribute(decode_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  decode_kernel<D, MODE><<<sms, kThreads, smem, stream>>>(p);
+  decode_kernel<D, MODE><<<ctas, Ring<D>::threads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
   // the joins may start while the last tiles run (and then wait for them)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(sms, H);
-  cfg.blockDim = dim3(kThreads);
+  // where units are few each has many parts: a block for two of its heads
+  const bool few = (int64_t)pb.B * pb.Hkv * p.chunks * 4 < ctas;
+  cfg.gridDim = few ? dim3(pb.B * pb.Hkv * p.chunks, H / 2) : dim3(ctas);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, H>, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  return cudaLaunchKernelEx(&cfg, few ? join_kernel<D, H, 2> : join_kernel<D, H, H>, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
 
 size_t paged_bf16_workspace(const PagedProblem& pb, int sms) {
-  return (size_t)sms * (sizeof(int4) + (2 + kWarps) * part_bytes(pb));
+  static_assert(Ring<64>::warps == Ring<128>::warps, "parts");
+  return (size_t)sms * (sizeof(int4) + (2 + Ring<128>::warps) * part_bytes(pb));
 }
 
 int launch_paged_bf16(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
