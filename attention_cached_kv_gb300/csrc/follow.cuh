@@ -1,0 +1,35 @@
+// follow.cuh -- kernels that may be put on the GPU while the one before them on the stream
+// still runs (programmatic dependent launch).  Such a kernel sets itself up, then
+// waits for everything before it, before its first access to global memory; so the order of a
+// stream holds, and only the time between two kernels is saved.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace gattn {
+
+// The next kernel may be put on the GPU from here on.
+__device__ __forceinline__ void let_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Everything before this kernel on its stream is done, and its results can be read.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that calls wait_before(); `cluster` CTAs a cluster along x (0: none).
+template <class... P, class... A>
+inline bool launch_following(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+}
+
+}  // namespace gattn

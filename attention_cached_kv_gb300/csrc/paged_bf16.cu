@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "follow.cuh"
 #include "frag.cuh"
 #include "kernels.h"
 #include "paged.cuh"
@@ -132,11 +133,12 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
   __shared__ int units_here;
   __shared__ float part_weight[2 * kWarps][H], unit_top[2 * kWarps][H], unit_sum[2 * kWarps][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_follow();
   // the frequencies are read here, while nothing else can be done: each line of them is a miss
   // of the constant cache, and a warp that waits for one issues nothing
   __shared__ uint64_t turn[D / 2];
   if (tid < D / 2) turn[tid] = p.turn[tid];
+  wait_before();
 
   // ---- this CTA's run of tiles, and the request that it begins in
   bool bad = false;
@@ -551,7 +553,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int tid = threadIdx.x, h0 = blockIdx.y * HB, lane = tid & 31, warp = tid >> 5;
   if (HB < H && tid == 0) begins_in = -1;
   if (HB < H) __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_follow();
+  wait_before();
   const int4 other = tid < p.ctas ? p.head[tid] : make_int4(-1, -1, -1, -1);
   int4 id;
   if (HB < H) {
@@ -668,21 +671,13 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   constexpr int smem = Ring<D>::bytes;
   if (cudaFuncSetAttribute(decode_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  decode_kernel<D, MODE><<<ctas, Ring<D>::threads, smem, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
-  // the joins may start while the last tiles run (and then wait for them)
-  cudaLaunchConfig_t cfg{};
+  if (!launch_following(decode_kernel<D, MODE>, dim3(ctas), dim3(Ring<D>::threads), smem, stream, 0, p)) return GIST_ATTN_ERR_LAUNCH;
   // where units are few each has many parts: a block for two of its heads
   const bool few = (int64_t)pb.B * pb.Hkv * p.chunks * 4 < ctas;
-  cfg.gridDim = few ? dim3(pb.B * pb.Hkv * p.chunks, H / 2) : dim3(ctas);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few ? join_kernel<D, H, 2> : join_kernel<D, H, H>, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  const dim3 grid = few ? dim3(pb.B * pb.Hkv * p.chunks, H / 2) : dim3(ctas);
+  return launch_following(few ? join_kernel<D, H, 2> : join_kernel<D, H, H>, grid, dim3(kJoinThreads), 0, stream, 0, p)
+             ? GIST_ATTN_OK
+             : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace

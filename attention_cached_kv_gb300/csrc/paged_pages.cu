@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "follow.cuh"
 #include "kernels.h"
 
 namespace cg = cooperative_groups;
@@ -34,12 +35,6 @@ constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kSeg = 128;  // entries of one row that a warp takes at a time
 constexpr int kAlone = 512, kAloneIds = 16384;  // segments and ids that one cluster does alone
 constexpr int kFew = 64, kFewIds = 4096;         // that one CTA does, whose barriers cost next to nothing
-
-// A kernel that follows another on its stream: may start early, waits here for its results.
-__device__ __forceinline__ void follow() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 
 // Blocks of a request: the live entries of its row.
 __device__ __forceinline__ int blocks_of(int len, int block_len, int W, bool& bad) {
@@ -180,13 +175,13 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads) tables_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, gw = cta * kWarps + warp;
 
+  let_follow();
+  wait_before();
   if constexpr (ALONE) {
     for (int b = cta * kThreads + tid; b < a.num_blocks; b += CTAS * kThreads) a.ids[b] = 0;
     sync();
     mark<COMPACT>(a, gw, CTAS * kWarps);
     sync();
-  } else {
-    follow();
   }
 
   // each warp's slice of the ids: how many are in use
@@ -264,16 +259,19 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads) tables_
 }
 
 __global__ void __launch_bounds__(kThreads) zero_kernel(const __grid_constant__ PagesArgs a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_follow();
+  wait_before();
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.num_blocks; b += gridDim.x * kThreads) a.ids[b] = 0;
 }
 template <bool COMPACT>
 __global__ void __launch_bounds__(kThreads) mark_kernel(const __grid_constant__ PagesArgs a) {
-  follow();
+  let_follow();
+  wait_before();
   mark<COMPACT>(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
 }
 __global__ void __launch_bounds__(kThreads) rename_kernel(const __grid_constant__ PagesArgs a) {
-  follow();
+  let_follow();
+  wait_before();
   rename(a, blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps);
 }
 
@@ -285,6 +283,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const __grid_constant__ 
   extern __shared__ int take[];  // [B] index among the blocks taken; -1: none needed, -2: not served, -3: not forked
   __shared__ int warp_sum[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_follow();
+  wait_before();
   const int per = (a.B + kThreads - 1) / kThreads;
   const int r0 = min(tid * per, a.B), r1 = min(r0 + per, a.B);
   const int begin = max(a.free_range[0], 0), end = max(min(a.free_range[1], a.num_free), 0);
@@ -377,6 +377,8 @@ constexpr int kCopyThreads = 256;
 
 template <int V>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+  let_follow();
+  wait_before();
   const int n = a.count ? min(max(*a.count, 0), a.n) : a.n;
   const int row = a.plane / a.block_len;  // pieces of a row
   const int whole = a.planes * a.plane;
@@ -422,34 +424,20 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 
 int launch_pages_tables(const PagesArgs& a, bool compact, int sms, cudaStream_t stream) {
   const int64_t segments = (int64_t)a.B * ((a.W + kSeg - 1) / kSeg);
-  if (segments <= kAlone && a.num_blocks <= kAloneIds) {
-    const bool few = segments <= kFew && a.num_blocks <= kFewIds;
-    if (few && compact) tables_kernel<true, true, 1><<<1, kThreads, 0, stream>>>(a);
-    else if (few) tables_kernel<false, true, 1><<<1, kThreads, 0, stream>>>(a);
-    else if (compact) tables_kernel<true, true, kCtas><<<kCtas, kThreads, 0, stream>>>(a);
-    else tables_kernel<false, true, kCtas><<<kCtas, kThreads, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  auto launch = [&](void (*kernel)(PagesArgs), int grid) { return launch_following(kernel, dim3(grid), dim3(kThreads), 0, stream, 0, a); };
+  bool ok;
+  if (segments <= kFew && a.num_blocks <= kFewIds) {
+    ok = launch(compact ? tables_kernel<true, true, 1> : tables_kernel<false, true, 1>, 1);
+  } else if (segments <= kAlone && a.num_blocks <= kAloneIds) {
+    ok = launch(compact ? tables_kernel<true, true, kCtas> : tables_kernel<false, true, kCtas>, kCtas);
+  } else {
+    const int64_t want = (segments + kWarps * kAtOnce - 1) / (kWarps * kAtOnce);
+    const int wide = want < 1 ? 1 : want > sms ? sms : (int)want;
+    const int zeros = (a.num_blocks - 1) / (4 * kThreads) + 1;
+    ok = launch(zero_kernel, zeros < sms ? zeros : sms) && launch(compact ? mark_kernel<true> : mark_kernel<false>, wide) &&
+         launch(compact ? tables_kernel<true, false, kCtas> : tables_kernel<false, false, kCtas>, kCtas);
+    if (compact) ok = ok && launch(rename_kernel, wide);
   }
-  const int64_t want = (segments + kWarps * kAtOnce - 1) / (kWarps * kAtOnce);
-  const int wide = want < 1 ? 1 : want > sms ? sms : (int)want;
-  const int zeros = (a.num_blocks - 1) / (4 * kThreads) + 1;
-  zero_kernel<<<zeros < sms ? zeros : sms, kThreads, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return GIST_ATTN_ERR_LAUNCH;
-  auto next = [&](void (*kernel)(PagesArgs), int grid) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess;
-  };
-  bool ok = next(compact ? mark_kernel<true> : mark_kernel<false>, wide) &&
-            next(compact ? tables_kernel<true, false, kCtas> : tables_kernel<false, false, kCtas>, kCtas);
-  if (compact) ok = ok && next(rename_kernel, wide);
   return ok ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
@@ -460,8 +448,7 @@ int launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
       cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanRequests * (int)sizeof(int)) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
   const int want = (a.B + kWarps - 1) / kWarps, grid = want < 1 ? 1 : want > 64 ? 64 : want;
-  fork_kernel<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  return launch_following(fork_kernel, dim3(grid), dim3(kThreads), smem, stream, 0, a) ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
 }
 
 int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream) {
@@ -471,9 +458,10 @@ int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream) {
     const int64_t chunks = (int64_t)a.n * ((a.planes * (int64_t)a.plane + kCopyThreads * V - 1) / (kCopyThreads * V));
     return (int)(chunks < most ? chunks : most);
   };
-  if (pieces >= (int64_t)most * kCopyThreads * 8) copy_kernel<8><<<grid(8), kCopyThreads, 0, stream>>>(a);
-  else copy_kernel<2><<<grid(2), kCopyThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  const bool large = pieces >= (int64_t)most * kCopyThreads * 8;
+  return launch_following(large ? copy_kernel<8> : copy_kernel<2>, dim3(grid(large ? 8 : 2)), dim3(kCopyThreads), 0, stream, 0, a)
+             ? GIST_ATTN_OK
+             : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace gattn

@@ -21,6 +21,7 @@
 // Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
 #include <cooperative_groups.h>
 
+#include "follow.cuh"
 #include "proj_w4.cuh"
 
 namespace cg = cooperative_groups;
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   const int staged = min(TN, p.T);  // rows of x in shared memory; MMA columns behind them repeat the last
   const uint32_t ring = xs + staged * pitch + warp * (kStages * MR * 1024);
 
+  let_follow();
+  wait_before();
   // ---- weights: rows of 64 bytes, 16 a row tile; chunk c of row r at c ^ (r / 2 mod 4)
   int row[MR], apart = 8;
 #pragma unroll
@@ -228,18 +231,9 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
   if (smem > kMostSmem || token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(w4_kernel<NT, MR, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks * split, token_blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_kernel<NT, MR, WR>, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  return launch_following(w4_kernel<NT, MR, WR>, dim3(blocks * split, token_blocks), dim3(kThreads), smem, stream, split, p)
+             ? GIST_ATTN_OK
+             : GIST_ATTN_ERR_LAUNCH;
 }
 
 int launch(const W4Params& p, int sms, cudaStream_t stream) {

@@ -19,6 +19,7 @@
 // Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
 #include <cooperative_groups.h>
 
+#include "follow.cuh"
 #include "proj_w4.cuh"
 #include "tcgen05.cuh"
 
@@ -94,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int k0 = part * p.slice, k1 = max(min(k0 + p.slice, p.K), k0);
   const int chunks = (k1 - k0 + kChunk - 1) / kChunk;
 
+  let_follow();
+  wait_before();
   // ---- warps 0-3: the first codes are asked for before anything else
   const uint32_t ring = base + L::raw + (warp & 3) * (kRaw * 2048);
   const int c4 = lane & 3, most = k1 - k0 - c4 * 32;  // this lane's 32 inputs of chunk i exist where i kChunk < most
@@ -333,18 +336,9 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
   if (token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(w4_tc_kernel<TN, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * split, token_blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4_tc_kernel<TN, PG>, tm, p) == cudaSuccess ? GIST_ATTN_OK : GIST_ATTN_ERR_LAUNCH;
+  return launch_following(w4_tc_kernel<TN, PG>, dim3(tiles * split, token_blocks), dim3(kThreads), smem, stream, split, tm, p)
+             ? GIST_ATTN_OK
+             : GIST_ATTN_ERR_LAUNCH;
 }
 
 }  // namespace
