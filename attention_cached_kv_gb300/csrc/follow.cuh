@@ -29,7 +29,9 @@ inline bool launch_following(void (*kernel)(P...), dim3 grid, dim3 block, int sm
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess) return true;
+  cudaGetLastError();  // reported by the return code, not to a later call
+  return false;
 }
 
 }  // namespace gattn

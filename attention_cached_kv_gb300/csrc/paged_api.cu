@@ -217,8 +217,9 @@ int check_decode(const gist_paged_dims* dims, PagedProblem* pb) {
   const int rc = check_attn(dims, pb);
   if (rc != GIST_ATTN_OK) return rc;
   if (pb->max_new != 1) return GIST_ATTN_ERR_UNSUPPORTED;
-  const double tiles = (double)pb->B * pb->Hkv * ((pb->G + 15) / 16) * ((double)pb->W * pb->block_len / 16 + 1);
-  return tiles > 2147483647.0 ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
+  const double units = (double)pb->Hkv * ((pb->G + 15) / 16);  // a request's, counted in 24 bits
+  const double tiles = pb->B * units * ((double)pb->W * pb->block_len / 16 + 1);
+  return units > 1 << 23 || pb->Hkv > 1 << 20 || tiles > 2147483647.0 ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
 }
 
 // Sizes of the calls on blocks.

@@ -453,13 +453,14 @@ int launch_pages_fork(const ForkArgs& a, cudaStream_t stream) {
 
 int launch_pages_copy(const CopyArgs& a, int sms, cudaStream_t stream) {
   const int64_t pieces = (int64_t)a.n * a.planes * a.plane;
-  const int most = 8 * sms;
-  auto grid = [&](int V) {
-    const int64_t chunks = (int64_t)a.n * ((a.planes * (int64_t)a.plane + kCopyThreads * V - 1) / (kCopyThreads * V));
-    return (int)(chunks < most ? chunks : most);
-  };
-  const bool large = pieces >= (int64_t)most * kCopyThreads * 8;
-  return launch_following(large ? copy_kernel<8> : copy_kernel<2>, dim3(grid(large ? 8 : 2)), dim3(kCopyThreads), 0, stream, 0, a)
+  // small copies: less a thread, so that all SMs take part; large ones: several waves of CTAs, as
+  // SMs are not equally near to memory (32 an SM 79.4, 8 an SM 84.6, 4 an SM 88.9 us a compaction
+  // of 238 MB; a CTA a chunk of what the list can hold 105)
+  const bool large = pieces >= (int64_t)sms * 8 * kCopyThreads * 8;
+  const int V = large ? 8 : 2;
+  const int64_t chunks = (int64_t)a.n * ((a.planes * (int64_t)a.plane + kCopyThreads * V - 1) / (kCopyThreads * V));
+  const int grid = (int)(chunks < 32 * sms ? chunks : 32 * sms);
+  return launch_following(large ? copy_kernel<8> : copy_kernel<2>, dim3(grid), dim3(kCopyThreads), 0, stream, 0, a)
              ? GIST_ATTN_OK
              : GIST_ATTN_ERR_LAUNCH;
 }

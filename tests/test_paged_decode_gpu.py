@@ -51,6 +51,34 @@ def test_batches_cut_anywhere(lens, Hq, Hkv, d):
     assert torch.equal(got, binding.gist_attn_paged_decode(*pb.args(), dims=pb.dims))  # the same bits again
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,d,bl", [
+    ([70000, 3, 71001], 8, 4, 64, 64),                        # few units, each over all CTAs
+    ([150000, 40], 16, 4, 128, 256),
+    ([int(x) for x in np.random.default_rng(0).integers(1, 2200, 140)], 16, 4, 64, 32),
+    ([int(x) for x in np.random.default_rng(1).integers(300, 2000, 40)], 32, 16, 128, 16),
+    ([5000] * 8 + [0, 1] + [4999] * 7, 64, 8, 64, 64),
+    ([9000] * 9 + [17], 96, 8, 128, 64),
+])
+def test_large_batches(lens, Hq, Hkv, d, bl):
+    """Runs of many tiles a warp, units over many CTAs; the same bits every time."""
+    pb = su.Decode(lens, Hq, Hkv, d, bl, seed=3, layers=1, layer=0)
+    args = pb.args()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = binding.gist_attn_paged_decode(*args, dims=pb.dims, status=status)
+    for _ in range(20):
+        assert torch.equal(got, binding.gist_attn_paged_decode(*args, dims=pb.dims))
+    assert int(status) == 0
+    su.near(got, *pb.expected(), str(lens[:4]))
+    # a bad block near the end of the last request of some length
+    r = max(i for i, n in enumerate(lens) if n > bl)
+    bad = args[2].clone()
+    bad[r, lens[r] // bl - 1] = -1
+    out = binding.gist_attn_paged_decode(*args[:2], bad, args[3], dims=pb.dims, status=status)
+    assert not out[r].any() and int(status) == binding.STATUS_BAD_BLOCK
+    keep = [i for i in range(len(lens)) if i != r]
+    assert torch.equal(out[keep], got[keep])
+
+
 def test_scale_and_rotation_given():
     pb = su.Decode([300, 40], 8, 2, 128, 16, seed=5)
     pb.dims |= dict(softmax_scale=0.3, flags=binding.FLAG_PREROTATED)

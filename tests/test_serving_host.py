@@ -49,6 +49,7 @@ def decode(lib, **kw):
     (dict(q_start=P16 + 1), ALIGN), (dict(d=dict(BASE, max_new=2)), UNSUPPORTED), (dict(d=dict(BASE, block_len=24)), UNSUPPORTED),
     (dict(d=dict(BASE, head_dim=96)), UNSUPPORTED), (dict(d=dict(BASE, num_q_heads=258)), UNSUPPORTED),
     (dict(d=dict(BASE, max_blocks=(1 << 26) + 1)), UNSUPPORTED), (dict(d=dict(BASE, num_requests=1 << 26, max_blocks=64)), UNSUPPORTED),
+    (dict(d=dict(BASE, num_q_heads=(1 << 23) + 1, num_kv_heads=(1 << 23) + 1, num_layers=1, layer=0, max_blocks=1)), UNSUPPORTED),
     (dict(q_start=0, d=dict(BASE, num_tokens=2)), DIMS), (dict(d=dict(BASE, num_kv_heads=3)), DIMS),
     (dict(d=dict(BASE, layer=2)), DIMS), (dict(d=dict(BASE, flags=2)), DIMS), (dict(d=dict(BASE, softmax_scale=float("inf"))), DIMS),
     (dict(d=dict(BASE, num_requests=-1)), DIMS), (dict(d=dict(BASE, num_blocks=0)), DIMS),
