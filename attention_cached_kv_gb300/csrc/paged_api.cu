@@ -229,6 +229,12 @@ int check_pages(const gist_paged_dims* dims) {
   if (rc != GIST_ATTN_OK) return rc;
   return dims->num_blocks > 1 << 30 ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
 }
+// Those on whole tables: segments of 128 entries are counted in 31 bits.
+int check_tables(const gist_paged_dims* dims) {
+  const int rc = check_pages(dims);
+  if (rc != GIST_ATTN_OK) return rc;
+  return (double)dims->num_requests * (dims->max_blocks / 128 + 1) > 1 << 30 ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
+}
 }  // namespace
 }  // namespace gattn
 
@@ -271,7 +277,7 @@ extern "C" int gist_attn_paged_decode(const void* q, const void* kv_pool, const 
 extern "C" int gist_pages_free(const int32_t* cached_len, const int32_t* block_table,
                                int32_t* ref_count, int32_t* free_blocks, int32_t* free_range,
                                const gist_paged_dims* dims, cudaStream_t stream) {
-  const int rc = gattn::check_pages(dims);
+  const int rc = gattn::check_tables(dims);
   if (rc != GIST_ATTN_OK) return rc;
   if ((dims->num_requests > 0 && (!cached_len || !block_table)) || !ref_count || !free_blocks || !free_range)
     return GIST_ATTN_ERR_NULL;
@@ -299,7 +305,7 @@ extern "C" int gist_pages_compact(const int32_t* cached_len, const int32_t* bloc
                                   int32_t* copy_dst, int32_t* num_copies, int32_t* free_blocks,
                                   int32_t* free_range, const gist_paged_dims* dims,
                                   cudaStream_t stream) {
-  const int rc = gattn::check_pages(dims);
+  const int rc = gattn::check_tables(dims);
   if (rc != GIST_ATTN_OK) return rc;
   if ((dims->num_requests > 0 && (!cached_len || !block_table || !block_table_out)) || !new_id ||
       (dims->num_blocks > 1 && (!copy_src || !copy_dst)) || !num_copies || !free_blocks || !free_range)

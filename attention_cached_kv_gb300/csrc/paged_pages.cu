@@ -49,20 +49,21 @@ __device__ __forceinline__ int blocks_of(int len, int block_len, int W, bool& ba
 // are in flight together.
 constexpr int kAtOnce = 4;
 template <class Visit>
-__device__ __forceinline__ void each_segment(const PagesArgs& a, int warp, int warps, bool& bad, Visit visit) {
+__device__ __forceinline__ void each_segment(const PagesArgs& a, unsigned warp, unsigned warps, bool& bad, Visit visit) {
   const int lane = threadIdx.x & 31;
-  const int per_row = (a.W + kSeg - 1) / kSeg;
-  const int64_t units = (int64_t)a.B * per_row;
-  const int64_t u0 = units * warp / warps, u1 = units * (warp + 1) / warps;
-  for (int64_t base = u0; base < u1; base += 32) {
-    const int64_t mine = base + lane;  // each lane reads the length of one of 32 units
+  // (counted in 31 bits; each warp does these divisions, so they are not of 64 bits)
+  const unsigned per_row = ((unsigned)a.W + kSeg - 1) / kSeg, units = (unsigned)a.B * per_row;
+  const unsigned share = (units + warps - 1) / warps;
+  const unsigned u0 = min(warp * share, units), u1 = min(u0 + share, units);
+  for (unsigned base = u0; base < u1; base += 32) {
+    const unsigned mine = base + lane;  // each lane reads the length of one of 32 units
     int row = 0, seg = 0, n = -1;
     if (mine < u1) {
-      row = (int)(mine / per_row);
-      seg = (int)(mine - (int64_t)row * per_row);
+      row = (int)(per_row == 1 ? mine : mine / per_row);
+      seg = (int)(mine - row * per_row);
       n = blocks_of(a.cached_len[row], a.block_len, a.W, bad);
     }
-    const int m = (int)min((int64_t)32, u1 - base);
+    const int m = (int)min(32u, u1 - base);
     for (int i = 0; i < m; i += kAtOnce) {
       int r[kAtOnce], j0[kAtOnce], live[kAtOnce];
 #pragma unroll
@@ -102,8 +103,9 @@ struct Slice {
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
+        if (b + 32 * k >= b1) break;
         if (READ && lane == (((b - b0) / 32 + k) & 31)) kept = m[k];
-        if (b + 32 * k < b1) visit(b + 32 * k, m[k]);
+        visit(b + 32 * k, m[k]);
       }
     }
   }
@@ -188,7 +190,7 @@ __global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kThreads) tables_
   const int per = ((a.num_blocks + CTAS * kWarps - 1) / (CTAS * kWarps) + 31) & ~31;
   Slice s;
   s.ids = a.ids;
-  s.b0 = (int)min((int64_t)gw * per, (int64_t)a.num_blocks);
+  s.b0 = min(gw * per, a.num_blocks);  // 2^30 ids at most, so this is below 2^31
   s.b1 = min(s.b0 + per, a.num_blocks);
   s.kept = 0;
   int used = 0;
@@ -398,6 +400,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     const uint4* from = a.pool + (int64_t)s * whole;
     uint4* to = a.pool + (int64_t)d * whole;
     const int run = rows * row, pieces = run * a.planes;  // of the planes' parts that are copied
+    const unsigned inverse = run > 1 ? 0xffffffffu / (unsigned)run : 0;  // x / run is umulhi(x, inverse) or one more
     if (a.scale && first == 0)
       for (int k = threadIdx.x; k < a.planes; k += kCopyThreads)
         a.scale[(int64_t)d * a.planes + k] = a.scale[(int64_t)s * a.planes + k];
@@ -408,8 +411,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       const int x = first + k * kCopyThreads + threadIdx.x;
       off[k] = x < pieces ? x : -1;
       if (rows != a.block_len && x < pieces) {
-        const int pl = x / run;
-        off[k] = pl * a.plane + (x - pl * run);
+        int pl = (int)__umulhi((unsigned)x, inverse), rest = x - pl * run;
+        while (rest >= run) {
+          ++pl;
+          rest -= run;
+        }
+        off[k] = pl * a.plane + rest;
       }
       if (off[k] >= 0) v[k] = __ldcs(from + off[k]);
     }

@@ -584,7 +584,7 @@ int gist_attn_paged_decode(const void* q, const void* kv_pool, const int32_t* bl
  * overlap an input or another output except where said.  These calls read
  * num_requests, block_len, max_blocks, num_blocks and status of dims (gist_pages_copy:
  * num_blocks, num_layers, num_kv_heads, block_len, head_dim and status).  num_blocks is at
- * most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).
+ * most 2^30, and so is B times W / 128 + 1 (GIST_ATTN_ERR_UNSUPPORTED).
  *
  * gist_pages_free -- who holds what, and the free list, from the tables alone:
  *   cached_len  int32 [B], block_table int32 [B][W], read only

@@ -91,6 +91,8 @@ def test_pages_refuse_null_and_unaligned(lib, which, name):
 @pytest.mark.parametrize("which,kw,code", [(w, dict(d=None), NULL) for w in PAGES] + [
     (w, dict(d=dict(BASE, **bad)), DIMS) for w in PAGES for bad in (dict(num_blocks=0), dict(block_len=0), dict(max_blocks=0))] + [
     (w, dict(d=dict(BASE, block_len=1, num_blocks=(1 << 30) + 1)), UNSUPPORTED) for w in PAGES] + [
+    ("free", dict(d=dict(BASE, num_requests=1 << 24, max_blocks=1 << 13)), UNSUPPORTED),
+    ("compact", dict(d=dict(BASE, num_requests=(1 << 30) + 1, max_blocks=1)), UNSUPPORTED),
     ("fork", dict(num_free=-1), DIMS), ("fork", dict(d=dict(BASE, num_requests=16385)), UNSUPPORTED),
     ("fork", dict(cached_len_out=P16), DIMS), ("fork", dict(free_range_out=P16 + 256 * 5), DIMS),
     ("copy", dict(elem_bytes=4), DIMS), ("copy", dict(max_copies=-1), DIMS), ("copy", dict(d=dict(BASE, head_dim=32)), UNSUPPORTED),
