@@ -534,16 +534,19 @@ def _index(t, name):
     """The CUDA device number of tensor `t`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def _sized(t, dtype, name, numel, dev):
     """Raw pointer of a contiguous tensor on CUDA device `dev` with at least `numel` elements."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor: said below
+        pass
     _check(t, dtype, name)
     if t.get_device() != dev:
         raise TypeError(f"{name} must be on cuda:{dev}, got {t.device}")
@@ -559,7 +562,7 @@ def _pool_ptr(pool, dims, dev):
 
 def _call(dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current, on `stream` or the device's current one."""
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, fn, *args)
     rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
@@ -748,15 +751,15 @@ def gist_pages_copy(kv_pool, kv_scale, copy_src, copy_dst, copy_rows=None, num_c
     lib = load_library()
     dev, i32 = _index(kv_pool, "kv_pool"), torch.int32
     _index(copy_src, "copy_src")
-    n = copy_src.numel()
-    if kv_pool.dtype not in _POOL_BYTES:
+    n, elem_bytes = copy_src.numel(), _POOL_BYTES.get(kv_pool.dtype)
+    if elem_bytes is None:
         raise TypeError(f"kv_pool must be bfloat16, float8_e4m3fn or uint8, got {kv_pool.dtype}")
     planes = dims["num_blocks"] * dims["num_layers"] * 2 * dims["num_kv_heads"]
     D = make_paged_dims(dims, status)
     _call(dev, stream, lib.gist_pages_copy,
           _sized(kv_pool, kv_pool.dtype, "kv_pool", planes * dims["block_len"] * dims["head_dim"], dev),
           None if kv_scale is None else _sized(kv_scale, torch.float32, "kv_scale", planes, dev),
-          _POOL_BYTES[kv_pool.dtype], _sized(copy_src, i32, "copy_src", n, dev), _sized(copy_dst, i32, "copy_dst", n, dev),
+          elem_bytes, _sized(copy_src, i32, "copy_src", n, dev), _sized(copy_dst, i32, "copy_dst", n, dev),
           None if copy_rows is None else _sized(copy_rows, i32, "copy_rows", n, dev),
           None if num_copies is None else _sized(num_copies, i32, "num_copies", 1, dev), n, ctypes.byref(D))
     return kv_pool
