@@ -35,7 +35,7 @@ TOKENS = [1, 2, 7, 8, 9, 16, 17, 32, 33, 64, 65, 130]
 
 
 @pytest.mark.parametrize("T", TOKENS)
-@pytest.mark.parametrize("Hq,Hkv,d,K,group", [(14, 2, 64, 896, 32), (4, 1, 128, 96, 32), (8, 8, 128, 1088, 64), (2, 1, 64, 4096, 128)])
+@pytest.mark.parametrize("Hq,Hkv,d,K,group", [(14, 2, 64, 896, 32), (1, 1, 64, 32, 32), (4, 1, 128, 96, 32), (8, 8, 128, 1088, 64), (2, 1, 64, 4096, 128)])
 def test_qkv(T, Hq, Hkv, d, K, group):
     N = (Hq + 2 * Hkv) * d
     w = su.W4(N, K, group, seed=T)
