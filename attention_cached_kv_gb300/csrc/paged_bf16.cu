@@ -204,6 +204,10 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
   };
   const uint32_t ring = smem_u32(smem) + warp * Ring<D>::warp;
   const int c16 = lane % PIECES, r16 = lane / PIECES;
+  constexpr int kSpots = 8 / (32 / PIECES);  // copies after which the swizzle repeats: eight rows
+  uint32_t spot[kSpots];
+#pragma unroll
+  for (int i = 0; i < kSpots; ++i) spot[i] = swz<D>(r16 + i * (32 / PIECES), c16);
   auto issue = [&](int x) {
     if (x < w1) {
       if (x > w0 && (x - w0) % 32 == 0) resolve(x);
@@ -211,14 +215,24 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
       const int keys = t.at < 0 ? 0 : (int)(t.info & 31);
       const uint32_t st = ring + (x - w0) % S * Ring<D>::stage;
       const bf16* k = p.pool + (t.at < 0 ? 0 : t.at) + c16 * 8;
+      if (keys == kKeys) {  // nearly all of them: addresses but for constants
+        const bf16* from = k + r16 * D;
 #pragma unroll
-      for (int i = 0; i < kKeys * PIECES / 32; ++i) {
-        const int r = r16 + i * (32 / PIECES);
-        const int bytes = r < keys ? 16 : 0;  // rows that nothing sees are zeros
-        const bf16* from = k + (r < keys ? r * D : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + swz<D>(r, c16)), "l"(from), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + Ring<D>::tile + swz<D>(r, c16)), "l"(from + v_off), "r"(bytes)
-                     : "memory");
+        for (int i = 0; i < kKeys * PIECES / 32; ++i) {
+          const uint32_t to = st + spot[i % kSpots] + i / kSpots * (kSpots * (32 / PIECES) * 2 * D);
+          cp_async16(to, from + i * (32 / PIECES) * D);
+          cp_async16(to + Ring<D>::tile, from + i * (32 / PIECES) * D + v_off);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kKeys * PIECES / 32; ++i) {
+          const int r = r16 + i * (32 / PIECES);
+          const int bytes = r < keys ? 16 : 0;  // rows that nothing sees are zeros
+          const bf16* from = k + (r < keys ? r * D : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + swz<D>(r, c16)), "l"(from), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + Ring<D>::tile + swz<D>(r, c16)), "l"(from + v_off), "r"(bytes)
+                       : "memory");
+        }
       }
     }
     cp_async_commit();
