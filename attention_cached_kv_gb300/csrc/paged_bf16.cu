@@ -20,12 +20,14 @@
 // and 4-7 for lo of one MMA, more take two MMAs.  The maximum moves only where a score
 // is more than 8 (log2) above it, so that a tile needs one vote in place of a reduction.
 //
-// Eight warps an SM with 128 KB and more on their way are enough: 12 and 16 warps gave the
-// same times, 6 are 8 % slower.
+// Warps an SM: twelve with rings of two tiles of 128-wide heads (192 KB) take 2 % less than
+// eight with three (123.7 and 121.1 us at the 48 requests below; 11: 121.3, 10: 121.9, six: 8 %
+// more), but leave 168 registers a thread, which sixteen heads (255) do not fit.  Heads of 64
+// keep eight with six tiles: twelve cost six short conversations 0.7 us and gain nothing.
 //
 // Bound: HBM (every K/V byte is read once; at most 32 flops a byte).  48 requests of
-// 200-9000 keys, 32/8 heads of 128 (757 MB): 125 us, 0.89 of the copy rate; 32/32 heads
-// 0.91.  What is left there: SMs are not equally near to memory, with equal runs
+// 200-9000 keys, 32/8 heads of 128 (757 MB): 121 us, 0.92 of the copy rate; 32/32 heads
+// 0.94.  What is left there: SMs are not equally near to memory, with equal runs
 // some take 1.13 times the mean.  One sequence of 180 k keys, 14/2 heads of 64 (92 MB):
 // 25 us, 4.5 of them before the first keys and 5.6 in the two joins.  Six short
 // conversations: 9.8 us.
@@ -96,10 +98,11 @@ struct __align__(16) Tile {
 };
 constexpr uint32_t kFirst = 32, kLast = 64;
 
-template <int D>
+template <int D, int MODE>
 struct Ring {
-  static constexpr int warps = 8, threads = warps * 32;
-  static constexpr int stages = D == 128 ? 3 : 6;
+  static constexpr bool many = D == 128 && MODE < 2;
+  static constexpr int warps = many ? 12 : 8, threads = warps * 32;
+  static constexpr int stages = many ? 2 : D == 128 ? 3 : 6;
   static constexpr uint32_t tile = kKeys * D * 2, stage = 2 * tile;
   static constexpr uint32_t warp = stages * stage;
   static constexpr uint32_t windows = warps * warp;
@@ -131,9 +134,10 @@ __device__ __forceinline__ float weight(float m, float top) { return m == top ? 
 
 // MODE 0: up to four heads, hi and lo side by side; 1: up to eight; 2: up to sixteen.
 template <int D, int MODE>
-__global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
+__global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
   constexpr int H = MODE == 0 ? 4 : MODE == 1 ? 8 : 16, NT = MODE == 2 ? 2 : 1, KS = D / 16, HK = KS / 2;
-  constexpr int kWarps = Ring<D>::warps, kThreads = Ring<D>::threads, S = Ring<D>::stages, PIECES = D / 8;  // 16-byte pieces of a row
+  using R = Ring<D, MODE>;
+  constexpr int kWarps = R::warps, kThreads = R::threads, S = R::stages, PIECES = D / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sum[kWarps], start_r, start_pre, total;
   __shared__ int4 piece[2 * kWarps];  // the warps' open parts: request, unit, whether it begins and ends there
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
   const int w0 = min(lo + warp * share, hi), w1 = min(w0 + share, hi);
 
   // ---- the run's tiles resolved, 32 at a time, a lane a tile
-  Tile* window = reinterpret_cast<Tile*>(smem + Ring<D>::windows) + warp * kWindow;
+  Tile* window = reinterpret_cast<Tile*>(smem + R::windows) + warp * kWindow;
   const int per_block = p.block_len / kKeys;
   const int64_t plane = (int64_t)p.block_len * D, v_off = p.Hkv * plane;
   int walk_r = start_r, walk_pre = start_pre;  // first tile of request walk_r
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
     walk_pre = __shfl_sync(0xffffffffu, walk_pre, last);
     __syncwarp();
   };
-  const uint32_t ring = smem_u32(smem) + warp * Ring<D>::warp;
+  const uint32_t ring = smem_u32(smem) + warp * R::warp;
   const int c16 = lane % PIECES, r16 = lane / PIECES;
   constexpr int kSpots = 8 / (32 / PIECES);  // copies after which the swizzle repeats: eight rows
   uint32_t spot[kSpots];
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
       if (x > w0 && (x - w0) % 32 == 0) resolve(x);
       const Tile t = window[(x - w0) % kWindow];
       const int keys = t.at < 0 ? 0 : (int)(t.info & 31);
-      const uint32_t st = ring + (x - w0) % S * Ring<D>::stage;
+      const uint32_t st = ring + (x - w0) % S * R::stage;
       const bf16* k = p.pool + (t.at < 0 ? 0 : t.at) + c16 * 8;
       if (keys == kKeys) {  // nearly all of them: addresses but for constants
         const bf16* from = k + r16 * D;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
         for (int i = 0; i < kKeys * PIECES / 32; ++i) {
           const uint32_t to = st + spot[i % kSpots] + i / kSpots * (kSpots * (32 / PIECES) * 2 * D);
           cp_async16(to, from + i * (32 / PIECES) * D);
-          cp_async16(to + Ring<D>::tile, from + i * (32 / PIECES) * D + v_off);
+          cp_async16(to + R::tile, from + i * (32 / PIECES) * D + v_off);
         }
       } else {
 #pragma unroll 1
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
           const int bytes = r < keys ? 16 : 0;  // rows that nothing sees are zeros
           const bf16* from = k + (r < keys ? r * D : 0);
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + swz<D>(r, c16)), "l"(from), "r"(bytes) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + Ring<D>::tile + swz<D>(r, c16)), "l"(from + v_off), "r"(bytes)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(st + R::tile + swz<D>(r, c16)), "l"(from + v_off), "r"(bytes)
                        : "memory");
         }
       }
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
   // ---- the tiles
   constexpr int P = kPart<D, H>;
   float* kept = p.kept + ((int64_t)blockIdx.x * kWarps + warp) * P;
-  float* left = reinterpret_cast<float*>(smem + warp * Ring<D>::warp);  // once the ring is done with
+  float* left = reinterpret_cast<float*>(smem + warp * R::warp);  // once the ring is done with
   bool wrong = false, begins = false;  // the unit met a bad block id; its first tile is in this run
   if (lane < 2) piece[2 * warp + lane] = make_int4(-1, -1, 0, 0);
   __syncwarp();
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
     if (x + 1 < w1 && (window[(x + 1 - w0) % kWindow].info & kFirst)) fetch_q(window[(x + 1 - w0) % kWindow]);
     wrong |= t.at < 0;
     const int keys = t.info & 31;
-    const uint32_t st = ring + (x - w0) % S * Ring<D>::stage;
+    const uint32_t st = ring + (x - w0) % S * R::stage;
     float s[NT][4], s2[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
     for (int d = 0; d < KS; ++d) {
       uint32_t a[4];
       // matrices: (keys 0-7, dims 0-7), (keys 0-7, dims 8-15), (keys 8-15, dims 0-7), (8-15, 8-15)
-      ldsm_x4_trans(st + Ring<D>::tile + swz<D>((lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)), a);
+      ldsm_x4_trans(st + R::tile + swz<D>((lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)), a);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mma_16816(o[d][n], a, ph[n][0], ph[n][1]);
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(Ring<D>::threads, 1) decode_kernel(const __gri
   constexpr int kParts = 2 * kWarps;
   static_assert(kParts <= 32, "a lane a part");
   auto part = [&](int j) -> const float* {
-    return j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * Ring<D>::warp) : p.kept + ((int64_t)blockIdx.x * kWarps + (j >> 1)) * P;
+    return j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * R::warp) : p.kept + ((int64_t)blockIdx.x * kWarps + (j >> 1)) * P;
   };
   {
     const int4 id = lane < kParts ? piece[lane] : make_int4(-1, -1, 0, 0);
@@ -686,14 +690,14 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   p.num_blocks = pb.num_blocks;
   p.L = pb.L;
   p.layer = pb.layer;
-  p.least = Ring<D>::warps;
+  p.least = Ring<D, MODE>::warps;
   p.ctas = ctas;
   p.scale_log2 = pb.scale_log2;
   for (int j = 0; j < 64; ++j) p.turn[j] = pb.turn[j];
-  constexpr int smem = Ring<D>::bytes;
+  constexpr int smem = Ring<D, MODE>::bytes;
   if (cudaFuncSetAttribute(decode_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  if (!launch_following(decode_kernel<D, MODE>, dim3(ctas), dim3(Ring<D>::threads), smem, stream, 0, p)) return GIST_ATTN_ERR_LAUNCH;
+  if (!launch_following(decode_kernel<D, MODE>, dim3(ctas), dim3(Ring<D, MODE>::threads), smem, stream, 0, p)) return GIST_ATTN_ERR_LAUNCH;
   // where units are few each has many parts: a block for two of its heads
   const bool few = (int64_t)pb.B * pb.Hkv * p.chunks * 4 < ctas;
   const dim3 grid = few ? dim3(pb.B * pb.Hkv * p.chunks, H / 2) : dim3(ctas);
@@ -705,8 +709,8 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
 }  // namespace
 
 size_t paged_bf16_workspace(const PagedProblem& pb, int sms) {
-  static_assert(Ring<64>::warps == Ring<128>::warps, "parts");
-  return (size_t)sms * (sizeof(int4) + (2 + Ring<128>::warps) * part_bytes(pb));
+  const int warps = pb.d == 64 ? Ring<64, 0>::warps : pb.G <= 8 ? Ring<128, 0>::warps : Ring<128, 2>::warps;
+  return (size_t)sms * (sizeof(int4) + (2 + warps) * part_bytes(pb));
 }
 
 int launch_paged_bf16(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
