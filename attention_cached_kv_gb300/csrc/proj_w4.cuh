@@ -41,17 +41,15 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t c) {
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(c), "r"(0x000f000fu), "r"(0x43004300u));  // (c & mask) | 128.0
   return less136(v);
 }
-// The eight codes of a word less 8, as bf16 pairs in their order.  Half of the work is left
-// to the FMA pipe, which is twice as wide as the one for shifts, masks and permutes.
+// The eight codes of a word less 8, over 64, as bf16 pairs in their order: ten instructions.
+// Up to its lowest exponent a bf16 is a count of 2^-133, so that a code in bits 0-3 is c 2^-133
+// and one in bits 4-7 is c 2^-129; one fma takes both, times 2^127 and 2^123, to (c - 8) / 64, exactly.
 __device__ __forceinline__ void word_to_bf16(uint32_t u, uint32_t* a) {
-  const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;  // a code a byte
-  constexpr uint32_t sel[4] = {0x8480, 0x8581, 0x8682, 0x8783};         // byte j of both, zeros (their signs) between
+  const uint32_t even = u & 0x0f0f0f0fu, odd = u & 0xf0f0f0f0u;
+  constexpr uint32_t sel[4] = {0x8480, 0x9591, 0xa6a2, 0xb7b3};  // byte j of both, zeros (the signs of even's) between
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t v;
-    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(v) : "r"(permute(even, odd, sel[j])), "r"(1u), "r"(0x43004300u));
-    a[j] = less136(v);
-  }
+  for (int j = 0; j < 4; ++j)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[j]) : "r"(permute(even, odd, sel[j])), "r"(0x7d007f00u), "r"(0xbe00be00u));
 }
 
 // Where row n of the QKV projection goes for token t (heads of d = 1 << shift).

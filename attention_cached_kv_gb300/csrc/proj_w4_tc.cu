@@ -34,12 +34,12 @@ namespace {
 
 constexpr int kRows = 128, kPairs = 64, kThreads = 320, kMma = 8;  // kMma: the warp that issues MMAs
 constexpr int kChunk = 128;          // inputs of a stage of codes: 64 bytes a row
-constexpr int kRaw = 5;              // stages of a warp's ring of codes, 2 KB each
+constexpr int kRaw = 5;              // stages of codes, 8 KB each
 constexpr int kSA = 2, kSB = 3;      // stages of converted weights in TMEM, of x in shared memory
 constexpr int kCols = 256;           // TMEM columns: kSA x 64, then two accumulators
 
 struct Bars {
-  uint64_t a_full[kSA], a_empty[kSA], b_full[kSB], b_empty[kSB], d_full[2], d_empty[2], sums;
+  uint64_t a_full[kSA], a_empty[kSA], b_full[kSB], b_empty[kSB], c_full[kRaw], c_empty[kRaw], d_full[2], d_empty[2], sums;
   uint32_t tmem;
 };
 
@@ -47,7 +47,7 @@ template <int TN>
 struct Layout {
   static constexpr uint32_t tile_b = 2 * TN * 128;  // two tiles of 64 inputs
   static constexpr uint32_t raw = kSB * tile_b;
-  static constexpr uint32_t bars = raw + 4 * kRaw * 2048;
+  static constexpr uint32_t bars = raw + kRaw * (kRows * 64);
   static constexpr uint32_t bytes = bars + 256 + 1024;  // + alignment
   // over the rings: this CTA's sums [pair][2][TN], then the parts of the pairs that it adds up
   static constexpr uint32_t sums = kRows * TN * 4;
@@ -74,6 +74,9 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // an
       : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // One lane of a warp that has converged.  Under elect.sync the compiler keeps the operands of
 // tcgen05.mma in uniform registers; behind `lane == 0` it moves them there for each MMA, which
 // takes 47 cycles an MMA in place of the 16 (32 tokens) or 32 (64) that the tensor core needs.
@@ -86,7 +89,8 @@ __device__ __forceinline__ bool elected() {
 // TN tokens, groups of 16 PG inputs (PG MMAs).
 template <int TN, int PG>
 __global__ void __launch_bounds__(kThreads, 2)
-    w4_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ W4Params p) {
+    w4_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                 const __grid_constant__ W4Params p) {
   using L = Layout<TN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -101,39 +105,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   let_follow();
   wait_before();
-  // ---- warps 0-3: the first codes are asked for before anything else
-  const uint32_t ring = base + L::raw + (warp & 3) * (kRaw * 2048);
-  const int c4 = lane & 3, most = k1 - k0 - c4 * 32;  // this lane's 32 inputs of chunk i exist where i kChunk < most
-  const uint8_t* src[4];
-  uint32_t to[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = j * 8 + (lane >> 2);
-    src[j] = p.w + (int64_t)min(n0 + (warp & 3) * 32 + r, p.N - 1) * (p.K / 2) + (k0 + c4 * 32) / 2;  // rows past N are not written
-    to[j] = ring + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4);
-  }
-  int slot = 0;
-  auto issue = [&](int i) {
-    if (i < chunks) {
-      const bool in = i * kChunk < most;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        cp_async16_or_zero(to[j] + slot * 2048, in ? src[j] : p.w, in);
-        src[j] += kChunk / 2;
-      }
-    }
-    slot = slot == kRaw - 1 ? 0 : slot + 1;
-    cp_async_commit();
+  // ---- the loading warp asks for the first stages before anything else
+  auto load_codes = [&](int i) {  // inputs past K and rows past N are zeros (and counted)
+    const int s = i % kRaw;
+    mbar_arrive_expect_tx(&bars.c_full[s], kRows * 64);
+    tma_load_2d(base + L::raw + s * (kRows * 64), &tm_w, &bars.c_full[s], (k0 + i * kChunk) / 2, n0);
   };
-  if (warp < 4)
-    for (int i = 0; i < kRaw - 1; ++i) issue(i);
+  auto load_x = [&](int i) {  // inputs past K and tokens past T likewise
+    const int s = i % kSB;
+    mbar_arrive_expect_tx(&bars.b_full[s], L::tile_b);
+    tma_load_2d(base + s * L::tile_b, &tm_x, &bars.b_full[s], k0 + i * kChunk, t0);
+    tma_load_2d(base + s * L::tile_b + TN * 128, &tm_x, &bars.b_full[s], k0 + i * kChunk + 64, t0);
+  };
+  if (warp > kMma && elected()) {
+    for (int s = 0; s < kRaw; ++s) mbar_init(&bars.c_full[s], 1), mbar_init(&bars.c_empty[s], 4);
+    for (int s = 0; s < kSB; ++s) mbar_init(&bars.b_full[s], 1), mbar_init(&bars.b_empty[s], 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    for (int i = 0; i < min(chunks, kRaw); ++i) load_codes(i);
+    for (int i = 0; i < min(chunks, kSB); ++i) load_x(i);
+  }
   if (warp == kMma) {
     tc::tmem_alloc(smem_u32(&bars.tmem), kCols);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
     for (int s = 0; s < kSA; ++s) mbar_init(&bars.a_full[s], 4), mbar_init(&bars.a_empty[s], 1);
-    for (int s = 0; s < kSB; ++s) mbar_init(&bars.b_full[s], 1), mbar_init(&bars.b_empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bars.d_full[s], 1), mbar_init(&bars.d_empty[s], 4);
     mbar_init(&bars.sums, 1);
     fence_mbar_init();
@@ -152,34 +149,33 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp < 4) {
     // ---------------------------------------------------------- codes to bf16
-    int at = 0;
+    const uint32_t row = base + L::raw + tid * 64, swap = (lane >> 1 & 3) << 4;
     for (int i = 0; i < chunks && !failed; ++i) {
-      cp_async_wait_group<kRaw - 2>();
-      __syncwarp();
-      const uint32_t from = ring + at * 2048 + lane * 64;
-      at = at == kRaw - 1 ? 0 : at + 1;
-      const int s = i % kSA;
+      const int at = i % kRaw, s = i % kSA;
+      if (!wait(&bars.c_full[at], i / kRaw)) break;
+      uint32_t u[16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = lds16(row + at * (kRows * 64) + ((c << 4) ^ swap));
+        u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+      }
       if (i >= kSA && !wait(&bars.a_empty[s], i / kSA - 1)) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t u[8], a[32];
+        uint32_t a[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 v = lds16(from + (((2 * h + c) ^ ((lane >> 1) & 3)) << 4));
-          u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) word_to_bf16(u[j], a + 4 * j);
+        for (int j = 0; j < 8; ++j) word_to_bf16(u[8 * h + j], a + 4 * j);
         st32(tmem + lanes + s * 64 + h * 32, a);
       }
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.a_full[s]);
-      issue(i + kRaw - 1);
+      if (lane == 0) {
+        mbar_arrive(&bars.a_full[s]);
+        mbar_arrive(&bars.c_empty[at]);
+      }
     }
-    cp_async_wait_all();
   } else if (warp < kMma) {
     // ------------------------------------------------- the groups' sums, scaled and added
 #pragma unroll
@@ -246,22 +242,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------------- x
+    // ------------------------------------------------------- codes and x, further stages
     if (elected()) {
-      tma_prefetch_map(&tm_x);
-      for (int i = 0; i < chunks && !failed; ++i) {
-        const int s = i % kSB;
-        if (i >= kSB && !mbar_wait(&bars.b_empty[s], (i / kSB - 1) & 1)) {
-          failed = true;
-          break;
+      int xs = min(chunks, kSB), cs = min(chunks, kRaw);  // asked for so far
+      while (cs < chunks || xs < chunks) {
+        if (xs < chunks) {
+          if (!mbar_wait(&bars.b_empty[xs % kSB], (xs / kSB - 1) & 1)) break;
+          load_x(xs++);
         }
-        mbar_arrive_expect_tx(&bars.b_full[s], L::tile_b);
-        // inputs past K and tokens past T are zeros (and counted)
-        tma_load_2d(base + s * L::tile_b, &tm_x, &bars.b_full[s], k0 + i * kChunk, t0);
-        tma_load_2d(base + s * L::tile_b + TN * 128, &tm_x, &bars.b_full[s], k0 + i * kChunk + 64, t0);
+        if (cs < chunks) {
+          if (!mbar_wait(&bars.c_empty[cs % kRaw], (cs / kRaw - 1) & 1)) break;
+          load_codes(cs++);
+        }
       }
+      failed = xs < chunks || cs < chunks;
       // none of the copies is left in flight
-      for (int i = max(chunks - kSB, 0); i < chunks && !failed; ++i) failed = !mbar_wait(&bars.b_full[i % kSB], i / kSB & 1);
+      for (int i = max(xs - kSB, 0); i < xs; ++i) failed |= !mbar_wait(&bars.b_full[i % kSB], i / kSB & 1);
+      for (int i = max(cs - kRaw, 0); i < cs; ++i) failed |= !mbar_wait(&bars.c_full[i % kRaw], i / kRaw & 1);
     }
     __syncwarp();
   }
@@ -271,12 +268,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   // each other; 16-byte chunk c of a row of sums at c ^ (pair mod 8)
   tc::fence_before_sync();
   __syncthreads();  // the rings are done with
+  const int half = p.position ? p.shift - 1 : 6;  // rows of a pair are 1 << half apart
+  const int own = kPairs / split, q0 = part * own;  // the pairs that this CTA adds up
+  const int bytes = own * 2 * TN * 4;
+  if (tid == 0) mbar_arrive_expect_tx(&bars.sums, split * bytes);
+  __syncwarp();
+  cluster_arrive();
   if (warp == kMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kCols);
   }
-  const int half = p.position ? p.shift - 1 : 6;  // rows of a pair are 1 << half apart
-  const int own = kPairs / split, q0 = part * own;  // the pairs that this CTA adds up
   if (warp >= 4 && warp < kMma) {
     const int r = (warp & 3) * 32 + lane, pair = r >> (half + 1) << half | (r & ((1 << half) - 1)), which = r >> half & 1;
     const uint32_t row = base + (2 * pair + which) * (TN * 4);
@@ -286,9 +287,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                       __float_as_uint(acc[4 * c + 2]), __float_as_uint(acc[4 * c + 3])));
     fence_proxy_async_smem();
   }
-  const int bytes = own * 2 * TN * 4;
-  if (tid == 0) mbar_arrive_expect_tx(&bars.sums, split * bytes);
-  cluster.sync();
+  __syncthreads();
+  cluster_wait();  // the others' rings are done with too
   if (tid < split) {
     uint32_t dst, bar;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(base + L::sums + part * bytes), "r"(tid));
@@ -297,7 +297,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                  "r"(base + tid * bytes), "r"(bytes), "r"(bar)
                  : "memory");
   }
-  if (!mbar_wait(&bars.sums, 0)) {
+  const bool arrived = mbar_wait(&bars.sums, 0);
+  __syncwarp();
+  cluster_arrive();
+  if (!arrived) {
     if (lane == 0) report(p.status, GIST_ATTN_STATUS_TIMEOUT);
   } else {
     const int tokens = min(TN, p.T - t0);
@@ -314,21 +317,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (c * 4 + e < tokens) finish_pair(p, t0 + c * 4 + e, n, 1 << half, a[e], b[e]);
+        if (c * 4 + e < tokens) finish_pair(p, t0 + c * 4 + e, n, 1 << half, 64.f * a[e], 64.f * b[e]);
     }
   }
-  cluster.sync();  // no CTA leaves while its sums are being sent
+  __syncwarp();
+  cluster_wait();  // no CTA leaves while its sums are being sent
 }
 
 template <int TN, int PG>
 int launch_as(W4Params p, int sms, cudaStream_t stream) {
   const EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return GIST_ATTN_ERR_LAUNCH;
-  alignas(64) CUtensorMap tm;
-  const cuuint64_t dims[2] = {(cuuint64_t)p.K, (cuuint64_t)p.T}, strides[1] = {(cuuint64_t)p.K * 2};
-  const cuuint32_t box[2] = {64, TN}, estr[2] = {1, 1};
-  if (enc(&tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(p.x), dims, strides, box, estr,
+  alignas(64) CUtensorMap tm_x, tm_w;
+  const cuuint32_t each[2] = {1, 1};
+  const cuuint64_t dims_x[2] = {(cuuint64_t)p.K, (cuuint64_t)p.T}, stride_x[1] = {(cuuint64_t)p.K * 2};
+  const cuuint64_t dims_w[2] = {(cuuint64_t)p.K / 2, (cuuint64_t)p.N}, stride_w[1] = {(cuuint64_t)p.K / 2};
+  const cuuint32_t box_x[2] = {64, TN}, box_w[2] = {kChunk / 2, kRows};
+  if (enc(&tm_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(p.x), dims_x, stride_x, box_x, each,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      enc(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.w), dims_w, stride_w, box_w, each,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return GIST_ATTN_ERR_UNSUPPORTED;
   const int tiles = (p.N + kRows - 1) / kRows, token_blocks = (p.T + TN - 1) / TN, chunks = (p.K + kChunk - 1) / kChunk;
@@ -340,7 +349,7 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
   if (token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(w4_tc_kernel<TN, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  return launch_following(w4_tc_kernel<TN, PG>, dim3(tiles * split, token_blocks), dim3(kThreads), smem, stream, split, tm, p)
+  return launch_following(w4_tc_kernel<TN, PG>, dim3(tiles * split, token_blocks), dim3(kThreads), smem, stream, split, tm_x, tm_w, p)
              ? GIST_ATTN_OK
              : GIST_ATTN_ERR_LAUNCH;
 }
