@@ -74,6 +74,11 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // an
       : "memory");
 }
 
+__device__ __forceinline__ uint32_t load_scale(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -122,8 +127,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = 0; s < kSB; ++s) mbar_init(&bars.b_full[s], 1), mbar_init(&bars.b_empty[s], 1);
     fence_mbar_init();
     fence_proxy_async_smem();
-    for (int i = 0; i < min(chunks, kRaw); ++i) load_codes(i);
-    for (int i = 0; i < min(chunks, kSB); ++i) load_x(i);
+    for (int i = 0; i < min(chunks, max(kRaw, kSB)); ++i) {
+      if (i < kRaw) load_codes(i);
+      if (i < kSB) load_x(i);
+    }
   }
   if (warp == kMma) {
     tc::tmem_alloc(smem_u32(&bars.tmem), kCols);
@@ -183,16 +190,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = n0 + (warp & 3) * 32 + lane;
     const uint16_t* scale = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)min(n, p.N - 1) * (p.K / p.group) + k0 / p.group;
     constexpr int kAhead = 4;  // scales are read so many groups ahead (and converted when used)
-    uint16_t next[kAhead];
+    uint32_t next[kAhead];
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) next[g] = g < groups ? __ldg(scale + g) : 0;
+    for (int g = 0; g < kAhead; ++g) next[g] = g < groups ? load_scale(scale + g) : 0;
     for (int g0 = 0; g0 < groups && !failed; g0 += kAhead) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int g = g0 + j;
         if (g >= groups) break;
-        const float now = __uint_as_float((uint32_t)next[j] << 16);
-        next[j] = g + kAhead < groups ? __ldg(scale + g + kAhead) : 0;
+        const float now = __uint_as_float(next[j] << 16);
+        next[j] = g + kAhead < groups ? load_scale(scale + g + kAhead) : 0;
         if (!wait(&bars.d_full[g & 1], g >> 1)) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + lanes + kSA * 64 + (g & 1) * TN;
@@ -303,21 +310,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!arrived) {
     if (lane == 0) report(p.status, GIST_ATTN_STATUS_TIMEOUT);
   } else {
-    const int tokens = min(TN, p.T - t0);
-    for (int i = tid; i < own * (TN / 4); i += kThreads) {
-      const int q = i & (own - 1), c = i / own, pair = q0 + q;  // a pair of rows, four tokens
+    const int tokens = min(TN, p.T - t0), own_log2 = 31 - __clz(own);
+#pragma unroll 1  // once through straight code costs more, in misses of instructions
+    for (int i = tid; i < own * tokens; i += kThreads) {
+      const int q = i & (own - 1), t = i >> own_log2, pair = q0 + q;  // a pair of rows, a token
       const int n = n0 + (pair >> half << (half + 1) | (pair & ((1 << half) - 1)));
-      if (c * 4 >= tokens || n >= p.N) continue;
-      const uint32_t from = base + L::sums + q * 2 * (TN * 4) + ((c ^ (pair & 7)) << 4);
-      float a[4] = {}, b[4] = {};
+      if (n >= p.N) continue;
+      const float* from = reinterpret_cast<const float*>(smem + L::sums + q * 2 * (TN * 4) + (((t >> 2) ^ (pair & 7)) << 4)) + (t & 3);
+      float a = 0.f, b = 0.f;
       for (int s = 0; s < split; ++s) {
-        const uint4 x = lds16(from + s * bytes), y = lds16(from + s * bytes + TN * 4);
-        a[0] += __uint_as_float(x.x), a[1] += __uint_as_float(x.y), a[2] += __uint_as_float(x.z), a[3] += __uint_as_float(x.w);
-        b[0] += __uint_as_float(y.x), b[1] += __uint_as_float(y.y), b[2] += __uint_as_float(y.z), b[3] += __uint_as_float(y.w);
+        a += from[s * (bytes / 4)];
+        b += from[s * (bytes / 4) + TN];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c * 4 + e < tokens) finish_pair(p, t0 + c * 4 + e, n, 1 << half, 64.f * a[e], 64.f * b[e]);
+      finish_pair(p, t0 + t, n, 1 << half, 64.f * a, 64.f * b);
     }
   }
   __syncwarp();
