@@ -12,13 +12,16 @@
 //
 // A CTA has a tile of 128 rows and a part of K; the CTAs of a cluster have the parts
 // of one tile, send each other the rows that the other adds up (bulk copies between
-// their shared memories) and write those.  Warps: 0-3 convert (a thread a row: codes by
-// cp.async into a ring of the warp's own, then into TMEM), the next four for each 32
-// tokens scale and add (a thread a row), one issues MMAs, one loads x by TMA.
+// their shared memories) and write those.  Warps: 0-3 convert (a thread a row, codes
+// into TMEM), 4-7 scale and add (a thread a row), one issues MMAs, one loads codes and x by TMA.
 //
-// 64 tokens, 8192 -> 8192 (36.7 MB): 18.0 us for a floor of 5.4; 32 tokens, 4096 -> 4096: 8.4 us.
-// Bound: the conversion (15 instructions for 8 codes; 9.3 of the 18 us), the exchange (3.7 us).
-// Two CTAs an SM: one, with half as many parts of K, takes 19.8 us, three spill (34 us).
+// 64 tokens, 8192 -> 8192 (36.7 MB): 17.1 us for a floor of 5.4; 32 tokens, 4096 -> 4096: 8.0 us.
+// Bound: no one stage (a stage of 128 inputs takes 1300 cycles, two CTAs an SM; without the
+// conversion 1.0 us less, without the sums 1.7, without x 0.6, without most MMAs 0.6): one chunk
+// and the exchange take 7.4 us, the 15 further chunks 10, and 104 of 152 SMs have two CTAs.
+// Two CTAs an SM: one, with half as many parts of K, takes 19.8 us, three spill (34 us).  Twice
+// the converting and adding warps: 20.0; twice the adding ones: 17.0-17.5.  Sums stored straight
+// into the other CTAs' memory: 19.0, but 7.6 with 32 tokens.
 //
 // Pages: [Gist page] "把 item 压成 KV：gist 能不能用在相关性任务上".
 #include <cooperative_groups.h>
@@ -74,6 +77,7 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // an
       : "memory");
 }
 
+// A scale, read where it stands: the compiler may move a plain load down to its use.
 __device__ __forceinline__ uint32_t load_scale(const uint16_t* p) {
   uint16_t v;
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
