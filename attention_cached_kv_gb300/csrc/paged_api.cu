@@ -219,7 +219,9 @@ int check_decode(const gist_paged_dims* dims, PagedProblem* pb) {
   if (pb->max_new != 1) return GIST_ATTN_ERR_UNSUPPORTED;
   const double units = (double)pb->Hkv * ((pb->G + 15) / 16);  // a request's, counted in 24 bits
   const double tiles = pb->B * units * ((double)pb->W * pb->block_len / 16 + 1);
-  return units > 1 << 23 || pb->Hkv > 1 << 20 || tiles > 2147483647.0 ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
+  // tiles are counted in 31 bits, and a CTA's run (at most 2^25 of them) past the last one's begin
+  const double most = 2147483648.0 - (1 << 25);
+  return units > 1 << 23 || pb->Hkv > 1 << 20 || tiles > most ? GIST_ATTN_ERR_UNSUPPORTED : GIST_ATTN_OK;
 }
 
 // Sizes of the calls on blocks.

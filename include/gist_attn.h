@@ -559,12 +559,13 @@ int gist_attn_paged_fp8kv(const void* q, const void* kv_pool_e4m3, const float* 
  *               gist_attn_paged_decode_workspace_bytes(dims) bytes (GIST_ATTN_ERR_SCRATCH
  *               otherwise): scratch, overwritten by every call; two calls that may
  *               overlap on the GPU need one each
- * max_new must be 1, block_len a multiple of 16, Hq / Hkv at most 128, Hkv at most 2^20
- * and W * block_len at most 2^30 (GIST_ATTN_ERR_UNSUPPORTED).  A request with kv_len <= 0 gets zeros.  Cached
- * rows past kv_len may hold anything; a V of its keys that is not finite makes its column of
- * the request's row not finite.  out must not overlap what the call reads; rows of no
- * request are left as they were.  A block id outside the pool among those of the
- * request's keys, or a kv_len past W * block_len, zeroes the request's row and sets
+ * max_new must be 1, block_len a multiple of 16, Hq / Hkv at most 128, Hkv at most 2^20,
+ * W * block_len at most 2^30 and B * Hkv * (W * block_len / 16 + 1) at most 2^31 - 2^25 (times
+ * the number of 16-head parts of a group past 16 heads; GIST_ATTN_ERR_UNSUPPORTED).  A request
+ * with kv_len <= 0 gets zeros.  Cached rows past kv_len may hold anything; a V of its keys that
+ * is not finite makes its column of the request's row not finite.  out must not overlap what
+ * the call reads; rows of no request are left as they were.  A block id outside the pool
+ * among those of the request's keys, or a kv_len past W * block_len, zeroes the request's row and sets
  * GIST_ATTN_STATUS_BAD_BLOCK; a q_start pair outside [0, T], out of order or more than
  * one apart skips the request and sets it too.  GIST_ATTN_STATUS_RANGE as elsewhere.  The
  * order of all sums is fixed: the same call gives the same bits.

@@ -66,6 +66,15 @@ def test_decode_of_nothing(lib):
     assert binding.paged_decode_workspace_bytes(dict(BASE, block_len=24)) == 0
 
 
+def test_decode_refuses_more_tiles_than_it_counts(lib):
+    """B Hkv (W block_len / 16 + 1) up to 2^31 - 2^25: the last run's end is counted in 31 bits too."""
+    d = dict(BASE, max_blocks=64)  # 130 tiles a request
+    most = ((1 << 31) - (1 << 25)) // 130
+    assert decode(lib, d=dict(d, num_requests=most + 1)) == UNSUPPORTED
+    assert decode(lib, d=dict(d, num_requests=most), q=0) == NULL  # counted, and refused for another reason
+    assert binding.paged_decode_workspace_bytes(dict(d, num_requests=most + 1)) == 0
+
+
 FREE = ["cached_len", "block_table", "ref_count", "free_blocks", "free_range"]
 COMPACT = ["cached_len", "block_table", "block_table_out", "new_id", "copy_src", "copy_dst", "num_copies", "free_blocks", "free_range"]
 FORK = ["cached_len", "parent", "block_table", "free_blocks", "num_free", "free_range", "cached_len_out", "copy_src", "copy_dst",
