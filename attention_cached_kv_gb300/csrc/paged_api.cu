@@ -436,7 +436,7 @@ extern "C" int gist_out_proj_w4(const void* attn_out, const void* w, const void*
   PagedProblem pb{};
   int rc = gattn::check_w4(dims, d_model, group, false, &pb);
   if (rc != GIST_ATTN_OK) return rc;
-  if (d_model % 16 != 0 || pb.Hq * pb.d % group != 0) return GIST_ATTN_ERR_UNSUPPORTED;
+  if (d_model % 16 != 0 || pb.Hq * pb.d % group != 0 || pb.Hq * pb.d > gattn::kMostModel) return GIST_ATTN_ERR_UNSUPPORTED;
   if (pb.T == 0) return GIST_ATTN_OK;
   if (!attn_out || !w || !w_scale || !y) return GIST_ATTN_ERR_NULL;
   if (!aligned(attn_out, 16) || !aligned(w, 16) || !aligned(w_scale, 2) || !aligned(y, 16) ||

@@ -9,7 +9,7 @@
 // Up to 16 tokens here, more in proj_w4_tc.cu.
 //
 // The weights are read once and dominate the bytes: HBM bound (one token, 4096 -> 6144, 13 MB:
-// 7.2 us, of which the floor is 1.9; 5 tokens, 896 -> 1152: 3.6 us, launch and latency).  The codes less 8 are
+// 7.0 us, of which the floor is 1.9; 5 tokens, 896 -> 1152: 3.6 us, launch and latency).  The codes less 8 are
 // exact in bf16, so the inner sums run on mma.sync m16n8k16 with the weights
 // as the 16 rows and the tokens as the N (even one token is cheaper there than on
 // the CUDA cores, which would spend an FMA and a conversion a weight); the scale
@@ -96,6 +96,29 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   };
   for (int i = 0; i < kStages - 1; ++i) issue(i);
 
+  // ---- scales of a step, a step ahead
+  const int shift = 31 - __clz(p.group), per32 = p.group / 32;
+  const uint16_t* scale[MR][2];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      scale[m][h] = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)(max(row[m], 0) + h * apart + g8) * (p.K >> shift);
+  uint32_t next[MR][4][2] = {};
+  auto load_scales = [&](int i) {
+    const int k = k0 + (wk + i * WK) * kStep;
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kk = k + 32 * q;
+          if (q % per32 == per32 - 1) next[m][q][h] = row[m] >= 0 && i < mine && kk < k1 ? load_scale(scale[m][h] + (kk >> shift)) : 0;
+        }
+  };
+  load_scales(0);
+
   // ---- x: eight inputs as the pairs (k, k + 4), zeros past the inputs
   const int pieces = p.slice / 8;
   for (int i = tid; i < staged * pieces; i += kThreads) {
@@ -112,26 +135,17 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   for (int m = 0; m < MR; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-  const int shift = 31 - __clz(p.group), per32 = p.group / 32;
-  const uint16_t* scale[MR][2];
-#pragma unroll
-  for (int m = 0; m < MR; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      scale[m][h] = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)(max(row[m], 0) + h * apart + g8) * (p.K >> shift);
 
   for (int i = 0; i < mine; ++i) {
     const int k = k0 + (wk + i * WK) * kStep;
-    uint16_t sc[MR][4][2];
+    uint32_t sc[MR][4][2];
 #pragma unroll
     for (int m = 0; m < MR; ++m)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kk = k + 32 * q;
-          if (q % per32 == per32 - 1) sc[m][q][h] = row[m] >= 0 && kk < k1 ? __ldg(scale[m][h] + (kk >> shift)) : 0;
-        }
+        for (int h = 0; h < 2; ++h) sc[m][q][h] = next[m][q][h];
+    load_scales(i + 1);
     cp_async_wait_group<kStages - 2>();
     __syncwarp();
     const uint32_t st = ring + (i % kStages) * MR * 1024;
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(sum[m][n][e], __uint_as_float((uint32_t)sc[m][q][e >> 1] << 16), acc[m][n][e]);
+            for (int e = 0; e < 4; ++e) acc[m][n][e] = fmaf(sum[m][n][e], __uint_as_float(sc[m][q][e >> 1] << 16), acc[m][n][e]);
       }
     }
     __syncwarp();

@@ -77,12 +77,6 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // an
       : "memory");
 }
 
-// A scale, read where it stands: the compiler may move a plain load down to its use.
-__device__ __forceinline__ uint32_t load_scale(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 

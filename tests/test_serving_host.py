@@ -199,3 +199,10 @@ def test_packed_weights_by_hand():
     code = np.stack([w.w.numpy() & 15, w.w.numpy() >> 4], -1).reshape(4, 64).astype(float) - 8
     want = sum((x[:, 32 * g:32 * g + 32] @ code[:, 32 * g:32 * g + 32].T) * w.scale.double().numpy()[:, g] for g in range(2))
     np.testing.assert_allclose(w.times(x)[0], want, rtol=1e-12)
+
+
+def test_out_proj_refuses_more_inputs_than_it_stages(lib):
+    """K = Hq d up to 65536, for any number of tokens."""
+    for T in (1, 8, 64):
+        assert out_proj(lib, d=dict(BASE, num_tokens=T, num_q_heads=1026, num_kv_heads=2)) == UNSUPPORTED  # 1026 heads of 64
+        assert out_proj(lib, d=dict(BASE, num_tokens=T, num_q_heads=1024, num_kv_heads=2), w=0) == NULL
