@@ -15,15 +15,19 @@
 // kernel; the order of the sums is fixed.
 //
 // A tile: S^T = K q^T on mma.sync m16n8k16 (the keys are the 16 rows, the heads the N),
-// then O^T += V^T P with V^T by ldmatrix.trans and P by movmatrix.  q (rotated in
-// fp32) and P keep 16 bits as bf16 hi + lo; up to four heads take columns 0-3 for hi
-// and 4-7 for lo of one MMA, more take two MMAs.  The maximum moves only where a score
-// is more than 8 (log2) above it, so that a tile needs one vote in place of a reduction.
+// then O^T += V^T P with V^T by ldmatrix.trans and P by movmatrix.  q (rotated in fp32) and P
+// are sums of three bf16 terms, which hold all of fp32's bits: products are exact, sums fp32,
+// and of the outputs 0.03 % are not the exact value's bf16 (0.1 % where scores pass a hundred); with
+// two terms, 17 bits, 0.4 and 0.6 %, and large scores lost their last digits to q's.  The third
+// term costs 1.5 % of the time of the 48 requests below.  Up to two heads have the terms side by
+// side in the columns of one MMA, up to four in those of two, more take three MMAs.  The
+// maximum moves only where a score is more than 8 (log2) above it, so that a tile needs one vote
+// in place of a reduction.
 //
-// Warps an SM: twelve with rings of two tiles of 128-wide heads (192 KB) take 2 % less than
-// eight with three (123.7 and 121.1 us at the 48 requests below; 11: 121.3, 10: 121.9, six: 8 %
-// more), but leave 168 registers a thread, which sixteen heads (255) do not fit.  Heads of 64
-// keep eight with six tiles: twelve cost six short conversations 0.7 us and gain nothing.
+// Warps an SM: twelve with rings of two tiles of 128-wide heads (192 KB) take the least time of
+// 48 requests (123.1 us; 11: 124.0, 10: 124.4; with two terms eight with three tiles took 2 % more than
+// twelve, six 8 %), but leave 168 registers a thread, which sixteen heads (255) do not fit.  Heads of
+// 64 keep eight with six tiles: twelve cost six short conversations 0.7 us and gain nothing.
 //
 // Bound: HBM (every K/V byte is read once; at most 32 flops a byte).  48 requests of
 // 200-9000 keys, 32/8 heads of 128 (757 MB): 121 us, 0.92 of the copy rate; 32/32 heads
@@ -98,9 +102,16 @@ struct __align__(16) Tile {
 };
 constexpr uint32_t kFirst = 32, kLast = 64;
 
-template <int D, int MODE>
+// Heads a unit: 2, 4, 8 or 16.  q and P are sums of three bf16 terms; a step of 16 dimensions (keys) is one
+// MMA with them side by side in the columns (up to two heads), one of two and one of the third (four), or
+// three.
+template <int H>
+struct Terms {
+  static constexpr int beside = H == 2 ? 3 : H == 4 ? 2 : 1, mmas = H == 2 ? 1 : H == 4 ? 2 : 3;
+};
+template <int D, int H>
 struct Ring {
-  static constexpr bool many = D == 128 && MODE < 2;
+  static constexpr bool many = D == 128 && H < 16;
   static constexpr int warps = many ? 12 : 8, threads = warps * 32;
   static constexpr int stages = many ? 2 : D == 128 ? 3 : 6;
   static constexpr uint32_t tile = kKeys * D * 2, stage = 2 * tile;
@@ -129,14 +140,29 @@ __device__ __forceinline__ void write_pair(const Bf16Params& p, int r, int unit,
   *reinterpret_cast<uint32_t*>(p.out + ((int64_t)p.row(r) * p.Hq + g * p.G + head) * D + e) =
       none ? 0u : float2_to_bf16x2(a * inv, b * inv);
 }
+// Two fp32 as sums of three bf16, each the rounded remainder of the ones before: all of their bits.
+__device__ __forceinline__ void terms3(uint64_t v, uint32_t (&t)[3]) {
+  t[0] = f2_to_bf16x2(v);
+  v = f2_sub(v, bf16x2_to_f2(t[0]));
+  t[1] = f2_to_bf16x2(v);
+  t[2] = f2_to_bf16x2(f2_sub(v, bf16x2_to_f2(t[1])));
+}
+// The term that the `part`-th part of the columns has in MMA i of a step (none: zeros).
+template <int H>
+__device__ __forceinline__ uint32_t term_of(const uint32_t (&t)[3], int i, int part) {
+  const int beside = Terms<H>::beside;
+  if (beside == 1) return t[i];
+  if (beside == 2) return i == 0 ? (part == 0 ? t[0] : t[1]) : part == 0 ? t[2] : 0u;
+  return part == 0 ? t[0] : part == 1 ? t[1] : part == 2 ? t[2] : 0u;
+}
 // What a part with maximum m counts for beside a common maximum `top`.
 __device__ __forceinline__ float weight(float m, float top) { return m == top ? 1.f : ex2_approx(m - top); }
 
-// MODE 0: up to four heads, hi and lo side by side; 1: up to eight; 2: up to sixteen.
-template <int D, int MODE>
-__global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
-  constexpr int H = MODE == 0 ? 4 : MODE == 1 ? 8 : 16, NT = MODE == 2 ? 2 : 1, KS = D / 16, HK = KS / 2;
-  using R = Ring<D, MODE>;
+template <int D, int H>
+__global__ void __launch_bounds__(Ring<D, H>::threads, 1) decode_kernel(const __grid_constant__ Bf16Params p) {
+  constexpr int NT = H == 16 ? 2 : 1, KS = D / 16, HK = KS / 2, BESIDE = Terms<H>::beside, MMAS = Terms<H>::mmas,
+                COLS = H < 8 ? H : 8, SUMS = MMAS == 3 ? 3 : 2 * MMAS;
+  using R = Ring<D, H>;
   constexpr int kWarps = R::warps, kThreads = R::threads, S = R::stages, PIECES = D / 8;  // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int warp_sum[kWarps], start_r, start_pre, total;
@@ -250,7 +276,7 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
     const bf16* rows = p.q + ((int64_t)p.row(t.r) * p.Hq + g * p.G + h0) * D + t4 * 8;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int col = MODE == 0 ? g8 & 3 : n * 8 + g8;
+      const int col = n * 8 + (g8 & (COLS - 1));
 #pragma unroll
       for (int i = 0; i < CQ; ++i)
         raw[n][i] = h0 + col < p.G ? *reinterpret_cast<const uint4*>(rows + col * D + i * 32) : make_uint4(0, 0, 0, 0);
@@ -262,7 +288,7 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
   }
   for (int x = w0; x < w0 + S - 1; ++x) issue(x);
 
-  uint32_t qh[NT][KS][2], ql[NT][KS][2];
+  uint32_t qt[NT][MMAS][KS][2];
   float m[NT][2], l[NT][2], o[KS][NT][4];
   auto turn_q = [&](const Tile& t) {
     const int pos = max(p.length(t.r) - 1, 0);
@@ -297,13 +323,14 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
         for (int n = 0; n < NT; ++n) {
           const uint64_t x = bf16x2_to_f2(word[n][ks][e]), y = bf16x2_to_f2(word[n][ks + HK][e]);
           const uint64_t a = f2_sub(f2_mul(x, cs), f2_mul(y, sn)), b = f2_fma(x, sn, f2_mul(y, cs));
-          const uint32_t ah = f2_to_bf16x2(a), bh = f2_to_bf16x2(b);
-          const uint32_t al = f2_to_bf16x2(f2_sub(a, bf16x2_to_f2(ah))), bl = f2_to_bf16x2(f2_sub(b, bf16x2_to_f2(bh)));
-          const bool low = MODE == 0 && g8 >= 4;
-          qh[n][ks][e] = low ? al : ah;
-          qh[n][ks + HK][e] = low ? bl : bh;
-          ql[n][ks][e] = al;
-          ql[n][ks + HK][e] = bl;
+          uint32_t at[3], bt[3];
+          terms3(a, at);
+          terms3(b, bt);
+#pragma unroll
+          for (int i = 0; i < MMAS; ++i) {
+            qt[n][i][ks][e] = term_of<H>(at, i, g8 / COLS);
+            qt[n][i][ks + HK][e] = term_of<H>(bt, i, g8 / COLS);
+          }
         }
       }
 #pragma unroll
@@ -336,23 +363,15 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
     wrong |= t.at < 0;
     const int keys = t.info & 31;
     const uint32_t st = ring + (x - w0) % S * R::stage;
-    float s[NT][4], s2[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+    float s[NT][4], sums[NT][SUMS][4] = {};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t a[4];
       ldsm_x4(st + swz<D>(lane & 15, 2 * ks + (lane >> 4)), a);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (MODE == 0 && (ks & 1)) {
-          mma_16816(s2[n], a, qh[n][ks][0], qh[n][ks][1]);
-        } else {
-          mma_16816(s[n], a, qh[n][ks][0], qh[n][ks][1]);
-          if (MODE != 0) mma_16816(s2[n], a, ql[n][ks][0], ql[n][ks][1]);
-        }
+#pragma unroll
+        for (int i = 0; i < MMAS; ++i) mma_16816(sums[n][(i + ks * MMAS) % SUMS], a, qt[n][i][ks][0], qt[n][i][ks][1]);
       }
     }
     bool rise = false;
@@ -360,8 +379,11 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float v = s[n][e] + s2[n][e];
-        if (MODE == 0) v += __shfl_xor_sync(0xffffffffu, v, 2);
+        float v = sums[n][0][e];
+#pragma unroll
+        for (int i = 1; i < SUMS; ++i) v += sums[n][i][e];
+#pragma unroll
+        for (int sh = COLS / 2; sh < 4; sh <<= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
         v *= p.scale_log2;
         if (g8 + (e >> 1) * 8 >= keys) v = -INFINITY;
         s[n][e] = v;
@@ -386,7 +408,7 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
           }
         }
     }
-    uint32_t ph[NT][2], pl[NT][2];
+    uint32_t pt[NT][MMAS][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
@@ -395,10 +417,10 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
         const float a = ex2_approx(s[n][2 * h] - m0), b = ex2_approx(s[n][2 * h + 1] - m1);
         l[n][0] += a;
         l[n][1] += b;
-        const uint32_t hi2 = float2_to_bf16x2(a, b);
-        const uint32_t lo2 = f2_to_bf16x2(f2_sub(f2_make(a, b), bf16x2_to_f2(hi2)));
-        ph[n][h] = movmatrix_trans(MODE == 0 && t4 >= 2 ? lo2 : hi2);
-        if (MODE != 0) pl[n][h] = movmatrix_trans(lo2);
+        uint32_t t3[3];
+        terms3(f2_make(a, b), t3);
+#pragma unroll
+        for (int i = 0; i < MMAS; ++i) pt[n][i][h] = movmatrix_trans(term_of<H>(t3, i, 2 * t4 / COLS));
       }
     }
 #pragma unroll
@@ -408,8 +430,8 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
       ldsm_x4_trans(st + R::tile + swz<D>((lane & 7) + ((lane >> 4) << 3), 2 * d + ((lane >> 3) & 1)), a);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        mma_16816(o[d][n], a, ph[n][0], ph[n][1]);
-        if (MODE != 0) mma_16816(o[d][n], a, pl[n][0], pl[n][1]);
+#pragma unroll
+        for (int i = 0; i < MMAS; ++i) mma_16816(o[d][n], a, pt[n][i][0], pt[n][i][1]);
       }
     }
     __syncwarp();
@@ -424,13 +446,13 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], sh);
         if (wrong) l[n][c] = kBad;
-        if (MODE == 0) {
+#pragma unroll
+        for (int sh = COLS / 2; sh < 4; sh <<= 1)
 #pragma unroll
           for (int d = 0; d < KS; ++d) {
-            o[d][n][c] += __shfl_xor_sync(0xffffffffu, o[d][n][c], 2);
-            o[d][n][c + 2] += __shfl_xor_sync(0xffffffffu, o[d][n][c + 2], 2);
+            o[d][n][c] += __shfl_xor_sync(0xffffffffu, o[d][n][c], sh);
+            o[d][n][c + 2] += __shfl_xor_sync(0xffffffffu, o[d][n][c + 2], sh);
           }
-        }
       }
     const int unit = t.info >> 8;
     if (begins && ends) {
@@ -442,7 +464,7 @@ __global__ void __launch_bounds__(Ring<D, MODE>::threads, 1) decode_kernel(const
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int h = n * 8 + (MODE == 0 ? (t4 & 1) * 2 : t4 * 2) + c;
+          const int h = n * 8 + 2 * t4 % COLS + c;
           if (lane < 4 && h0 + h < p.G && !none && !(l[n][c] > 0.f && l[n][c] <= 3.0e38f)) report(p.status, GIST_ATTN_STATUS_RANGE);
         }
         const float i0 = 1.f / l[n][0], i1 = 1.f / l[n][1];
@@ -661,13 +683,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   write_pair<D>(p, id.z, id.w, h0 + h, e + 2, o.z, o.w, unit_sum[h]);
 }
 
-int heads_of(const PagedProblem& pb) { return pb.G <= 4 ? 4 : pb.G <= 8 ? 8 : 16; }
+int heads_of(const PagedProblem& pb) { return pb.G <= 2 ? 2 : pb.G <= 4 ? 4 : pb.G <= 8 ? 8 : 16; }
 size_t part_bytes(const PagedProblem& pb) { return (size_t)heads_of(pb) * (pb.d + 2) * sizeof(float); }
 
-template <int D, int MODE>
+template <int D, int H>
 int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
   const int ctas = sms < kMostCtas ? sms : kMostCtas;
-  constexpr int H = MODE == 0 ? 4 : MODE == 1 ? 8 : 16;
   Bf16Params p{};
   p.q = static_cast<const bf16*>(pb.q);
   p.pool = reinterpret_cast<const bf16*>(pb.pool);
@@ -690,16 +711,16 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
   p.num_blocks = pb.num_blocks;
   p.L = pb.L;
   p.layer = pb.layer;
-  p.least = Ring<D, MODE>::warps;
+  p.least = Ring<D, H>::warps;
   p.ctas = ctas;
   p.scale_log2 = pb.scale_log2;
   for (int j = 0; j < 64; ++j) p.turn[j] = pb.turn[j];
-  constexpr int smem = Ring<D, MODE>::bytes;
-  if (cudaFuncSetAttribute(decode_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  constexpr int smem = Ring<D, H>::bytes;
+  if (cudaFuncSetAttribute(decode_kernel<D, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GIST_ATTN_ERR_LAUNCH;
-  if (!launch_following(decode_kernel<D, MODE>, dim3(ctas), dim3(Ring<D, MODE>::threads), smem, stream, 0, p)) return GIST_ATTN_ERR_LAUNCH;
+  if (!launch_following(decode_kernel<D, H>, dim3(ctas), dim3(Ring<D, H>::threads), smem, stream, 0, p)) return GIST_ATTN_ERR_LAUNCH;
   // where units are few each has many parts: a block for two of its heads
-  const bool few = (int64_t)pb.B * pb.Hkv * p.chunks * 4 < ctas;
+  const bool few = H > 2 && (int64_t)pb.B * pb.Hkv * p.chunks * 4 < ctas;
   const dim3 grid = few ? dim3(pb.B * pb.Hkv * p.chunks, H / 2) : dim3(ctas);
   return launch_following(few ? join_kernel<D, H, 2> : join_kernel<D, H, H>, grid, dim3(kJoinThreads), 0, stream, 0, p)
              ? GIST_ATTN_OK
@@ -709,18 +730,21 @@ int launch(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream
 }  // namespace
 
 size_t paged_bf16_workspace(const PagedProblem& pb, int sms) {
-  const int warps = pb.d == 64 ? Ring<64, 0>::warps : pb.G <= 8 ? Ring<128, 0>::warps : Ring<128, 2>::warps;
+  const int warps = pb.d == 64 ? Ring<64, 8>::warps : pb.G <= 8 ? Ring<128, 8>::warps : Ring<128, 16>::warps;
   return (size_t)sms * (sizeof(int4) + (2 + warps) * part_bytes(pb));
 }
 
 int launch_paged_bf16(const PagedProblem& pb, void* workspace, int sms, cudaStream_t stream) {
+  const int H = heads_of(pb);
   if (pb.d == 64)
-    return pb.G <= 4   ? launch<64, 0>(pb, workspace, sms, stream)
-           : pb.G <= 8 ? launch<64, 1>(pb, workspace, sms, stream)
-                       : launch<64, 2>(pb, workspace, sms, stream);
-  return pb.G <= 4   ? launch<128, 0>(pb, workspace, sms, stream)
-         : pb.G <= 8 ? launch<128, 1>(pb, workspace, sms, stream)
-                     : launch<128, 2>(pb, workspace, sms, stream);
+    return H == 2   ? launch<64, 2>(pb, workspace, sms, stream)
+           : H == 4 ? launch<64, 4>(pb, workspace, sms, stream)
+           : H == 8 ? launch<64, 8>(pb, workspace, sms, stream)
+                    : launch<64, 16>(pb, workspace, sms, stream);
+  return H == 2   ? launch<128, 2>(pb, workspace, sms, stream)
+         : H == 4 ? launch<128, 4>(pb, workspace, sms, stream)
+         : H == 8 ? launch<128, 8>(pb, workspace, sms, stream)
+                  : launch<128, 16>(pb, workspace, sms, stream);
 }
 
 }  // namespace gattn
