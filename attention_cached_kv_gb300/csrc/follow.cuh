@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 namespace gattn {
 
@@ -12,6 +13,19 @@ namespace gattn {
 __device__ __forceinline__ void let_follow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Everything before this kernel on its stream is done, and its results can be read.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads behind wait_before() of what the kernel before may have written.  Not ld.global.nc (__ldg): that is
+// for data which nothing writes while the kernel runs, and this one may have been on the GPU then,
+// on an SM that still holds what the same buffer had before.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load2(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // Launches a kernel that calls wait_before(); `cluster` CTAs a cluster along x (0: none).
 template <class... P, class... A>

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int kk = k + 32 * q;
-          if (q % per32 == per32 - 1) next[m][q][h] = row[m] >= 0 && i < mine && kk < k1 ? load_scale(scale[m][h] + (kk >> shift)) : 0;
+          if (q % per32 == per32 - 1) next[m][q][h] = row[m] >= 0 && i < mine && kk < k1 ? load2(scale[m][h] + (kk >> shift)) : 0;
         }
   };
   load_scales(0);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
   for (int i = tid; i < staged * pieces; i += kThreads) {
     const int t = i / pieces, c = i - t * pieces, k = k0 + c * 8;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (t < tokens && k < k1) v = ldg16(p.x + (int64_t)(t0 + t) * p.K + k);
+    if (t < tokens && k < k1) v = load16(p.x + (int64_t)(t0 + t) * p.K + k);
     sts16(xs + t * pitch + c * 16, make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
   }

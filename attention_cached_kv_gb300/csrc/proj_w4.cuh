@@ -23,12 +23,6 @@ struct W4Params {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-// A scale, read where it stands: the compiler may move a plain load down to its use.
-__device__ __forceinline__ uint32_t load_scale(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
-}
 // Bytes of x (0-3) and y (4-7) by a selector; with bit 3 of a selector's digit set, the byte's sign.
 __device__ __forceinline__ uint32_t permute(uint32_t x, uint32_t y, uint32_t sel) {
   uint32_t r;

@@ -187,17 +187,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int e = 0; e < TN; ++e) acc[e] = 0.f;
     const int n = n0 + (warp & 3) * 32 + lane;
     const uint16_t* scale = reinterpret_cast<const uint16_t*>(p.scale) + (int64_t)min(n, p.N - 1) * (p.K / p.group) + k0 / p.group;
-    constexpr int kAhead = 4;  // scales are read so many groups ahead (and converted when used)
+    constexpr int kAhead = 4;  // scales are read so many groups ahead (where load2 stands: it is volatile), converted when used
     uint32_t next[kAhead];
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) next[g] = g < groups ? load_scale(scale + g) : 0;
+    for (int g = 0; g < kAhead; ++g) next[g] = g < groups ? load2(scale + g) : 0;
     for (int g0 = 0; g0 < groups && !failed; g0 += kAhead) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int g = g0 + j;
         if (g >= groups) break;
         const float now = __uint_as_float(next[j] << 16);
-        next[j] = g + kAhead < groups ? load_scale(scale + g + kAhead) : 0;
+        next[j] = g + kAhead < groups ? load2(scale + g + kAhead) : 0;
         if (!wait(&bars.d_full[g & 1], g >> 1)) break;
         tc::fence_after_sync();
         const uint32_t d = tmem + lanes + kSA * 64 + (g & 1) * TN;
