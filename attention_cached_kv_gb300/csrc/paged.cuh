@@ -139,10 +139,11 @@ struct Requests {
 
 // Sums count(r) over the requests (the NT threads of a CTA, all of them), finds the
 // request that holds unit at(total) of the running sum and the units before it.
-// *start_r is -1 where there is no such unit.
+// *start_r is -1 where there is no such unit.  Thread t's requests are the t-th (B + NT - 1) / NT ones; the
+// units before them go to before_thread[t], if it is given.
 template <int NT, class Int, class Count, class At>
 __device__ __forceinline__ void scan_requests(int B, Count count, Int* warp_sum, int* start_r, Int* start_pre,
-                                              Int* total, At at) {
+                                              Int* total, At at, Int* before_thread = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (B + NT - 1) / NT;
   const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
@@ -165,6 +166,7 @@ __device__ __forceinline__ void scan_requests(int B, Count count, Int* warp_sum,
     all += s;
   }
   if (tid == 0) *total = all;
+  if (before_thread) before_thread[tid] = before;
   const Int x = at(all);
   if (x >= before && x < before + own) {
     for (int r = r0; r < r1; ++r) {
