@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(Ring<D, H>::threads, 1) decode_kernel(const __
       while (x >= pre + n * p.units()) {
         pre += n * p.units();
         n = p.tiles(++r);
-        // a request without a token: there may be thousands, so on to the thread's requests that
-        // hold the tile, which are 43 at most of 16384 (two requests 16 k slots apart: 34 us, 1740 with a walk over them all)
+        // a request without a token: there may be thousands, so on to the thread's requests that hold
+        // the tile, 43 of 16384 at most (two requests 16 k slots apart: 34 us, 1740 with a walk over
+        // them all)
         if (n == 0 && !jumped) {
           jumped = true;
           int t = 0;
