@@ -1,21 +1,11 @@
 // paged_tc.cuh -- tcgen05 wrappers of the paged kernels beside those of tcgen05.cuh:
-// products of 8-bit operands, and one lane to issue them.
+// products of 8-bit operands.
 #pragma once
 
 #include "tcgen05.cuh"
 
 namespace gattn {
 namespace tc {
-
-// One lane of a converged warp, the same one every time.  The compiler knows the code
-// under it to be a single thread's and keeps descriptors in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
-}
 
 // Instruction descriptor for kind::f8f6f4 with E4M3 A and B, fp32 accumulate.
 // a_mn_major: A stored with M contiguous.

@@ -25,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "follow.cuh"
+#include "frag.cuh"
 #include "proj_w4.cuh"
 
 namespace cg = cooperative_groups;
@@ -37,11 +38,6 @@ constexpr int kStep = 128;   // inputs of a ring stage
 constexpr int kStages = 8;   // of a warp's ring, 1 KB a row tile each
 constexpr int kMaxX = 72 * 1024;  // staged x of a CTA, at most
 
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 // First row of a tile, and its other eight rows' distance.
 __device__ __forceinline__ int tile_row(const W4Params& p, int tile, int& apart) {
   if (!p.position) {

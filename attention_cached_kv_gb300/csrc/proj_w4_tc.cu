@@ -67,27 +67,9 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {  // and waits
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// One lane of a warp that has converged.  Under elect.sync the compiler keeps the operands of
-// tcgen05.mma in uniform registers; behind `lane == 0` it moves them there for each MMA, which
-// takes 47 cycles an MMA in place of the 16 (32 tokens) or 32 (64) that the tensor core needs.
-__device__ __forceinline__ bool elected() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e != 0;
-}
 
 // TN tokens, groups of 16 PG inputs (PG MMAs).
 template <int TN, int PG>
@@ -120,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_load_2d(base + s * L::tile_b, &tm_x, &bars.b_full[s], k0 + i * kChunk, t0);
     tma_load_2d(base + s * L::tile_b + TN * 128, &tm_x, &bars.b_full[s], k0 + i * kChunk + 64, t0);
   };
-  if (warp > kMma && elected()) {
+  if (warp > kMma && tc::elect_one()) {
     for (int s = 0; s < kRaw; ++s) mbar_init(&bars.c_full[s], 1), mbar_init(&bars.c_empty[s], 4);
     for (int s = 0; s < kSB; ++s) mbar_init(&bars.b_full[s], 1), mbar_init(&bars.b_empty[s], 1);
     fence_mbar_init();
@@ -204,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int h = 0; h < TN / 16; ++h) {
           uint32_t v[16];
-          ld16(d + 16 * h, v);
+          tc::ld16_wait(d + 16 * h, v);
           if (h == TN / 16 - 1) {
             tc::fence_before_sync();  // the accumulator is read: the next group but one may have it
             __syncwarp();
@@ -217,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == kMma) {
     // ------------------------------------------ MMAs, by one thread and with few instructions
-    if (elected()) {
+    if (tc::elect_one()) {
       constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, TN, 0);
       const uint64_t x0 = tc::smem_desc_sw128(base, 16, 1024);  // addresses in units of 16 bytes
       constexpr int kGroups = 8 / PG;  // of a chunk
@@ -248,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     // ------------------------------------------------------- codes and x, further stages
-    if (elected()) {
+    if (tc::elect_one()) {
       int xs = min(chunks, kSB), cs = min(chunks, kRaw);  // asked for so far
       while (cs < chunks || xs < chunks) {
         if (xs < chunks) {
