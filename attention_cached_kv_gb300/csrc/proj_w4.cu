@@ -6,7 +6,7 @@
 //
 //   y[t][n] = sum over groups of  s[n][group] * sum_{k in group} (c[n][k] - 8) x[t][k]
 //
-// Up to 16 tokens here, more in proj_w4_tc.cu.
+// Few tokens here (one or two, more of small weights: few_tokens() below), more in proj_w4_tc.cu.
 //
 // The weights are read once and dominate the bytes: HBM bound (one token, 4096 -> 6144, 13 MB:
 // 7.0 us, of which the floor is 1.9; 5 tokens, 896 -> 1152: 3.6 us, launch and latency).  The codes less 8 are
@@ -249,11 +249,22 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
              : GIST_ATTN_ERR_LAUNCH;
 }
 
+// Which kernel: this one reads the weights again for each eight tokens, that of proj_w4_tc.cu once for up to
+// 64, but it has to fill 128 rows a CTA, and its clusters to exchange sums.  With M = 2^20 weights this one
+// takes about 2 us and 0.5 a M and eight tokens, that one 4.3 us and 0.35 a chunk of 128 inputs that a
+// CTA has (us, this / that: 1 M, 32 tokens 3.3-3.5 / 5.0-7.2; 2 M, 16: 3.1 / 4.6, 24: 5.5 / 4.9; 4 M, 16: 8.6 / 5.7;
+// 25 M, 16: 28.6 / 9.6; 64 M, 16: 86 / 14.0; 64 rows of 65536 inputs, 32: 20.8 / 26.8, 64: 31.3 / 29.1).
+// (3 M, eight: 4.5 / 4.7; 5 M, eight: 6.7 / 6.1; 6 M, three and eight: 5.1, 9.4 / 5.6; 12 M, four and eight: 9.3, 11.0 /
+// 6.9).  One or two tokens take this one, which is 3 us ahead (25 M, one: 7.1 / 9.6; 48 M: 13.7 / 16.5) or 2 behind
+// (64 M: 15.8 / 13.4; where K is split over a cluster).  Past 64 tokens that one always.
+bool few_tokens(const W4Params& p, int sms) {
+  if (p.T <= 2 || p.T > 64) return p.T <= 2;
+  const int64_t m = 1 << 20;
+  return (int64_t)p.N * p.K * ((p.T + 7) / 8) <= 3 * m + w4_tc_chunks(p, sms) * (m / 2);
+}
+
 int launch(const W4Params& p, int sms, cudaStream_t stream) {
-  if (p.T > 16) return launch_w4_tc(p, sms, stream);
-  // the tokens in one pass where their part of x fits beside the rings, in two where not
-  const int rc = p.T > 8 ? launch_as<2, 1, 1>(p, sms, stream) : GIST_ATTN_ERR_UNSUPPORTED;
-  return rc == GIST_ATTN_ERR_UNSUPPORTED ? launch_as<1, 1, 1>(p, sms, stream) : rc;
+  return few_tokens(p, sms) ? launch_as<1, 1, 1>(p, sms, stream) : launch_w4_tc(p, sms, stream);
 }
 
 }  // namespace

@@ -95,7 +95,8 @@ __device__ __forceinline__ void finish_pair(const W4Params& p, int t, int n, int
   y[far] = __float2bfloat16(b);
 }
 
-// Many tokens (proj_w4_tc.cu).
+// Many tokens (proj_w4_tc.cu), and the chunks of 128 inputs that a CTA of it has.
 int launch_w4_tc(const W4Params& p, int sms, cudaStream_t stream);
+int w4_tc_chunks(const W4Params& p, int sms);
 
 }  // namespace gattn

@@ -1,5 +1,5 @@
-// proj_w4_tc.cu -- the 4-bit projections of 17 tokens and more on the 5th-generation
-// tensor core: 128 rows of weights are M, up to 64 tokens are N, so that the weights are
+// proj_w4_tc.cu -- the 4-bit projections of more than a few tokens (few_tokens() of
+// proj_w4.cu says which) on the 5th-generation tensor core: 128 rows of weights are M, up to 64 tokens are N, so that the weights are
 // still read once.
 //
 //   D[n][t] = sum_{k in group} (c[n][k] - 8) x[t][k]     (tcgen05 kind::f16, A in TMEM)
@@ -309,6 +309,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_wait();  // no CTA leaves while its sums are being sent
 }
 
+// Chunks of K for each of `split` CTAs.
+int chunks_of(int K, int split) { return ((K + kChunk - 1) / kChunk + split - 1) / split; }
+// Parts of K: two CTAs an SM, where K has a few chunks for each.
+int parts_of(const W4Params& p, int token_blocks, int sms) {
+  const int64_t tiles = (p.N + kRows - 1) / kRows;
+  int split = 1;
+  while (split < 8 && tiles * token_blocks * split * 2 <= 2 * sms && split * 4 <= chunks_of(p.K, 1)) split *= 2;
+  return split;
+}
+
 template <int TN, int PG>
 int launch_as(W4Params p, int sms, cudaStream_t stream) {
   const EncodeTiledFn enc = encode_tiled_fn();
@@ -325,11 +335,8 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return GIST_ATTN_ERR_UNSUPPORTED;
-  const int tiles = (p.N + kRows - 1) / kRows, token_blocks = (p.T + TN - 1) / TN, chunks = (p.K + kChunk - 1) / kChunk;
-  // two CTAs an SM, where K has a few chunks for each
-  int split = 1;
-  while (split < 8 && (int64_t)tiles * token_blocks * split * 2 <= 2 * sms && split * 4 <= chunks) split *= 2;
-  p.slice = (chunks + split - 1) / split * kChunk;
+  const int tiles = (p.N + kRows - 1) / kRows, token_blocks = (p.T + TN - 1) / TN, split = parts_of(p, token_blocks, sms);
+  p.slice = chunks_of(p.K, split) * kChunk;
   constexpr int smem = Layout<TN>::bytes;
   if (token_blocks > 65535) return GIST_ATTN_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(w4_tc_kernel<TN, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -340,6 +347,8 @@ int launch_as(W4Params p, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int w4_tc_chunks(const W4Params& p, int sms) { return chunks_of(p.K, parts_of(p, 1, sms)); }
 
 int launch_w4_tc(const W4Params& p, int sms, cudaStream_t stream) {
   if (p.T <= 32)

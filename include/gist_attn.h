@@ -691,8 +691,8 @@ int gist_pages_copy(void* kv_pool, float* kv_scale, int32_t elem_bytes, const in
  * GIST_ATTN_ERR_UNSUPPORTED otherwise), K = Hq d.
  *   attn_out bf16 [T][Hq][d], y bf16 [T][d_model] (written)
  * T is num_tokens; sums are fp32 in a fixed order.  More than 64 tokens run as several
- * passes over the weights (use gist_qkv_rope and gist_out_proj for prompts).  Calls of more than 16
- * tokens wait for their copies and products for a second at most, then set
+ * passes over the weights (use gist_qkv_rope and gist_out_proj for prompts).  Calls of more than
+ * two tokens wait for their copies and products for a second at most, then set
  * GIST_ATTN_STATUS_TIMEOUT: outputs are unspecified where it is set.  Reads
  * num_tokens, num_q_heads, num_kv_heads, head_dim, status and (QKV) rope_theta of dims.  K and
  * d_model are at most 65536, (Hq + 2 Hkv) d at most 2^18 and T at most 2^20
