@@ -29,12 +29,14 @@
 // twelve, six 8 %), but leave 168 registers a thread, which sixteen heads (255) do not fit.  Heads of
 // 64 keep eight with six tiles: twelve cost six short conversations 0.7 us and gain nothing.
 //
-// Bound: HBM (every K/V byte is read once; at most 32 flops a byte).  48 requests of
-// 200-9000 keys, 32/8 heads of 128 (757 MB): 121 us, 0.92 of the copy rate; 32/32 heads
+// Bound: HBM, up to 16 heads a KV head (every K/V byte is read once; at most 32 flops a byte).  48
+// requests of 200-9000 keys, 32/8 heads of 128 (757 MB): 122 us, 0.92 of the copy rate; 32/32 heads 124 us,
 // 0.94.  What is left there: SMs are not equally near to memory, with equal runs
 // some take 1.13 times the mean.  One sequence of 180 k keys, 14/2 heads of 64 (92 MB):
-// 25 us, 4.5 of them before the first keys and 5.6 in the two joins.  Six short
-// conversations: 9.8 us.
+// 26 us, 4.5 of them before the first keys and 5.6 in the two joins.  Six short
+// conversations: 9.8 us.  More than 16 heads a KV head are units of 16, each of which reads the keys
+// again, from L2 where it can: 16 requests of 4000 keys with 2 KV heads of 128 (66 MB) take 31.5 us with
+// 32 heads, 39 with 64 and 58 with 128; 32 of them with one KV head and 128 heads 99 us.
 //
 // Pages: [KV page] "为什么自回归推理缓存 KV，而不缓存历史 Q？";
 //        [Suffix page] icman.com.cn news 64898.

@@ -8,8 +8,10 @@
 //
 // Few tokens here (one or two, more of small weights: few_tokens() below), more in proj_w4_tc.cu.
 //
-// The weights are read once and dominate the bytes: HBM bound (one token, 4096 -> 6144, 13 MB:
-// 7.0 us, of which the floor is 1.9; 5 tokens, 896 -> 1152: 3.6 us, launch and latency).  The codes less 8 are
+// Bound: latency.  Its floor is the weights' bytes, but a CTA asks for all of its part (32 KB of codes, then
+// 8 KB of x at 4096 inputs) at once, and start, one round of loads and the sums of its warps follow
+// one another: one token, 4096 -> 6144, 13 MB: 7.1 us, 8.0 with weights that L2 has not, for a floor of
+// 1.9; 5 tokens, 896 -> 1152: 3.6 us.  The codes less 8 are
 // exact in bf16, so the inner sums run on mma.sync m16n8k16 with the weights
 // as the 16 rows and the tokens as the N (even one token is cheaper there than on
 // the CUDA cores, which would spend an FMA and a conversion a weight); the scale

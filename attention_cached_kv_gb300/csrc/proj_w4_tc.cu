@@ -5,17 +5,19 @@
 //   D[n][t] = sum_{k in group} (c[n][k] - 8) x[t][k]     (tcgen05 kind::f16, A in TMEM)
 //   acc[n][t] += s[n][group] D[n][t]                     (fp32 registers)
 //
-// The codes less 8 are exact in bf16; the group's scale cannot go into them (the product
-// has up to twelve bits), so each group's sums are read out of TMEM and scaled.  The
-// converted weights go through TMEM and not through shared memory: writing and reading
-// them there would cost 32 bytes for each 4 of codes, more than its bandwidth.
+// The codes less 8 are exact in bf16; with the group's scale they would be the sum of two bf16 (the
+// product has up to twelve bits) and take two MMAs, which has not been tried: here each group's
+// sums are read out of TMEM and scaled.  The converted weights go through TMEM and not through
+// shared memory: writing and reading them there would cost 32 bytes for each 4 of codes, more than its
+// bandwidth.
 //
 // A CTA has a tile of 128 rows and a part of K; the CTAs of a cluster have the parts
 // of one tile, send each other the rows that the other adds up (bulk copies between
 // their shared memories) and write those.  Warps: 0-3 convert (a thread a row, codes
 // into TMEM), 4-7 scale and add (a thread a row), one issues MMAs, one loads codes and x by TMA.
 //
-// 64 tokens, 8192 -> 8192 (36.7 MB): 17.1 us for a floor of 5.4; 32 tokens, 4096 -> 4096: 8.0 us.
+// 64 tokens, 8192 -> 8192 (36.7 MB): 17.3 us, 17.8 with weights that L2 has not, for a floor of 5.4; 32 tokens,
+// 4096 -> 4096: 8.0 and 8.3.
 // Bound: no one stage (a stage of 128 inputs takes 1300 cycles, two CTAs an SM; without the
 // conversion 1.0 us less, without the sums 1.7, without x 0.6, without most MMAs 0.6): one chunk
 // and the exchange take 7.4 us, the 15 further chunks 10, and 104 of 152 SMs have two CTAs.
