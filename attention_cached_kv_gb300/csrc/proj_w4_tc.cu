@@ -1,6 +1,6 @@
 // proj_w4_tc.cu -- the 4-bit projections of more than a few tokens (few_tokens() of
-// proj_w4.cu says which) on the 5th-generation tensor core: 128 rows of weights are M, up to 64 tokens are N, so that the weights are
-// still read once.
+// proj_w4.cu says which) on the 5th-generation tensor core: 128 rows of weights are M, up
+// to 64 tokens are N, so that the weights are still read once.
 //
 //   D[n][t] = sum_{k in group} (c[n][k] - 8) x[t][k]     (tcgen05 kind::f16, A in TMEM)
 //   acc[n][t] += s[n][group] D[n][t]                     (fp32 registers)
