@@ -19,7 +19,8 @@
 // are sums of three bf16 terms, which hold all of fp32's bits: products are exact, sums fp32,
 // and of the outputs 0.03 % are not the exact value's bf16 (0.1 % where scores pass a hundred); with
 // two terms, 17 bits, 0.4 and 0.6 %, and large scores lost their last digits to q's.  The third
-// term costs 1.5 % of the time of the 48 requests below.  Up to two heads have the terms side by
+// term costs 1.5 % of the time of the 48 requests below, 1-3 % where HBM is the bound, and up to a
+// fifth where the products are (128 heads on one KV head: 81 and 99 us).  Up to two heads have the terms side by
 // side in the columns of one MMA, up to four in those of two, more take three MMAs.  The
 // maximum moves only where a score is more than 8 (log2) above it, so that a tile needs one vote
 // in place of a reduction.
